@@ -340,6 +340,151 @@ rnnt_status_t rnnt_loss_fused_noalloc(const void *logits, rnnt_dtype_t dt, int64
  */
 rnnt_status_t rnnt_selftest_wait_timeout(int32_t *status_dev, int32_t polls, rnnt_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The label side of a transducer: the embedding that feeds the prediction
+ * network the labels the loss takes, and the beam search over the joiner's
+ * outputs.  No counterpart on the pages, which stop at the loss.
+ *
+ * All of these enqueue on `stream`, allocate nothing and never synchronise.
+ * status_dev (device int32, or NULL) receives RNNT_OK, or RNNT_INVALID_VALUE
+ * for what only the device can see.  Host-side errors are returned before
+ * anything is enqueued.  Unless said otherwise pointers are device pointers
+ * aligned to their element size; wider alignment (16 bytes, row strides too)
+ * gives wider accesses.
+ */
+
+/*
+ * rnnt_embed -- label embedding with scaling.
+ *
+ * Each of the B sequences has P = S + (has_start ? 1 : 0) places.  With
+ * has_start, place 0 holds `start` (blank, as a rule: the prediction network's
+ * first input); place p after it holds tokens[b][p - has_start].
+ *
+ *   out[b, p, :] = round(scale * weight[token, :]), in float32 and rounded
+ *   once; zeros where the token is negative or stands at or past lengths[b].
+ *
+ *   weight         (V, D) in dt, rows weight_stride >= D elements apart.
+ *   tokens         int32 (B, S), rows tokens_stride >= S apart; NULL if S = 0.
+ *                  Any negative token is padding (rnnt_beam_select writes -1
+ *                  for hypotheses that emit nothing).  Tokens at or past
+ *                  lengths[b] are not read.
+ *   lengths        int32 [B], or NULL: every token counts.
+ *   start          in [-V, V-1], a negative value counting from the end;
+ *                  ignored without has_start.
+ *   out            (B, P, D) contiguous in dt; must not overlap weight.
+ *   status_dev     RNNT_INVALID_VALUE for a token >= V (its place gets
+ *                  zeros) or a length outside [0, S] (taken as the nearer bound).
+ * 1 <= D <= 2^24, 1 <= B * P < 2^31.
+ */
+rnnt_status_t rnnt_embed(const void *weight, rnnt_dtype_t dt, int32_t V, int32_t D,
+                         int64_t weight_stride, const int32_t *tokens, int64_t tokens_stride,
+                         const int32_t *lengths, int32_t B, int32_t S, int32_t has_start,
+                         int32_t start, float scale, void *out, int32_t *status_dev,
+                         rnnt_stream_t stream);
+
+/* rnnt_embed_grad_workspace_size -- bytes of device scratch of rnnt_embed_grad:
+ * about 16 + D/4 bytes per place and a byte per id. */
+rnnt_status_t rnnt_embed_grad_workspace_size(int32_t B, int32_t S, int32_t has_start, int32_t V,
+                                             int32_t D, size_t *bytes);
+
+/*
+ * rnnt_embed_grad -- gradient of rnnt_embed with respect to weight:
+ *
+ *   grad_weight[v, :] = round(scale * sum over places with token v of grad_out[b, p, :])
+ *
+ * and zeros for ids that do not occur.  The places are sorted by id; sums are
+ * float32 in an order that depends on the tokens alone, so the same inputs
+ * give the same bits.  grad_out at padding is not read.
+ *
+ *   grad_out       (B, P, D) contiguous in dt.
+ *   grad_weight    (V, D) contiguous in dt, every row written; must not
+ *                  overlap grad_out.
+ *   workspace      rnnt_embed_grad_workspace_size() bytes, 256-byte aligned;
+ *                  contents are rewritten every call.
+ * tokens, lengths, start and status_dev as for rnnt_embed.
+ */
+rnnt_status_t rnnt_embed_grad(const void *grad_out, rnnt_dtype_t dt, const int32_t *tokens,
+                              int64_t tokens_stride, const int32_t *lengths, int32_t B, int32_t S,
+                              int32_t has_start, int32_t start, int32_t V, int32_t D, float scale,
+                              void *grad_weight, void *workspace, size_t workspace_bytes,
+                              int32_t *status_dev, rnnt_stream_t stream);
+
+/* Most hypotheses of a batch item, and the largest vocabulary, of the beam search. */
+#define RNNT_MAX_BEAM 64
+#define RNNT_MAX_BEAM_VOCAB (1 << 20)
+
+/* rnnt_beam_workspace_size -- bytes of device scratch of rnnt_beam_select. */
+rnnt_status_t rnnt_beam_workspace_size(int32_t B, int32_t K, int32_t V, int32_t Ko,
+                                       rnnt_dtype_t dt, size_t *bytes);
+
+/*
+ * rnnt_beam_select -- one step of beam search: of every batch item the Ko best
+ * extensions of its K hypotheses.
+ *
+ * Hypothesis k with score s offers, for each output v whose logit is above
+ * -inf, the candidate s + x_v - logsumexp(x) (s + x_v without
+ * fused_log_softmax).  A finished hypothesis offers itself alone: its score
+ * unchanged and token -1; its logits are not read.  One of score -inf offers
+ * nothing and its logits are not read.  Candidates are ordered by value (the
+ * values are compared in 64 bits), equal ones by hypothesis, then by token.
+ *
+ *   logits         (B, K, V) in dt: item b's hypothesis k starts at element
+ *                  b * batch_stride + k * beam_stride, its V logits adjacent.
+ *   scores         float [B, K].
+ *   finished       uint8 [B, K] (0 or not), or NULL: none.
+ *   out_scores     float [B, Ko], best first (each rounded once from 64 bits).
+ *   out_tokens     int32 [B, Ko]: the selected output, -1 for a finished one.
+ *   out_parents    int32 [B, Ko]: the hypothesis it extends.
+ *                  Places left over when fewer than Ko candidates exist get
+ *                  score -inf, token -1, parent -1.  The outputs must not
+ *                  overlap the inputs.
+ *   workspace      rnnt_beam_workspace_size() bytes, 256-byte aligned.
+ *   status_dev     RNNT_INVALID_VALUE for a score of +inf or NaN, or a
+ *                  hypothesis whose logits hold one; such a hypothesis offers
+ *                  nothing.
+ */
+rnnt_status_t rnnt_beam_select(const void *logits, rnnt_dtype_t dt, int32_t B, int32_t K, int32_t V,
+                               int64_t batch_stride, int64_t beam_stride, const float *scores,
+                               const uint8_t *finished, int32_t Ko, int32_t fused_log_softmax,
+                               float *out_scores, int32_t *out_tokens, int32_t *out_parents,
+                               void *workspace, size_t workspace_bytes, int32_t *status_dev,
+                               rnnt_stream_t stream);
+
+/* Most states of one rnnt_beam_reorder call. */
+#define RNNT_MAX_STATES 16
+
+/* A state of the hypotheses: rows of row_bytes adjacent bytes, one for every
+ * (batch item, hypothesis) and every index of up to three further axes (sizes
+ * n, 1 where unused).  Strides are in bytes and not negative. */
+typedef struct {
+    const void *src;
+    void *dst;
+    int64_t row_bytes;
+    int32_t n[3];
+    int64_t src_stride[3];
+    int64_t dst_stride[3];
+    int64_t src_batch;
+    int64_t src_beam;
+    int64_t dst_batch;
+    int64_t dst_beam;
+} rnnt_state_t;
+
+/*
+ * rnnt_beam_reorder -- the states of the selected hypotheses: for every state,
+ * batch item b and k < Ko, row(s) dst[b, k] = src[b, parents[b, k]]; zeros
+ * where the parent is -1.
+ *
+ *   states         HOST array of n_states (1 to RNNT_MAX_STATES); read during
+ *                  the call only.  No dst may overlap or interleave with a
+ *                  src (keep two buffers per state).
+ *   parents        int32 [B, Ko], each in [-1, K): out_parents of
+ *                  rnnt_beam_select.  Another value counts as -1 and sets
+ *                  status_dev to RNNT_INVALID_VALUE.
+ */
+rnnt_status_t rnnt_beam_reorder(const rnnt_state_t *states, int32_t n_states,
+                                const int32_t *parents, int32_t B, int32_t K, int32_t Ko,
+                                int32_t *status_dev, rnnt_stream_t stream);
+
 /* Static English description of a status code. */
 const char *rnnt_status_string(rnnt_status_t status);
 

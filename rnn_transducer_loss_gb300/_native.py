@@ -23,7 +23,9 @@ NOALLOC_SCRATCH_BYTES = 32 << 20     # RNNT_NOALLOC_SCRATCH_BYTES
 EXPORTS = ("rnnt_workspace_size", "rnnt_workspace_size_ex", "rnnt_loss_fused", "rnnt_loss_fused_ex",
            "rnnt_loss_fused_staged", "rnnt_grad_scale", "rnnt_set_trace",
            "rnnt_loss_fused_noalloc", "rnnt_selftest_wait_timeout", "rnnt_status_string",
-           "rnnt_abi_version", "rnnt_plan")
+           "rnnt_abi_version", "rnnt_plan", "rnnt_embed", "rnnt_embed_grad_workspace_size",
+           "rnnt_embed_grad", "rnnt_beam_workspace_size", "rnnt_beam_select",
+           "rnnt_beam_reorder")
 
 
 MAX_BIG_BLANKS = 8                    # RNNT_MAX_BIG_BLANKS
@@ -58,6 +60,20 @@ class Plan(ctypes.Structure):
     """rnnt_plan_t: whether one persistent kernel runs the call, and how many
     kernels the call enqueues."""
     _fields_ = [("persistent", ctypes.c_int32), ("launches", ctypes.c_int32)]
+
+
+MAX_BEAM = 64                         # RNNT_MAX_BEAM
+MAX_BEAM_VOCAB = 1 << 20              # RNNT_MAX_BEAM_VOCAB
+MAX_STATES = 16                       # RNNT_MAX_STATES
+
+
+class State(ctypes.Structure):
+    """rnnt_state_t: one state of rnnt_beam_reorder (strides in bytes)."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
+                ("row_bytes", ctypes.c_int64), ("n", ctypes.c_int32 * 3),
+                ("src_stride", ctypes.c_int64 * 3), ("dst_stride", ctypes.c_int64 * 3),
+                ("src_batch", ctypes.c_int64), ("src_beam", ctypes.c_int64),
+                ("dst_batch", ctypes.c_int64), ("dst_beam", ctypes.c_int64)]
 
 
 _lib = None
@@ -107,6 +123,20 @@ def load() -> ctypes.CDLL:
     lib.rnnt_plan.argtypes = [i32, i64, i32, i32, i32, i32, i32, ctypes.POINTER(Options),
                               ctypes.POINTER(Plan)]
     lib.rnnt_plan.restype = i32
+    lib.rnnt_embed.argtypes = [P, i32, i32, i32, i64, P, i64, P, i32, i32, i32, i32, f32, P, P, P]
+    lib.rnnt_embed.restype = i32
+    lib.rnnt_embed_grad_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.rnnt_embed_grad_workspace_size.restype = i32
+    lib.rnnt_embed_grad.argtypes = [P, i32, P, i64, P, i32, i32, i32, i32, i32, i32, f32, P, P, sz,
+                                    P, P]
+    lib.rnnt_embed_grad.restype = i32
+    lib.rnnt_beam_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.rnnt_beam_workspace_size.restype = i32
+    lib.rnnt_beam_select.argtypes = [P, i32, i32, i32, i32, i64, i64, P, P, i32, i32, P, P, P, P,
+                                     sz, P, P]
+    lib.rnnt_beam_select.restype = i32
+    lib.rnnt_beam_reorder.argtypes = [P, i32, P, i32, i32, i32, P, P]
+    lib.rnnt_beam_reorder.restype = i32
     _lib = lib
     return lib
 
@@ -211,3 +241,46 @@ def rnnt_plan(B, rows, V, dt, targets_stride, fused_log_softmax, want_grad=True,
     if rc != RNNT_OK:
         raise RNNTError(rc, "rnnt_plan")
     return {"persistent": bool(plan.persistent), "launches": int(plan.launches)}
+
+
+def rnnt_embed(weight, dt, V, D, weight_stride, tokens, tokens_stride, lengths, B, S, has_start,
+               start, scale, out, status_dev, stream) -> int:
+    """Raw call; pointer arguments are integers (device addresses) or None."""
+    return load().rnnt_embed(weight, dt, V, D, weight_stride, tokens, tokens_stride, lengths, B, S,
+                             has_start, start, scale, out, status_dev, stream)
+
+
+def rnnt_embed_grad_workspace_size(B, S, has_start, V, D) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().rnnt_embed_grad_workspace_size(B, S, has_start, V, D, ctypes.byref(out))
+    if rc != RNNT_OK:
+        raise RNNTError(rc, "rnnt_embed_grad_workspace_size")
+    return out.value
+
+
+def rnnt_embed_grad(grad_out, dt, tokens, tokens_stride, lengths, B, S, has_start, start, V, D,
+                    scale, grad_weight, workspace, workspace_bytes, status_dev, stream) -> int:
+    return load().rnnt_embed_grad(grad_out, dt, tokens, tokens_stride, lengths, B, S, has_start,
+                                  start, V, D, scale, grad_weight, workspace, workspace_bytes,
+                                  status_dev, stream)
+
+
+def rnnt_beam_workspace_size(B, K, V, Ko, dt) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().rnnt_beam_workspace_size(B, K, V, Ko, dt, ctypes.byref(out))
+    if rc != RNNT_OK:
+        raise RNNTError(rc, "rnnt_beam_workspace_size")
+    return out.value
+
+
+def rnnt_beam_select(logits, dt, B, K, V, batch_stride, beam_stride, scores, finished, Ko,
+                     fused_log_softmax, out_scores, out_tokens, out_parents, workspace,
+                     workspace_bytes, status_dev, stream) -> int:
+    return load().rnnt_beam_select(logits, dt, B, K, V, batch_stride, beam_stride, scores, finished,
+                                   Ko, fused_log_softmax, out_scores, out_tokens, out_parents,
+                                   workspace, workspace_bytes, status_dev, stream)
+
+
+def rnnt_beam_reorder(states, n_states, parents, B, K, Ko, status_dev, stream) -> int:
+    """states: a ctypes array of State (host memory)."""
+    return load().rnnt_beam_reorder(states, n_states, parents, B, K, Ko, status_dev, stream)
