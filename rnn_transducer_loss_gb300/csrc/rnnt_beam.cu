@@ -22,32 +22,35 @@ __device__ __forceinline__ uint32_t ordered(float x) {      // -0 counts as 0
 __device__ __forceinline__ float unordered(uint32_t o) {
     return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
-__device__ __forceinline__ uint64_t ordered(double x) {
-    const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
-    return b ^ ((b >> 63) ? ~0ull : 1ull << 63);
-}
-__device__ __forceinline__ double unordered(uint64_t o) {
-    return __longlong_as_double((long long)(o ^ ((o >> 63) ? 1ull << 63 : ~0ull)));
-}
-
 // ------------------------------------------------------------- rows of logits
-// A row is cut into splits of 16-byte vectors (counted from the row's first
-// address rounded down to 16); a CTA streams one split through registers in tiles
-// of kRowThreads * NV vectors, the next tile's loads in flight, and writes
+// A row is cut into splits of whole aligned 16-byte vectors (the few elements ahead of them
+// and behind them go to threads of split 0 one by one); a CTA streams one split through
+// registers and writes
 //   - the sum of exp(x - r) over the split and its reference r.  r is the first tile's
 //     maximum and changes only when a thread meets a value more than 16 above it, so
-//     that the running sum is (almost) never rescaled.
-//   - the n best elements in order.  The first tile's n-th best of the threads' bests
-//     bounds the n-th best element from below; later tiles only look for elements above
-//     the bound (one comparison a thread and tile, with the tile's maximum).
+//     that a sum is (almost) never rescaled.
+//   - the n best elements in order.  The stream keeps each thread's maximum of every
+//     tile and nothing else.  Every warp's ceil(n / 8)-th largest thread maximum bounds the
+//     n-th best element from below (the least of the eight does); the few tiles of a
+//     thread that reach the bound are read once more, from the cache, and their elements
+//     that reach it are ranked by counting.  Rows with a crowd of equal elements at the
+//     bound go through best_of_row instead, tile by tile.
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr float kLog2e = 1.44269504f;      // log2 e to 2^-26
 constexpr float kRescale = 16.0f;
 constexpr float kMostRef = 1e30f;          // larger references: computed again by exact_lse
+// Bound of a sum's relative error: 2^-22 of ex2.approx and 6 roundings of a tile's sum (a tree
+// over up to 33 elements; tiles are added with the rounding error carried along); half a
+// rounding of the exponent t = (x - ref) log2 e and 2^-26 of log2 e, both relative to t, whose
+// mean size over the distribution is at most log2 V - log2 S + 2 max(t, 0) (its entropy is at
+// most log2 V); rescalings, of which only the last two weigh anything.
+constexpr float kTermError = 2.4e-7f + 6 * 6e-8f;
+constexpr float kExponentError = 5.2e-8f;          // 1.25 * 2^-24 * ln 2
+constexpr float kRescaleError = 1e-6f;
 constexpr int kMaxLists = 256;             // splits of a batch item's rows
-constexpr int kBuf = 2560;                 // > RNNT_MAX_BEAM + (RNNT_MAX_BEAM - 1) * 32 + 1
-constexpr int kCrowd = 256;                // elements from which the buffer is cut to the n best
+constexpr int kSlots = 8;                  // of tiles, whose maxima a thread keeps
+constexpr int kBuf = 1024;                 // elements ranked: > RNNT_MAX_BEAM * 9 (best_of_row)
 
 struct SelectParams {
     const char* logits;
@@ -57,8 +60,8 @@ struct SelectParams {
     int32_t B, K, V, Ko, fused;
     int32_t splits, split_vecs;            // splits of a row, vectors of a split
     int32_t n;                             // elements a split lists: min(Ko, V)
-    double2* stat;                         // [row][split]: reference, sum of exp(x - reference)
-                                           // (negative if it was rescaled)
+    float4* stat;                          // [row][split]: reference, sum of exp(x - reference) as
+                                           // a pair, bound of the sum's relative error
     uint64_t* list;                        // [row][split][n]: ordered value << 32 | ~element
     float* out_scores;
     int32_t* out_tokens;
@@ -70,6 +73,21 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two float32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d)
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d)
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return reinterpret_cast<float2&>(d);
 }
 
 // A pair of floats whose exact sum is the value: about 47 bits, on float32 units (of which
@@ -92,75 +110,94 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
     return fast_two_sum(s.h, s.l + (a.l + b.l));
 }
 
+__device__ __forceinline__ Pair shuffled(Pair a, int o) {
+    return {__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
+}
+// Without the last step of add: for sums of positive terms.
+__device__ __forceinline__ Pair add_loosely(Pair a, Pair b) {
+    const Pair s = two_sum(a.h, b.h);
+    return {s.h, s.l + (a.l + b.l)};
+}
+// Pairs in the order of their values: for |l| <= half a step of h, as add leaves them.
+__device__ __forceinline__ uint64_t ordered(Pair a) {
+    return (uint64_t)ordered(a.h) << 32 | ordered(a.l);
+}
+__device__ __forceinline__ float difference(uint64_t a, uint64_t b) {
+    return (unordered((uint32_t)(a >> 32)) - unordered((uint32_t)(b >> 32))) +
+           (unordered((uint32_t)a) - unordered((uint32_t)b));
+}
+
 // Whether beam `row` offers its logits' candidates.
-__device__ __forceinline__ bool reads_logits(const SelectParams& p, int64_t row) {
+__device__ __forceinline__ bool reads_logits(const SelectParams& p, uint32_t row) {
     if (p.finished && p.finished[row]) return false;
     const float s = p.scores[row];
     return s > -INFINITY && s < INFINITY;
 }
 
 template <typename T>
-__device__ __forceinline__ const T* row_of(const SelectParams& p, int64_t row) {
-    const int64_t b = row / p.K;
+__device__ __forceinline__ const T* row_of(const SelectParams& p, uint32_t row) {
+    const uint32_t b = row / (uint32_t)p.K;
     return reinterpret_cast<const T*>(p.logits + b * p.batch_stride +
                                       (row - b * p.K) * p.beam_stride);
 }
 
-// Rank of the thread's key among the block's (0: none, returns kRowThreads): the warps sort
-// theirs (bitonic) and each key is searched for in the other warps' orders.
-__device__ __forceinline__ int block_rank(uint64_t key, uint64_t (*order)[32]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Sorts the warp's keys in descending order (bitonic).
+template <typename Key>
+__device__ __forceinline__ Key warp_sorted(Key key) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int size = 2; size <= 32; size *= 2) {
 #pragma unroll
         for (int o = size / 2; o; o >>= 1) {
-            const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+            const Key other = __shfl_xor_sync(0xffffffffu, key, o);
             const bool larger = ((lane & o) == 0) == ((lane & size) == 0 || size == 32);
             if (larger == (other > key)) key = other;
         }
     }
-    order[warp][lane] = key;      // descending: this thread now stands for another's key
-    __syncthreads();
-    if (!key) return kRowThreads;
-    int rank = lane;
-#pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) {
-        if (w == warp) continue;
-        int lo = 0;
-#pragma unroll
-        for (int step = 16; step; step >>= 1)
-            if (order[w][lo + step - 1] > key) lo += step;
-        if (lo == 31 && order[w][31] > key) lo = 32;
-        rank += lo;
+    return key;
+}
+
+// Ranks the buffer's c different keys: best[r] = the r-th for r < n.  Four threads count for a
+// key.  Ends without a barrier.
+__device__ __forceinline__ void rank_keys(const uint64_t* buf, int c, uint64_t* best, int n) {
+    const int part = threadIdx.x & 3;
+    for (int i0 = 0; i0 < c; i0 += kRowThreads / 4) {
+        const int i = i0 + (threadIdx.x >> 2);
+        const uint64_t mine = i < c ? buf[i] : ~0ull;
+        int rank = 0;
+        if (i < c)
+            for (int j = part; j < c; j += 4) rank += buf[j] > mine;
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+        if (i < c && rank < n && part == 0) best[rank] = mine;
     }
-    return rank;
 }
 
 // Keeps the n best of the buffer's keys, in order; all threads call it.
 __device__ __noinline__ void keep_best(uint64_t* buf, uint64_t* best, int* count, int n) {
-    const int c = *count;
-    for (int i = threadIdx.x; i < c; i += kRowThreads) {
-        const uint64_t mine = buf[i];
-        int rank = 0;
-        for (int j = 0; j < c; ++j) rank += buf[j] > mine;
-        if (rank < n) best[rank] = mine;
-    }
+    const int c = *count, m = min(c, n);
+    rank_keys(buf, c, best, n);
     __syncthreads();
-    const int m = min(c, n);
     if (threadIdx.x < m) buf[threadIdx.x] = best[threadIdx.x];
     if (threadIdx.x == 0) *count = m;
     __syncthreads();
 }
 
-// Elements [e0, e0 + 16 bytes) of a row of V; those outside it are -inf.
-template <typename T>
-__device__ __noinline__ uint4 load_partly(const T* x0, int e0, int V) {
-    constexpr int E = 16 / (int)sizeof(T);
-    Pack<T, 16> v;
+// The elements of a vector, two by two.
+__device__ __forceinline__ void unpack(const Pack<float, 16>& v, float2* y) {
+    y[0] = make_float2(v.e[0], v.e[1]);
+    y[1] = make_float2(v.e[2], v.e[3]);
+}
+__device__ __forceinline__ void unpack(const Pack<__half, 16>& v, float2* y) {
+    const __half2* h = reinterpret_cast<const __half2*>(&v.raw);
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        v.e[e] = e0 + e >= 0 && e0 + e < V ? x0[e0 + e] : from_f32<T>(-INFINITY);
-    return v.raw;
+    for (int i = 0; i < 4; ++i) y[i] = __half22float2(h[i]);
+}
+__device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, 16>& v, float2* y) {
+    const uint32_t w[4] = {v.raw.x, v.raw.y, v.raw.z, v.raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
 // Largest element of a vector (NaN is passed over).
@@ -178,155 +215,208 @@ __device__ __forceinline__ float vec_max(const Pack<__nv_bfloat16, 16>& v) {
     return fmaxf(__low2float(m), __high2float(m));
 }
 
+__device__ __forceinline__ uint64_t key_of(float x, int element) {
+    return (uint64_t)ordered(x) << 32 | (uint32_t)~element;
+}
+
+__device__ __forceinline__ uint4 load_stream(const uint4* at) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+    return v;
+}
+
+// A split: `vecs` vectors from `aligned` on, the first of them at element `first` of the row.
+template <typename T>
+struct Split {
+    static constexpr int E = 16 / (int)sizeof(T);
+    const uint4* aligned;
+    int first, vecs;
+
+    __device__ __forceinline__ Split(const SelectParams& p, uint32_t row, int split) {
+        const T* x0 = row_of<T>(p, row);
+        const int ahead = min(p.V, (int)(-(uintptr_t)x0 & 15) / (int)sizeof(T));
+        const int vec0 = split * p.split_vecs;
+        vecs = max(0, min(p.split_vecs, (p.V - ahead) / E - vec0));
+        first = ahead + vec0 * E;
+        aligned = reinterpret_cast<const uint4*>(x0 + ahead) + vec0;
+    }
+    // Vector j, -inf from vecs on.
+    __device__ __forceinline__ Pack<T, 16> at(int j) const {
+        Pack<T, 16> v;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v.e[e] = from_f32<T>(-INFINITY);
+        if (j < vecs) v.raw = load_stream(aligned + j);
+        return v;
+    }
+};
+
+// The element ahead of the row's whole vectors or behind them that is this thread's, or -1.
+template <typename T>
+__device__ __forceinline__ int odd_element(const SelectParams& p, uint32_t row, int split) {
+    constexpr int E = 16 / (int)sizeof(T);
+    if (split || threadIdx.x >= 2 * E) return -1;
+    const int ahead = min(p.V, (int)(-(uintptr_t)row_of<T>(p, row) & 15) / (int)sizeof(T));
+    const int behind = ahead + (p.V - ahead) / E * E;
+    const int at = threadIdx.x < E ? threadIdx.x : behind + threadIdx.x - E;
+    return at < (threadIdx.x < E ? ahead : p.V) ? at : -1;
+}
+
+// The n best of a split to best: every tile of kRowThreads vectors gives its elements above the
+// bound, the n-th best so far; a tile that has too many gives them element by element of each
+// thread's vector.
+template <typename T>
+__device__ __noinline__ void best_of_row(const SelectParams& p, uint32_t row, int split,
+                                         uint64_t* buf, uint64_t* best, int* count) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const Split<T> sp(p, row, split);
+    const int tid = threadIdx.x, n = p.n;
+    __syncthreads();
+    if (tid == 0) *count = 0;
+    uint64_t least = (uint64_t)(ordered(-INFINITY) + 1) << 32;     // keys below it do not matter
+    __syncthreads();
+    const int odd = odd_element<T>(p, row, split);
+    if (odd >= 0) {
+        const float x = to_f32(row_of<T>(p, row)[odd]);
+        if (x > -INFINITY) buf[atomicAdd(count, 1)] = key_of(x, odd);
+    }
+    for (int t0 = 0; t0 < sp.vecs; t0 += kRowThreads) {
+        const Pack<T, 16> v = sp.at(t0 + tid);
+        const int at = sp.first + (t0 + tid) * E;
+        for (int e0 = 0; e0 < E;) {
+            // as many elements of each thread as surely fit
+            __syncthreads();
+            const int have = *count;
+            int hits = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float x = to_f32(v.e[e]);
+                hits += e >= e0 && x > -INFINITY && key_of(x, at + e) >= least;
+            }
+            const int threads = __syncthreads_count(hits > 0);
+            if (!threads) break;
+            const int e1 = have + threads * (E - e0) <= kBuf ? E : e0 + 1;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float x = to_f32(v.e[e]);
+                const uint64_t c = key_of(x, at + e);
+                if (e >= e0 && e < e1 && x > -INFINITY && c >= least)
+                    buf[atomicAdd(count, 1)] = c;
+            }
+            e0 = e1;
+            __syncthreads();
+            if (*count > kRowThreads) {
+                keep_best(buf, best, count, n);
+                least = max(least, buf[n - 1]);        // n < kRowThreads
+            }
+        }
+    }
+    __syncthreads();
+    rank_keys(buf, *count, best, n);
+    __syncthreads();
+}
+
 template <typename T, int NV, bool FUSED>
-__global__ void __launch_bounds__(kRowThreads, 4) k_rows(const SelectParams p) {
+__global__ void __launch_bounds__(kRowThreads, NV == 1 ? 6 : 4) k_rows(const SelectParams p) {
     constexpr int E = 16 / (int)sizeof(T);
     constexpr int kTileVecs = kRowThreads * NV;
     __shared__ uint64_t buf[kBuf], best[RNNT_MAX_BEAM];
-    __shared__ uint64_t order[kRowWarps][32];
     __shared__ Pair wsum[kRowWarps];
-    __shared__ float wmax[kRowWarps];
-    __shared__ int count;
-    __shared__ uint64_t bound;
+    __shared__ float wref[kRowWarps], wleast[kRowWarps], wover[kRowWarps];
+    __shared__ float tops[kSlots][kRowThreads];
+    __shared__ int hit[kSlots * kRowThreads];      // slots to be read once more
+    __shared__ int hits, count, bads, rescales;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / p.splits;
-    const int split = (int)(blockIdx.x - row * p.splits);
-    if (!reads_logits(p, row)) return;
-    const T* x0 = row_of<T>(p, row);
-    const int head = (int)((uintptr_t)x0 & 15) / (int)sizeof(T);
-    const int vec0 = split * p.split_vecs;
-    const int vecs = max(0, min(p.split_vecs, (p.V + head + E - 1) / E - vec0));
-    Pack<T, 16> none;
+    const uint32_t row = blockIdx.x / (uint32_t)p.splits;
+    const int split = (int)(blockIdx.x - row * (uint32_t)p.splits);
+    const Split<T> sp(p, row, split);
+    const int vecs = sp.vecs;
+    auto load_tile = [&](Pack<T, 16>* v, int t0) {
+        if (t0 + kTileVecs <= vecs) {                        // for the whole block
 #pragma unroll
-    for (int e = 0; e < E; ++e) none.e[e] = from_f32<T>(-INFINITY);
-
-    // Vector j of the split; elements outside the row and the split read as -inf.
-    auto load = [&](Pack<T, 16>& v, int j) {
-        const int e0 = (vec0 + j) * E - head;
-        v.raw = none.raw;
-        if (j < vecs) {
-            if (e0 >= 0 && e0 + E <= p.V) v.raw = __ldg(reinterpret_cast<const uint4*>(x0 + e0));
-            else v.raw = load_partly(x0, e0, p.V);
+            for (int i = 0; i < NV; ++i)
+                v[i].raw = load_stream(sp.aligned + t0 + i * kRowThreads + tid);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[i] = sp.at(t0 + i * kRowThreads + tid);
         }
     };
     Pack<T, 16> v[NV], next[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) load(v[i], i * kRowThreads + tid);
-    if (tid == 0) count = 0;
+    load_tile(v, 0);
+    const int odd = odd_element<T>(p, row, split);
+    const float odd_x = odd >= 0 ? to_f32(row_of<T>(p, row)[odd]) : -INFINITY;
+    if (!reads_logits(p, row)) return;             // asked for while the loads are in flight
+    if (tid == 0) hits = count = bads = rescales = 0;
 
     float ref = 0.0f, sum = 0.0f, low = 0.0f;      // sum + low: the running sum
-    float above = -INFINITY;                       // only elements above it can be listed
-    bool bad = false, rescaled = false;
+    float most = odd_x;                            // the thread's maximum
+    bool bad = !FUSED && !(odd_x < INFINITY), rescaled = false;
+    int shift_slot = 0;                            // tiles of a slot: 1 << shift_slot
+    while ((vecs - 1) / kTileVecs >> shift_slot >= kSlots) ++shift_slot;
+    float slot_top = -INFINITY;
     for (int t0 = 0; t0 < vecs || t0 == 0; t0 += kTileVecs) {
-        if (t0 + kTileVecs < vecs) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) load(next[i], t0 + kTileVecs + i * kRowThreads + tid);
-        }
-        const int e0 = (vec0 + t0 + tid) * E - head;         // of the tile's vector 0
-        float tops[NV], top = -INFINITY;
+        if (t0 + kTileVecs < vecs) load_tile(next, t0 + kTileVecs);
+        float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            tops[i] = vec_max(v[i]);
-            top = fmaxf(top, tops[i]);
+            top = fmaxf(top, vec_max(v[i]));
             if (!FUSED) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) bad |= !(to_f32(v[i].e[e]) < INFINITY);
             }
         }
-        // Lists the elements of the tile whose key reaches least.
-        auto collect = [&](uint64_t least) {
-            const float from = unordered((uint32_t)(least >> 32));
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (!(tops[i] >= from)) continue;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float x = to_f32(v[i].e[e]);
-                    if (x >= from) {
-                        const uint64_t c = (uint64_t)ordered(x) << 32 |
-                                           (uint32_t)~(e0 + i * kRowThreads * E + e);
-                        if (c >= least) buf[atomicAdd(&count, 1)] = c;
-                    }
-                }
-            }
-        };
-        // Selection.  Every path leaves `count` settled behind a barrier.
-        bool all = t0 == 0;          // select within the tile first
-        if (!all) {
-            const int have = count;                // settled until the barrier
-            const int hits = __syncthreads_count(top > above);
-            if (hits && have + hits * NV * E > kBuf) {
-                keep_best(buf, best, &count, p.n);
-                all = true;
-            } else if (hits) {
-                if (top > above) collect(((uint64_t)ordered(above) + 1) << 32);
-                __syncthreads();
-            }
+        most = fmaxf(most, top);
+        slot_top = fmaxf(slot_top, top);
+        const int tile = t0 / kTileVecs;
+        if (((tile + 1) & ((1 << shift_slot) - 1)) == 0 || t0 + kTileVecs >= vecs) {
+            tops[tile >> shift_slot][tid] = slot_top;
+            slot_top = -INFINITY;
         }
-        if (all) {
-            // The thread's best element (its maximum's first place).
-            int where = -1;
-            if (top > above) {
-#pragma unroll
-                for (int i = NV - 1; i >= 0; --i)
-#pragma unroll
-                    for (int e = E - 1; e >= 0; --e)
-                        if (to_f32(v[i].e[e]) == top) where = e0 + i * kRowThreads * E + e;
-            }
-            const uint64_t key = where >= 0 ? (uint64_t)ordered(top) << 32 | (uint32_t)~where : 0;
-            if (tid == 0) bound = 0;
+        if (FUSED) {
             if (t0 == 0) {
+                top = fmaxf(top, odd_x);
                 float m = top;
 #pragma unroll
                 for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                if (lane == 0) wmax[warp] = m;
-            }
-            const int rank = block_rank(key, order);
-            if (rank == p.n - 1) bound = order[warp][lane];
-            __syncthreads();
-            if (t0 == 0) {
-                ref = wmax[0];
+                if (lane == 0) wref[warp] = m;
+                __syncthreads();
+                ref = wref[0];
 #pragma unroll
-                for (int w = 1; w < kRowWarps; ++w) ref = fmaxf(ref, wmax[w]);
+                for (int w = 1; w < kRowWarps; ++w) ref = fmaxf(ref, wref[w]);
                 if (!(fabsf(ref) < kMostRef)) ref = 0.0f;
             }
-            const uint64_t reach = bound;
-            if (key && key >= reach)
-                collect(max(reach, ((uint64_t)ordered(above) + 1) << 32));
-            __syncthreads();
-            if (reach) above = fmaxf(above, unordered((uint32_t)(reach >> 32)));
-        }
-        if (count > kCrowd) {
-            keep_best(buf, best, &count, p.n);
-            above = fmaxf(above, unordered((uint32_t)(buf[p.n - 1] >> 32)));   // n < kCrowd
-        }
-        if (FUSED) {
             if (top - ref > kRescale) {
-                const float to = fminf(top, kMostRef), f = ex2((ref - to) * kLog2e);
+                const float to = fminf(top, kMostRef), f = ex2(__fmul_rn(ref, kLog2e) - __fmul_rn(to, kLog2e));
                 sum *= f;
                 low *= f;
                 ref = to;
                 rescaled = true;
             }
-            const float shift = -ref * kLog2e;
+            const float shift = -__fmul_rn(ref, kLog2e);
+            const float2 scale2 = make_float2(kLog2e, kLog2e), shift2 = make_float2(shift, shift);
             float s[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 s[i] = 0.0f;
                 if (i && t0 + i * kRowThreads >= vecs) continue;     // for the whole block
-                float y[E];
+                float2 y[E / 2];
+                unpack(v[i], y);
 #pragma unroll
-                for (int e = 0; e < E; ++e) y[e] = ex2(__fmaf_rn(to_f32(v[i].e[e]), kLog2e, shift));
+                for (int e = 0; e < E / 2; ++e) {
+                    const float2 t = fma2(y[e], scale2, shift2);
+                    y[e] = make_float2(ex2(t.x), ex2(t.y));
+                }
 #pragma unroll
-                for (int o = E / 2; o; o /= 2)
+                for (int o = E / 4; o; o /= 2)
 #pragma unroll
-                    for (int e = 0; e < o; ++e) y[e] += y[e + o];
-                s[i] = y[0];
+                    for (int e = 0; e < o; ++e) y[e] = add2(y[e], y[e + o]);
+                s[i] = y[0].x + y[0].y;
             }
 #pragma unroll
             for (int o = NV / 2; o; o /= 2)
 #pragma unroll
                 for (int i = 0; i < o; ++i) s[i] += s[i + o];
+            if (t0 == 0) s[0] += ex2(__fmaf_rn(odd_x, kLog2e, shift));
             const float to = sum + s[0], part = to - sum;       // the sum's rounding error
             low += (sum - (to - part)) + (s[0] - part);
             sum = to;
@@ -334,60 +424,124 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_rows(const SelectParams p) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) v[i].raw = next[i].raw;
     }
-    // The threads' sums at the largest of their references.
-    float at = ref;
+    // The bound.
+    const int whole = min(vecs / 32, kRowWarps);       // warps whose threads all have a maximum
+    const int nth = (p.n - 1) / max(whole, 1);         // of each one's, from 0
+    float least = most;
+    if (nth == 0) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) least = fmaxf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    } else {
+        least = unordered(__shfl_sync(0xffffffffu, warp_sorted(ordered(most)), nth & 31));
+    }
+    if (lane == 0) wleast[warp] = least;
+    if (bad) bads = 1;
+    if (rescaled) rescales = 1;
+    __syncthreads();
+    least = whole && nth < 32 ? INFINITY : -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w)
+        if (w < whole) least = fminf(least, wleast[w]);
+    const int span = kTileVecs << shift_slot;
+    for (int t = 0; t * span < vecs; ++t) {
+        const bool reaches = tops[t][tid] >= least && tops[t][tid] > -INFINITY;
+        const unsigned who = __ballot_sync(0xffffffffu, reaches);
+        if (!who) continue;
+        int to = 0;
+        if (lane == 0) to = atomicAdd(&hits, __popc(who));
+        to = __shfl_sync(0xffffffffu, to, 0) + __popc(who & ((1u << lane) - 1));
+        if (reaches) hit[to] = t * kRowThreads + tid;
+    }
+    float at = ref;                                // the largest of the threads' references
     if (FUSED) {
-        const int any = __syncthreads_or(rescaled);
-        if (any) {
+        Pair total{sum, low};
+        float over = sum * fmaxf(0.0f, most - ref);
+        if (rescales) {
             float m = ref;
 #pragma unroll
             for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane == 0) wmax[warp] = m;
+            if (lane == 0) wref[warp] = m;
             __syncthreads();
-            at = wmax[0];
+            at = wref[0];
 #pragma unroll
-            for (int w = 1; w < kRowWarps; ++w) at = fmaxf(at, wmax[w]);
-            const float f = at != ref ? ex2((ref - at) * kLog2e) : 1.0f;
-            sum *= f;
-            low *= f;
+            for (int w = 1; w < kRowWarps; ++w) at = fmaxf(at, wref[w]);
+            const float f = at != ref ? ex2(__fmul_rn(ref, kLog2e) - __fmul_rn(at, kLog2e)) : 1.0f;
+            total = Pair{total.h * f, total.l * f};
+            over *= f;
         }
-        rescaled = any;
-        Pair total = two_sum(sum, low);
 #pragma unroll
-        for (int o = 16; o; o >>= 1)
-            total = add(total, Pair{__shfl_xor_sync(0xffffffffu, total.h, o),
-                                    __shfl_xor_sync(0xffffffffu, total.l, o)});
-        if (lane == 0) wsum[warp] = total;
+        for (int o = 16; o; o >>= 1) {
+            total = add_loosely(total, shuffled(total, o));
+            over += __shfl_xor_sync(0xffffffffu, over, o);
+        }
+        if (lane == 0) {
+            wsum[warp] = total;
+            wover[warp] = over;
+        }
     }
-    const int bads = __syncthreads_or(bad);
-    const int64_t unit = row * p.splits + split;
-    if (tid == 0) {
-        double r = (double)at, t = 0.0;
+    __syncthreads();
+    // Those slots' vectors once more: their elements that reach the bound.
+    const int per = NV << shift_slot;              // vectors of a slot
+    for (int i = tid; i < hits * per; i += kRowThreads) {
+        const int slot = hit[i / per];
+        const int j = slot / kRowThreads * span + i % per * kRowThreads + slot % kRowThreads;
+        const Pack<T, 16> w = sp.at(j);
+        unsigned which = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float x = to_f32(w.e[e]);
+            which |= (x >= least && x > -INFINITY ? 1u : 0u) << e;
+        }
+        if (which) {
+            int to = atomicAdd(&count, __popc(which));
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (which >> e & 1) {
+                    if (to < kBuf) buf[to] = key_of(to_f32(w.e[e]), sp.first + j * E + e);
+                    ++to;
+                }
+        }
+    }
+    if (odd_x >= least && odd_x > -INFINITY) {
+        const int to = atomicAdd(&count, 1);
+        if (to < kBuf) buf[to] = key_of(odd_x, odd);
+    }
+    __syncthreads();
+    const bool crowd = count > kBuf;
+    const uint32_t unit = blockIdx.x;
+    if (warp == kRowWarps - 1) {                   // the keys are ranked by the first ones
+        Pair total{0.0f, 0.0f};
+        float over = 0.0f, err = 0.0f;
         if (FUSED) {
-            Pair total = wsum[0];
+            if (lane < kRowWarps) {
+                total = wsum[lane];
+                over = wover[lane];
+            }
 #pragma unroll
-            for (int w = 1; w < kRowWarps; ++w) total = add(total, wsum[w]);
-            // x * log2e - round(at * log2e) = (x - r) * log2e
-            const float shift = -at * kLog2e;
-            r -= (double)__fmaf_rn(at, kLog2e, shift) * (1.0 / (double)kLog2e);
-            t = (double)total.h + (double)total.l;
-            if (rescaled) t = -t;
+            for (int o = kRowWarps / 2; o; o >>= 1) {
+                total = add(total, shuffled(total, o));
+                over += __shfl_xor_sync(0xffffffffu, over, o);
+            }
+            // x log2e - round(at log2e) = (x - at) log2e + off
+            const float off = __fmaf_rn(at, kLog2e, -__fmul_rn(at, kLog2e)) * (-1.0f / kLog2e);
+            if (fabsf(off) > 1e-3f) total = Pair{NAN, NAN};        // |at| above 10^4 or so
+            total = mul(total, two_sum(1.0f, off + 0.5f * off * off));
+            err = kTermError + (rescales ? kRescaleError : 0.0f) +
+                  kExponentError * (1e-3f + __log2f((float)p.V) - __log2f(total.h) +
+                                    2.9f * over / total.h);
         }
-        p.stat[unit] = make_double2(bads ? nan("") : r, t);
+        if (lane == 0)
+            p.stat[unit] = make_float4(FUSED ? at : bads ? NAN : 0.0f, total.h, total.l, err);
     }
-    const int c = count;
-    uint64_t* list = p.list + unit * p.n;
-    for (int i = tid; i < c; i += kRowThreads) {
-        const uint64_t mine = buf[i];
-        int rank = 0;
-        for (int j = 0; j < c; ++j) rank += buf[j] > mine;
-        if (rank < p.n) list[rank] = mine;
-    }
-    for (int i = c + tid; i < p.n; i += kRowThreads) list[i] = 0;
+    if (!crowd) rank_keys(buf, count, best, p.n);
+    __syncthreads();
+    if (crowd) best_of_row<T>(p, row, split, buf, best, &count);
+    for (int i = tid; i < p.n; i += kRowThreads)
+        p.list[(int64_t)unit * p.n + i] = i < min(count, p.n) ? best[i] : 0;
 }
 
 // ------------------------------------------------------- the logarithm, exactly
-// exp(x - ref) for x <= ref, relative error below 2^-43 down to e^-60: with
+// exp(x - ref) for x <= ref, relative error below 2^-40 down to e^-60: with
 // x - ref = n ln 2 + g (Cody and Waite's reduction: ln 2 in three parts, the first with few
 // bits so that n times it is exact), e^(g/16) - 1 by its Taylor series and four times
 // (1 + q)^2 - 1.
@@ -420,37 +574,35 @@ __device__ __forceinline__ Pair exp_pair(float x, float ref) {
     return {e.h * s1 * s2, e.l * s1 * s2};
 }
 
-// log s for 1 <= s < 2^140, off by less than 1e-12: one Newton step from the float32
+// log s for 1 <= s < 2^140, off by less than 2^-40: one Newton step from the float32
 // logarithm y, y + (s e^-y - 1).
-__device__ __forceinline__ double log_pair(double s) {
-    const float y = logf((float)s);
-    const Pair e = exp_pair(0.0f, y);
-    return (double)y + (s * ((double)e.h + (double)e.l) - 1.0);
+__device__ __forceinline__ Pair log_pair(Pair s) {
+    const float y = logf(s.h);
+    const Pair e = add(mul(s, exp_pair(0.0f, y)), Pair{-1.0f, 0.0f});
+    return add(Pair{y, 0.0f}, e);
 }
 
 // --------------------------------------------------------- the Ko best of all
-// One CTA per batch item; a list (beam, split) has four threads.  Lists whose head is not
+// One CTA per batch item; a list (beam, split) has kParts threads.  Lists whose head is not
 // among the Ko best heads hold nothing; of the others the elements from the Ko-th best
 // head on are ranked by counting.
 //
-// The fast sums leave a log-sum-exp off by error[k]: 2^-22 of ex2.approx; 5 roundings of
-// a tile's sum (a tree over up to 32 elements), tiles being added with the rounding error
-// carried along; half a rounding of the exponent t = (x - r) log2 e and 2^-26 of log2 e,
-// both relative to t, whose mean size over the distribution is at most
-// log2 V - log2 S + 2 t_max (its entropy is at most log2 V).  Where the order of two
-// candidates of different beams is closer than that, the beams' log-sum-exps are computed
+// The streamed sums leave a log-sum-exp off by error[k] (see kTermError).  Where the order of
+// two candidates of different beams is closer than that, the beams' log-sum-exps are computed
 // again to 40 bits and the selection is repeated.  With 50000 outputs the bound is about
 // 1e-6, and 1 call in 15 of 64 items x 16 beams meets such a pair.
-constexpr float kTermError = 2.4e-7f + 5 * 6e-8f;
-constexpr float kExponentError = 5.2e-8f;          // 1.25 * 2^-24 * ln 2
-constexpr float kRescaleError = 1e-6f;
-constexpr int kPickThreads = 1024;
+constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kParts = kPickThreads / kMaxLists;     // threads of a list
+constexpr int kTokenBits = 20;              // a candidate's number: beam, then token
+constexpr uint32_t kTokenMask = (1u << kTokenBits) - 1;
+static_assert(RNNT_MAX_BEAM_VOCAB <= 1 << kTokenBits, "a token fits");
 constexpr int kCand = RNNT_MAX_BEAM * (RNNT_MAX_BEAM + 1) / 2;
 
-// log sum exp of a row by the whole block, the same for equal rows wherever they lie.
+// log sum exp of a row by the whole block, the same for equal rows wherever they lie; NaN
+// where the row holds NaN or +inf.
 template <typename T>
-__device__ __noinline__ double exact_lse(const T* x, int V, Pair* sums, float* tops) {
+__device__ __noinline__ Pair exact_lse(const T* x, int V, Pair* sums, float* tops) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float top = -INFINITY;
     for (int i = tid; i < V; i += kPickThreads) top = fmaxf(top, to_f32(x[i]));
@@ -458,23 +610,24 @@ __device__ __noinline__ double exact_lse(const T* x, int V, Pair* sums, float* t
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) tops[warp] = top;
     __syncthreads();
-    top = tops[lane];
+    top = tops[lane & (kPickWarps - 1)];
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     Pair s{0.0f, 0.0f};
 #pragma unroll 2
-    for (int i = tid; i < V; i += kPickThreads) s = add(s, exp_pair(to_f32(x[i]), top));
+    for (int i = tid; i < V; i += kPickThreads) {
+        const float y = to_f32(x[i]);
+        s = add(s, y < INFINITY ? exp_pair(y, top) : Pair{NAN, NAN});
+    }
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        s = add(s, Pair{__shfl_xor_sync(0xffffffffu, s.h, o), __shfl_xor_sync(0xffffffffu, s.l, o)});
+    for (int o = 16; o; o >>= 1) s = add(s, shuffled(s, o));
     if (lane == 0) sums[warp] = s;
     __syncthreads();
-    s = sums[lane];
+    s = lane < kPickWarps ? sums[lane] : Pair{0.0f, 0.0f};
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        s = add(s, Pair{__shfl_xor_sync(0xffffffffu, s.h, o), __shfl_xor_sync(0xffffffffu, s.l, o)});
+    for (int o = 16; o; o >>= 1) s = add(s, shuffled(s, o));
     __syncthreads();
-    return (double)top + log_pair((double)s.h + (double)s.l);
+    return add(Pair{top, 0.0f}, log_pair(s));
 }
 
 template <typename T>
@@ -485,10 +638,9 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
     __shared__ uint64_t heads[kMaxLists];
     __shared__ uint64_t oval[RNNT_MAX_BEAM];           // the best, in order
     __shared__ uint32_t oid[RNNT_MAX_BEAM];
-    __shared__ double2 stat[kMaxLists];
-    __shared__ double lse[RNNT_MAX_BEAM];
-    __shared__ float score[RNNT_MAX_BEAM];
-    __shared__ double error[RNNT_MAX_BEAM];
+    __shared__ float4 stat[kMaxLists];
+    __shared__ Pair lse[RNNT_MAX_BEAM];
+    __shared__ float score[RNNT_MAX_BEAM], error[RNNT_MAX_BEAM];
     __shared__ uint8_t kind[RNNT_MAX_BEAM];            // 0 nothing, 1 logits, 2 finished
     __shared__ unsigned long long doubt, border;       // beams, a bit each
     __shared__ Pair sums[kPickWarps];
@@ -496,10 +648,10 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
     __shared__ int count, outside;
     __shared__ uint64_t bound;
     const int tid = threadIdx.x;
-    const int64_t b = blockIdx.x;
+    const uint32_t b = blockIdx.x;
     const int nlists = p.K * p.splits;
-    if (tid < nlists) stat[tid] = p.stat[b * nlists + tid];
-    for (int i = tid; i < nlists * p.n; i += kPickThreads) lists[i] = p.list[b * nlists * p.n + i];
+    const float4* all_stat = p.stat + (int64_t)b * nlists;
+    const uint64_t* all_list = p.list + (int64_t)b * nlists * p.n;
     float s = 0.0f;
     bool done = false;
     if (tid < p.K) {
@@ -507,46 +659,45 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
         done = p.finished && p.finished[b * p.K + tid];
     }
     if (tid == 0) doubt = 0;
+    if (tid < nlists) stat[tid] = all_stat[tid];
+    for (int i = tid; i < nlists * p.n; i += kPickThreads) lists[i] = all_list[i];
     __syncthreads();
     if (tid < p.K) {
         bool bad = !(s < INFINITY);
         int what = bad || s == -INFINITY ? 0 : done ? 2 : 1;
-        double l = 0.0, err = 0.0;
+        Pair l{0.0f, 0.0f};
+        float err = 0.0f;
         if (what == 1) {
-            const double2* st = stat + tid * p.splits;
-            double top = -INFINITY, sum = 0.0;
-            float high = -INFINITY;
+            const float4* st = stat + tid * p.splits;
+            const uint64_t* first = lists + tid * p.splits * p.n;
+            float top = -INFINITY, high = -INFINITY;
             for (int g = 0; g < p.splits; ++g) {
-                const uint64_t c = lists[(tid * p.splits + g) * p.n];
+                const uint64_t c = first[g * p.n];
                 if (c) high = fmaxf(high, unordered((uint32_t)(c >> 32)));
-                bad |= st[g].x != st[g].x || st[g].y != st[g].y;
-                if (st[g].y != 0.0) top = fmax(top, st[g].x);
+                bad |= st[g].x != st[g].x;
+                if (st[g].y != 0.0f) top = fmaxf(top, st[g].x);
             }
             bad |= high == INFINITY;
-            if (bad || high == -INFINITY) {
-                what = 0;
-            } else if (p.fused) {
-                const float logv = 1e-3f + __log2f((float)p.V);
+            if (p.fused && !bad) {
                 bool sure = top > -INFINITY;
-                float worst = 0.0f;
+                Pair sum{0.0f, 0.0f};                  // at the reference `top`
                 for (int g = 0; g < p.splits; ++g) {
-                    const double y = fabs(st[g].y);
-                    if (y == 0.0) continue;
-                    sure &= y < 1e30 && y > 1e-30;
-                    sum += st[g].x == top ? y : y * exp(st[g].x - top);
-                    const uint64_t c = lists[(tid * p.splits + g) * p.n];
-                    const float over = fmaxf(0.0f, unordered((uint32_t)(c >> 32)) - (float)st[g].x);
-                    worst = fmaxf(worst, kTermError + (st[g].y < 0.0 ? kRescaleError : 0.0f) +
-                                  kExponentError * (logv - __log2f((float)y) + 2.9f * over));
+                    const float4 q = st[g];
+                    if (q.y == 0.0f) continue;
+                    sure &= q.y < 1e30f && q.y > 1e-30f;           // not NaN either
+                    const Pair part{q.y, q.z};
+                    sum = add(sum, q.x == top ? part : mul(part, exp_pair(q.x, top)));
+                    err = fmaxf(err, q.w);
                 }
-                sure &= sum >= 1.0 && sum < 1e40;
+                sure &= sum.h >= 1.0f && sum.h < 1e30f;
                 if (sure) {
-                    l = top + log_pair(sum);
-                    err = (double)worst + 1e-9;
-                } else {
-                    atomicOr(&doubt, 1ull << tid);     // out of the fast sum's range
+                    l = add(Pair{top, 0.0f}, log_pair(sum));
+                } else if (high > -INFINITY || sum.h != sum.h) {
+                    atomicOr(&doubt, 1ull << tid);     // NaN, or out of the streamed sum's range
+                    high = 0.0f;
                 }
             }
+            if (bad || high == -INFINITY) what = 0;
         }
         if (bad && p.status) *p.status = RNNT_INVALID_VALUE;
         lse[tid] = l;
@@ -555,14 +706,18 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
         kind[tid] = (uint8_t)what;
     }
     __syncthreads();
-    const int list = tid >> 2, k = list / p.splits;    // of this thread
+    const int list = tid / kParts, part = tid % kParts, k = list / p.splits;    // of this thread
     for (unsigned long long again = doubt;;) {
         for (; again; again &= again - 1) {
             const int kk = __ffsll((long long)again) - 1;
-            const double l = exact_lse(row_of<T>(p, b * p.K + kk), p.V, sums, tops);
+            const Pair l = exact_lse(row_of<T>(p, b * p.K + kk), p.V, sums, tops);
             if (tid == 0) {
                 lse[kk] = l;
-                error[kk] = 0.0;
+                error[kk] = 0.0f;
+                if (l.h != l.h) {                      // it holds NaN
+                    kind[kk] = 0;
+                    if (p.status) *p.status = RNNT_INVALID_VALUE;
+                }
             }
         }
         if (tid == 0) {
@@ -574,28 +729,29 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
         const int what = list < nlists ? kind[k] : 0;
         // Ordered value of the list's element j, 0 if there is none.
         auto value = [&](int j) -> uint64_t {
-            if (what == 2) return list == k * p.splits && j == 0 ? ordered((double)score[k]) : 0;
+            if (what == 2) return list == k * p.splits && j == 0 ? ordered(Pair{score[k], 0.0f}) : 0;
             const uint64_t c = what == 1 && j < p.n ? lists[list * p.n + j] : 0;
-            return c ? ordered((double)score[k] + ((double)unordered((uint32_t)(c >> 32)) - lse[k]))
-                     : 0;
+            if (!c) return 0;
+            const Pair v = two_sum(score[k], unordered((uint32_t)(c >> 32)));
+            return ordered(add(v, Pair{-lse[k].h, -lse[k].l}));
         };
         auto number = [&](int j) {
-            return (uint32_t)k * (uint32_t)p.V + (what == 2 ? 0u : ~(uint32_t)lists[list * p.n + j]);
+            return (uint32_t)k << kTokenBits | (what == 2 ? 0u : ~(uint32_t)lists[list * p.n + j]);
         };
         const uint64_t first = value(0);
-        if ((tid & 3) == 0 && list < nlists) heads[list] = first;
+        if (part == 0 && list < nlists) heads[list] = first;
         __syncthreads();
         int rank = 0;
-        if (list < nlists)
-            for (int j = tid & 3; j < nlists; j += 4)
+        if (first)
+            for (int j = part; j < nlists; j += kParts)
                 rank += heads[j] > first || (heads[j] == first && j < list);
-        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+#pragma unroll
+        for (int o = 1; o < kParts; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
         if (first && rank == p.Ko - 1) bound = first;
         __syncthreads();
         // element j of the list of rank r has j + r better ones
         if (first && rank < p.Ko)
-            for (int j = tid & 3; j + rank < p.Ko; j += 4) {
+            for (int j = part; j + rank < p.Ko; j += kParts) {
                 const uint64_t v = value(j);
                 if (v < bound) break;
                 const int to = atomicAdd(&count, 1);
@@ -604,16 +760,18 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
             }
         __syncthreads();
         const int c = count, found = min(c, p.Ko);
-        for (int i0 = 0; i0 < c; i0 += kPickThreads / 4) {
-            const int i = i0 + (tid >> 2);
-            const uint64_t v = i < c ? cval[i] : 0;
+        constexpr int kCount = 4;                      // threads that count for a candidate
+        for (int i0 = 0; i0 < c; i0 += kPickThreads / kCount) {
+            const int i = i0 + tid / kCount;
+            const uint64_t v = i < c ? cval[i] : ~0ull;
             const uint32_t d = i < c ? cid[i] : 0;
             int r = 0;
-            for (int j = tid & 3; j < c; j += 4)
-                r += cval[j] > v || (cval[j] == v && cid[j] < d);
-            r += __shfl_xor_sync(0xffffffffu, r, 1);
-            r += __shfl_xor_sync(0xffffffffu, r, 2);
-            if (i < c && r < p.Ko && (tid & 3) == 0) {
+            if (i < c)
+                for (int j = tid % kCount; j < c; j += kCount)
+                    r += cval[j] > v || (cval[j] == v && cid[j] < d);
+#pragma unroll
+            for (int o = 1; o < kCount; o *= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
+            if (i < c && r < p.Ko && tid % kCount == 0) {
                 oval[r] = v;
                 oid[r] = d;
             }
@@ -622,24 +780,23 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
         if (!p.fused || found == 0) break;
         // Neighbours of different beams whose order is in doubt.
         if (tid + 1 < found) {
-            const int k0 = oid[tid] / p.V, k1 = oid[tid + 1] / p.V;
-            if (k0 != k1 &&
-                unordered(oval[tid]) - unordered(oval[tid + 1]) < error[k0] + error[k1])
-                atomicOr(&doubt, (error[k0] > 0.0 ? 1ull << k0 : 0) |
-                                 (error[k1] > 0.0 ? 1ull << k1 : 0));
+            const int k0 = oid[tid] >> kTokenBits, k1 = oid[tid + 1] >> kTokenBits;
+            if (k0 != k1 && difference(oval[tid], oval[tid + 1]) < error[k0] + error[k1])
+                atomicOr(&doubt, (error[k0] > 0.0f ? 1ull << k0 : 0) |
+                                 (error[k1] > 0.0f ? 1ull << k1 : 0));
         }
         // Beams with candidates as near to the last one, some of them left out.
         if (found == p.Ko && first) {
-            const double last = unordered(oval[found - 1]);
-            const double within = error[k] + error[oid[found - 1] / p.V];
-            const uint64_t lo = ordered(last - within), hi = ordered(last + within);
-            for (int j = tid & 3; j < p.n; j += 4) {
+            const uint64_t last = oval[found - 1];
+            const float within = error[k] + error[oid[found - 1] >> kTokenBits];
+            for (int j = part; j < p.n; j += kParts) {
                 const uint64_t v = value(j);
-                if (!v || v < lo) break;
-                if (v > hi) continue;
+                if (!v) break;
+                const float d = difference(v, last);
+                if (d < -within) break;
+                if (d > within) continue;
                 atomicOr(&border, 1ull << k);
-                if (v < oval[found - 1] || (v == oval[found - 1] && number(j) > oid[found - 1]))
-                    outside = 1;
+                if (v < last || (v == last && number(j) > oid[found - 1])) outside = 1;
             }
         }
         __syncthreads();
@@ -647,16 +804,16 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
         if (outside && __popcll(border) > 1)
             for (unsigned long long left = border; left; left &= left - 1) {
                 const int kk = __ffsll((long long)left) - 1;
-                if (error[kk] > 0.0) again |= 1ull << kk;
+                if (error[kk] > 0.0f) again |= 1ull << kk;
             }
-        __syncthreads();       // `doubt` and `border` have been read
         if (!again) break;
+        __syncthreads();       // `doubt` and `border` have been read
     }
     for (int r = tid; r < p.Ko; r += kPickThreads) {
-        const int64_t o = b * p.Ko + r;
-        const int from = r < min(count, p.Ko) ? (int)(oid[r] / p.V) : -1;
-        p.out_scores[o] = from < 0 ? -INFINITY : (float)unordered(oval[r]);
-        p.out_tokens[o] = from < 0 || kind[from] == 2 ? -1 : (int)(oid[r] - from * p.V);
+        const int64_t o = (int64_t)b * p.Ko + r;
+        const int from = r < min(count, p.Ko) ? (int)(oid[r] >> kTokenBits) : -1;
+        p.out_scores[o] = from < 0 ? -INFINITY : unordered((uint32_t)(oval[r] >> 32));
+        p.out_tokens[o] = from < 0 || kind[from] == 2 ? -1 : (int)(oid[r] & kTokenMask);
         p.out_parents[o] = from;
     }
 }
@@ -668,17 +825,17 @@ struct SelectLayout {
 SelectLayout select_layout(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt) {
     SelectLayout L;
     const int E = 16 / elem_size(dt);
-    const int64_t vecs = ((int64_t)V + 2 * (E - 1)) / E;      // the most, whatever the alignment
-    constexpr int64_t kWanted = 152 * 4;                      // CTAs that fill the device
-    int64_t splits = (kWanted + (int64_t)B * K - 1) / ((int64_t)B * K);
-    splits = std::min(splits, (vecs + kRowThreads - 1) / kRowThreads);
+    const int64_t vecs = std::max(1, V / E);                 // the most, whatever the alignment
+    // one tile a CTA where that gives no more than a wave of 6 CTAs an SM, else a wave of 4
+    const int64_t rows = (int64_t)B * K, tiles = (vecs + kRowThreads - 1) / kRowThreads;
+    int64_t splits = rows * tiles <= 152 * 6 ? tiles : std::min(tiles, 152 * 4 / rows);
     splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxLists / K));
     L.split_vecs = (int32_t)((vecs + splits - 1) / splits);
     L.splits = (int32_t)((vecs + L.split_vecs - 1) / L.split_vecs);
     L.n = std::min(Ko, V);
     const size_t units = (size_t)B * K * L.splits;
     L.stat = 0;
-    L.list = align256(units * sizeof(double2));
+    L.list = align256(units * sizeof(float4));
     L.total = align256(L.list + units * L.n * sizeof(uint64_t));
     return L;
 }
@@ -859,7 +1016,7 @@ extern "C" rnnt_status_t rnnt_beam_select(const void* logits, rnnt_dtype_t dt, i
     p.splits = L.splits;
     p.split_vecs = L.split_vecs;
     p.n = L.n;
-    p.stat = reinterpret_cast<double2*>(ws + L.stat);
+    p.stat = reinterpret_cast<float4*>(ws + L.stat);
     p.list = reinterpret_cast<uint64_t*>(ws + L.list);
     p.out_scores = out_scores;
     p.out_tokens = out_tokens;

@@ -88,8 +88,9 @@ def select(logits, scores, beam, finished=None, fused=True):
             if np.isnan(x).any() or (x == np.inf).any() or not (x > -np.inf).any():
                 continue
             top = x.max()
-            lse = top + np.log(np.sum(np.exp(x - top))) if fused else 0.0
-            cand += [(-(s + (x[v] - lse)), k, v) for v in np.flatnonzero(x > -np.inf)]
+            # in this order: top + log(..) would lose the logarithm where top is -3.4e38
+            p = (x - top) - np.log(np.sum(np.exp(x - top))) if fused else x
+            cand += [(-(s + p[v]), k, v) for v in np.flatnonzero(x > -np.inf)]
         for r, (c, k, v) in enumerate(sorted(cand)[:beam]):
             out[0][b, r], out[1][b, r], out[2][b, r] = -c, v, k
     return out
