@@ -424,15 +424,16 @@ rnnt_status_t rnnt_beam_workspace_size(int32_t B, int32_t K, int32_t V, int32_t 
  * Hypothesis k with score s offers, for each output v whose logit is above
  * -inf, the candidate s + x_v - logsumexp(x) (s + x_v without
  * fused_log_softmax).  A finished hypothesis offers itself alone: its score
- * unchanged and token -1; its logits are not read.  One of score -inf offers
- * nothing and its logits are not read.  Candidates are ordered by value (the
- * values are compared in 64 bits), equal ones by hypothesis, then by token.
+ * unchanged and token -1, whatever its logits hold.  One of score -inf offers
+ * nothing.  Candidates are ordered by value (to 40 bits), equal ones by
+ * hypothesis, then by token.
  *
  *   logits         (B, K, V) in dt: item b's hypothesis k starts at element
  *                  b * batch_stride + k * beam_stride, its V logits adjacent.
  *   scores         float [B, K].
  *   finished       uint8 [B, K] (0 or not), or NULL: none.
- *   out_scores     float [B, Ko], best first (each rounded once from 64 bits).
+ *   out_scores     float [B, Ko], best first; within 5e-6 of the value and one
+ *                  float32 rounding (without fused_log_softmax: the rounding).
  *   out_tokens     int32 [B, Ko]: the selected output, -1 for a finished one.
  *   out_parents    int32 [B, Ko]: the hypothesis it extends.
  *                  Places left over when fewer than Ko candidates exist get

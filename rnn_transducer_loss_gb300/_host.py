@@ -1,4 +1,9 @@
-"""What the label-side entry points share: argument checks, the current stream, the status word."""
+"""What the label-side entry points share: argument checks, the current stream, the status word.
+
+A small call's time is the host's (a Python call, the checks, one ctypes call, a launch), so
+these take few steps: one combined test of the arguments, whose parts are looked at again
+only to say what is wrong.
+"""
 from __future__ import annotations
 
 import torch
@@ -6,6 +11,9 @@ import torch
 from . import _native as N
 
 DTYPES = {torch.float32: N.RNNT_F32, torch.float16: N.RNNT_F16, torch.bfloat16: N.RNNT_BF16}
+
+current_device = torch._C._cuda_getDevice
+stream_of = torch._C._cuda_getCurrentRawStream      # of a device index, as an integer
 
 
 def int32(name, t, device):
@@ -15,28 +23,24 @@ def int32(name, t, device):
         raise ValueError(f"{name} must be on {device}")
 
 
-def stream_of(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def status_word(check, device):
+def status_word(device):
     """The device word a checked call reports to (the call itself resets it)."""
-    return torch.empty(1, dtype=torch.int32, device=device) if check else None
+    return torch.empty(1, dtype=torch.int32, device=device)
 
 
 def call(where, device, fn, *args):
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args)
+    """fn(*args, stream) with `device` current."""
+    index = device.index
+    if current_device() == index:
+        rc = fn(*args, stream_of(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args)
-    if rc != N.RNNT_OK:
+            rc = fn(*args, stream_of(index))
+    if rc:
         raise N.RNNTError(rc, where)
 
 
 def finish(where, status, wanted):
-    if status is None:
-        return
     code = int(status.item())
     if code == N.RNNT_INVALID_VALUE:
         raise ValueError(f"{where}: {N.status_string(code)} (wanted: {wanted})")

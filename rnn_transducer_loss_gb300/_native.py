@@ -7,6 +7,7 @@ missing the call raises (build it with ``python -m rnn_transducer_loss_gb300.bui
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -250,6 +251,7 @@ def rnnt_embed(weight, dt, V, D, weight_stride, tokens, tokens_stride, lengths, 
                              has_start, start, scale, out, status_dev, stream)
 
 
+@functools.lru_cache(maxsize=256)          # by the sizes alone
 def rnnt_embed_grad_workspace_size(B, S, has_start, V, D) -> int:
     out = ctypes.c_size_t(0)
     rc = load().rnnt_embed_grad_workspace_size(B, S, has_start, V, D, ctypes.byref(out))
@@ -265,6 +267,7 @@ def rnnt_embed_grad(grad_out, dt, tokens, tokens_stride, lengths, B, S, has_star
                                   status_dev, stream)
 
 
+@functools.lru_cache(maxsize=256)
 def rnnt_beam_workspace_size(B, K, V, Ko, dt) -> int:
     out = ctypes.c_size_t(0)
     rc = load().rnnt_beam_workspace_size(B, K, V, Ko, dt, ctypes.byref(out))

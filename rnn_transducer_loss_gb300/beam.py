@@ -2,11 +2,15 @@
 hypotheses) and ``rnnt_beam_reorder`` (the states of the selected ones)."""
 from __future__ import annotations
 
+from functools import lru_cache
+
 import torch
 
 from . import _native as N
 from ._host import DTYPES as _DT
-from ._host import call, finish, int32, status_word, stream_of
+from ._host import call, finish, int32, status_word
+
+_F32, _I32 = torch.float32, torch.int32
 
 
 def rnnt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beam: int | None = None,
@@ -20,61 +24,67 @@ def rnnt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beam: int | Non
     log-probabilities so far, ``beam`` (default K) how many to keep.  A
     hypothesis offers its score plus the log-probability of every output whose
     logit is above -inf; one that is ``finished`` ((B, K) bool or uint8) offers
-    itself alone, with its score unchanged and token -1, and its logits are not
-    read; one of score -inf offers nothing.  Values are compared in 64 bits,
-    ties go to the lowest hypothesis, then the lowest token.  ``parents`` says
-    which hypothesis each result extends (for :func:`rnnt_beam_reorder`); places
-    left over get score -inf, token -1, parent -1.  ``check`` reads the device
-    status word (one synchronisation) and raises on scores or logits that are
-    NaN or +inf; without it a hypothesis that holds one offers nothing.
+    itself alone, with its score unchanged and token -1, whatever its logits
+    hold; one of score -inf offers nothing.  The order is that of the exact
+    values to 40 bits (a returned score is within 5e-6 of its value and one
+    float32 rounding), ties go to the lowest hypothesis, then the lowest token.
+    ``parents`` says which hypothesis each result extends (for
+    :func:`rnnt_beam_reorder`); places left over get score -inf, token -1,
+    parent -1.  ``check`` reads the device status word (one synchronisation) and
+    raises on scores or logits that are NaN or +inf; without it a hypothesis
+    that holds one offers nothing.
     """
-    if not logits.is_cuda:
+    dt = _DT.get(logits.dtype)
+    device = logits.device
+    if device.type != "cuda":
         raise ValueError("logits must be a CUDA tensor")
-    if logits.dtype not in _DT:
+    if dt is None:
         raise ValueError(f"logits must be float32, float16 or bfloat16, got {logits.dtype}")
     if logits.dim() != 3:
         raise ValueError("logits must be (B, K, V)")
-    dev = logits.device
-    B, K, V = logits.shape
-    if K < 1 or K > N.MAX_BEAM or V < 1 or V > N.MAX_BEAM_VOCAB:
+    B, K, V = shape = logits.shape
+    if not 1 <= K <= N.MAX_BEAM or not 1 <= V <= N.MAX_BEAM_VOCAB:
         raise ValueError(f"logits must have 1 to {N.MAX_BEAM} hypotheses and 1 to "
                          f"{N.MAX_BEAM_VOCAB} outputs")
     beam = K if beam is None else int(beam)
-    if beam < 1 or beam > N.MAX_BEAM:
+    if not 1 <= beam <= N.MAX_BEAM:
         raise ValueError(f"beam must be in [1, {N.MAX_BEAM}]")
-    if scores.dtype != torch.float32 or scores.shape != (B, K) or scores.device != dev:
-        raise ValueError(f"scores must be float32 ({B}, {K}) on {dev}")
+    if scores.dtype is not _F32 or scores.shape != shape[:2] or scores.device != device:
+        raise ValueError(f"scores must be float32 ({B}, {K}) on {device}")
     if finished is not None:
-        if finished.dtype not in (torch.bool, torch.uint8) or finished.shape != (B, K) \
-                or finished.device != dev:
-            raise ValueError(f"finished must be bool or uint8 ({B}, {K}) on {dev}")
+        if finished.dtype not in (torch.bool, torch.uint8) or finished.shape != shape[:2] \
+                or finished.device != device:
+            raise ValueError(f"finished must be bool or uint8 ({B}, {K}) on {device}")
         finished = finished.contiguous()
-    if V > 1 and logits.stride(2) != 1:
-        logits = logits.contiguous()
     scores = scores.contiguous()
-    out_scores = torch.empty((B, beam), dtype=torch.float32, device=dev)
-    out = torch.empty((2, B, beam), dtype=torch.int32, device=dev)
-    tokens, parents = out.unbind(0)
-    if B == 0:
+    # one allocation: tokens, parents and (as they are) the scores
+    out = torch.empty((3, B, beam), dtype=_I32, device=device)
+    tokens, parents, out_scores = out.unbind(0)
+    out_scores = out_scores.view(_F32)
+    if not B:
         return out_scores, tokens, parents
-    dt = _DT[logits.dtype]
+    item, row, step = logits.stride()
+    if V > 1 and step != 1:
+        logits = logits.contiguous()
+        item, row, step = logits.stride()
     nbytes = N.rnnt_beam_workspace_size(B, K, V, beam, dt)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    status = status_word(check, dev)
-    call("rnnt_beam_select", dev, N.rnnt_beam_select, logits.data_ptr(), dt, B, K, V,
-         logits.stride(0), logits.stride(1), scores.data_ptr(),
-         None if finished is None else finished.data_ptr(), beam, 1 if fused_log_softmax else 0,
-         out_scores.data_ptr(), tokens.data_ptr(), parents.data_ptr(), ws.data_ptr(), nbytes,
-         None if status is None else status.data_ptr(), stream_of(dev))
-    finish("rnnt_beam_select", status, "finite scores or -inf, logits below +inf and not NaN")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    status = status_word(device) if check else None
+    at, each = out.data_ptr(), 4 * B * beam
+    call("rnnt_beam_select", device, N.load().rnnt_beam_select, logits.data_ptr(), dt, B, K, V,
+         item, row, scores.data_ptr(), None if finished is None else finished.data_ptr(), beam,
+         1 if fused_log_softmax else 0, at + 2 * each, at, at + each, ws.data_ptr(), nbytes,
+         None if status is None else status.data_ptr())
+    if check:
+        finish("rnnt_beam_select", status, "finite scores or -inf, logits below +inf and not NaN")
     return out_scores, tokens, parents
 
 
-def _describe(state, x, out, d, src, dst):
-    """Fills a State with the rows of x and out: the batch axis d, the beam axis d + 1, the
-    trailing axes that are adjacent in both as a row, and up to three further axes."""
-    size = x.element_size()
-    xs, os, shape = x.stride(), out.stride(), x.shape
+@lru_cache(maxsize=256)
+def _describe(shape, xs, os, size, d):
+    """(row bytes, n, strides of x, strides of out, batch and beam strides) of a state's rows: its
+    batch axis is d, its beam axis d + 1, the trailing axes that are adjacent in both tensors
+    are a row, and up to three axes are left.  Strides go in as elements and come out as bytes."""
     row, last = 1, len(shape) - 1
     while last > d + 1 and (shape[last] == 1 or xs[last] == row and os[last] == row):
         row *= shape[last]
@@ -92,12 +102,21 @@ def _describe(state, x, out, d, src, dst):
     if len(axes) > 3:
         raise ValueError("a state has more than three axes that are not adjacent in memory; "
                          "make it contiguous")
-    state.src, state.dst, state.row_bytes = src, dst, row * size
-    for j in range(3):
-        n, a, b = axes[j][:3] if j < len(axes) else (1, 0, 0)
-        state.n[j], state.src_stride[j], state.dst_stride[j] = n, a * size, b * size
-    state.src_batch, state.src_beam = xs[d] * size, xs[d + 1] * size
-    state.dst_batch, state.dst_beam = os[d] * size, os[d + 1] * size
+    axes += [(1, 0, 0, False)] * (3 - len(axes))
+    return (row * size, tuple(a[0] for a in axes), tuple(a[1] * size for a in axes),
+            tuple(a[2] * size for a in axes), xs[d] * size, xs[d + 1] * size, os[d] * size,
+            os[d + 1] * size)
+
+
+@lru_cache(maxsize=256)
+def _contiguous(shape, d, Ko):
+    """Shape and strides of a new result."""
+    shape = shape[:d + 1] + (Ko,) + shape[d + 2:]
+    strides, n = [], 1
+    for m in reversed(shape):
+        strides.append(n)
+        n *= max(m, 1)
+    return shape, tuple(reversed(strides)), 0 not in shape
 
 
 def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, check: bool = True):
@@ -118,49 +137,55 @@ def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, chec
     states = list(states)
     if not states:
         return []
-    dev = states[0].device
-    if not states[0].is_cuda:
+    device = states[0].device
+    if device.type != "cuda":
         raise ValueError("states must be CUDA tensors")
-    int32("parents", parents, dev)
+    if parents.dtype is not _I32 or parents.device != device:
+        int32("parents", parents, device)
     if parents.dim() != 2 or parents.shape[1] < 1:
         raise ValueError("parents must be (B, K') with K' >= 1")
     B, Ko = parents.shape
-    dims = [batch_dim] * len(states) if isinstance(batch_dim, int) else list(batch_dim)
+    dims = [batch_dim] * len(states) if isinstance(batch_dim, int) else batch_dim
     if len(dims) != len(states):
         raise ValueError("batch_dim must be one number, or one per state")
-    K = None
-    for i, (x, d) in enumerate(zip(states, dims)):
-        if x.device != dev:
-            raise ValueError(f"states must be on {dev}")
-        d = dims[i] = d + x.dim() if d < 0 else d
-        if not 0 <= d < x.dim() - 1:
-            raise ValueError("batch_dim must leave a beam axis behind it")
-        if K is None:
-            K = x.shape[d + 1]
-        if x.shape[d] != B or x.shape[d + 1] != K or K < 1:
-            raise ValueError(f"states must have a batch axis of {B} and, behind it, a beam axis "
-                             "of the same size, at least 1")
-    parents = parents.contiguous()
-    shapes = [x.shape[:d + 1] + (Ko,) + x.shape[d + 2:] for x, d in zip(states, dims)]
-    if out is None:
-        out = [torch.empty(s, dtype=x.dtype, device=dev) for s, x in zip(shapes, states)]
-    else:
+    if out is not None:
         out = list(out)
         if len(out) != len(states):
             raise ValueError("out must have one tensor per state")
-        for o, x, s in zip(out, states, shapes):
-            if o.device != dev or o.dtype != x.dtype or o.shape != s:
-                raise ValueError(f"out must be {x.dtype} {tuple(s)} on {dev}")
-            if any(n > 1 and a == 0 for n, a in zip(o.shape, o.stride())):
+    K, results, rows = None, [], []
+    for i, (x, d) in enumerate(zip(states, dims)):
+        shape = tuple(x.shape)
+        if x.device != device:
+            raise ValueError(f"states must be on {device}")
+        if d < 0:
+            d += len(shape)
+        if not 0 <= d < len(shape) - 1:
+            raise ValueError("batch_dim must leave a beam axis behind it")
+        if K is None:
+            K = shape[d + 1]
+        if shape[d] != B or shape[d + 1] != K or K < 1:
+            raise ValueError(f"states must have a batch axis of {B} and, behind it, a beam axis "
+                             "of the same size, at least 1")
+        new, strides, some = _contiguous(shape, d, Ko)
+        if out is None:
+            y = torch.empty(new, dtype=x.dtype, device=device)
+        else:
+            y, strides = out[i], out[i].stride()
+            if y.device != device or y.dtype != x.dtype or y.shape != new:
+                raise ValueError(f"out must be {x.dtype} {new} on {device}")
+            if any(n > 1 and a == 0 for n, a in zip(new, strides)):
                 raise ValueError("out must not be an expanded tensor")
-    todo = [(x, o, d) for x, o, d in zip(states, out, dims) if o.numel()]
-    status = status_word(check, dev) if todo else None
-    for i in range(0, len(todo), N.MAX_STATES):
-        part = todo[i:i + N.MAX_STATES]
-        array = (N.State * len(part))()
-        for s, (x, o, d) in zip(array, part):
-            _describe(s, x, o, d, x.data_ptr(), o.data_ptr())
-        call("rnnt_beam_reorder", dev, N.rnnt_beam_reorder, array, len(part), parents.data_ptr(),
-             B, K, Ko, None if status is None or i else status.data_ptr(), stream_of(dev))
-    finish("rnnt_beam_reorder", status, f"parents in [-1, {K})")
-    return out
+        results.append(y)
+        if some:
+            r = _describe(shape, x.stride(), strides, x.element_size(), d)
+            rows.append(N.State(x.data_ptr(), y.data_ptr(), *r))
+    parents = parents.contiguous()
+    status = status_word(device) if check and rows else None
+    for i in range(0, len(rows), N.MAX_STATES):
+        part = rows[i:i + N.MAX_STATES]
+        call("rnnt_beam_reorder", device, N.load().rnnt_beam_reorder,
+             (N.State * len(part))(*part), len(part), parents.data_ptr(), B, K, Ko,
+             None if status is None or i else status.data_ptr())
+    if status is not None:
+        finish("rnnt_beam_reorder", status, f"parents in [-1, {K})")
+    return results

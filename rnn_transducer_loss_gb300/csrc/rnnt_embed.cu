@@ -26,21 +26,34 @@ struct Places {
     int32_t B, S, first, start, V;
 };
 
-// The id at place i (row-major over (B, P)), -1 for padding; `bad` is set for
-// an id that is no row of the table and a length outside [0, S].
-__device__ __forceinline__ int place_id(const Places& p, int64_t i, bool& bad) {
-    const int P = p.S + p.first;
-    const int64_t b = i / P;
-    const int j = (int)(i - b * P) - p.first;
-    if (j < 0) return p.start;
-    if (p.lengths) {
-        const int n = __ldg(p.lengths + b);
-        bad |= n < 0 || n > p.S;
-        if (j >= n) return -1;
+// The ids at I places (row-major over (B, P)), -1 for padding and from place `end` on; `bad` is
+// set for an id that is no row of the table and a length outside [0, S].  The I lengths are
+// asked for together, then the I tokens.
+template <int I>
+__device__ __forceinline__ void place_ids(const Places& p, const uint32_t* place, uint32_t end,
+                                          int* id, bool& bad) {
+    const uint32_t P = (uint32_t)p.S + (uint32_t)p.first;
+    uint32_t b[I];
+    int j[I], n[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+        b[i] = place[i] / P;
+        j[i] = (int)(place[i] - b[i] * P) - p.first;
+        n[i] = p.S;
+        if (p.lengths && place[i] < end && j[i] >= 0) n[i] = __ldg(p.lengths + b[i]);
     }
-    const int t = __ldg(p.tokens + b * p.stride + j);
-    bad |= t >= p.V;
-    return t < 0 || t >= p.V ? -1 : t;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+        bad |= n[i] < 0 || n[i] > p.S;
+        id[i] = -1;
+        if (place[i] < end && j[i] < min(n[i], p.S))
+            id[i] = j[i] < 0 ? p.start : __ldg(p.tokens + (int64_t)b[i] * p.stride + j[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+        bad |= id[i] >= p.V;
+        if (id[i] < 0 || id[i] >= p.V) id[i] = -1;
+    }
 }
 
 // ------------------------------------------------------------------ forward
@@ -74,7 +87,8 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed(const EmbedParams p) {
     const int rows = (int)min((int64_t)p.rows, p.N - row0);
     if (threadIdx.x < rows) {
         bool bad = false;
-        ids[threadIdx.x] = place_id(p.pl, row0 + threadIdx.x, bad);
+        const uint32_t place = (uint32_t)row0 + threadIdx.x;
+        place_ids<1>(p.pl, &place, (uint32_t)p.N, ids + threadIdx.x, bad);
         if (bad && p.status) *p.status = RNNT_INVALID_VALUE;
     }
     __syncthreads();
@@ -110,257 +124,365 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed(const EmbedParams p) {
 
 // ----------------------------------------------------- gradient: sorted places
 // One cluster sorts the places by id (stable, so places of an id stay in
-// order): least-significant-digit radix sort, one to three digits of up to 11
+// order): least-significant-digit radix sort, one to four digits of up to 10
 // bits.  A CTA owns a contiguous range of the input; per digit it counts its
 // range, the CTAs exchange counts through distributed shared memory, and each
-// writes its places behind those of smaller digits and of earlier CTAs.
+// writes its places, brought into order in shared memory first so that the writes are
+// runs, behind those of smaller digits and of earlier CTAs.
+//
+// Latency bounds it (64000 places of 50000 ids are 0.25 MB to read), so the rest of the
+// device spends the time on zeroing grad_weight, whose rows without places k_sum does not
+// come to.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortItems = 8;                             // places of a thread and chunk
-constexpr int kSortChunk = kSortThreads * kSortItems;
-constexpr int kMaxBits = 11;
+constexpr int kSortItems = 4;                             // places of a thread and chunk, at most
+constexpr int kMaxBits = 10;
 constexpr int kMaxBins = 1 << kMaxBits;
-
+constexpr int kCountStride = kSortWarps + 2;              // 17 words: neighbouring digits' counts
+                                                          // lie in different banks
 struct SortParams {
     Places pl;
     int64_t N;
     int32_t bits, passes;      // digits of `bits` bits
-    int32_t* key[2];           // pass i writes key[i & 1] / place[i & 1]
-    int32_t* place[2];
-    uint8_t* present;          // [V]: id occurs
+    int2* out[2];              // {id, place}: pass i writes out[i & 1]
     int32_t* count;            // places that are not padding
     int32_t* status;
+    char* grad_weight;         // zeroed by the clusters behind the first
+    int64_t bytes;
+    int32_t unit;
 };
 
-constexpr size_t kSortShared = sizeof(uint16_t) * kSortWarps * kMaxBins;
+// Counts and digits' totals, and the chunk's places in order; at least so much that a CTA has an
+// SM to itself.
+constexpr size_t sort_shared(int bits) {
+    return std::max<size_t>(120 << 10, ((sizeof(uint16_t) * kCountStride + sizeof(int32_t)) << bits) +
+                                           sizeof(int2) * kSortThreads * kSortItems);
+}
+
+template <int UB>
+__device__ __forceinline__ void zero_fill(char* at, int64_t bytes, int64_t i, int64_t step) {
+    using U = typename Unit<UB>::type;
+    for (; i < bytes / UB; i += step) reinterpret_cast<U*>(at)[i] = U{};
+}
+
+// x becomes the sum of the earlier threads' x; returns the block's sum.
+__device__ __forceinline__ int exclusive_scan(int& x, int32_t* scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    int upto = scratch[lane];                           // the warps' sums, once more
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    const int before = __shfl_sync(0xffffffffu, upto, max(warp, 1) - 1);
+    x = incl - x + (warp ? before : 0);
+    return __shfl_sync(0xffffffffu, upto, 31);
+}
 
 __global__ void __launch_bounds__(kSortThreads) k_sort(const SortParams p) {
     cg::cluster_group cluster = cg::this_cluster();
-    extern __shared__ uint16_t wh[];          // [warp][bin]: counts, then starts
+    extern __shared__ __align__(16) char sort_space[];
+    int2* ordered = reinterpret_cast<int2*>(sort_space);      // the chunk's places
+    // [digit][warp], 16 bits: counts, then starts
+    uint32_t* counts32 = reinterpret_cast<uint32_t*>(ordered + kSortThreads * kSortItems);
+    uint16_t* counts = reinterpret_cast<uint16_t*>(counts32);
     __shared__ int32_t total[kMaxBins];       // this CTA's count of each digit
     __shared__ int32_t base[kMaxBins];        // where its next place of a digit goes
-    __shared__ int32_t chunk[kMaxBins];       // the current chunk's count of each digit
+    __shared__ int32_t chunk[kMaxBins];       // the current chunk's count of each digit, and where
+    __shared__ int32_t start[kMaxBins];       // the digit starts in `ordered`
     __shared__ int32_t scan[kSortWarps];
+    static_assert(kSortWarps == 32, "exclusive_scan takes a warp's sums by a warp");
     const int bins = 1 << p.bits;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    if ((int)blockIdx.x >= C) {
+        const int64_t i = (int64_t)(blockIdx.x - C) * kSortThreads + tid;
+        const int64_t step = (int64_t)(gridDim.x - C) * kSortThreads;
+        if (p.unit == 16) zero_fill<16>(p.grad_weight, p.bytes, i, step);
+        else if (p.unit >= 4) zero_fill<4>(p.grad_weight, p.bytes, i, step);
+        else zero_fill<2>(p.grad_weight, p.bytes, i, step);
+        return;
+    }
 
-    for (int64_t v = rank * kSortThreads + tid; v < p.pl.V; v += (int64_t)C * kSortThreads)
-        p.present[v] = 0;
-
-    int64_t n = p.N;
+    uint32_t n = (uint32_t)p.N;
     for (int pass = 0; pass < p.passes; ++pass) {
         const bool last = pass + 1 == p.passes;
         const int shift = pass * p.bits;
-        const int64_t per = (n + C - 1) / C;
-        const int64_t lo = min(n, per * rank), hi = min(n, lo + per);
-        int key[kSortItems], place[kSortItems];
-        int ahead[kSortItems];                // places of the same warp and digit ahead
-        // The chunk at c0: its items, their order within the warp, the warp's counts.
-        auto rank_chunk = [&](int64_t c0) {
-            __syncthreads();                  // readers of the previous counts are done
-            for (int i = tid; i < bins * kSortWarps / 2; i += kSortThreads)
-                reinterpret_cast<uint32_t*>(wh)[i] = 0;
+        const uint32_t per = (n + C - 1) / C;
+        const uint32_t lo = min(n, per * rank), hi = min(n, lo + per);
+        // a warp's places are adjacent: 32 * items of them
+        const int items = (int)min((uint32_t)kSortItems, (hi - lo + kSortThreads - 1) / kSortThreads);
+        const uint32_t step = (uint32_t)items * kSortThreads;
+        const int2* in = pass & 1 ? p.out[0] : p.out[1];
+        int key[kSortItems], ahead[kSortItems];     // ahead: places of the same warp and digit
+        uint32_t place[kSortItems];                 // ahead of it
+        // The chunk at c0: its items, their order within the warp, per digit the warps'
+        // starts and the count.
+        auto rank_chunk = [&](uint32_t c0) {
+            __syncthreads();                        // readers of the previous counts are done
+            for (int i = tid; i < bins * kCountStride / 2; i += kSortThreads) counts32[i] = 0;
             __syncthreads();
-            uint16_t* mine = wh + warp * bins;
+            const uint32_t at = c0 + warp * 32 * items + lane;
 #pragma unroll
             for (int i = 0; i < kSortItems; ++i) {
-                const int64_t at = c0 + warp * (32 * kSortItems) + i * 32 + lane;
+                place[i] = at + i * 32;
                 key[i] = -1;
-                place[i] = (int)at;
-                if (at < hi) {
-                    if (pass == 0) {
-                        bool bad = false;
-                        key[i] = place_id(p.pl, at, bad);
-                        if (bad && p.status) *p.status = RNNT_INVALID_VALUE;
-                    } else {
-                        key[i] = __ldcg(p.key[(pass & 1) ^ 1] + at);
-                        place[i] = __ldcg(p.place[(pass & 1) ^ 1] + at);
+            }
+            if (pass == 0) {
+                bool bad = false;
+                place_ids<kSortItems>(p.pl, place, min(hi, at - lane + 32 * items), key, bad);
+                if (bad && p.status) *p.status = RNNT_INVALID_VALUE;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kSortItems; ++i)
+                    if (i < items && place[i] < hi) {
+                        const int2 v = __ldcg(in + place[i]);
+                        key[i] = v.x;
+                        place[i] = (uint32_t)v.y;
                     }
-                }
             }
 #pragma unroll
             for (int i = 0; i < kSortItems; ++i) {
+                if (i >= items) break;
                 const int d = (key[i] >> shift) & (bins - 1);
-                const unsigned same = __match_any_sync(0xffffffffu, key[i] < 0 ? -1 : d);
-                const int before = mine[d];
+                unsigned same = __ballot_sync(0xffffffffu, key[i] >= 0);
+                for (int bit = 0; bit < p.bits; ++bit) {
+                    const bool one = d >> bit & 1;
+                    const unsigned ones = __ballot_sync(0xffffffffu, one);
+                    same &= one ? ones : ~ones;
+                }
+                uint16_t* mine = counts + d * kCountStride + warp;
+                const int before = key[i] >= 0 ? *mine : 0;
                 ahead[i] = before + __popc(same & ((1u << lane) - 1));
                 __syncwarp();
                 if (key[i] >= 0 && lane == __ffs(same) - 1)
-                    mine[d] = (uint16_t)(before + __popc(same));
+                    *mine = (uint16_t)(before + __popc(same));
                 __syncwarp();
+            }
+            __syncthreads();
+            for (int b = tid; b < bins; b += kSortThreads) {
+                uint32_t* row = counts32 + b * (kCountStride / 2);
+                uint32_t c[kSortWarps / 2], s = 0;
+#pragma unroll
+                for (int w = 0; w < kSortWarps / 2; ++w) c[w] = row[w];
+#pragma unroll
+                for (int w = 0; w < kSortWarps / 2; ++w) {
+                    const uint32_t a = c[w] & 0xffffu, z = c[w] >> 16;
+                    row[w] = s | (s + a) << 16;
+                    s += a + z;
+                }
+                chunk[b] = (int)s;
             }
             __syncthreads();
         };
         for (int b = tid; b < bins; b += kSortThreads) total[b] = 0;
-        for (int64_t c0 = lo; c0 < hi; c0 += kSortChunk) {
+        for (uint32_t c0 = lo; c0 < hi; c0 += step) {
             rank_chunk(c0);
-            for (int b = tid; b < bins; b += kSortThreads) {
-                int s = 0;
-                for (int w = 0; w < kSortWarps; ++w) s += wh[w * bins + b];
-                total[b] += s;
-            }
+            for (int b = tid; b < bins; b += kSortThreads) total[b] += chunk[b];
         }
         cluster.sync();
-        // base[b] = places of smaller digits + places of digit b in earlier CTAs.
-        int all[kMaxBins / kSortThreads], mineb[kMaxBins / kSortThreads];
-        int sum = 0;
-#pragma unroll
-        for (int q = 0; q < kMaxBins / kSortThreads; ++q) {
-            const int b = tid * (kMaxBins / kSortThreads) + q;
-            all[q] = mineb[q] = 0;
+        // base[b] = places of smaller digits + places of digit b in earlier CTAs; four threads
+        // read a digit's counts.
+        for (int b0 = 0; b0 < bins; b0 += kSortThreads / 4) {
+            const int b = b0 + tid / 4;
+            int all = 0, ours = 0;
             if (b < bins)
-                for (int r = 0; r < C; ++r) {
+                for (int r = tid & 3; r < C; r += 4) {
                     const int c = *cluster.map_shared_rank(total + b, r);
-                    if (r < rank) mineb[q] += c;
-                    all[q] += c;
+                    if (r < rank) ours += c;
+                    all += c;
                 }
+            all += __shfl_xor_sync(0xffffffffu, all, 1);
+            ours += __shfl_xor_sync(0xffffffffu, ours, 1);
+            all += __shfl_xor_sync(0xffffffffu, all, 2);
+            ours += __shfl_xor_sync(0xffffffffu, ours, 2);
+            if (b < bins && (tid & 3) == 0) base[b] = ours;
+            if (b < bins && (tid & 3) == 1) counts32[bins * kCountStride / 2 + b] = all;
+        }
+        __syncthreads();
+        const int32_t* alls = reinterpret_cast<int32_t*>(counts32) + bins * kCountStride / 2;
+        constexpr int kEach = kMaxBins / kSortThreads;
+        int all[kEach], sum = 0;
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            const int b = tid * kEach + q;
+            all[q] = b < bins ? alls[b] : 0;
             sum += all[q];
         }
-        int incl = sum;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
-        }
-        if (lane == 31) scan[warp] = incl;
-        __syncthreads();
-        int off = 0, full = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            if (w < warp) off += scan[w];
-            full += scan[w];
-        }
-        off += incl - sum;
+        int off = sum;
+        const int full = exclusive_scan(off, scan);
 #pragma unroll
-        for (int q = 0; q < kMaxBins / kSortThreads; ++q) {
-            const int b = tid * (kMaxBins / kSortThreads) + q;
-            if (b < bins) base[b] = off + mineb[q];
+        for (int q = 0; q < kEach; ++q) {
+            const int b = tid * kEach + q;
+            if (b < bins) base[b] += off;
             off += all[q];
         }
         if (rank == 0 && tid == 0 && pass == 0) *p.count = full;
-        for (int64_t c0 = lo; c0 < hi; c0 += kSortChunk) {
-            if (hi - lo > kSortChunk) rank_chunk(c0);     // one chunk: still at hand
-            __syncthreads();
-            for (int b = tid; b < bins; b += kSortThreads) {
-                int s = 0;
-                for (int w = 0; w < kSortWarps; ++w) {
-                    const int c = wh[w * bins + b];
-                    wh[w * bins + b] = (uint16_t)s;
-                    s += c;
-                }
-                chunk[b] = s;
+        __syncthreads();
+        int2* out = p.out[pass & 1];
+        for (uint32_t c0 = lo; c0 < hi; c0 += step) {
+            if (hi - lo > step) rank_chunk(c0);         // one chunk: still at hand
+            int each[kEach], first = 0;
+#pragma unroll
+            for (int q = 0; q < kEach; ++q) {
+                each[q] = tid * kEach + q < bins ? chunk[tid * kEach + q] : 0;
+                first += each[q];
+            }
+            const int held = exclusive_scan(first, scan);
+#pragma unroll
+            for (int q = 0; q < kEach; ++q) {
+                if (tid * kEach + q < bins) start[tid * kEach + q] = first;
+                first += each[q];
             }
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < kSortItems; ++i) {
-                if (key[i] < 0) continue;
+                if (i >= items || key[i] < 0) continue;
                 const int d = (key[i] >> shift) & (bins - 1);
-                const int to = base[d] + wh[warp * bins + d] + ahead[i];
-                p.key[pass & 1][to] = key[i];
-                p.place[pass & 1][to] = place[i];
-                if (last) p.present[key[i]] = 1;
+                ordered[start[d] + counts[d * kCountStride + warp] + ahead[i]] =
+                    make_int2(key[i], (int)place[i]);
             }
             __syncthreads();
-            for (int b = tid; b < bins; b += kSortThreads) base[b] += chunk[b];
+            for (int i = tid; i < held; i += kSortThreads) {
+                const int2 v = ordered[i];
+                const int d = (v.x >> shift) & (bins - 1);
+                out[base[d] + i - start[d]] = v;
+            }
+            if (c0 + step < hi) {
+                __syncthreads();
+                for (int b = tid; b < bins; b += kSortThreads) base[b] += chunk[b];
+            }
         }
-        n = full;
-        cluster.sync();
+        n = (uint32_t)full;
+        if (!last) cluster.sync();
     }
+    cluster.sync();                                     // others may still read `total`
 }
 
 // -------------------------------------------------- gradient: sums of sorted rows
-// The sorted places are cut into tiles of kTile; a group of threads adds a
-// tile's rows, one unit of columns a thread, and stores each id that begins
-// and ends inside its tile.  The rows of an id that crosses tiles go as
-// float32 partial sums to the workspace (slot 0: begun in an earlier tile,
-// slot 1: goes on in a later one), which k_join adds in order.
+// The sorted places are cut into tiles of kTile; a group of threads adds a tile's rows, one
+// unit of columns a thread.  An id belongs to the tile that it begins in: where it ends less
+// than kTile places behind that tile its group goes on to its end, and the next tile's
+// group begins behind it.  A longer one's rows are added tile by tile, to float32 partial
+// sums in the workspace (slot 0 of a tile: begun in an earlier one, slot 1: begun in it),
+// which k_join adds in order.
 constexpr int kTile = 32;
 constexpr int kSumThreads = 128;
 constexpr int kAhead = 8;                 // rows a thread has in flight
-constexpr int kZeroRows = 64;             // ids of a CTA that zeroes the rows of absent ids
 
 struct SumParams {
     const char* grad_out;
     char* grad_weight;
-    const int32_t* key;
-    const int32_t* place;
-    const uint8_t* present;
+    const int2* sorted;      // {id, place}
     const int32_t* count;
     float* partial;          // [tile][2][D]
     int64_t tiles;           // upper bound: tiles of all places
     int32_t V, D, nunits, group;   // group: threads of a tile, a power of two
     float scale;
-    unsigned sum_ctas;       // CTAs that add; the others zero
 };
 
 template <typename T, int UB>
-__device__ __forceinline__ void store_row_unit(const SumParams& p, int64_t id, int unit,
-                                               const float* acc) {
+__device__ __forceinline__ void store_unit(char* grad_weight, int64_t id, int nunits, int unit,
+                                           const float* acc, float scale) {
     constexpr int E = UB / (int)sizeof(T);
     Pack<T, UB> o;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o.e[e] = from_f32<T>(acc[e] * p.scale);
-    reinterpret_cast<typename Unit<UB>::type*>(p.grad_weight)[id * p.nunits + unit] = o.raw;
+    for (int e = 0; e < E; ++e) o.e[e] = from_f32<T>(acc[e] * scale);
+    reinterpret_cast<typename Unit<UB>::type*>(grad_weight)[id * nunits + unit] = o.raw;
+}
+
+// E float32 sums of a unit, in the workspace.
+template <int E>
+__device__ __forceinline__ void put_sums(float* to, const float* acc) {
+    if constexpr (E % 4 == 0) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4)
+            *reinterpret_cast<float4*>(to + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) to[e] = acc[e];
+    }
+}
+template <int E>
+__device__ __forceinline__ void add_sums(const float* from, float* acc) {
+    if constexpr (E % 4 == 0) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(from + e);
+            acc[e] += v.x;
+            acc[e + 1] += v.y;
+            acc[e + 2] += v.z;
+            acc[e + 3] += v.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += from[e];
+    }
 }
 
 template <typename T, int UB>
-__global__ void __launch_bounds__(kSumThreads) k_sum(const SumParams p) {
+__global__ void __launch_bounds__(kSumThreads, 7) k_sum(const SumParams p) {
     using U = typename Unit<UB>::type;
     constexpr int E = UB / (int)sizeof(T);
-    if (blockIdx.x >= p.sum_ctas) {
-        const int64_t v0 = (int64_t)(blockIdx.x - p.sum_ctas) * kZeroRows;
-        const int n = (int)min((int64_t)kZeroRows, p.V - v0);
-        Pack<T, UB> zero;
-#pragma unroll
-        for (int e = 0; e < E; ++e) zero.e[e] = from_f32<T>(0.0f);
-        __shared__ uint8_t present[kZeroRows];
-        if (threadIdx.x < n) present[threadIdx.x] = p.present[v0 + threadIdx.x];
-        __syncthreads();
-        for (int r = 0; r < n; ++r) {
-            if (present[r]) continue;
-            U* row = reinterpret_cast<U*>(p.grad_weight) + (v0 + r) * p.nunits;
-            for (int u = blockIdx.y * kSumThreads + threadIdx.x; u < p.nunits;
-                 u += gridDim.y * kSumThreads)
-                row[u] = zero.raw;
-        }
-        return;
-    }
-    const int g = threadIdx.x / p.group, groups = kSumThreads / p.group;
+    constexpr int kEntries = 2 * kTile;
+    extern __shared__ int2 entries[];              // of each group's tile, and of the next
+    const int g = threadIdx.x / p.group, in_group = threadIdx.x & (p.group - 1);
+    const int groups = kSumThreads / p.group;
     const int64_t t = (int64_t)blockIdx.x * groups + g;
-    const int unit = blockIdx.y * p.group + (threadIdx.x & (p.group - 1));
+    const int unit = blockIdx.y * p.group + in_group;
     const int64_t n = *p.count, j0 = t * kTile;
+    int2* mine = entries + g * kEntries;
+    for (int i = in_group; i < kEntries; i += p.group)
+        mine[i] = j0 + i < n ? __ldg(p.sorted + j0 + i) : make_int2(-1, 0);
+    int before = -1, before2 = -1;                 // the last ids of the two tiles ahead
+    if (j0 > 0 && j0 < n) before = __ldg(&p.sorted[j0 - 1].x);
+    if (j0 > kTile && j0 < n) before2 = __ldg(&p.sorted[j0 - kTile - 1].x);
+    __syncthreads();
     if (j0 >= n || unit >= p.nunits) return;
-    const int cnt = (int)min((int64_t)kTile, n - j0);
+    const int last = (int)min((int64_t)kTile, n - j0) - 1;
+    int j = 0, end = last + 1;
+    bool head = mine[0].x == before;               // the first id began earlier
+    if (head && before2 != before && mine[kTile - 1].x != before) {
+        while (j < kTile && mine[j].x == before) ++j;        // and ends here: not this tile's
+        head = false;
+        if (j == end) return;
+    }
+    // the last id goes on: to its end if that is near (mine[2 kTile - 1] is another's)
+    const bool goes_on = mine[last + 1].x == mine[last].x;
+    const bool begun_here = !(head && mine[last].x == before);
+    if (goes_on && begun_here && mine[kEntries - 1].x != mine[last].x)
+        while (mine[end].x == mine[last].x) ++end;
     float acc[E] = {};
-    int cur = p.key[j0];
-    bool head = j0 > 0 && p.key[j0 - 1] == cur;
+    int cur = mine[j].x;
     float* part = p.partial + t * 2 * p.D + unit * E;
     const U* src = reinterpret_cast<const U*>(p.grad_out) + unit;
-    for (int j = 0; j < cnt; j += kAhead) {
+    for (; j < end; j += kAhead) {
         Pack<T, UB> v[kAhead];
-        int next[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (j + i < end) v[i].raw = __ldg(src + (int64_t)mine[j + i].y * p.nunits);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (j + i < cnt) {
-                v[i].raw = __ldg(src + (int64_t)p.place[j0 + j + i] * p.nunits);
-                next[i] = j0 + j + i + 1 < n ? p.key[j0 + j + i + 1] : -1;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (j + i >= cnt) break;
+            if (j + i >= end) break;
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] += to_f32(v[i].e[e]);
-            if (next[i] != cur || j + i + 1 == cnt) {
-                const bool ends = next[i] != cur;
-                if (head || !ends) {
-                    float* to = part + (head ? 0 : p.D);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) to[e] = acc[e];
-                } else {
-                    store_row_unit<T, UB>(p, cur, unit, acc);
-                }
+            // the tile's last place may be followed by more of its id, which other tiles add
+            const int next = j + i + 1 < kEntries ? mine[j + i + 1].x : -1;
+            const bool ends = next != cur;
+            if (ends || j + i + 1 == end) {
+                if (head || !ends) put_sums<E>(part + (head ? 0 : p.D), acc);
+                else store_unit<T, UB>(p.grad_weight, cur, p.nunits, unit, acc, p.scale);
                 head = false;
-                cur = next[i];
+                cur = next;
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[e] = 0.0f;
             }
@@ -368,27 +490,68 @@ __global__ void __launch_bounds__(kSumThreads) k_sum(const SumParams p) {
     }
 }
 
-// The id that begins in tile t and goes on: its partial sums, tile after tile.
+// The long id that begins in tile t: its partial sums, tile after tile.  A CTA takes
+// kJoinTiles tiles and a slice of columns; its groups of threads add stretches of the id's
+// tiles, which are then added in order.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinTiles = 4;
 template <typename T, int UB>
-__global__ void __launch_bounds__(kSumThreads) k_join(const SumParams p) {
+__global__ void __launch_bounds__(kJoinThreads) k_join(const SumParams p) {
     constexpr int E = UB / (int)sizeof(T);
-    const int g = threadIdx.x / p.group, groups = kSumThreads / p.group;
-    int64_t t = (int64_t)blockIdx.x * groups + g;
-    const int unit = blockIdx.y * p.group + (threadIdx.x & (p.group - 1));
+    __shared__ float partly[kJoinThreads * E];
+    const int group = min(p.group, 32), groups = kJoinThreads / group;
+    const int g = threadIdx.x / group, lane = threadIdx.x & 31;
     const int64_t n = *p.count;
-    if ((t + 1) * kTile >= n || unit >= p.nunits) return;    // no later tile
-    const int id = p.key[(t + 1) * kTile - 1];
-    if (p.key[(t + 1) * kTile] != id || (t > 0 && p.key[t * kTile - 1] == id)) return;
-    float acc[E];
-    const float* part = p.partial + unit * E;
+    // the tiles that own such an id, a lane each
+    int mine = -1;
+    const int64_t t0 = (int64_t)blockIdx.x * kJoinTiles;
+    if (lane < kJoinTiles && (t0 + lane + 1) * kTile < n) {
+        const int64_t end = (t0 + lane + 1) * kTile;
+        const int before = t0 + lane > 0 ? p.sorted[end - kTile - 1].x : -1;
+        const int far = end + kTile - 1 < n ? p.sorted[end + kTile - 1].x : -1;
+        mine = p.sorted[end - 1].x;
+        if (far != mine || before == mine) mine = -1;
+    }
+    for (unsigned owners = __ballot_sync(0xffffffffu, mine >= 0); owners; owners &= owners - 1) {
+    const int which = __ffs(owners) - 1, id = __shfl_sync(0xffffffffu, mine, which);
+    const int64_t t = t0 + which;
+        // Tiles t + 1 .. t + m hold more of it: the first that ends with another id is the last.
+        __shared__ int runs[kJoinThreads / 32];
+        int64_t m = 0;
+        for (;;) {
+            const int64_t at = (t + 1 + m + threadIdx.x + 1) * kTile;      // the tile behind
+            const unsigned go = __ballot_sync(0xffffffffu, at < n && p.sorted[at].x == id);
+            __syncthreads();
+            if (lane == 0) runs[threadIdx.x / 32] = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
+            __syncthreads();
+            int run = 0;
+            for (int w = 0; w < kJoinThreads / 32 && run == 32 * w; ++w) run += runs[w];
+            m += run < kJoinThreads ? run + 1 : run;
+            if (run < kJoinThreads) break;
+        }
+        const int64_t each = (m + groups - 1) / groups;          // a group's stretch
+        for (int u0 = blockIdx.y * group; u0 < p.nunits; u0 += gridDim.y * group) {
+        const int unit = u0 + (threadIdx.x & (group - 1));
+        float acc[E] = {};
+        if (unit < p.nunits) {
+            const float* part = p.partial + (t + 1) * 2 * p.D + unit * E;
+            if (g == 0) add_sums<E>(part - p.D, acc);            // of tile t, slot 1
+            const int64_t end = min(m, (g + 1) * each);
+#pragma unroll 8
+            for (int64_t i = g * each; i < end; ++i) add_sums<E>(part + i * 2 * p.D, acc);
+        }
+        __syncthreads();
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = part[(t * 2 + 1) * p.D + e];
-    do {
-        ++t;
+        for (int e = 0; e < E; ++e) partly[threadIdx.x * E + e] = acc[e];
+        __syncthreads();
+        if (g == 0 && unit < p.nunits) {
+            for (int i = 1; i < groups; ++i)
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += part[t * 2 * p.D + e];
-    } while ((t + 1) * kTile < n && p.key[(t + 1) * kTile] == id);
-    store_row_unit<T, UB>(p, id, unit, acc);
+                for (int e = 0; e < E; ++e) acc[e] += partly[(i * group + threadIdx.x) * E + e];
+            store_unit<T, UB>(p.grad_weight, id, p.nunits, unit, acc, p.scale);
+        }
+    }
+    }
 }
 
 // Calls f(T{}, unit) with the unit's width as a constant; units are never
@@ -412,34 +575,57 @@ bool places_ok(const Places& p) {
            (int64_t)p.B * (p.S + p.first) <= INT32_MAX;
 }
 
-// k_sort's shared memory limit, raised once per device.
-bool sort_prepared() {
+// The CTAs of k_sort's largest cluster (16 where the device runs such clusters, else 8) and how
+// many of these clusters run at once; size 0 on an error.  k_sort's own limits are raised
+// once per device.
+struct SortLimits {
+    int size, fit;
+};
+int clusters_of(int size) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = sort_shared(kMaxBits);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, k_sort, &cfg) == cudaSuccess ? n : 0;
+}
+SortLimits sort_limits() {
     constexpr int kDevices = 64;
-    static std::atomic<bool> done[kDevices];
+    static std::atomic<int> known[kDevices];           // size << 16 | fit
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return false;
-    if (done[dev].load(std::memory_order_acquire)) return true;
-    if (cudaFuncSetAttribute(k_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSortShared) != cudaSuccess) {
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return {0, 0};
+    int v = known[dev].load(std::memory_order_acquire);
+    if (!v) {
+        if (cudaFuncSetAttribute(k_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)sort_shared(kMaxBits)) == cudaSuccess &&
+            cudaFuncSetAttribute(k_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                cudaSuccess) {
+            for (int size = 16; size >= 8 && !v; size /= 2)
+                if (const int n = clusters_of(size)) v = size << 16 | n;
+        }
         cudaGetLastError();
-        return false;
+        if (v) known[dev].store(v, std::memory_order_release);
     }
-    done[dev].store(true, std::memory_order_release);
-    return true;
+    return {v >> 16, v & 0xffff};
 }
 
 struct GradLayout {
-    size_t key[2], place[2], present, count, partial, total;
+    size_t out[2], count, partial, total;
     int64_t tiles;
 };
-GradLayout grad_layout(int64_t N, int32_t V, int32_t D) {
+GradLayout grad_layout(int64_t N, int32_t D) {
     GradLayout L;
     size_t at = 0;
     for (int i = 0; i < 2; ++i) {
-        L.key[i] = at;   at = align256(at + sizeof(int32_t) * (size_t)N);
-        L.place[i] = at; at = align256(at + sizeof(int32_t) * (size_t)N);
+        L.out[i] = at;
+        at = align256(at + sizeof(int2) * (size_t)N);
     }
-    L.present = at; at = align256(at + (size_t)V);
     L.count = at;   at = align256(at + sizeof(int32_t));
     L.tiles = (N + kTile - 1) / kTile;
     L.partial = at; at = align256(at + sizeof(float) * 2 * (size_t)L.tiles * (size_t)D);
@@ -496,7 +682,7 @@ extern "C" rnnt_status_t rnnt_embed_grad_workspace_size(int32_t B, int32_t S, in
     if (!bytes || B < 1 || S < 0 || S == INT32_MAX || S + first < 1 || V < 1 || D < 1 ||
         D > kMaxWidth ||        (int64_t)B * (S + first) > INT32_MAX)
         return RNNT_INVALID_VALUE;
-    *bytes = grad_layout((int64_t)B * (S + first), V, D).total;
+    *bytes = grad_layout((int64_t)B * (S + first), D).total;
     return RNNT_OK;
 }
 
@@ -519,7 +705,7 @@ extern "C" rnnt_status_t rnnt_embed_grad(const void* grad_out, rnnt_dtype_t dt,
         return RNNT_INVALID_VALUE;
     if (overlaps(grad_out, (uint64_t)N * D * es, grad_weight, (uint64_t)V * D * es))
         return RNNT_INVALID_VALUE;
-    const GradLayout L = grad_layout(N, V, D);
+    const GradLayout L = grad_layout(N, D);
     if (workspace_bytes < L.total) return RNNT_WORKSPACE_TOO_SMALL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
@@ -531,44 +717,46 @@ extern "C" rnnt_status_t rnnt_embed_grad(const void* grad_out, rnnt_dtype_t dt,
     while (k < 31 && ((int64_t)1 << k) < V) ++k;
     s.passes = (k + kMaxBits - 1) / kMaxBits;
     s.bits = (k + s.passes - 1) / s.passes;
-    for (int i = 0; i < 2; ++i) {
-        s.key[i] = reinterpret_cast<int32_t*>(ws + L.key[i]);
-        s.place[i] = reinterpret_cast<int32_t*>(ws + L.place[i]);
-    }
-    s.present = reinterpret_cast<uint8_t*>(ws + L.present);
+    for (int i = 0; i < 2; ++i) s.out[i] = reinterpret_cast<int2*>(ws + L.out[i]);
     s.count = reinterpret_cast<int32_t*>(ws + L.count);
     s.status = status_dev;
     SumParams q{};
     const int unit = unit_of((uintptr_t)grad_out | (uintptr_t)grad_weight | (uint64_t)D * es);
     q.grad_out = static_cast<const char*>(grad_out);
     q.grad_weight = static_cast<char*>(grad_weight);
-    q.key = s.key[(s.passes - 1) & 1];
-    q.place = s.place[(s.passes - 1) & 1];
-    q.present = s.present;
+    q.sorted = s.out[(s.passes - 1) & 1];
     q.count = s.count;
     q.partial = reinterpret_cast<float*>(ws + L.partial);
     q.tiles = L.tiles;
     q.V = V;
     q.D = D;
     q.nunits = (int32_t)((int64_t)D * es / unit);
-    q.group = 1;
+    q.group = 4;             // at least: the groups' entries fit shared memory
     while (q.group < kSumThreads && q.group < q.nunits) q.group *= 2;
     q.scale = scale;
     const int groups = kSumThreads / q.group;
-    q.sum_ctas = (unsigned)((L.tiles + groups - 1) / groups);
-    const unsigned zero_ctas = (unsigned)(((int64_t)V + kZeroRows - 1) / kZeroRows);
+    const int64_t sum_ctas = (L.tiles + groups - 1) / groups;
     const unsigned cols = (unsigned)((q.nunits + q.group - 1) / q.group);
-    if (cols > 65535 || (uint64_t)q.sum_ctas + zero_ctas > INT32_MAX) return RNNT_INVALID_VALUE;
+    if (cols > 65535 || sum_ctas > INT32_MAX) return RNNT_INVALID_VALUE;
 
     if (!clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
-    const size_t shared = sizeof(uint16_t) * kSortWarps * ((size_t)1 << s.bits);
-    if (!sort_prepared()) return RNNT_LAUNCH_FAILED;
+    s.grad_weight = q.grad_weight;
+    s.bytes = (int64_t)V * D * es;
+    s.unit = unit >= 16 ? 16 : unit >= 4 ? 4 : 2;
     int C = 1;
-    while (C < 8 && (int64_t)C * kSortChunk < N) C *= 2;
+    const SortLimits limits = sort_limits();
+    if (!limits.size) return RNNT_LAUNCH_FAILED;
+    while (C < limits.size && (int64_t)C * kSortThreads < N) C *= 2;
+    // The clusters that zero: no more than run beside the first at once (a cluster that has to
+    // wait for another's end costs its whole time: 102 MB take 31 us by 8 clusters of 16
+    // where 7 fit, 19 by 7).
+    const int64_t fit = C == limits.size ? limits.fit : 128 / C;
+    const int64_t units = (s.bytes / s.unit + kSortThreads - 1) / kSortThreads;
+    const int64_t zero = std::min<int64_t>(std::max<int64_t>(fit - 1, 1), (units + C - 1) / C);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(C);
+    cfg.gridDim = dim3((unsigned)(C * (1 + zero)));
     cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = shared;
+    cfg.dynamicSmemBytes = sort_shared(s.bits);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -582,10 +770,11 @@ extern "C" rnnt_status_t rnnt_embed_grad(const void* grad_out, rnnt_dtype_t dt,
     }
     with_unit(dt, unit, [&](auto tag, auto ub) {
         k_sum<decltype(tag), decltype(ub)::value>
-            <<<dim3(q.sum_ctas + zero_ctas, cols), kSumThreads, 0, st>>>(q);
+            <<<dim3((unsigned)sum_ctas, cols), kSumThreads, sizeof(int2) * groups * 2 * kTile, st>>>(q);
         if (L.tiles > 1)
             k_join<decltype(tag), decltype(ub)::value>
-                <<<dim3(q.sum_ctas, cols), kSumThreads, 0, st>>>(q);
+                <<<dim3((unsigned)((L.tiles + kJoinTiles - 1) / kJoinTiles), std::min(cols * ((unsigned)q.group + 31) / 32, 65535u)),
+                   kJoinThreads, 0, st>>>(q);
     });
     return launched();
 }

