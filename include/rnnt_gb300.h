@@ -374,7 +374,7 @@ rnnt_status_t rnnt_selftest_wait_timeout(int32_t *status_dev, int32_t polls, rnn
  *   out            (B, P, D) contiguous in dt; must not overlap weight.
  *   status_dev     RNNT_INVALID_VALUE for a token >= V (its place gets
  *                  zeros) or a length outside [0, S] (taken as the nearer bound).
- * 1 <= D <= 2^24, 1 <= B * P < 2^31.
+ * 1 <= D <= 2^20, 1 <= B * P < 2^31.
  */
 rnnt_status_t rnnt_embed(const void *weight, rnnt_dtype_t dt, int32_t V, int32_t D,
                          int64_t weight_stride, const int32_t *tokens, int64_t tokens_stride,
@@ -383,7 +383,7 @@ rnnt_status_t rnnt_embed(const void *weight, rnnt_dtype_t dt, int32_t V, int32_t
                          rnnt_stream_t stream);
 
 /* rnnt_embed_grad_workspace_size -- bytes of device scratch of rnnt_embed_grad:
- * about 16 + D/4 bytes per place and a byte per id. */
+ * 0 up to 2048 places, else about 16 + D/4 bytes per place. */
 rnnt_status_t rnnt_embed_grad_workspace_size(int32_t B, int32_t S, int32_t has_start, int32_t V,
                                              int32_t D, size_t *bytes);
 
@@ -399,8 +399,8 @@ rnnt_status_t rnnt_embed_grad_workspace_size(int32_t B, int32_t S, int32_t has_s
  *   grad_out       (B, P, D) contiguous in dt.
  *   grad_weight    (V, D) contiguous in dt, every row written; must not
  *                  overlap grad_out.
- *   workspace      rnnt_embed_grad_workspace_size() bytes, 256-byte aligned;
- *                  contents are rewritten every call.
+ *   workspace      rnnt_embed_grad_workspace_size() bytes, 256-byte aligned (NULL
+ *                  if that is 0); contents are rewritten every call.
  * tokens, lengths, start and status_dev as for rnnt_embed.
  */
 rnnt_status_t rnnt_embed_grad(const void *grad_out, rnnt_dtype_t dt, const int32_t *tokens,

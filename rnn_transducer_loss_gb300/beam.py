@@ -2,6 +2,7 @@
 hypotheses) and ``rnnt_beam_reorder`` (the states of the selected ones)."""
 from __future__ import annotations
 
+import struct
 from functools import lru_cache
 
 import torch
@@ -108,15 +109,34 @@ def _describe(shape, xs, os, size, d):
             os[d + 1] * size)
 
 
-@lru_cache(maxsize=256)
-def _contiguous(shape, d, Ko):
-    """Shape and strides of a new result."""
-    shape = shape[:d + 1] + (Ko,) + shape[d + 2:]
-    strides, n = [], 1
-    for m in reversed(shape):
-        strides.append(n)
+# rnnt_state_t behind its two pointers (row_bytes, n, padding, strides, batch and beam strides)
+_ROWS = struct.Struct("=q3i4x3q3q4q")
+_POINTERS = struct.Struct("=QQ")
+
+
+def _pack(rows):
+    r = rows
+    return _ROWS.pack(r[0], *r[1], *r[2], *r[3], *r[4:])
+
+
+@lru_cache(maxsize=1024)
+def _plan(shape, strides, size, d, B, K, Ko):
+    """(shape of a new result, its strides, packed rows or None if there are none) of a state by
+    its layout; raises if it is no state of (B, K)."""
+    if d < 0:
+        d += len(shape)
+    if not 0 <= d < len(shape) - 1:
+        raise ValueError("batch_dim must leave a beam axis behind it")
+    if shape[d] != B or shape[d + 1] != K or K < 1:
+        raise ValueError(f"states must have a batch axis of {B} and, behind it, a beam axis "
+                         "of the same size, at least 1")
+    new = shape[:d + 1] + (Ko,) + shape[d + 2:]
+    out, n = [], 1
+    for m in reversed(new):
+        out.append(n)
         n *= max(m, 1)
-    return shape, tuple(reversed(strides)), 0 not in shape
+    out = tuple(reversed(out))
+    return new, out, None if 0 in new else _pack(_describe(shape, strides, out, size, d))
 
 
 def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, check: bool = True):
@@ -148,44 +168,43 @@ def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, chec
     dims = [batch_dim] * len(states) if isinstance(batch_dim, int) else batch_dim
     if len(dims) != len(states):
         raise ValueError("batch_dim must be one number, or one per state")
+    first = tuple(states[0].shape)
+    d = dims[0] + len(first) if dims[0] < 0 else dims[0]
+    if not 0 <= d < len(first) - 1:
+        raise ValueError("batch_dim must leave a beam axis behind it")
+    K = first[d + 1]
     if out is not None:
         out = list(out)
         if len(out) != len(states):
             raise ValueError("out must have one tensor per state")
-    K, results, rows = None, [], []
-    for i, (x, d) in enumerate(zip(states, dims)):
-        shape = tuple(x.shape)
+    results, rows = [], []
+    for i, x in enumerate(states):
         if x.device != device:
             raise ValueError(f"states must be on {device}")
-        if d < 0:
-            d += len(shape)
-        if not 0 <= d < len(shape) - 1:
-            raise ValueError("batch_dim must leave a beam axis behind it")
-        if K is None:
-            K = shape[d + 1]
-        if shape[d] != B or shape[d + 1] != K or K < 1:
-            raise ValueError(f"states must have a batch axis of {B} and, behind it, a beam axis "
-                             "of the same size, at least 1")
-        new, strides, some = _contiguous(shape, d, Ko)
+        shape, strides, size = tuple(x.shape), x.stride(), x.element_size()
+        new, _, packed = _plan(shape, strides, size, dims[i], B, K, Ko)
         if out is None:
             y = torch.empty(new, dtype=x.dtype, device=device)
         else:
-            y, strides = out[i], out[i].stride()
+            y = out[i]
             if y.device != device or y.dtype != x.dtype or y.shape != new:
                 raise ValueError(f"out must be {x.dtype} {new} on {device}")
-            if any(n > 1 and a == 0 for n, a in zip(new, strides)):
+            if any(n > 1 and a == 0 for n, a in zip(new, y.stride())):
                 raise ValueError("out must not be an expanded tensor")
+            if packed is not None:
+                d = dims[i] + len(shape) if dims[i] < 0 else dims[i]
+                packed = _pack(_describe(shape, strides, y.stride(), size, d))
         results.append(y)
-        if some:
-            r = _describe(shape, x.stride(), strides, x.element_size(), d)
-            rows.append(N.State(x.data_ptr(), y.data_ptr(), *r))
+        if packed is not None:
+            rows.append(_POINTERS.pack(x.data_ptr(), y.data_ptr()) + packed)
+    if not rows:
+        return results
     parents = parents.contiguous()
-    status = status_word(device) if check and rows else None
+    status = status_word(device) if check else None
     for i in range(0, len(rows), N.MAX_STATES):
         part = rows[i:i + N.MAX_STATES]
-        call("rnnt_beam_reorder", device, N.load().rnnt_beam_reorder,
-             (N.State * len(part))(*part), len(part), parents.data_ptr(), B, K, Ko,
-             None if status is None or i else status.data_ptr())
+        call("rnnt_beam_reorder", device, N.load().rnnt_beam_reorder, b"".join(part), len(part),
+             parents.data_ptr(), B, K, Ko, None if status is None or i else status.data_ptr())
     if status is not None:
         finish("rnnt_beam_reorder", status, f"parents in [-1, {K})")
     return results

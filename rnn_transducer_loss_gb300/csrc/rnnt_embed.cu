@@ -17,7 +17,7 @@ using namespace rnnt_labels;
 
 namespace {
 
-constexpr int32_t kMaxWidth = 1 << 24;    // of a row: keeps unit numbers in 32 bits
+constexpr int32_t kMaxWidth = 1 << 20;    // of a row: column slices fit a grid's second axis
 
 struct Places {
     const int32_t* tokens;
@@ -554,6 +554,134 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const SumParams p) {
     }
 }
 
+// ------------------------------------------------- gradient: few places, one launch
+// With up to kFewPlaces places every CTA looks at all of them.  It takes a range of ids and a
+// slice of 32 units of columns: it collects the places of its ids, sorts them (id, then
+// place) in shared memory, gives each warp an equal stretch of them to add, joins the sums
+// of ids that cross stretches in order, and zeroes the rows of ids without places.
+constexpr int kFewPlaces = 2048;
+constexpr int kFewBits = 11;              // of a place in a key; the rest is the id's number
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewIds = 4096;             // ids of a CTA, at most
+
+struct FewParams {
+    Places pl;
+    const char* grad_out;
+    char* grad_weight;
+    int32_t N, ids, nunits;
+    float scale;
+    int32_t* status;
+};
+
+template <typename T, int UB>
+__global__ void __launch_bounds__(kFewThreads) k_few(const FewParams p) {
+    using U = typename Unit<UB>::type;
+    constexpr int E = UB / (int)sizeof(T);
+    __shared__ uint32_t key[kFewPlaces];
+    __shared__ uint32_t present[kFewIds / 32];
+    __shared__ float partly[2][kFewWarps][32 * E];     // begun in an earlier stretch / goes on
+    __shared__ int count;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int v0 = blockIdx.x * p.ids, ids = min(p.ids, p.pl.V - v0);
+    const int unit = blockIdx.y * 32 + lane;
+    for (int i = tid; i < (ids + 31) / 32; i += kFewThreads) present[i] = 0;
+    if (tid == 0) count = 0;
+    __syncthreads();
+    for (int c = 0; c < p.N; c += 4 * kFewThreads) {
+        uint32_t place[4];
+        int id[4];
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) place[i] = c + i * kFewThreads + tid;
+        place_ids<4>(p.pl, place, p.N, id, bad);
+        if (bad && p.status) *p.status = RNNT_INVALID_VALUE;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int mine = id[i] - v0;
+            if (id[i] >= 0 && mine >= 0 && mine < ids) {
+                key[atomicAdd(&count, 1)] = (uint32_t)mine << kFewBits | place[i];
+                atomicOr(&present[mine >> 5], 1u << (mine & 31));
+            }
+        }
+    }
+    __syncthreads();
+    const int n = count;
+    // bitonic sort of the next power of two
+    int size = 1;
+    while (size < n) size *= 2;
+    for (int i = n + tid; i < size; i += kFewThreads) key[i] = 0xffffffffu;
+    for (int k = 2; k <= size; k *= 2)
+        for (int o = k / 2; o; o /= 2) {
+            __syncthreads();
+            for (int i = tid; i < size / 2; i += kFewThreads) {
+                const int a = (i & ~(o - 1)) << 1 | (i & (o - 1)), b = a + o;
+                const uint32_t x = key[a], y = key[b];
+                if ((x > y) == ((a & k) == 0)) {
+                    key[a] = y;
+                    key[b] = x;
+                }
+            }
+        }
+    __syncthreads();
+    // A warp's stretch: ids that begin and end in it are stored, the others' sums kept.
+    const int each = (n + kFewWarps - 1) / kFewWarps;
+    const int lo = min(n, warp * each), hi = min(n, lo + each);
+    if (unit < p.nunits && lo < hi) {
+        const U* src = reinterpret_cast<const U*>(p.grad_out) + unit;
+        float acc[E] = {};
+        int cur = (int)(key[lo] >> kFewBits);
+        bool head = lo > 0 && (int)(key[lo - 1] >> kFewBits) == cur;
+        constexpr int kRows = 8;
+        for (int j = lo; j < hi; j += kRows) {
+            Pack<T, UB> v[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                if (j + i < hi)
+                    v[i].raw = __ldg(src + (int64_t)(key[j + i] & (kFewPlaces - 1)) * p.nunits);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                if (j + i >= hi) break;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] += to_f32(v[i].e[e]);
+                const int next = j + i + 1 < n ? (int)(key[j + i + 1] >> kFewBits) : -1;
+                if (next != cur || j + i + 1 == hi) {
+                    if (head || next == cur) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) partly[head ? 0 : 1][warp][lane * E + e] = acc[e];
+                    } else {
+                        store_unit<T, UB>(p.grad_weight, v0 + cur, p.nunits, unit, acc, p.scale);
+                    }
+                    head = false;
+                    cur = next;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (unit < p.nunits && lo < hi && hi < n) {
+        const int id = (int)(key[hi - 1] >> kFewBits);
+        const bool begun = lo == 0 || (int)(key[lo - 1] >> kFewBits) != id;
+        if (begun && (int)(key[hi] >> kFewBits) == id) {
+            float acc[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = partly[1][warp][lane * E + e];
+            for (int w = warp + 1; w * each < n && (int)(key[w * each] >> kFewBits) == id; ++w)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] += partly[0][w][lane * E + e];
+            store_unit<T, UB>(p.grad_weight, v0 + id, p.nunits, unit, acc, p.scale);
+        }
+    }
+    if (unit < p.nunits) {
+        float zero[E] = {};
+        for (int r = warp; r < ids; r += kFewWarps)
+            if (!(present[r >> 5] >> (r & 31) & 1))
+                store_unit<T, UB>(p.grad_weight, v0 + r, p.nunits, unit, zero, 1.0f);
+    }
+}
+
 // Calls f(T{}, unit) with the unit's width as a constant; units are never
 // narrower than an element.
 template <typename F>
@@ -619,9 +747,11 @@ struct GradLayout {
     size_t out[2], count, partial, total;
     int64_t tiles;
 };
+bool few_places(int64_t N) { return N <= kFewPlaces; }
 GradLayout grad_layout(int64_t N, int32_t D) {
-    GradLayout L;
+    GradLayout L{};
     size_t at = 0;
+    if (few_places(N)) return L;             // needs none
     for (int i = 0; i < 2; ++i) {
         L.out[i] = at;
         at = align256(at + sizeof(int2) * (size_t)N);
@@ -693,7 +823,7 @@ extern "C" rnnt_status_t rnnt_embed_grad(const void* grad_out, rnnt_dtype_t dt,
                                          float scale, void* grad_weight, void* workspace,
                                          size_t workspace_bytes, int32_t* status_dev,
                                          rnnt_stream_t stream) {
-    if (!grad_out || !grad_weight || !workspace || !valid_dtype(dt) || V < 1 || D < 1 ||
+    if (!grad_out || !grad_weight || !valid_dtype(dt) || V < 1 || D < 1 ||
         D > kMaxWidth)
         return RNNT_INVALID_VALUE;
     Places pl{tokens, tokens_stride, lengths, B, S, has_start ? 1 : 0,
@@ -706,9 +836,32 @@ extern "C" rnnt_status_t rnnt_embed_grad(const void* grad_out, rnnt_dtype_t dt,
     if (overlaps(grad_out, (uint64_t)N * D * es, grad_weight, (uint64_t)V * D * es))
         return RNNT_INVALID_VALUE;
     const GradLayout L = grad_layout(N, D);
+    if (L.total && !workspace) return RNNT_INVALID_VALUE;
     if (workspace_bytes < L.total) return RNNT_WORKSPACE_TOO_SMALL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
+    const int unit = unit_of((uintptr_t)grad_out | (uintptr_t)grad_weight | (uint64_t)D * es);
+    const int64_t nunits = (int64_t)D * es / unit;
+    if (few_places(N)) {
+        FewParams f{};
+        f.pl = pl;
+        f.grad_out = static_cast<const char*>(grad_out);
+        f.grad_weight = static_cast<char*>(grad_weight);
+        f.N = (int32_t)N;
+        f.nunits = (int32_t)nunits;
+        f.scale = scale;
+        f.status = status_dev;
+        const int64_t slices = (nunits + 31) / 32;
+        // four CTAs an SM, or one an id
+        const int64_t ctas = std::max<int64_t>(1, 152 * 4 / slices);
+        f.ids = (int32_t)std::min<int64_t>(kFewIds, (V + ctas - 1) / ctas);
+        if (!clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
+        with_unit(dt, unit, [&](auto tag, auto ub) {
+            k_few<decltype(tag), decltype(ub)::value>
+                <<<dim3((unsigned)((V + f.ids - 1) / f.ids), (unsigned)slices), kFewThreads, 0, st>>>(f);
+        });
+        return launched();
+    }
 
     SortParams s{};
     s.pl = pl;
@@ -721,7 +874,6 @@ extern "C" rnnt_status_t rnnt_embed_grad(const void* grad_out, rnnt_dtype_t dt,
     s.count = reinterpret_cast<int32_t*>(ws + L.count);
     s.status = status_dev;
     SumParams q{};
-    const int unit = unit_of((uintptr_t)grad_out | (uintptr_t)grad_weight | (uint64_t)D * es);
     q.grad_out = static_cast<const char*>(grad_out);
     q.grad_weight = static_cast<char*>(grad_weight);
     q.sorted = s.out[(s.passes - 1) & 1];
@@ -730,14 +882,14 @@ extern "C" rnnt_status_t rnnt_embed_grad(const void* grad_out, rnnt_dtype_t dt,
     q.tiles = L.tiles;
     q.V = V;
     q.D = D;
-    q.nunits = (int32_t)((int64_t)D * es / unit);
+    q.nunits = (int32_t)nunits;
     q.group = 4;             // at least: the groups' entries fit shared memory
     while (q.group < kSumThreads && q.group < q.nunits) q.group *= 2;
     q.scale = scale;
     const int groups = kSumThreads / q.group;
     const int64_t sum_ctas = (L.tiles + groups - 1) / groups;
     const unsigned cols = (unsigned)((q.nunits + q.group - 1) / q.group);
-    if (cols > 65535 || sum_ctas > INT32_MAX) return RNNT_INVALID_VALUE;
+    if (sum_ctas > INT32_MAX) return RNNT_INVALID_VALUE;
 
     if (!clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
     s.grad_weight = q.grad_weight;

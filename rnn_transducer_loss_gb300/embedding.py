@@ -100,11 +100,11 @@ def _gradient(grad_out, tokens, V, lengths, start, scale, check):
         lengths = lengths.contiguous()
     grad = torch.empty((V, D), dtype=grad_out.dtype, device=device)
     nbytes = N.rnnt_embed_grad_workspace_size(B, S, has, V, D)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     status = status_word(device) if check else None
     call("rnnt_embed_grad", device, N.load().rnnt_embed_grad, grad_out.data_ptr(), dt,
          tokens.data_ptr(), row, None if lengths is None else lengths.data_ptr(), B, S, has, first,
-         V, D, scale, grad.data_ptr(), ws.data_ptr(), nbytes,
+         V, D, scale, grad.data_ptr(), ws.data_ptr() if nbytes else None, nbytes,
          None if status is None else status.data_ptr())
     if check:
         finish("rnnt_embed_grad", status, _WANTED)

@@ -27,7 +27,7 @@ def embed(**kw):
 
 @pytest.mark.parametrize("bad", [
     dict(weight=None), dict(out=None), dict(tokens=None), dict(dt=3), dict(V=0), dict(D=0),
-    dict(D=(1 << 24) + 1, weight_stride=1 << 25), dict(weight_stride=7), dict(tokens_stride=4),
+    dict(D=(1 << 20) + 1, weight_stride=1 << 25), dict(weight_stride=7), dict(tokens_stride=4),
     dict(B=0), dict(S=-1), dict(S=0), dict(B=1 << 20, S=1 << 12, tokens_stride=1 << 12),
     dict(has_start=1, start=10), dict(has_start=1, start=-11), dict(scale=float("nan")),
     dict(weight=(1 << 20) + 2), dict(out=(1 << 21) + 1), dict(out=(1 << 20) + 64),
@@ -45,19 +45,22 @@ def embed_grad(**kw):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(grad_out=None), dict(grad_weight=None), dict(workspace=None), dict(tokens=None),
+    dict(grad_out=None), dict(grad_weight=None), dict(tokens=None),
+    dict(workspace=None, S=2000, tokens_stride=2000, grad_weight=1 << 24),
     dict(dt=-1), dict(V=0), dict(D=0), dict(B=0), dict(S=0), dict(tokens_stride=4),
     dict(has_start=1, start=10), dict(scale=float("nan")), dict(workspace=(1 << 22) + 64),
-    dict(grad_out=(1 << 20) + 1), dict(grad_weight=(1 << 20) + 64), dict(D=(1 << 24) + 1),
+    dict(grad_out=(1 << 20) + 1), dict(grad_weight=(1 << 20) + 64), dict(D=(1 << 20) + 1),
 ], ids=str)
 def test_embed_grad_refuses(bad):
     assert embed_grad(**bad) == N.RNNT_INVALID_VALUE
 
 
 def test_embed_grad_workspace():
-    n = N.rnnt_embed_grad_workspace_size(2, 5, 0, 10, 8)
+    assert N.rnnt_embed_grad_workspace_size(2, 1024, 0, 10, 8) == 0       # 2048 places: none
+    n = N.rnnt_embed_grad_workspace_size(2, 2000, 0, 10, 8)
     assert n > 0 and n % 256 == 0
-    assert embed_grad(workspace_bytes=n - 1) == N.RNNT_WORKSPACE_TOO_SMALL
+    assert embed_grad(workspace_bytes=n - 1, S=2000, tokens_stride=2000, grad_weight=1 << 24) \
+        == N.RNNT_WORKSPACE_TOO_SMALL
     big = N.rnnt_embed_grad_workspace_size(64, 1023, 1, 50000, 1024)
     assert 65536 * 16 <= big <= 65536 * (16 + 4 * 1024 // 8)
     for args in ((0, 5, 0, 10, 8), (2, 0, 0, 10, 8), (2, 5, 0, 0, 8), (2, 5, 0, 10, 0),
@@ -145,7 +148,7 @@ def test_describe(shape, view, d, row, axes):
     assert got[0] == row
     assert [(n, a) for n, a in zip(got[1], got[2]) if n > 1] == axes
     assert got[4:] == (x.stride(d) * 4, x.stride(d + 1) * 4, y.stride(d) * 4, y.stride(d + 1) * 4)
-    s = N.State(64, 128, *got)
+    s = N.State.from_buffer_copy(beam._POINTERS.pack(64, 128) + beam._pack(got))
     assert (s.src, s.dst, s.row_bytes, s.n[0], s.dst_beam) == (64, 128, row, got[1][0], got[7])
 
 
