@@ -413,7 +413,8 @@ rnnt_status_t rnnt_embed_grad(const void *grad_out, rnnt_dtype_t dt, const int32
 #define RNNT_MAX_BEAM 64
 #define RNNT_MAX_BEAM_VOCAB (1 << 20)
 
-/* rnnt_beam_workspace_size -- bytes of device scratch of rnnt_beam_select. */
+/* rnnt_beam_workspace_size -- bytes of device scratch of rnnt_beam_select; 0 where a
+ * batch item's logits are few, or the items many. */
 rnnt_status_t rnnt_beam_workspace_size(int32_t B, int32_t K, int32_t V, int32_t Ko,
                                        rnnt_dtype_t dt, size_t *bytes);
 
@@ -439,7 +440,8 @@ rnnt_status_t rnnt_beam_workspace_size(int32_t B, int32_t K, int32_t V, int32_t 
  *                  Places left over when fewer than Ko candidates exist get
  *                  score -inf, token -1, parent -1.  The outputs must not
  *                  overlap the inputs.
- *   workspace      rnnt_beam_workspace_size() bytes, 256-byte aligned.
+ *   workspace      rnnt_beam_workspace_size() bytes, 256-byte aligned (NULL if that is
+ *                  0).
  *   status_dev     RNNT_INVALID_VALUE for a score of +inf or NaN, or a
  *                  hypothesis whose logits hold one; such a hypothesis offers
  *                  nothing.

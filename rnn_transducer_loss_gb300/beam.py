@@ -69,12 +69,12 @@ def rnnt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beam: int | Non
         logits = logits.contiguous()
         item, row, step = logits.stride()
     nbytes = N.rnnt_beam_workspace_size(B, K, V, beam, dt)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     status = status_word(device) if check else None
     at, each = out.data_ptr(), 4 * B * beam
     call("rnnt_beam_select", device, N.load().rnnt_beam_select, logits.data_ptr(), dt, B, K, V,
          item, row, scores.data_ptr(), None if finished is None else finished.data_ptr(), beam,
-         1 if fused_log_softmax else 0, at + 2 * each, at, at + each, ws.data_ptr(), nbytes,
+         1 if fused_log_softmax else 0, at + 2 * each, at, at + each, ws.data_ptr() if nbytes else None, nbytes,
          None if status is None else status.data_ptr())
     if check:
         finish("rnnt_beam_select", status, "finite scores or -inf, logits below +inf and not NaN")

@@ -6,10 +6,13 @@
 // log-probabilities); a finished beam offers itself, with its score and token
 // -1; a beam of score -inf offers nothing.  The Ko best of a batch item are
 // selected, ties going to the lowest beam and then the lowest token.
+#include <cooperative_groups.h>
+
 #include <atomic>
 
 #include "rnnt_labels.cuh"
 
+namespace cg = cooperative_groups;
 using namespace rnnt_labels;
 
 namespace {
@@ -48,7 +51,7 @@ constexpr float kMostRef = 1e30f;          // larger references: computed again 
 constexpr float kTermError = 2.4e-7f + 6 * 6e-8f;
 constexpr float kExponentError = 5.2e-8f;          // 1.25 * 2^-24 * ln 2
 constexpr float kRescaleError = 1e-6f;
-constexpr int kMaxLists = 256;             // splits of a batch item's rows
+constexpr int kMaxLists = 128;             // splits of a batch item's rows
 constexpr int kSlots = 8;                  // of tiles, whose maxima a thread keeps
 constexpr int kBuf = 1024;                 // elements ranked: > RNNT_MAX_BEAM * 9 (best_of_row)
 
@@ -316,19 +319,33 @@ __device__ __noinline__ void best_of_row(const SelectParams& p, uint32_t row, in
     __syncthreads();
 }
 
+struct RowShared {
+    uint64_t buf[kBuf], best[RNNT_MAX_BEAM];       // best: the split's list
+    float4 stat;
+    Pair wsum[kRowWarps];
+    float wref[kRowWarps], wleast[kRowWarps], wover[kRowWarps];
+    float tops[kSlots][kRowThreads];
+    int hit[kSlots * kRowThreads];                 // slots to be read once more
+    int hits, count, bads, rescales;
+};
+
+// Leaves the split's statistics and list (zeros behind its end) in sh, behind a barrier; returns
+// false, at once, for a beam that offers no logits.
 template <typename T, int NV, bool FUSED>
-__global__ void __launch_bounds__(kRowThreads, NV == 1 ? 6 : 4) k_rows(const SelectParams p) {
+__device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, int split,
+                                         RowShared& sh) {
     constexpr int E = 16 / (int)sizeof(T);
     constexpr int kTileVecs = kRowThreads * NV;
-    __shared__ uint64_t buf[kBuf], best[RNNT_MAX_BEAM];
-    __shared__ Pair wsum[kRowWarps];
-    __shared__ float wref[kRowWarps], wleast[kRowWarps], wover[kRowWarps];
-    __shared__ float tops[kSlots][kRowThreads];
-    __shared__ int hit[kSlots * kRowThreads];      // slots to be read once more
-    __shared__ int hits, count, bads, rescales;
+    auto& buf = sh.buf;
+    auto& best = sh.best;
+    auto& wsum = sh.wsum;
+    auto& wref = sh.wref;
+    auto& wleast = sh.wleast;
+    auto& wover = sh.wover;
+    auto& tops = sh.tops;
+    auto& hit = sh.hit;
+    int &hits = sh.hits, &count = sh.count, &bads = sh.bads, &rescales = sh.rescales;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t row = blockIdx.x / (uint32_t)p.splits;
-    const int split = (int)(blockIdx.x - row * (uint32_t)p.splits);
     const Split<T> sp(p, row, split);
     const int vecs = sp.vecs;
     auto load_tile = [&](Pack<T, 16>* v, int t0) {
@@ -345,8 +362,9 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 ? 6 : 4) k_rows(const Sel
     load_tile(v, 0);
     const int odd = odd_element<T>(p, row, split);
     const float odd_x = odd >= 0 ? to_f32(row_of<T>(p, row)[odd]) : -INFINITY;
-    if (!reads_logits(p, row)) return;             // asked for while the loads are in flight
+    if (!reads_logits(p, row)) return false;       // asked for while the loads are in flight
     if (tid == 0) hits = count = bads = rescales = 0;
+    __syncthreads();
 
     float ref = 0.0f, sum = 0.0f, low = 0.0f;      // sum + low: the running sum
     float most = odd_x;                            // the thread's maximum
@@ -508,7 +526,6 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 ? 6 : 4) k_rows(const Sel
     }
     __syncthreads();
     const bool crowd = count > kBuf;
-    const uint32_t unit = blockIdx.x;
     if (warp == kRowWarps - 1) {                   // the keys are ranked by the first ones
         Pair total{0.0f, 0.0f};
         float over = 0.0f, err = 0.0f;
@@ -531,13 +548,25 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 ? 6 : 4) k_rows(const Sel
                                     2.9f * over / total.h);
         }
         if (lane == 0)
-            p.stat[unit] = make_float4(FUSED ? at : bads ? NAN : 0.0f, total.h, total.l, err);
+            sh.stat = make_float4(FUSED ? at : bads ? NAN : 0.0f, total.h, total.l, err);
     }
     if (!crowd) rank_keys(buf, count, best, p.n);
     __syncthreads();
     if (crowd) best_of_row<T>(p, row, split, buf, best, &count);
-    for (int i = tid; i < p.n; i += kRowThreads)
-        p.list[(int64_t)unit * p.n + i] = i < min(count, p.n) ? best[i] : 0;
+    for (int i = count + tid; i < p.n; i += kRowThreads) best[i] = 0;
+    __syncthreads();
+    return true;
+}
+
+template <typename T, int NV, bool FUSED>
+__global__ void __launch_bounds__(kRowThreads, NV == 1 ? 6 : 4) k_rows(const SelectParams p) {
+    __shared__ RowShared sh;
+    const uint32_t row = blockIdx.x / (uint32_t)p.splits;
+    const int split = (int)(blockIdx.x - row * (uint32_t)p.splits);
+    if (!row_pass<T, NV, FUSED>(p, row, split, sh)) return;
+    uint64_t* list = p.list + (int64_t)blockIdx.x * p.n;
+    if (threadIdx.x < p.n) list[threadIdx.x] = sh.best[threadIdx.x];
+    if (threadIdx.x == 0) p.stat[blockIdx.x] = sh.stat;
 }
 
 // ------------------------------------------------------- the logarithm, exactly
@@ -583,26 +612,28 @@ __device__ __forceinline__ Pair log_pair(Pair s) {
 }
 
 // --------------------------------------------------------- the Ko best of all
-// One CTA per batch item; a list (beam, split) has kParts threads.  Lists whose head is not
-// among the Ko best heads hold nothing; of the others the elements from the Ko-th best
-// head on are ranked by counting.
+// One CTA per batch item.  Every (beam, split) list is in order, so the best candidate is among
+// the lists' heads: one warp holds them, up to 4 a lane, and takes Ko times the largest.
 //
 // The streamed sums leave a log-sum-exp off by error[k] (see kTermError).  Where the order of
 // two candidates of different beams is closer than that, the beams' log-sum-exps are computed
 // again to 40 bits and the selection is repeated.  With 50000 outputs the bound is about
 // 1e-6, and 1 call in 15 of 64 items x 16 beams meets such a pair.
-constexpr int kPickThreads = 512;
-constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kParts = kPickThreads / kMaxLists;     // threads of a list
-constexpr int kTokenBits = 20;              // a candidate's number: beam, then token
-constexpr uint32_t kTokenMask = (1u << kTokenBits) - 1;
-static_assert(RNNT_MAX_BEAM_VOCAB <= 1 << kTokenBits, "a token fits");
-constexpr int kCand = RNNT_MAX_BEAM * (RNNT_MAX_BEAM + 1) / 2;
+constexpr int kPickThreads = 512;          // of k_pick
+// a[i] of an array in registers.
+template <int L>
+__device__ __forceinline__ int sel(const int (&a)[L], int i) {
+    int x = a[0];
+#pragma unroll
+    for (int q = 1; q < L; ++q) x = i == q ? a[q] : x;
+    return x;
+}
 
 // log sum exp of a row by the whole block, the same for equal rows wherever they lie; NaN
 // where the row holds NaN or +inf.
-template <typename T>
+template <typename T, int THREADS>
 __device__ __noinline__ Pair exact_lse(const T* x, int V, Pair* sums, float* tops) {
+    constexpr int kPickThreads = THREADS, kPickWarps = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float top = -INFINITY;
     for (int i = tid; i < V; i += kPickThreads) top = fmaxf(top, to_f32(x[i]));
@@ -630,58 +661,62 @@ __device__ __noinline__ Pair exact_lse(const T* x, int V, Pair* sums, float* top
     return add(Pair{top, 0.0f}, log_pair(s));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
-    extern __shared__ uint64_t lists[];                // [K * splits][n]
-    __shared__ uint64_t cval[kCand];                   // candidates: ordered value, number
-    __shared__ uint32_t cid[kCand];
-    __shared__ uint64_t heads[kMaxLists];
-    __shared__ uint64_t oval[RNNT_MAX_BEAM];           // the best, in order
-    __shared__ uint32_t oid[RNNT_MAX_BEAM];
-    __shared__ float4 stat[kMaxLists];
-    __shared__ Pair lse[RNNT_MAX_BEAM];
-    __shared__ float score[RNNT_MAX_BEAM], error[RNNT_MAX_BEAM];
-    __shared__ uint8_t kind[RNNT_MAX_BEAM];            // 0 nothing, 1 logits, 2 finished
-    __shared__ unsigned long long doubt, border;       // beams, a bit each
-    __shared__ Pair sums[kPickWarps];
-    __shared__ float tops[kPickWarps];
-    __shared__ int count, outside;
-    __shared__ uint64_t bound;
-    const int tid = threadIdx.x;
-    const uint32_t b = blockIdx.x;
-    const int nlists = p.K * p.splits;
-    const float4* all_stat = p.stat + (int64_t)b * nlists;
-    const uint64_t* all_list = p.list + (int64_t)b * nlists * p.n;
-    float s = 0.0f;
-    bool done = false;
-    if (tid < p.K) {
-        s = p.scores[b * p.K + tid];
-        done = p.finished && p.finished[b * p.K + tid];
-    }
-    if (tid == 0) doubt = 0;
-    if (tid < nlists) stat[tid] = all_stat[tid];
-    for (int i = tid; i < nlists * p.n; i += kPickThreads) lists[i] = all_list[i];
+struct PickShared {
+    uint64_t oval[RNNT_MAX_BEAM];           // the best, in order: ordered value, list << 8 | element
+    uint32_t oid[RNNT_MAX_BEAM];
+    uint8_t obeam[RNNT_MAX_BEAM];
+    Pair lse[RNNT_MAX_BEAM];
+    float score[RNNT_MAX_BEAM], error[RNNT_MAX_BEAM];
+    uint8_t kind[RNNT_MAX_BEAM];            // 0 nothing, 1 logits, 2 finished
+    unsigned long long again;               // beams whose log-sum-exp is wanted exactly
+    Pair sums[32];
+    float tops[32];
+    int found;
+};
+
+__device__ __forceinline__ unsigned long long or_lanes(unsigned long long x) {
+    return (unsigned long long)__reduce_or_sync(0xffffffffu, (uint32_t)(x >> 32)) << 32 |
+           __reduce_or_sync(0xffffffffu, (uint32_t)x);
+}
+
+// The selection of item b from its lists ([K * splits][n]) and statistics, in shared memory
+// already (behind the barrier here); values: as large as the lists.
+template <typename T, int THREADS>
+__device__ __forceinline__ void pick(const SelectParams& p, uint32_t b, const uint64_t* lists,
+                                     uint64_t* values, const float4* stat, PickShared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid == 0) sh.again = 0;
     __syncthreads();
-    if (tid < p.K) {
-        bool bad = !(s < INFINITY);
-        int what = bad || s == -INFINITY ? 0 : done ? 2 : 1;
+    // A beam's log-sum-exp from its splits: by one thread, or a warp's lanes together.
+    const int group = p.splits == 1 ? 1 : 32;
+    for (int k = tid / group; k < p.K; k += THREADS / group) {
+        const float score = p.scores[b * p.K + k];
+        const bool done = p.finished && p.finished[b * p.K + k];
+        const float4* st = stat + k * p.splits;
+        const uint64_t* first = lists + k * p.splits * p.n;
+        bool bad = !(score < INFINITY);
+        int what = bad || score == -INFINITY ? 0 : done ? 2 : 1;
         Pair l{0.0f, 0.0f};
         float err = 0.0f;
         if (what == 1) {
-            const float4* st = stat + tid * p.splits;
-            const uint64_t* first = lists + tid * p.splits * p.n;
             float top = -INFINITY, high = -INFINITY;
-            for (int g = 0; g < p.splits; ++g) {
+            bool nan = false;
+            for (int g = tid & (group - 1); g < p.splits; g += group) {
                 const uint64_t c = first[g * p.n];
                 if (c) high = fmaxf(high, unordered((uint32_t)(c >> 32)));
-                bad |= st[g].x != st[g].x;
+                nan |= st[g].x != st[g].x;
                 if (st[g].y != 0.0f) top = fmaxf(top, st[g].x);
             }
-            bad |= high == INFINITY;
+            for (int o = group / 2; o; o >>= 1) {
+                high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                nan |= __shfl_xor_sync(0xffffffffu, (int)nan, o) != 0;
+            }
+            bad = nan || high == INFINITY;
             if (p.fused && !bad) {
                 bool sure = top > -INFINITY;
                 Pair sum{0.0f, 0.0f};                  // at the reference `top`
-                for (int g = 0; g < p.splits; ++g) {
+                for (int g = tid & (group - 1); g < p.splits; g += group) {
                     const float4 q = st[g];
                     if (q.y == 0.0f) continue;
                     sure &= q.y < 1e30f && q.y > 1e-30f;           // not NaN either
@@ -689,150 +724,227 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
                     sum = add(sum, q.x == top ? part : mul(part, exp_pair(q.x, top)));
                     err = fmaxf(err, q.w);
                 }
+                for (int o = group / 2; o; o >>= 1) {
+                    sum = add(sum, shuffled(sum, o));
+                    err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, o));
+                    sure &= __shfl_xor_sync(0xffffffffu, (int)sure, o) != 0;
+                }
                 sure &= sum.h >= 1.0f && sum.h < 1e30f;
                 if (sure) {
                     l = add(Pair{top, 0.0f}, log_pair(sum));
                 } else if (high > -INFINITY || sum.h != sum.h) {
-                    atomicOr(&doubt, 1ull << tid);     // NaN, or out of the streamed sum's range
+                    // NaN, or out of the streamed sum's range
+                    if ((tid & (group - 1)) == 0) atomicOr(&sh.again, 1ull << k);
                     high = 0.0f;
                 }
             }
             if (bad || high == -INFINITY) what = 0;
         }
-        if (bad && p.status) *p.status = RNNT_INVALID_VALUE;
-        lse[tid] = l;
-        score[tid] = s;
-        error[tid] = err;
-        kind[tid] = (uint8_t)what;
+        if ((tid & (group - 1)) == 0) {
+            if (bad && p.status) *p.status = RNNT_INVALID_VALUE;
+            sh.lse[k] = l;
+            sh.score[k] = score;
+            sh.error[k] = err;
+            sh.kind[k] = (uint8_t)what;
+        }
     }
     __syncthreads();
-    const int list = tid / kParts, part = tid % kParts, k = list / p.splits;    // of this thread
-    for (unsigned long long again = doubt;;) {
+    const int nlists = p.K * p.splits;
+    unsigned long long again = sh.again;
+    for (int turn = 0; turn <= RNNT_MAX_BEAM; ++turn) {        // each settles a beam at least
         for (; again; again &= again - 1) {
-            const int kk = __ffsll((long long)again) - 1;
-            const Pair l = exact_lse(row_of<T>(p, b * p.K + kk), p.V, sums, tops);
+            const int k = __ffsll((long long)again) - 1;
+            const Pair l = exact_lse<T, THREADS>(row_of<T>(p, b * p.K + k), p.V, sh.sums, sh.tops);
             if (tid == 0) {
-                lse[kk] = l;
-                error[kk] = 0.0f;
+                sh.lse[k] = l;
+                sh.error[k] = 0.0f;
                 if (l.h != l.h) {                      // it holds NaN
-                    kind[kk] = 0;
+                    sh.kind[k] = 0;
                     if (p.status) *p.status = RNNT_INVALID_VALUE;
                 }
             }
         }
-        if (tid == 0) {
-            count = outside = 0;
-            doubt = border = 0;
-            bound = 1;
+        __syncthreads();
+        // Ordered values of the lists' elements, 0: none.
+        for (int m = tid; m < nlists * p.n; m += THREADS) {
+            const int i = m / p.n, k = i / p.splits, what = sh.kind[k];
+            uint64_t v = 0;
+            if (what == 2) {
+                if (m == k * p.splits * p.n) v = ordered(Pair{sh.score[k], 0.0f});
+            } else if (const uint64_t c = what == 1 ? lists[m] : 0) {
+                const Pair x = two_sum(sh.score[k], unordered((uint32_t)(c >> 32)));
+                v = ordered(add(x, Pair{-sh.lse[k].h, -sh.lse[k].l}));
+            }
+            values[m] = v;
         }
         __syncthreads();
-        const int what = list < nlists ? kind[k] : 0;
-        // Ordered value of the list's element j, 0 if there is none.
-        auto value = [&](int j) -> uint64_t {
-            if (what == 2) return list == k * p.splits && j == 0 ? ordered(Pair{score[k], 0.0f}) : 0;
-            const uint64_t c = what == 1 && j < p.n ? lists[list * p.n + j] : 0;
-            if (!c) return 0;
-            const Pair v = two_sum(score[k], unordered((uint32_t)(c >> 32)));
-            return ordered(add(v, Pair{-lse[k].h, -lse[k].l}));
-        };
-        auto number = [&](int j) {
-            return (uint32_t)k << kTokenBits | (what == 2 ? 0u : ~(uint32_t)lists[list * p.n + j]);
-        };
-        const uint64_t first = value(0);
-        if (part == 0 && list < nlists) heads[list] = first;
-        __syncthreads();
-        int rank = 0;
-        if (first)
-            for (int j = part; j < nlists; j += kParts)
-                rank += heads[j] > first || (heads[j] == first && j < list);
+        if (tid < 32) {
+            constexpr int L = kMaxLists / 32;
+            uint64_t head[L];
+            int at[L];
 #pragma unroll
-        for (int o = 1; o < kParts; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-        if (first && rank == p.Ko - 1) bound = first;
-        __syncthreads();
-        // element j of the list of rank r has j + r better ones
-        if (first && rank < p.Ko)
-            for (int j = part; j + rank < p.Ko; j += kParts) {
-                const uint64_t v = value(j);
-                if (v < bound) break;
-                const int to = atomicAdd(&count, 1);
-                cval[to] = v;
-                cid[to] = number(j);
+            for (int q = 0; q < L; ++q) {
+                const int i = q * 32 + lane;
+                at[q] = 0;
+                head[q] = i < nlists ? values[i * p.n] : 0;
             }
-        __syncthreads();
-        const int c = count, found = min(c, p.Ko);
-        constexpr int kCount = 4;                      // threads that count for a candidate
-        for (int i0 = 0; i0 < c; i0 += kPickThreads / kCount) {
-            const int i = i0 + tid / kCount;
-            const uint64_t v = i < c ? cval[i] : ~0ull;
-            const uint32_t d = i < c ? cid[i] : 0;
-            int r = 0;
-            if (i < c)
-                for (int j = tid % kCount; j < c; j += kCount)
-                    r += cval[j] > v || (cval[j] == v && cid[j] < d);
+            int found = 0;
+            for (; found < p.Ko; ++found) {
+                uint64_t v = head[0];
+                int q0 = 0;
 #pragma unroll
-            for (int o = 1; o < kCount; o *= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
-            if (i < c && r < p.Ko && tid % kCount == 0) {
-                oval[r] = v;
-                oid[r] = d;
+                for (int q = 1; q < L; ++q)
+                    if (head[q] > v) {                 // equal: the lower list
+                        v = head[q];
+                        q0 = q;
+                    }
+                const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+                if (!hi) break;
+                const uint32_t lo = __reduce_max_sync(
+                    0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+                // of equal values the lowest list: the lowest beam, and token
+                const uint32_t list = __reduce_min_sync(
+                    0xffffffffu, v == ((uint64_t)hi << 32 | lo) ? (uint32_t)(q0 * 32 + lane)
+                                                                : 0xffffffffu);
+                if ((list & 31) == lane) {
+                    sh.oval[found] = v;
+                    sh.oid[found] = list << 8 | sel(at, q0);
+#pragma unroll
+                    for (int q = 0; q < L; ++q)
+                        if (q == q0) {
+                            ++at[q];
+                            head[q] = at[q] < p.n ? values[list * p.n + at[q]] : 0;
+                        }
+                }
+            }
+            __syncwarp();
+            for (int r = lane; r < found; r += 32) sh.obeam[r] = (uint8_t)((sh.oid[r] >> 8) / p.splits);
+            __syncwarp();
+            unsigned long long doubt = 0;
+            if (p.fused && found) {
+                // Neighbours of different beams whose order is in doubt.
+                for (int r = lane; r + 1 < found; r += 32) {
+                    const int k0 = sh.obeam[r], k1 = sh.obeam[r + 1];
+                    const float e0 = sh.error[k0], e1 = sh.error[k1];
+                    if (k0 != k1 && difference(sh.oval[r], sh.oval[r + 1]) < e0 + e1)
+                        doubt |= (e0 > 0.0f ? 1ull << k0 : 0) | (e1 > 0.0f ? 1ull << k1 : 0);
+                }
+                // Beams as near to the last one with candidates left out, and the selected ones
+                // there: where that is more than one beam, any of them may belong.
+                const uint64_t last = sh.oval[found - 1];
+                const float own = sh.error[sh.obeam[found - 1]];
+                unsigned long long out = 0, in = 0;
+#pragma unroll
+                for (int q = 0; q < L; ++q) {
+                    const int i = q * 32 + lane, k = i < nlists ? i / p.splits : 0;
+                    if (i < nlists && head[q] && difference(last, head[q]) <= own + sh.error[k])
+                        out |= 1ull << k;
+                }
+                for (int r = lane; r < found; r += 32) {
+                    const int k = sh.obeam[r];
+                    if (difference(sh.oval[r], last) <= own + sh.error[k]) in |= 1ull << k;
+                }
+                out = or_lanes(out);
+                in = or_lanes(in);
+                doubt = or_lanes(doubt);
+                if (out && __popcll(in | out) > 1)
+                    for (unsigned long long left = in | out; left; left &= left - 1) {
+                        const int k = __ffsll((long long)left) - 1;
+                        if (sh.error[k] > 0.0f) doubt |= 1ull << k;
+                    }
+            }
+            if (lane == 0) {
+                sh.again = doubt;
+                sh.found = found;
             }
         }
         __syncthreads();
-        if (!p.fused || found == 0) break;
-        // Neighbours of different beams whose order is in doubt.
-        if (tid + 1 < found) {
-            const int k0 = oid[tid] >> kTokenBits, k1 = oid[tid + 1] >> kTokenBits;
-            if (k0 != k1 && difference(oval[tid], oval[tid + 1]) < error[k0] + error[k1])
-                atomicOr(&doubt, (error[k0] > 0.0f ? 1ull << k0 : 0) |
-                                 (error[k1] > 0.0f ? 1ull << k1 : 0));
-        }
-        // Beams with candidates as near to the last one, some of them left out.
-        if (found == p.Ko && first) {
-            const uint64_t last = oval[found - 1];
-            const float within = error[k] + error[oid[found - 1] >> kTokenBits];
-            for (int j = part; j < p.n; j += kParts) {
-                const uint64_t v = value(j);
-                if (!v) break;
-                const float d = difference(v, last);
-                if (d < -within) break;
-                if (d > within) continue;
-                atomicOr(&border, 1ull << k);
-                if (v < last || (v == last && number(j) > oid[found - 1])) outside = 1;
-            }
-        }
-        __syncthreads();
-        again = doubt;
-        if (outside && __popcll(border) > 1)
-            for (unsigned long long left = border; left; left &= left - 1) {
-                const int kk = __ffsll((long long)left) - 1;
-                if (error[kk] > 0.0f) again |= 1ull << kk;
-            }
+        again = sh.again;
         if (!again) break;
-        __syncthreads();       // `doubt` and `border` have been read
     }
-    for (int r = tid; r < p.Ko; r += kPickThreads) {
+    for (int r = tid; r < p.Ko; r += THREADS) {
         const int64_t o = (int64_t)b * p.Ko + r;
-        const int from = r < min(count, p.Ko) ? (int)(oid[r] >> kTokenBits) : -1;
-        p.out_scores[o] = from < 0 ? -INFINITY : unordered((uint32_t)(oval[r] >> 32));
-        p.out_tokens[o] = from < 0 || kind[from] == 2 ? -1 : (int)(oid[r] & kTokenMask);
+        const int from = r < sh.found ? sh.obeam[r] : -1;
+        p.out_scores[o] = from < 0 ? -INFINITY : unordered((uint32_t)(sh.oval[r] >> 32));
+        p.out_tokens[o] = from < 0 || sh.kind[from] == 2
+                              ? -1 : (int)~(uint32_t)lists[(sh.oid[r] >> 8) * p.n + (sh.oid[r] & 255)];
         p.out_parents[o] = from;
     }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
+    extern __shared__ uint64_t lists[];                // [K * splits][n], twice
+    __shared__ float4 stat[kMaxLists];
+    __shared__ PickShared sh;
+    const uint32_t b = blockIdx.x;
+    const int nlists = p.K * p.splits;
+    const uint64_t* from = p.list + (int64_t)b * nlists * p.n;
+    if (threadIdx.x < nlists) stat[threadIdx.x] = p.stat[(int64_t)b * nlists + threadIdx.x];
+    for (int i = threadIdx.x; i < nlists * p.n; i += kPickThreads) lists[i] = from[i];
+    pick<T, kPickThreads>(p, b, lists, lists + nlists * p.n, stat, sh);
+}
+
+// ------------------------------------------------------- both, by a cluster an item
+// A cluster of up to 8 CTAs takes a batch item: each streams a row and leaves its list and
+// statistics in the first CTA's shared memory, which picks.  One launch and no workspace.
+struct ClusterShared {
+    union {
+        RowShared rows;
+        PickShared pick;
+    };
+    float4 stat[RNNT_MAX_BEAM];
+};
+
+template <typename T, int NV, bool FUSED>
+__global__ void __launch_bounds__(kRowThreads, 4) k_search(const SelectParams p) {
+    cg::cluster_group cluster = cg::this_cluster();
+    extern __shared__ __align__(16) char search_space[];
+    ClusterShared& sh = *reinterpret_cast<ClusterShared*>(search_space);
+    uint64_t* lists = reinterpret_cast<uint64_t*>(search_space + sizeof(ClusterShared));
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const uint32_t b = blockIdx.x / (uint32_t)C;
+    cluster.barrier_arrive();                          // that every CTA has started:
+    uint64_t* to_lists = cluster.map_shared_rank(lists, 0);
+    float4* to_stat = cluster.map_shared_rank(sh.stat, 0);
+    const bool reads = row_pass<T, NV, FUSED>(p, b * p.K + rank, 0, sh.rows);
+    cluster.barrier_wait();                            // here it is to be known
+    if (reads) {
+        if (threadIdx.x < p.n) to_lists[rank * p.n + threadIdx.x] = sh.rows.best[threadIdx.x];
+        if (threadIdx.x == 0) to_stat[rank] = sh.rows.stat;
+    }
+    cluster.sync();
+    if (rank == 0) pick<T, kRowThreads>(p, b, lists, lists + p.K * p.n, sh.stat, sh.pick);
 }
 
 struct SelectLayout {
     size_t stat, list, total;
     int32_t splits, split_vecs, n;
+    int32_t cluster;                       // CTAs of an item's cluster, or 0: two launches
 };
+constexpr int64_t kClusterBytes = 128 << 10, kClusterRows = 304;
 SelectLayout select_layout(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt) {
-    SelectLayout L;
-    const int E = 16 / elem_size(dt);
+    SelectLayout L{};
+    const int es = elem_size(dt), E = 16 / es;
     const int64_t vecs = std::max(1, V / E);                 // the most, whatever the alignment
+    L.n = std::min(Ko, V);
+    L.splits = 1;
+    L.split_vecs = (int32_t)vecs;
+    // A cluster's CTAs take a row each, whole (two rows in turn measured slower than two
+    // launches: 17.0 against 14.7 us for 10 beams).  For an item of 4 beams of 1024 float16 the
+    // cluster takes 8.8 us and two launches 10.1, of 20000 10.3 and 11.3, of 50000 12.9 and
+    // 11.6, and a launch and a workspace cost the host 6 us; longer rows want splits over the
+    // whole device, unless there are many (16 items of 4 x 50000: 13.8 and 14.2).
+    if (K <= 8 && ((int64_t)V * es <= kClusterBytes || (int64_t)B * K >= kClusterRows)) {
+        L.cluster = K;
+        return L;
+    }
     // one tile a CTA where that gives no more than a wave of 6 CTAs an SM, else a wave of 4
     const int64_t rows = (int64_t)B * K, tiles = (vecs + kRowThreads - 1) / kRowThreads;
     int64_t splits = rows * tiles <= 152 * 6 ? tiles : std::min(tiles, 152 * 4 / rows);
     splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxLists / K));
     L.split_vecs = (int32_t)((vecs + splits - 1) / splits);
     L.splits = (int32_t)((vecs + L.split_vecs - 1) / L.split_vecs);
-    L.n = std::min(Ko, V);
     const size_t units = (size_t)B * K * L.splits;
     L.stat = 0;
     L.list = align256(units * sizeof(float4));
@@ -842,38 +954,66 @@ SelectLayout select_layout(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt) 
 bool select_ok(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt) {
     return B >= 1 && K >= 1 && K <= RNNT_MAX_BEAM && Ko >= 1 && Ko <= RNNT_MAX_BEAM && V >= 1 &&
            V <= RNNT_MAX_BEAM_VOCAB && valid_dtype(dt) &&
-           (int64_t)B * K * select_layout(B, K, V, Ko, dt).splits <= INT32_MAX;
+           (int64_t)B * K <= INT32_MAX / kMaxLists;
 }
 
 template <typename T>
-void launch_select(const SelectParams& p, cudaStream_t st) {
-    const unsigned grid = (unsigned)(p.B * p.K * p.splits);
-    auto rows = [&](auto nv) {
+bool launch_select(const SelectParams& p, int cluster, cudaStream_t st) {
+    auto launch = [&](auto nv, auto fused) {
         constexpr int NV = decltype(nv)::value;
-        if (p.fused) k_rows<T, NV, true><<<grid, kRowThreads, 0, st>>>(p);
-        else k_rows<T, NV, false><<<grid, kRowThreads, 0, st>>>(p);
+        constexpr bool FUSED = decltype(fused)::value;
+        if (!cluster) {
+            k_rows<T, NV, FUSED><<<(unsigned)(p.B * p.K * p.splits), kRowThreads, 0, st>>>(p);
+            return true;
+        }
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)(p.B * cluster));
+        cfg.blockDim = dim3(kRowThreads);
+        cfg.dynamicSmemBytes = sizeof(ClusterShared) + 2 * sizeof(uint64_t) * p.K * p.n;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, k_search<T, NV, FUSED>, p) == cudaSuccess;
     };
-    if (p.split_vecs <= kRowThreads) rows(std::integral_constant<int, 1>{});
-    else if (p.split_vecs <= 2 * kRowThreads) rows(std::integral_constant<int, 2>{});
-    else rows(std::integral_constant<int, 4>{});
-    const size_t shared = sizeof(uint64_t) * p.K * p.splits * p.n;
-    k_pick<T><<<(unsigned)p.B, kPickThreads, shared, st>>>(p);
+    auto by_size = [&](auto fused) {
+        if (p.split_vecs <= kRowThreads) return launch(std::integral_constant<int, 1>{}, fused);
+        if (p.split_vecs <= 2 * kRowThreads) return launch(std::integral_constant<int, 2>{}, fused);
+        return launch(std::integral_constant<int, 4>{}, fused);
+    };
+    if (!(p.fused ? by_size(std::true_type{}) : by_size(std::false_type{}))) {
+        cudaGetLastError();
+        return false;
+    }
+    if (!cluster)
+        k_pick<T><<<(unsigned)p.B, kPickThreads, 2 * sizeof(uint64_t) * p.K * p.splits * p.n, st>>>(p);
+    return true;
 }
 
-// k_pick's shared memory limit, raised once per device.
-bool pick_prepared() {
+// The kernels' shared memory limits, raised once per device.
+template <typename T>
+bool raise_limits() {
+    const auto raise = [](auto kernel, size_t most) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)most) == cudaSuccess;
+    };
+    const size_t lists = 2 * sizeof(uint64_t) * 8 * RNNT_MAX_BEAM;       // of up to 8 beams
+    const size_t most = sizeof(ClusterShared) + lists;
+    return raise(k_pick<T>, 2 * sizeof(uint64_t) * kMaxLists * RNNT_MAX_BEAM) &&
+           raise(k_search<T, 1, true>, most) && raise(k_search<T, 1, false>, most) &&
+           raise(k_search<T, 2, true>, most) && raise(k_search<T, 2, false>, most) &&
+           raise(k_search<T, 4, true>, most) && raise(k_search<T, 4, false>, most);
+}
+bool select_prepared() {
     constexpr int kDevices = 64;
     static std::atomic<bool> done[kDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return false;
     if (done[dev].load(std::memory_order_acquire)) return true;
-    const int most = (int)(sizeof(uint64_t) * kMaxLists * RNNT_MAX_BEAM);
-    bool ok = true;
-    for (int dt = 0; dt < 3 && ok; ++dt)
-        ok = with_type(dt, [&](auto tag) {
-            return cudaFuncSetAttribute(k_pick<decltype(tag)>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        }) == cudaSuccess;
+    const bool ok = raise_limits<float>() && raise_limits<__half>() && raise_limits<__nv_bfloat16>();
     if (ok) done[dev].store(true, std::memory_order_release);
     else cudaGetLastError();
     return ok;
@@ -992,13 +1132,13 @@ extern "C" rnnt_status_t rnnt_beam_select(const void* logits, rnnt_dtype_t dt, i
                                           int32_t* out_tokens, int32_t* out_parents,
                                           void* workspace, size_t workspace_bytes,
                                           int32_t* status_dev, rnnt_stream_t stream) {
-    if (!logits || !scores || !out_scores || !out_tokens || !out_parents || !workspace)
-        return RNNT_INVALID_VALUE;
+    if (!logits || !scores || !out_scores || !out_tokens || !out_parents) return RNNT_INVALID_VALUE;
     if (!select_ok(B, K, V, Ko, dt) || batch_stride < 0 || beam_stride < 0)
         return RNNT_INVALID_VALUE;
     const int es = elem_size(dt);
     if (((uintptr_t)logits & (es - 1)) || ((uintptr_t)workspace & 255)) return RNNT_INVALID_VALUE;
     const SelectLayout L = select_layout(B, K, V, Ko, dt);
+    if (L.total && !workspace) return RNNT_INVALID_VALUE;
     if (workspace_bytes < L.total) return RNNT_WORKSPACE_TOO_SMALL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
@@ -1022,11 +1162,9 @@ extern "C" rnnt_status_t rnnt_beam_select(const void* logits, rnnt_dtype_t dt, i
     p.out_tokens = out_tokens;
     p.out_parents = out_parents;
     p.status = status_dev;
-    if (!pick_prepared() || !clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
-    with_type(dt, [&](auto tag) {
-        launch_select<decltype(tag)>(p, st);
-        return 0;
-    });
+    if (!select_prepared() || !clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
+    if (!with_type(dt, [&](auto tag) { return launch_select<decltype(tag)>(p, L.cluster, st); }))
+        return RNNT_LAUNCH_FAILED;
     return launched();
 }
 

@@ -80,7 +80,7 @@ def select(**kw):
 
 @pytest.mark.parametrize("bad", [
     dict(logits=None), dict(scores=None), dict(out_scores=None), dict(out_tokens=None),
-    dict(out_parents=None), dict(workspace=None), dict(dt=9), dict(B=0), dict(K=0), dict(K=65),
+    dict(out_parents=None), dict(workspace=None, V=1 << 18), dict(dt=9), dict(B=0), dict(K=0), dict(K=65),
     dict(V=0), dict(V=(1 << 20) + 1), dict(Ko=0), dict(Ko=65), dict(batch_stride=-1),
     dict(beam_stride=-1), dict(logits=(1 << 20) + 2), dict(workspace=(1 << 21) + 16),
     dict(B=1 << 29),
@@ -90,10 +90,11 @@ def test_select_refuses(bad):
 
 
 def test_select_workspace():
-    n = N.rnnt_beam_workspace_size(2, 4, 30, 4, N.RNNT_F32)
-    assert n > 0
-    assert select(workspace_bytes=n - 1) == N.RNNT_WORKSPACE_TOO_SMALL
-    assert N.rnnt_beam_workspace_size(2, 4, 1 << 20, 4, N.RNNT_F32) > n
+    assert N.rnnt_beam_workspace_size(2, 4, 30, 4, N.RNNT_F32) == 0        # one launch: none
+    n = N.rnnt_beam_workspace_size(2, 4, 1 << 18, 4, N.RNNT_F32)
+    assert n > 0 and n % 256 == 0
+    assert select(V=1 << 18, workspace_bytes=n - 1) == N.RNNT_WORKSPACE_TOO_SMALL
+    assert N.rnnt_beam_workspace_size(2, 4, 1 << 20, 8, N.RNNT_F32) > n
     for args in ((0, 4, 30, 4, 0), (2, 65, 30, 4, 0), (2, 4, 30, 0, 0), (2, 4, 30, 4, 3)):
         with pytest.raises(N.RNNTError):
             N.rnnt_beam_workspace_size(*args)
