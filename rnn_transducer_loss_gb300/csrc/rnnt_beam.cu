@@ -561,6 +561,7 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
 template <typename T, int NV, bool FUSED>
 __global__ void __launch_bounds__(kRowThreads, NV == 1 ? 6 : 4) k_rows(const SelectParams p) {
     __shared__ RowShared sh;
+    let_next_start();
     const uint32_t row = blockIdx.x / (uint32_t)p.splits;
     const int split = (int)(blockIdx.x - row * (uint32_t)p.splits);
     if (!row_pass<T, NV, FUSED>(p, row, split, sh)) return;
@@ -874,6 +875,7 @@ __device__ __forceinline__ void pick(const SelectParams& p, uint32_t b, const ui
 
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
+    wait_for_previous();
     extern __shared__ uint64_t lists[];                // [K * splits][n], twice
     __shared__ float4 stat[kMaxLists];
     __shared__ PickShared sh;
@@ -988,9 +990,12 @@ bool launch_select(const SelectParams& p, int cluster, cudaStream_t st) {
         cudaGetLastError();
         return false;
     }
-    if (!cluster)
-        k_pick<T><<<(unsigned)p.B, kPickThreads, 2 * sizeof(uint64_t) * p.K * p.splits * p.n, st>>>(p);
-    return true;
+    if (cluster) return true;
+    if (launch_after(k_pick<T>, dim3((unsigned)p.B), kPickThreads,
+                     2 * sizeof(uint64_t) * p.K * p.splits * p.n, st, p))
+        return true;
+    cudaGetLastError();
+    return false;
 }
 
 // The kernels' shared memory limits, raised once per device.

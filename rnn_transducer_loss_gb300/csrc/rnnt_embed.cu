@@ -137,7 +137,9 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortItems = 4;                             // places of a thread and chunk, at most
 constexpr int kMaxBits = 10;
-constexpr int kMaxBins = 1 << kMaxBits;
+constexpr int kMaxBins = 1 << kMaxBits;                   // a thread each
+constexpr int kMaxCluster = 16;
+static_assert(kMaxBins <= kSortThreads, "a digit has a thread");
 constexpr int kCountStride = kSortWarps + 2;              // 17 words: neighbouring digits' counts
                                                           // lie in different banks
 struct SortParams {
@@ -152,10 +154,11 @@ struct SortParams {
     int32_t unit;
 };
 
-// Counts and digits' totals, and the chunk's places in order; at least so much that a CTA has an
-// SM to itself.
+// The chunk's places in order, its counts, and every CTA's totals; at least so much that a CTA
+// has an SM to itself.
 constexpr size_t sort_shared(int bits) {
-    return std::max<size_t>(120 << 10, ((sizeof(uint16_t) * kCountStride + sizeof(int32_t)) << bits) +
+    return std::max<size_t>(120 << 10, ((sizeof(uint16_t) * kCountStride +
+                                             sizeof(int32_t) * kMaxCluster) << bits) +
                                            sizeof(int2) * kSortThreads * kSortItems);
 }
 
@@ -165,27 +168,40 @@ __device__ __forceinline__ void zero_fill(char* at, int64_t bytes, int64_t i, in
     for (; i < bytes / UB; i += step) reinterpret_cast<U*>(at)[i] = U{};
 }
 
-// x becomes the sum of the earlier threads' x; returns the block's sum.
-__device__ __forceinline__ int exclusive_scan(int& x, int32_t* scratch) {
+// x and y become the sums of the earlier threads' x and y; returns the block's sum of x, and of y
+// in all_y.
+__device__ __forceinline__ int exclusive_scan(int& x, int& y, int& all_y, int2* scratch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = x;
+    int2 incl = make_int2(x, y);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        const int a = __shfl_up_sync(0xffffffffu, incl.x, o);
+        const int b = __shfl_up_sync(0xffffffffu, incl.y, o);
+        if (lane >= o) {
+            incl.x += a;
+            incl.y += b;
+        }
     }
     __syncthreads();
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
-    int upto = scratch[lane];                           // the warps' sums, once more
+    int2 upto = scratch[lane];                          // the warps' sums, once more
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
+        const int a = __shfl_up_sync(0xffffffffu, upto.x, o);
+        const int b = __shfl_up_sync(0xffffffffu, upto.y, o);
+        if (lane >= o) {
+            upto.x += a;
+            upto.y += b;
+        }
     }
-    const int before = __shfl_sync(0xffffffffu, upto, max(warp, 1) - 1);
-    x = incl - x + (warp ? before : 0);
-    return __shfl_sync(0xffffffffu, upto, 31);
+    const int before = max(warp, 1) - 1;
+    const int bx = __shfl_sync(0xffffffffu, upto.x, before);
+    const int by = __shfl_sync(0xffffffffu, upto.y, before);
+    x = incl.x - x + (warp ? bx : 0);
+    y = incl.y - y + (warp ? by : 0);
+    all_y = __shfl_sync(0xffffffffu, upto.y, 31);
+    return __shfl_sync(0xffffffffu, upto.x, 31);
 }
 
 __global__ void __launch_bounds__(kSortThreads) k_sort(const SortParams p) {
@@ -199,9 +215,10 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const SortParams p) {
     __shared__ int32_t base[kMaxBins];        // where its next place of a digit goes
     __shared__ int32_t chunk[kMaxBins];       // the current chunk's count of each digit, and where
     __shared__ int32_t start[kMaxBins];       // the digit starts in `ordered`
-    __shared__ int32_t scan[kSortWarps];
+    __shared__ int2 scan[kSortWarps];
     static_assert(kSortWarps == 32, "exclusive_scan takes a warp's sums by a warp");
     const int bins = 1 << p.bits;
+    int32_t* given = reinterpret_cast<int32_t*>(counts32 + bins * kCountStride / 2);   // [CTA][digit]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     if ((int)blockIdx.x >= C) {
@@ -212,6 +229,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const SortParams p) {
         else zero_fill<2>(p.grad_weight, p.bytes, i, step);
         return;
     }
+    cluster.barrier_arrive();
 
     uint32_t n = (uint32_t)p.N;
     for (int pass = 0; pass < p.passes; ++pass) {
@@ -289,61 +307,41 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const SortParams p) {
             rank_chunk(c0);
             for (int b = tid; b < bins; b += kSortThreads) total[b] += chunk[b];
         }
-        cluster.sync();
-        // base[b] = places of smaller digits + places of digit b in earlier CTAs; four threads
-        // read a digit's counts.
-        for (int b0 = 0; b0 < bins; b0 += kSortThreads / 4) {
-            const int b = b0 + tid / 4;
-            int all = 0, ours = 0;
-            if (b < bins)
-                for (int r = tid & 3; r < C; r += 4) {
-                    const int c = *cluster.map_shared_rank(total + b, r);
-                    if (r < rank) ours += c;
-                    all += c;
-                }
-            all += __shfl_xor_sync(0xffffffffu, all, 1);
-            ours += __shfl_xor_sync(0xffffffffu, ours, 1);
-            all += __shfl_xor_sync(0xffffffffu, all, 2);
-            ours += __shfl_xor_sync(0xffffffffu, ours, 2);
-            if (b < bins && (tid & 3) == 0) base[b] = ours;
-            if (b < bins && (tid & 3) == 1) counts32[bins * kCountStride / 2 + b] = all;
-        }
         __syncthreads();
-        const int32_t* alls = reinterpret_cast<int32_t*>(counts32) + bins * kCountStride / 2;
-        constexpr int kEach = kMaxBins / kSortThreads;
-        int all[kEach], sum = 0;
-#pragma unroll
-        for (int q = 0; q < kEach; ++q) {
-            const int b = tid * kEach + q;
-            all[q] = b < bins ? alls[b] : 0;
-            sum += all[q];
+        if (pass == 0) cluster.barrier_wait();          // every CTA has started
+        // Every CTA hands its counts to the others.  base[b] = places of smaller digits, and of
+        // digit b in earlier CTAs; start[b] likewise within the first chunk.
+        for (int i = tid; i < bins * C; i += kSortThreads) {
+            const int r = i >> p.bits, b = i & (bins - 1);
+            *cluster.map_shared_rank(given + rank * bins + b, r) = total[b];
         }
-        int off = sum;
-        const int full = exclusive_scan(off, scan);
-#pragma unroll
-        for (int q = 0; q < kEach; ++q) {
-            const int b = tid * kEach + q;
-            if (b < bins) base[b] += off;
-            off += all[q];
+        cluster.sync();
+        int all = 0, ours = 0, held = 0, first = 0;
+        if (tid < bins) {
+            for (int r = 0; r < C; ++r) {
+                const int c = given[r * bins + tid];
+                if (r < rank) ours += c;
+                all += c;
+            }
+            first = lo < hi ? chunk[tid] : 0;
+        }
+        const int full = exclusive_scan(all, first, held, scan);
+        if (tid < bins) {
+            base[tid] = all + ours;
+            start[tid] = first;
         }
         if (rank == 0 && tid == 0 && pass == 0) *p.count = full;
         __syncthreads();
         int2* out = p.out[pass & 1];
         for (uint32_t c0 = lo; c0 < hi; c0 += step) {
-            if (hi - lo > step) rank_chunk(c0);         // one chunk: still at hand
-            int each[kEach], first = 0;
-#pragma unroll
-            for (int q = 0; q < kEach; ++q) {
-                each[q] = tid * kEach + q < bins ? chunk[tid * kEach + q] : 0;
-                first += each[q];
+            if (hi - lo > step) rank_chunk(c0);         // one chunk: still at hand, with its starts
+            if (hi - lo > step) {
+                int none = 0;
+                first = tid < bins ? chunk[tid] : 0;
+                exclusive_scan(none, first, held, scan);
+                if (tid < bins) start[tid] = first;
+                __syncthreads();
             }
-            const int held = exclusive_scan(first, scan);
-#pragma unroll
-            for (int q = 0; q < kEach; ++q) {
-                if (tid * kEach + q < bins) start[tid * kEach + q] = first;
-                first += each[q];
-            }
-            __syncthreads();
 #pragma unroll
             for (int i = 0; i < kSortItems; ++i) {
                 if (i >= items || key[i] < 0) continue;
@@ -365,7 +363,6 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const SortParams p) {
         n = (uint32_t)full;
         if (!last) cluster.sync();
     }
-    cluster.sync();                                     // others may still read `total`
 }
 
 // -------------------------------------------------- gradient: sums of sorted rows
@@ -439,6 +436,8 @@ __global__ void __launch_bounds__(kSumThreads, 7) k_sum(const SumParams p) {
     const int groups = kSumThreads / p.group;
     const int64_t t = (int64_t)blockIdx.x * groups + g;
     const int unit = blockIdx.y * p.group + in_group;
+    wait_for_previous();
+    let_next_start();
     const int64_t n = *p.count, j0 = t * kTile;
     int2* mine = entries + g * kEntries;
     for (int i = in_group; i < kEntries; i += p.group)
@@ -501,18 +500,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const SumParams p) {
     __shared__ float partly[kJoinThreads * E];
     const int group = min(p.group, 32), groups = kJoinThreads / group;
     const int g = threadIdx.x / group, lane = threadIdx.x & 31;
-    const int64_t n = *p.count;
+    const int64_t n = __ldcg(p.count);
     // the tiles that own such an id, a lane each
     int mine = -1;
     const int64_t t0 = (int64_t)blockIdx.x * kJoinTiles;
     if (lane < kJoinTiles && (t0 + lane + 1) * kTile < n) {
         const int64_t end = (t0 + lane + 1) * kTile;
-        const int before = t0 + lane > 0 ? p.sorted[end - kTile - 1].x : -1;
-        const int far = end + kTile - 1 < n ? p.sorted[end + kTile - 1].x : -1;
-        mine = p.sorted[end - 1].x;
+        const int before = t0 + lane > 0 ? __ldcg(&p.sorted[end - kTile - 1].x) : -1;
+        const int far = end + kTile - 1 < n ? __ldcg(&p.sorted[end + kTile - 1].x) : -1;
+        mine = __ldcg(&p.sorted[end - 1].x);
         if (far != mine || before == mine) mine = -1;
     }
-    for (unsigned owners = __ballot_sync(0xffffffffu, mine >= 0); owners; owners &= owners - 1) {
+    unsigned owners = __ballot_sync(0xffffffffu, mine >= 0);
+    wait_for_previous();               // so far only k_sort's results: it was over before k_sum began
+    for (; owners; owners &= owners - 1) {
     const int which = __ffs(owners) - 1, id = __shfl_sync(0xffffffffu, mine, which);
     const int64_t t = t0 + which;
         // Tiles t + 1 .. t + m hold more of it: the first that ends with another id is the last.
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const SumParams p) {
         int64_t m = 0;
         for (;;) {
             const int64_t at = (t + 1 + m + threadIdx.x + 1) * kTile;      // the tile behind
-            const unsigned go = __ballot_sync(0xffffffffu, at < n && p.sorted[at].x == id);
+            const unsigned go = __ballot_sync(0xffffffffu, at < n && __ldcg(&p.sorted[at].x) == id);
             __syncthreads();
             if (lane == 0) runs[threadIdx.x / 32] = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
             __syncthreads();
@@ -920,13 +921,21 @@ extern "C" rnnt_status_t rnnt_embed_grad(const void* grad_out, rnnt_dtype_t dt,
         cudaGetLastError();
         return RNNT_LAUNCH_FAILED;
     }
+    bool ok = true;
     with_unit(dt, unit, [&](auto tag, auto ub) {
-        k_sum<decltype(tag), decltype(ub)::value>
-            <<<dim3((unsigned)sum_ctas, cols), kSumThreads, sizeof(int2) * groups * 2 * kTile, st>>>(q);
-        if (L.tiles > 1)
-            k_join<decltype(tag), decltype(ub)::value>
-                <<<dim3((unsigned)((L.tiles + kJoinTiles - 1) / kJoinTiles), std::min(cols * ((unsigned)q.group + 31) / 32, 65535u)),
-                   kJoinThreads, 0, st>>>(q);
+        using T = decltype(tag);
+        constexpr int UB = decltype(ub)::value;
+        ok = launch_after(k_sum<T, UB>, dim3((unsigned)sum_ctas, cols), kSumThreads,
+                          sizeof(int2) * groups * 2 * kTile, st, q) &&
+             (L.tiles == 1 ||
+              launch_after(k_join<T, UB>,
+                           dim3((unsigned)((L.tiles + kJoinTiles - 1) / kJoinTiles),
+                                std::min(cols * ((unsigned)q.group + 31) / 32, 65535u)),
+                           kJoinThreads, 0, st, q));
     });
+    if (!ok) {
+        cudaGetLastError();
+        return RNNT_LAUNCH_FAILED;
+    }
     return launched();
 }

@@ -45,6 +45,31 @@ union Pack {
     __device__ Pack() {}
 };
 
+// A kernel launched by launch_after may start while the kernel before it in the stream runs its
+// last blocks; it calls wait_for_previous before it touches what that kernel writes (and only
+// kernels that have called it themselves call let_next_start).
+__device__ __forceinline__ void wait_for_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... Params, typename... Args>
+inline bool launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t shared,
+                         cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline bool valid_dtype(int dt) { return dt == RNNT_F32 || dt == RNNT_F16 || dt == RNNT_BF16; }
 inline int elem_size(int dt) { return dt == RNNT_F32 ? 4 : 2; }
