@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed(const EmbedParams p) {
 //
 // Latency bounds it (64000 places of 50000 ids are 0.25 MB to read), so the rest of the
 // device spends the time on zeroing grad_weight, whose rows without places k_sum does not
-// come to.
+// come to (finding those rows first, so as to zero no others, took 15 us longer than it saved
+// for 50000 ids of which a third occur).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortItems = 4;                             // places of a thread and chunk, at most
@@ -148,6 +149,7 @@ struct SortParams {
     int32_t bits, passes;      // digits of `bits` bits
     int2* out[2];              // {id, place}: pass i writes out[i & 1]
     int32_t* count;            // places that are not padding
+    int32_t* heavy;            // number of long ids, which k_sum lists: set to 0
     int32_t* status;
     char* grad_weight;         // zeroed by the clusters behind the first
     int64_t bytes;
@@ -330,7 +332,10 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const SortParams p) {
             base[tid] = all + ours;
             start[tid] = first;
         }
-        if (rank == 0 && tid == 0 && pass == 0) *p.count = full;
+        if (rank == 0 && tid == 0 && pass == 0) {
+            *p.count = full;
+            *p.heavy = 0;
+        }
         __syncthreads();
         int2* out = p.out[pass & 1];
         for (uint32_t c0 = lo; c0 < hi; c0 += step) {
@@ -374,13 +379,14 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const SortParams p) {
 // which k_join adds in order.
 constexpr int kTile = 32;
 constexpr int kSumThreads = 128;
-constexpr int kAhead = 8;                 // rows a thread has in flight
+constexpr int kRing = 8;                  // rows a thread has in flight, a power of two
 
 struct SumParams {
     const char* grad_out;
     char* grad_weight;
     const int2* sorted;      // {id, place}
     const int32_t* count;
+    int32_t* heavy;          // number of long ids, then the tiles that they begin in, in no order
     float* partial;          // [tile][2][D]
     int64_t tiles;           // upper bound: tiles of all places
     int32_t V, D, nunits, group;   // group: threads of a tile, a power of two
@@ -426,8 +432,28 @@ __device__ __forceinline__ void add_sums(const float* from, float* acc) {
     }
 }
 
+// One unit from global to shared memory, behind the thread's back: it reads it after
+// copies_left lets it (two-byte units, which have no such copy, at once).
+template <int UB>
+__device__ __forceinline__ void copy_unit(void* to, const void* from) {
+    if constexpr (UB == 2) {
+        *reinterpret_cast<uint16_t*>(to) = __ldg(reinterpret_cast<const uint16_t*>(from));
+    } else if constexpr (UB == 16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                     :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
+                     :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "n"(UB) : "memory");
+    }
+}
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_left() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
+}
+
 template <typename T, int UB>
-__global__ void __launch_bounds__(kSumThreads, 7) k_sum(const SumParams p) {
+__global__ void __launch_bounds__(kSumThreads, 12) k_sum(const SumParams p) {
     using U = typename Unit<UB>::type;
     constexpr int E = UB / (int)sizeof(T);
     constexpr int kEntries = 2 * kTile;
@@ -464,64 +490,62 @@ __global__ void __launch_bounds__(kSumThreads, 7) k_sum(const SumParams p) {
     int cur = mine[j].x;
     float* part = p.partial + t * 2 * p.D + unit * E;
     const U* src = reinterpret_cast<const U*>(p.grad_out) + unit;
-    for (; j < end; j += kAhead) {
-        Pack<T, UB> v[kAhead];
+    // the rows go through a ring in shared memory, a slot a row, each thread its own unit: it
+    // waits for its own copies only
+    __shared__ U ring[kRing][kSumThreads];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (j + i < end) v[i].raw = __ldg(src + (int64_t)mine[j + i].y * p.nunits);
+    for (int i = 0; i < kRing; ++i) {
+        if (j + i < end)
+            copy_unit<UB>(&ring[(j + i) & (kRing - 1)][threadIdx.x],
+                          src + (int64_t)mine[j + i].y * p.nunits);
+        copy_group();
+    }
+    for (; j < end; ++j) {
+        copies_left<kRing - 1>();
+        Pack<T, UB> v;
+        v.raw = ring[j & (kRing - 1)][threadIdx.x];
+        if (j + kRing < end)
+            copy_unit<UB>(&ring[j & (kRing - 1)][threadIdx.x],
+                          src + (int64_t)mine[j + kRing].y * p.nunits);
+        copy_group();
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (j + i >= end) break;
+        for (int e = 0; e < E; ++e) acc[e] += to_f32(v.e[e]);
+        // the tile's last place may be followed by more of its id, which other tiles add
+        const int next = j + 1 < kEntries ? mine[j + 1].x : -1;
+        const bool ends = next != cur;
+        if (ends || j + 1 == end) {
+            if (!head && !ends && unit == 0) p.heavy[1 + atomicAdd(p.heavy, 1)] = (int)t;
+            if (head || !ends) put_sums<E>(part + (head ? 0 : p.D), acc);
+            else store_unit<T, UB>(p.grad_weight, cur, p.nunits, unit, acc, p.scale);
+            head = false;
+            cur = next;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += to_f32(v[i].e[e]);
-            // the tile's last place may be followed by more of its id, which other tiles add
-            const int next = j + i + 1 < kEntries ? mine[j + i + 1].x : -1;
-            const bool ends = next != cur;
-            if (ends || j + i + 1 == end) {
-                if (head || !ends) put_sums<E>(part + (head ? 0 : p.D), acc);
-                else store_unit<T, UB>(p.grad_weight, cur, p.nunits, unit, acc, p.scale);
-                head = false;
-                cur = next;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-            }
+            for (int e = 0; e < E; ++e) acc[e] = 0.0f;
         }
     }
 }
 
-// The long id that begins in tile t: its partial sums, tile after tile.  A CTA takes
-// kJoinTiles tiles and a slice of columns; its groups of threads add stretches of the id's
-// tiles, which are then added in order.
+// The long ids' partial sums, tile after tile.  A CTA takes an id and a slice of columns; its
+// groups of threads add stretches of the id's tiles, which are then added in order.
 constexpr int kJoinThreads = 128;
-constexpr int kJoinTiles = 4;
 template <typename T, int UB>
 __global__ void __launch_bounds__(kJoinThreads) k_join(const SumParams p) {
     constexpr int E = UB / (int)sizeof(T);
     __shared__ float partly[kJoinThreads * E];
     const int group = min(p.group, 32), groups = kJoinThreads / group;
     const int g = threadIdx.x / group, lane = threadIdx.x & 31;
-    const int64_t n = __ldcg(p.count);
-    // the tiles that own such an id, a lane each
-    int mine = -1;
-    const int64_t t0 = (int64_t)blockIdx.x * kJoinTiles;
-    if (lane < kJoinTiles && (t0 + lane + 1) * kTile < n) {
-        const int64_t end = (t0 + lane + 1) * kTile;
-        const int before = t0 + lane > 0 ? __ldcg(&p.sorted[end - kTile - 1].x) : -1;
-        const int far = end + kTile - 1 < n ? __ldcg(&p.sorted[end + kTile - 1].x) : -1;
-        mine = __ldcg(&p.sorted[end - 1].x);
-        if (far != mine || before == mine) mine = -1;
-    }
-    unsigned owners = __ballot_sync(0xffffffffu, mine >= 0);
-    wait_for_previous();               // so far only k_sort's results: it was over before k_sum began
-    for (; owners; owners &= owners - 1) {
-    const int which = __ffs(owners) - 1, id = __shfl_sync(0xffffffffu, mine, which);
-    const int64_t t = t0 + which;
+    wait_for_previous();
+    const int64_t n = *p.count;
+    const int heavy = *p.heavy;
+    for (int which = blockIdx.x; which < heavy; which += gridDim.x) {
+        const int64_t t = p.heavy[1 + which];
+        const int id = p.sorted[(t + 1) * kTile - 1].x;
         // Tiles t + 1 .. t + m hold more of it: the first that ends with another id is the last.
         __shared__ int runs[kJoinThreads / 32];
         int64_t m = 0;
         for (;;) {
             const int64_t at = (t + 1 + m + threadIdx.x + 1) * kTile;      // the tile behind
-            const unsigned go = __ballot_sync(0xffffffffu, at < n && __ldcg(&p.sorted[at].x) == id);
+            const unsigned go = __ballot_sync(0xffffffffu, at < n && p.sorted[at].x == id);
             __syncthreads();
             if (lane == 0) runs[threadIdx.x / 32] = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
             __syncthreads();
@@ -745,7 +769,7 @@ SortLimits sort_limits() {
 }
 
 struct GradLayout {
-    size_t out[2], count, partial, total;
+    size_t out[2], count, heavy, partial, total;
     int64_t tiles;
 };
 bool few_places(int64_t N) { return N <= kFewPlaces; }
@@ -759,6 +783,7 @@ GradLayout grad_layout(int64_t N, int32_t D) {
     }
     L.count = at;   at = align256(at + sizeof(int32_t));
     L.tiles = (N + kTile - 1) / kTile;
+    L.heavy = at;   at = align256(at + sizeof(int32_t) * (size_t)(1 + L.tiles));
     L.partial = at; at = align256(at + sizeof(float) * 2 * (size_t)L.tiles * (size_t)D);
     L.total = at;
     return L;
@@ -879,6 +904,7 @@ extern "C" rnnt_status_t rnnt_embed_grad(const void* grad_out, rnnt_dtype_t dt,
     q.grad_weight = static_cast<char*>(grad_weight);
     q.sorted = s.out[(s.passes - 1) & 1];
     q.count = s.count;
+    q.heavy = s.heavy = reinterpret_cast<int32_t*>(ws + L.heavy);
     q.partial = reinterpret_cast<float*>(ws + L.partial);
     q.tiles = L.tiles;
     q.V = V;
@@ -929,7 +955,7 @@ extern "C" rnnt_status_t rnnt_embed_grad(const void* grad_out, rnnt_dtype_t dt,
                           sizeof(int2) * groups * 2 * kTile, st, q) &&
              (L.tiles == 1 ||
               launch_after(k_join<T, UB>,
-                           dim3((unsigned)((L.tiles + kJoinTiles - 1) / kJoinTiles),
+                           dim3((unsigned)std::min<int64_t>(L.tiles / 2 + 1, 304),
                                 std::min(cols * ((unsigned)q.group + 31) / 32, 65535u)),
                            kJoinThreads, 0, st, q));
     });

@@ -46,8 +46,7 @@ union Pack {
 };
 
 // A kernel launched by launch_after may start while the kernel before it in the stream runs its
-// last blocks; it calls wait_for_previous before it touches what that kernel writes (and only
-// kernels that have called it themselves call let_next_start).
+// last blocks; all its blocks call wait_for_previous, before they touch what that kernel writes.
 __device__ __forceinline__ void wait_for_previous() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
