@@ -38,8 +38,9 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 //     thread that reach the bound are read once more, from the cache, and their elements
 //     that reach it are ranked by counting.  Rows with a crowd of equal elements at the
 //     bound go through best_of_row instead, tile by tile.
-constexpr int kRowThreads = 256;
-constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kRowThreads = 128;           // of k_rows: 8 CTAs an SM hold 1024 rows at once (256
+                                           // threads, 4 CTAs: a second wave, 32 against 25 us)
+constexpr int kClusterThreads = 256;       // of k_search
 constexpr float kLog2e = 1.44269504f;      // log2 e to 2^-26
 constexpr float kRescale = 16.0f;
 constexpr float kMostRef = 1e30f;          // larger references: computed again by exact_lse
@@ -162,9 +163,10 @@ __device__ __forceinline__ Key warp_sorted(Key key) {
 
 // Ranks the buffer's c different keys: best[r] = the r-th for r < n.  Four threads count for a
 // key.  Ends without a barrier.
+template <int TH>
 __device__ __forceinline__ void rank_keys(const uint64_t* buf, int c, uint64_t* best, int n) {
     const int part = threadIdx.x & 3;
-    for (int i0 = 0; i0 < c; i0 += kRowThreads / 4) {
+    for (int i0 = 0; i0 < c; i0 += TH / 4) {
         const int i = i0 + (threadIdx.x >> 2);
         const uint64_t mine = i < c ? buf[i] : ~0ull;
         int rank = 0;
@@ -177,9 +179,10 @@ __device__ __forceinline__ void rank_keys(const uint64_t* buf, int c, uint64_t* 
 }
 
 // Keeps the n best of the buffer's keys, in order; all threads call it.
+template <int TH>
 __device__ __noinline__ void keep_best(uint64_t* buf, uint64_t* best, int* count, int n) {
     const int c = *count, m = min(c, n);
-    rank_keys(buf, c, best, n);
+    rank_keys<TH>(buf, c, best, n);
     __syncthreads();
     if (threadIdx.x < m) buf[threadIdx.x] = best[threadIdx.x];
     if (threadIdx.x == 0) *count = m;
@@ -265,10 +268,10 @@ __device__ __forceinline__ int odd_element(const SelectParams& p, uint32_t row, 
     return at < (threadIdx.x < E ? ahead : p.V) ? at : -1;
 }
 
-// The n best of a split to best: every tile of kRowThreads vectors gives its elements above the
+// The n best of a split to best: every tile of TH vectors gives its elements above the
 // bound, the n-th best so far; a tile that has too many gives them element by element of each
 // thread's vector.
-template <typename T>
+template <typename T, int TH>
 __device__ __noinline__ void best_of_row(const SelectParams& p, uint32_t row, int split,
                                          uint64_t* buf, uint64_t* best, int* count) {
     constexpr int E = 16 / (int)sizeof(T);
@@ -283,7 +286,7 @@ __device__ __noinline__ void best_of_row(const SelectParams& p, uint32_t row, in
         const float x = to_f32(row_of<T>(p, row)[odd]);
         if (x > -INFINITY) buf[atomicAdd(count, 1)] = key_of(x, odd);
     }
-    for (int t0 = 0; t0 < sp.vecs; t0 += kRowThreads) {
+    for (int t0 = 0; t0 < sp.vecs; t0 += TH) {
         const Pack<T, 16> v = sp.at(t0 + tid);
         const int at = sp.first + (t0 + tid) * E;
         for (int e0 = 0; e0 < E;) {
@@ -308,34 +311,35 @@ __device__ __noinline__ void best_of_row(const SelectParams& p, uint32_t row, in
             }
             e0 = e1;
             __syncthreads();
-            if (*count > kRowThreads) {
-                keep_best(buf, best, count, n);
-                least = max(least, buf[n - 1]);        // n < kRowThreads
+            if (*count > TH) {
+                keep_best<TH>(buf, best, count, n);
+                least = max(least, buf[n - 1]);        // n < TH
             }
         }
     }
     __syncthreads();
-    rank_keys(buf, *count, best, n);
+    rank_keys<TH>(buf, *count, best, n);
     __syncthreads();
 }
 
+template <int TH>
 struct RowShared {
     uint64_t buf[kBuf], best[RNNT_MAX_BEAM];       // best: the split's list
     float4 stat;
-    Pair wsum[kRowWarps];
-    float wref[kRowWarps], wleast[kRowWarps], wover[kRowWarps];
-    float tops[kSlots][kRowThreads];
-    int hit[kSlots * kRowThreads];                 // slots to be read once more
+    Pair wsum[(TH / 32)];
+    float wref[(TH / 32)], wleast[(TH / 32)], wover[(TH / 32)];
+    float tops[kSlots][TH];
+    int hit[kSlots * TH];                 // slots to be read once more
     int hits, count, bads, rescales;
 };
 
 // Leaves the split's statistics and list (zeros behind its end) in sh, behind a barrier; returns
 // false, at once, for a beam that offers no logits.
-template <typename T, int NV, bool FUSED>
+template <typename T, int NV, bool FUSED, int TH>
 __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, int split,
-                                         RowShared& sh) {
+                                         RowShared<TH>& sh) {
     constexpr int E = 16 / (int)sizeof(T);
-    constexpr int kTileVecs = kRowThreads * NV;
+    constexpr int kTileVecs = TH * NV;
     auto& buf = sh.buf;
     auto& best = sh.best;
     auto& wsum = sh.wsum;
@@ -352,10 +356,10 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
         if (t0 + kTileVecs <= vecs) {                        // for the whole block
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                v[i].raw = load_stream(sp.aligned + t0 + i * kRowThreads + tid);
+                v[i].raw = load_stream(sp.aligned + t0 + i * TH + tid);
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) v[i] = sp.at(t0 + i * kRowThreads + tid);
+            for (int i = 0; i < NV; ++i) v[i] = sp.at(t0 + i * TH + tid);
         }
     };
     Pack<T, 16> v[NV], next[NV];
@@ -400,7 +404,7 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
                 __syncthreads();
                 ref = wref[0];
 #pragma unroll
-                for (int w = 1; w < kRowWarps; ++w) ref = fmaxf(ref, wref[w]);
+                for (int w = 1; w < (TH / 32); ++w) ref = fmaxf(ref, wref[w]);
                 if (!(fabsf(ref) < kMostRef)) ref = 0.0f;
             }
             if (top - ref > kRescale) {
@@ -416,7 +420,7 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 s[i] = 0.0f;
-                if (i && t0 + i * kRowThreads >= vecs) continue;     // for the whole block
+                if (i && t0 + i * TH >= vecs) continue;     // for the whole block
                 float2 y[E / 2];
                 unpack(v[i], y);
 #pragma unroll
@@ -443,7 +447,7 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
         for (int i = 0; i < NV; ++i) v[i].raw = next[i].raw;
     }
     // The bound.
-    const int whole = min(vecs / 32, kRowWarps);       // warps whose threads all have a maximum
+    const int whole = min(vecs / 32, (TH / 32));       // warps whose threads all have a maximum
     const int nth = (p.n - 1) / max(whole, 1);         // of each one's, from 0
     float least = most;
     if (nth == 0) {
@@ -458,7 +462,7 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
     __syncthreads();
     least = whole && nth < 32 ? INFINITY : -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kRowWarps; ++w)
+    for (int w = 0; w < (TH / 32); ++w)
         if (w < whole) least = fminf(least, wleast[w]);
     const int span = kTileVecs << shift_slot;
     for (int t = 0; t * span < vecs; ++t) {
@@ -468,7 +472,7 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
         int to = 0;
         if (lane == 0) to = atomicAdd(&hits, __popc(who));
         to = __shfl_sync(0xffffffffu, to, 0) + __popc(who & ((1u << lane) - 1));
-        if (reaches) hit[to] = t * kRowThreads + tid;
+        if (reaches) hit[to] = t * TH + tid;
     }
     float at = ref;                                // the largest of the threads' references
     if (FUSED) {
@@ -482,7 +486,7 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
             __syncthreads();
             at = wref[0];
 #pragma unroll
-            for (int w = 1; w < kRowWarps; ++w) at = fmaxf(at, wref[w]);
+            for (int w = 1; w < (TH / 32); ++w) at = fmaxf(at, wref[w]);
             const float f = at != ref ? ex2(__fmul_rn(ref, kLog2e) - __fmul_rn(at, kLog2e)) : 1.0f;
             total = Pair{total.h * f, total.l * f};
             over *= f;
@@ -500,9 +504,9 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
     __syncthreads();
     // Those slots' vectors once more: their elements that reach the bound.
     const int per = NV << shift_slot;              // vectors of a slot
-    for (int i = tid; i < hits * per; i += kRowThreads) {
+    for (int i = tid; i < hits * per; i += TH) {
         const int slot = hit[i / per];
-        const int j = slot / kRowThreads * span + i % per * kRowThreads + slot % kRowThreads;
+        const int j = slot / TH * span + i % per * TH + slot % TH;
         const Pack<T, 16> w = sp.at(j);
         unsigned which = 0;
 #pragma unroll
@@ -526,16 +530,16 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
     }
     __syncthreads();
     const bool crowd = count > kBuf;
-    if (warp == kRowWarps - 1) {                   // the keys are ranked by the first ones
+    if (warp == (TH / 32) - 1) {                   // the keys are ranked by the first ones
         Pair total{0.0f, 0.0f};
         float over = 0.0f, err = 0.0f;
         if (FUSED) {
-            if (lane < kRowWarps) {
+            if (lane < (TH / 32)) {
                 total = wsum[lane];
                 over = wover[lane];
             }
 #pragma unroll
-            for (int o = kRowWarps / 2; o; o >>= 1) {
+            for (int o = (TH / 32) / 2; o; o >>= 1) {
                 total = add(total, shuffled(total, o));
                 over += __shfl_xor_sync(0xffffffffu, over, o);
             }
@@ -550,21 +554,21 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
         if (lane == 0)
             sh.stat = make_float4(FUSED ? at : bads ? NAN : 0.0f, total.h, total.l, err);
     }
-    if (!crowd) rank_keys(buf, count, best, p.n);
+    if (!crowd) rank_keys<TH>(buf, count, best, p.n);
     __syncthreads();
-    if (crowd) best_of_row<T>(p, row, split, buf, best, &count);
-    for (int i = count + tid; i < p.n; i += kRowThreads) best[i] = 0;
+    if (crowd) best_of_row<T, TH>(p, row, split, buf, best, &count);
+    for (int i = count + tid; i < p.n; i += TH) best[i] = 0;
     __syncthreads();
     return true;
 }
 
 template <typename T, int NV, bool FUSED>
-__global__ void __launch_bounds__(kRowThreads, NV == 1 ? 6 : 4) k_rows(const SelectParams p) {
-    __shared__ RowShared sh;
+__global__ void __launch_bounds__(kRowThreads, NV == 1 ? 12 : 8) k_rows(const SelectParams p) {
+    __shared__ RowShared<kRowThreads> sh;
     let_next_start();
     const uint32_t row = blockIdx.x / (uint32_t)p.splits;
     const int split = (int)(blockIdx.x - row * (uint32_t)p.splits);
-    if (!row_pass<T, NV, FUSED>(p, row, split, sh)) return;
+    if (!row_pass<T, NV, FUSED, kRowThreads>(p, row, split, sh)) return;
     uint64_t* list = p.list + (int64_t)blockIdx.x * p.n;
     if (threadIdx.x < p.n) list[threadIdx.x] = sh.best[threadIdx.x];
     if (threadIdx.x == 0) p.stat[blockIdx.x] = sh.stat;
@@ -892,14 +896,14 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
 // statistics in the first CTA's shared memory, which picks.  One launch and no workspace.
 struct ClusterShared {
     union {
-        RowShared rows;
+        RowShared<kClusterThreads> rows;
         PickShared pick;
     };
     float4 stat[RNNT_MAX_BEAM];
 };
 
 template <typename T, int NV, bool FUSED>
-__global__ void __launch_bounds__(kRowThreads, 4) k_search(const SelectParams p) {
+__global__ void __launch_bounds__(kClusterThreads, 4) k_search(const SelectParams p) {
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) char search_space[];
     ClusterShared& sh = *reinterpret_cast<ClusterShared*>(search_space);
@@ -909,14 +913,14 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_search(const SelectParams p)
     cluster.barrier_arrive();                          // that every CTA has started:
     uint64_t* to_lists = cluster.map_shared_rank(lists, 0);
     float4* to_stat = cluster.map_shared_rank(sh.stat, 0);
-    const bool reads = row_pass<T, NV, FUSED>(p, b * p.K + rank, 0, sh.rows);
+    const bool reads = row_pass<T, NV, FUSED, kClusterThreads>(p, b * p.K + rank, 0, sh.rows);
     cluster.barrier_wait();                            // here it is to be known
     if (reads) {
         if (threadIdx.x < p.n) to_lists[rank * p.n + threadIdx.x] = sh.rows.best[threadIdx.x];
         if (threadIdx.x == 0) to_stat[rank] = sh.rows.stat;
     }
     cluster.sync();
-    if (rank == 0) pick<T, kRowThreads>(p, b, lists, lists + p.K * p.n, sh.stat, sh.pick);
+    if (rank == 0) pick<T, kClusterThreads>(p, b, lists, lists + p.K * p.n, sh.stat, sh.pick);
 }
 
 struct SelectLayout {
@@ -941,9 +945,9 @@ SelectLayout select_layout(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt) 
         L.cluster = K;
         return L;
     }
-    // one tile a CTA where that gives no more than a wave of 6 CTAs an SM, else a wave of 4
+    // one tile a CTA where that gives no more than a wave of 12 CTAs an SM, else a wave of 8
     const int64_t rows = (int64_t)B * K, tiles = (vecs + kRowThreads - 1) / kRowThreads;
-    int64_t splits = rows * tiles <= 152 * 6 ? tiles : std::min(tiles, 152 * 4 / rows);
+    int64_t splits = rows * tiles <= 152 * 12 ? tiles : std::min(tiles, 152 * 8 / rows);
     splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxLists / K));
     L.split_vecs = (int32_t)((vecs + splits - 1) / splits);
     L.splits = (int32_t)((vecs + L.split_vecs - 1) / L.split_vecs);
@@ -970,7 +974,7 @@ bool launch_select(const SelectParams& p, int cluster, cudaStream_t st) {
         }
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)(p.B * cluster));
-        cfg.blockDim = dim3(kRowThreads);
+        cfg.blockDim = dim3(kClusterThreads);
         cfg.dynamicSmemBytes = sizeof(ClusterShared) + 2 * sizeof(uint64_t) * p.K * p.n;
         cfg.stream = st;
         cudaLaunchAttribute attr[1];
@@ -982,8 +986,9 @@ bool launch_select(const SelectParams& p, int cluster, cudaStream_t st) {
         return cudaLaunchKernelEx(&cfg, k_search<T, NV, FUSED>, p) == cudaSuccess;
     };
     auto by_size = [&](auto fused) {
-        if (p.split_vecs <= kRowThreads) return launch(std::integral_constant<int, 1>{}, fused);
-        if (p.split_vecs <= 2 * kRowThreads) return launch(std::integral_constant<int, 2>{}, fused);
+        const int threads = cluster ? kClusterThreads : kRowThreads;
+        if (p.split_vecs <= threads) return launch(std::integral_constant<int, 1>{}, fused);
+        if (p.split_vecs <= 2 * threads) return launch(std::integral_constant<int, 2>{}, fused);
         return launch(std::integral_constant<int, 4>{}, fused);
     };
     if (!(p.fused ? by_size(std::true_type{}) : by_size(std::false_type{}))) {
