@@ -40,7 +40,8 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 //     bound go through best_of_row instead, tile by tile.
 constexpr int kRowThreads = 128;           // of k_rows: 8 CTAs an SM hold 1024 rows at once (256
                                            // threads, 4 CTAs: a second wave, 32 against 25 us)
-constexpr int kClusterThreads = 256;       // of k_search
+constexpr int kClusterThreads = 128;       // of k_search
+constexpr int kMaxCluster = 16;
 constexpr float kLog2e = 1.44269504f;      // log2 e to 2^-26
 constexpr float kRescale = 16.0f;
 constexpr float kMostRef = 1e30f;          // larger references: computed again by exact_lse
@@ -684,12 +685,12 @@ __device__ __forceinline__ unsigned long long or_lanes(unsigned long long x) {
            __reduce_or_sync(0xffffffffu, (uint32_t)x);
 }
 
-// The selection of item b from its lists ([K * splits][n]) and statistics, in shared memory
-// already (behind the barrier here); values: as large as the lists.
-template <typename T, int THREADS>
-__device__ __forceinline__ void pick(const SelectParams& p, uint32_t b, const uint64_t* lists,
-                                     uint64_t* values, const float4* stat, PickShared& sh) {
-    const int tid = threadIdx.x, lane = tid & 31;
+// The beams of item b from their lists ([K * splits][n]) and statistics, in shared memory already
+// (behind the barrier here); leaves in sh.again the beams whose log-sum-exp is wanted exactly.
+template <int THREADS>
+__device__ __forceinline__ void weigh(const SelectParams& p, uint32_t b, const uint64_t* lists,
+                                      const float4* stat, PickShared& sh) {
+    const int tid = threadIdx.x;
     if (tid == 0) sh.again = 0;
     __syncthreads();
     // A beam's log-sum-exp from its splits: by one thread, or a warp's lanes together.
@@ -754,120 +755,125 @@ __device__ __forceinline__ void pick(const SelectParams& p, uint32_t b, const ui
         }
     }
     __syncthreads();
+}
+
+// What a beam's exact log-sum-exp changes, by one thread.
+__device__ __forceinline__ void settle(const SelectParams& p, PickShared& sh, int k, Pair l) {
+    sh.lse[k] = l;
+    sh.error[k] = 0.0f;
+    if (l.h != l.h) {                      // the row holds NaN
+        sh.kind[k] = 0;
+        if (p.status) *p.status = RNNT_INVALID_VALUE;
+    }
+}
+
+// The selection by the log-sum-exps at hand; leaves in sh.again the beams whose log-sum-exp it
+// wants exactly before it can be sure.  `values` is as large as the lists.
+template <int THREADS>
+__device__ __forceinline__ void choose(const SelectParams& p, const uint64_t* lists,
+                                       uint64_t* values, PickShared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31;
     const int nlists = p.K * p.splits;
-    unsigned long long again = sh.again;
-    for (int turn = 0; turn <= RNNT_MAX_BEAM; ++turn) {        // each settles a beam at least
-        for (; again; again &= again - 1) {
-            const int k = __ffsll((long long)again) - 1;
-            const Pair l = exact_lse<T, THREADS>(row_of<T>(p, b * p.K + k), p.V, sh.sums, sh.tops);
-            if (tid == 0) {
-                sh.lse[k] = l;
-                sh.error[k] = 0.0f;
-                if (l.h != l.h) {                      // it holds NaN
-                    sh.kind[k] = 0;
-                    if (p.status) *p.status = RNNT_INVALID_VALUE;
+    // Ordered values of the lists' elements, 0: none.
+    for (int m = tid; m < nlists * p.n; m += THREADS) {
+        const int i = m / p.n, k = i / p.splits, what = sh.kind[k];
+        uint64_t v = 0;
+        if (what == 2) {
+            if (m == k * p.splits * p.n) v = ordered(Pair{sh.score[k], 0.0f});
+        } else if (const uint64_t c = what == 1 ? lists[m] : 0) {
+            const Pair x = two_sum(sh.score[k], unordered((uint32_t)(c >> 32)));
+            v = ordered(add(x, Pair{-sh.lse[k].h, -sh.lse[k].l}));
+        }
+        values[m] = v;
+    }
+    __syncthreads();
+    if (tid < 32) {
+        constexpr int L = kMaxLists / 32;
+        uint64_t head[L];
+        int at[L];
+#pragma unroll
+        for (int q = 0; q < L; ++q) {
+            const int i = q * 32 + lane;
+            at[q] = 0;
+            head[q] = i < nlists ? values[i * p.n] : 0;
+        }
+        int found = 0;
+        for (; found < p.Ko; ++found) {
+            uint64_t v = head[0];
+            int q0 = 0;
+#pragma unroll
+            for (int q = 1; q < L; ++q)
+                if (head[q] > v) {                 // equal: the lower list
+                    v = head[q];
+                    q0 = q;
                 }
+            const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+            if (!hi) break;
+            const uint32_t lo = __reduce_max_sync(
+                0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+            // of equal values the lowest list: the lowest beam, and token
+            const uint32_t list = __reduce_min_sync(
+                0xffffffffu, v == ((uint64_t)hi << 32 | lo) ? (uint32_t)(q0 * 32 + lane)
+                                                            : 0xffffffffu);
+            if ((list & 31) == lane) {
+                sh.oval[found] = v;
+                sh.oid[found] = list << 8 | sel(at, q0);
+#pragma unroll
+                for (int q = 0; q < L; ++q)
+                    if (q == q0) {
+                        ++at[q];
+                        head[q] = at[q] < p.n ? values[list * p.n + at[q]] : 0;
+                    }
             }
         }
-        __syncthreads();
-        // Ordered values of the lists' elements, 0: none.
-        for (int m = tid; m < nlists * p.n; m += THREADS) {
-            const int i = m / p.n, k = i / p.splits, what = sh.kind[k];
-            uint64_t v = 0;
-            if (what == 2) {
-                if (m == k * p.splits * p.n) v = ordered(Pair{sh.score[k], 0.0f});
-            } else if (const uint64_t c = what == 1 ? lists[m] : 0) {
-                const Pair x = two_sum(sh.score[k], unordered((uint32_t)(c >> 32)));
-                v = ordered(add(x, Pair{-sh.lse[k].h, -sh.lse[k].l}));
+        __syncwarp();
+        for (int r = lane; r < found; r += 32) sh.obeam[r] = (uint8_t)((sh.oid[r] >> 8) / p.splits);
+        __syncwarp();
+        unsigned long long doubt = 0;
+        if (p.fused && found) {
+            // Neighbours of different beams whose order is in doubt.
+            for (int r = lane; r + 1 < found; r += 32) {
+                const int k0 = sh.obeam[r], k1 = sh.obeam[r + 1];
+                const float e0 = sh.error[k0], e1 = sh.error[k1];
+                if (k0 != k1 && difference(sh.oval[r], sh.oval[r + 1]) < e0 + e1)
+                    doubt |= (e0 > 0.0f ? 1ull << k0 : 0) | (e1 > 0.0f ? 1ull << k1 : 0);
             }
-            values[m] = v;
-        }
-        __syncthreads();
-        if (tid < 32) {
-            constexpr int L = kMaxLists / 32;
-            uint64_t head[L];
-            int at[L];
+            // Beams as near to the last one with candidates left out, and the selected ones
+            // there: where that is more than one beam, any of them may belong.
+            const uint64_t last = sh.oval[found - 1];
+            const float own = sh.error[sh.obeam[found - 1]];
+            unsigned long long out = 0, in = 0;
 #pragma unroll
             for (int q = 0; q < L; ++q) {
-                const int i = q * 32 + lane;
-                at[q] = 0;
-                head[q] = i < nlists ? values[i * p.n] : 0;
+                const int i = q * 32 + lane, k = i < nlists ? i / p.splits : 0;
+                if (i < nlists && head[q] && difference(last, head[q]) <= own + sh.error[k])
+                    out |= 1ull << k;
             }
-            int found = 0;
-            for (; found < p.Ko; ++found) {
-                uint64_t v = head[0];
-                int q0 = 0;
-#pragma unroll
-                for (int q = 1; q < L; ++q)
-                    if (head[q] > v) {                 // equal: the lower list
-                        v = head[q];
-                        q0 = q;
-                    }
-                const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
-                if (!hi) break;
-                const uint32_t lo = __reduce_max_sync(
-                    0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
-                // of equal values the lowest list: the lowest beam, and token
-                const uint32_t list = __reduce_min_sync(
-                    0xffffffffu, v == ((uint64_t)hi << 32 | lo) ? (uint32_t)(q0 * 32 + lane)
-                                                                : 0xffffffffu);
-                if ((list & 31) == lane) {
-                    sh.oval[found] = v;
-                    sh.oid[found] = list << 8 | sel(at, q0);
-#pragma unroll
-                    for (int q = 0; q < L; ++q)
-                        if (q == q0) {
-                            ++at[q];
-                            head[q] = at[q] < p.n ? values[list * p.n + at[q]] : 0;
-                        }
-                }
+            for (int r = lane; r < found; r += 32) {
+                const int k = sh.obeam[r];
+                if (difference(sh.oval[r], last) <= own + sh.error[k]) in |= 1ull << k;
             }
-            __syncwarp();
-            for (int r = lane; r < found; r += 32) sh.obeam[r] = (uint8_t)((sh.oid[r] >> 8) / p.splits);
-            __syncwarp();
-            unsigned long long doubt = 0;
-            if (p.fused && found) {
-                // Neighbours of different beams whose order is in doubt.
-                for (int r = lane; r + 1 < found; r += 32) {
-                    const int k0 = sh.obeam[r], k1 = sh.obeam[r + 1];
-                    const float e0 = sh.error[k0], e1 = sh.error[k1];
-                    if (k0 != k1 && difference(sh.oval[r], sh.oval[r + 1]) < e0 + e1)
-                        doubt |= (e0 > 0.0f ? 1ull << k0 : 0) | (e1 > 0.0f ? 1ull << k1 : 0);
+            out = or_lanes(out);
+            in = or_lanes(in);
+            doubt = or_lanes(doubt);
+            if (out && __popcll(in | out) > 1)
+                for (unsigned long long left = in | out; left; left &= left - 1) {
+                    const int k = __ffsll((long long)left) - 1;
+                    if (sh.error[k] > 0.0f) doubt |= 1ull << k;
                 }
-                // Beams as near to the last one with candidates left out, and the selected ones
-                // there: where that is more than one beam, any of them may belong.
-                const uint64_t last = sh.oval[found - 1];
-                const float own = sh.error[sh.obeam[found - 1]];
-                unsigned long long out = 0, in = 0;
-#pragma unroll
-                for (int q = 0; q < L; ++q) {
-                    const int i = q * 32 + lane, k = i < nlists ? i / p.splits : 0;
-                    if (i < nlists && head[q] && difference(last, head[q]) <= own + sh.error[k])
-                        out |= 1ull << k;
-                }
-                for (int r = lane; r < found; r += 32) {
-                    const int k = sh.obeam[r];
-                    if (difference(sh.oval[r], last) <= own + sh.error[k]) in |= 1ull << k;
-                }
-                out = or_lanes(out);
-                in = or_lanes(in);
-                doubt = or_lanes(doubt);
-                if (out && __popcll(in | out) > 1)
-                    for (unsigned long long left = in | out; left; left &= left - 1) {
-                        const int k = __ffsll((long long)left) - 1;
-                        if (sh.error[k] > 0.0f) doubt |= 1ull << k;
-                    }
-            }
-            if (lane == 0) {
-                sh.again = doubt;
-                sh.found = found;
-            }
         }
-        __syncthreads();
-        again = sh.again;
-        if (!again) break;
+        if (lane == 0) {
+            sh.again = doubt;
+            sh.found = found;
+        }
     }
-    for (int r = tid; r < p.Ko; r += THREADS) {
+    __syncthreads();
+}
+
+template <int THREADS>
+__device__ __forceinline__ void report(const SelectParams& p, uint32_t b, const uint64_t* lists,
+                                       const PickShared& sh) {
+    for (int r = threadIdx.x; r < p.Ko; r += THREADS) {
         const int64_t o = (int64_t)b * p.Ko + r;
         const int from = r < sh.found ? sh.obeam[r] : -1;
         p.out_scores[o] = from < 0 ? -INFINITY : unordered((uint32_t)(sh.oval[r] >> 32));
@@ -888,39 +894,69 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
     const uint64_t* from = p.list + (int64_t)b * nlists * p.n;
     if (threadIdx.x < nlists) stat[threadIdx.x] = p.stat[(int64_t)b * nlists + threadIdx.x];
     for (int i = threadIdx.x; i < nlists * p.n; i += kPickThreads) lists[i] = from[i];
-    pick<T, kPickThreads>(p, b, lists, lists + nlists * p.n, stat, sh);
+    weigh<kPickThreads>(p, b, lists, stat, sh);
+    for (int turn = 0; turn <= RNNT_MAX_BEAM; ++turn) {        // each settles a beam at least
+        for (unsigned long long again = sh.again; again; again &= again - 1) {
+            const int k = __ffsll((long long)again) - 1;
+            const Pair l = exact_lse<T, kPickThreads>(row_of<T>(p, b * p.K + k), p.V, sh.sums,
+                                                      sh.tops);
+            if (threadIdx.x == 0) settle(p, sh, k, l);
+        }
+        __syncthreads();
+        choose<kPickThreads>(p, lists, lists + nlists * p.n, sh);
+        if (!sh.again) break;
+    }
+    report<kPickThreads>(p, b, lists, sh);
 }
 
 // ------------------------------------------------------- both, by a cluster an item
-// A cluster of up to 8 CTAs takes a batch item: each streams a row and leaves its list and
-// statistics in the first CTA's shared memory, which picks.  One launch and no workspace.
+// A cluster takes a batch item: each CTA streams a row and leaves its list and statistics in the
+// first CTA's shared memory, which picks; where that wants exact log-sum-exps, each CTA
+// computes its own row's.  One launch and no workspace.
 struct ClusterShared {
     union {
         RowShared<kClusterThreads> rows;
         PickShared pick;
     };
-    float4 stat[RNNT_MAX_BEAM];
+    float4 stat[kMaxCluster];
 };
 
 template <typename T, int NV, bool FUSED>
-__global__ void __launch_bounds__(kClusterThreads, 4) k_search(const SelectParams p) {
+__global__ void __launch_bounds__(kClusterThreads, 8) k_search(const SelectParams p) {
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) char search_space[];
     ClusterShared& sh = *reinterpret_cast<ClusterShared*>(search_space);
     uint64_t* lists = reinterpret_cast<uint64_t*>(search_space + sizeof(ClusterShared));
-    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const uint32_t b = blockIdx.x / (uint32_t)C;
+    const int rank = (int)cluster.block_rank();
+    const uint32_t b = blockIdx.x / (uint32_t)p.K;
     cluster.barrier_arrive();                          // that every CTA has started:
+    ClusterShared& first = *cluster.map_shared_rank(&sh, 0);
     uint64_t* to_lists = cluster.map_shared_rank(lists, 0);
-    float4* to_stat = cluster.map_shared_rank(sh.stat, 0);
     const bool reads = row_pass<T, NV, FUSED, kClusterThreads>(p, b * p.K + rank, 0, sh.rows);
     cluster.barrier_wait();                            // here it is to be known
     if (reads) {
         if (threadIdx.x < p.n) to_lists[rank * p.n + threadIdx.x] = sh.rows.best[threadIdx.x];
-        if (threadIdx.x == 0) to_stat[rank] = sh.rows.stat;
+        if (threadIdx.x == 0) first.stat[rank] = sh.rows.stat;
     }
     cluster.sync();
-    if (rank == 0) pick<T, kClusterThreads>(p, b, lists, lists + p.K * p.n, sh.stat, sh.pick);
+    if (rank == 0) weigh<kClusterThreads>(p, b, lists, sh.stat, sh.pick);
+    for (int turn = 0; turn <= kMaxCluster; ++turn) {          // each settles a beam at least
+        if (rank == 0) {
+            if (turn || !sh.pick.again) choose<kClusterThreads>(p, lists, lists + p.K * p.n, sh.pick);
+        }
+        if (!p.fused) break;                           // exact as it is
+        cluster.sync();
+        const unsigned long long again = first.pick.again;
+        if (!again) break;
+        if (again >> rank & 1) {
+            const Pair l = exact_lse<T, kClusterThreads>(row_of<T>(p, b * p.K + rank), p.V,
+                                                         sh.pick.sums, sh.pick.tops);
+            if (threadIdx.x == 0) settle(p, first.pick, rank, l);
+        }
+        cluster.sync();
+    }
+    if (rank == 0) report<kClusterThreads>(p, b, lists, sh.pick);
+    if (p.fused) cluster.sync();                       // its memory has been read
 }
 
 struct SelectLayout {
@@ -928,7 +964,7 @@ struct SelectLayout {
     int32_t splits, split_vecs, n;
     int32_t cluster;                       // CTAs of an item's cluster, or 0: two launches
 };
-constexpr int64_t kClusterBytes = 128 << 10, kClusterRows = 304;
+constexpr int64_t kClusterBytes = 32 << 10;
 SelectLayout select_layout(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt) {
     SelectLayout L{};
     const int es = elem_size(dt), E = 16 / es;
@@ -936,12 +972,12 @@ SelectLayout select_layout(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt) 
     L.n = std::min(Ko, V);
     L.splits = 1;
     L.split_vecs = (int32_t)vecs;
-    // A cluster's CTAs take a row each, whole (two rows in turn measured slower than two
-    // launches: 17.0 against 14.7 us for 10 beams).  For an item of 4 beams of 1024 float16 the
-    // cluster takes 8.8 us and two launches 10.1, of 20000 10.3 and 11.3, of 50000 12.9 and
-    // 11.6, and a launch and a workspace cost the host 6 us; longer rows want splits over the
-    // whole device, unless there are many (16 items of 4 x 50000: 13.8 and 14.2).
-    if (K <= 8 && ((int64_t)V * es <= kClusterBytes || (int64_t)B * K >= kClusterRows)) {
+    // A cluster's CTAs take a row each, whole, against splits over the whole device and a second
+    // launch.  On the GPU they are level where rows are short (items of 4 and 16 rows of 5000
+    // float16: 9.9 and 13.2 us against 9.7 and 14.1), and the one launch without a workspace
+    // costs the host 6 us less; long rows (of 50000: 15.3 and 19.5 against 9.5 and 15.4) are
+    // faster split, and their exact sums by k_pick's larger block.
+    if (K <= kMaxCluster && (int64_t)V * es <= kClusterBytes) {
         L.cluster = K;
         return L;
     }
@@ -1008,9 +1044,11 @@ template <typename T>
 bool raise_limits() {
     const auto raise = [](auto kernel, size_t most) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)most) == cudaSuccess;
+                                    (int)most) == cudaSuccess &&
+               cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                   cudaSuccess;
     };
-    const size_t lists = 2 * sizeof(uint64_t) * 8 * RNNT_MAX_BEAM;       // of up to 8 beams
+    const size_t lists = 2 * sizeof(uint64_t) * kMaxCluster * RNNT_MAX_BEAM;
     const size_t most = sizeof(ClusterShared) + lists;
     return raise(k_pick<T>, 2 * sizeof(uint64_t) * kMaxLists * RNNT_MAX_BEAM) &&
            raise(k_search<T, 1, true>, most) && raise(k_search<T, 1, false>, most) &&

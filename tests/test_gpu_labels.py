@@ -203,6 +203,14 @@ def test_select(case, dtype, fused):
     check_select(x, scores, beam, None, fused)
 
 
+@pytest.mark.parametrize("K", list(range(1, 20)))
+def test_select_beams(K):
+    """Every number of hypotheses about the largest cluster, with a narrower and a wider result."""
+    x, scores = logits_of(3, K, 517, "f16", K)
+    for beam in (1, K, 2 * K):
+        check_select(x, scores, beam)
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("V", [31, 4099])
 def test_select_ties(dtype, V):
