@@ -25,6 +25,7 @@ __device__ __forceinline__ uint32_t ordered(float x) {      // -0 counts as 0
 __device__ __forceinline__ float unordered(uint32_t o) {
     return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
+
 // ------------------------------------------------------------- rows of logits
 // A row is cut into splits of whole aligned 16-byte vectors (the few elements ahead of them
 // and behind them go to threads of split 0 one by one); a CTA streams one split through
@@ -33,8 +34,8 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 //     maximum and changes only when a thread meets a value more than 16 above it, so
 //     that a sum is (almost) never rescaled.
 //   - the n best elements in order.  The stream keeps each thread's maximum of every
-//     tile and nothing else.  Every warp's ceil(n / 8)-th largest thread maximum bounds the
-//     n-th best element from below (the least of the eight does); the few tiles of a
+//     tile and nothing else.  Of every warp's largest thread maxima enough to make n together
+//     bound the n-th best element from below (the least of them does); the few tiles of a
 //     thread that reach the bound are read once more, from the cache, and their elements
 //     that reach it are ranked by counting.  Rows with a crowd of equal elements at the
 //     bound go through best_of_row instead, tile by tile.
@@ -55,7 +56,7 @@ constexpr float kExponentError = 5.2e-8f;          // 1.25 * 2^-24 * ln 2
 constexpr float kRescaleError = 1e-6f;
 constexpr int kMaxLists = 128;             // splits of a batch item's rows
 constexpr int kSlots = 8;                  // of tiles, whose maxima a thread keeps
-constexpr int kBuf = 1024;                 // elements ranked: > RNNT_MAX_BEAM * 9 (best_of_row)
+constexpr int kBuf = 1024;                 // elements ranked at a time: > 3 TH (best_of_row)
 
 struct SelectParams {
     const char* logits;
@@ -1262,6 +1263,7 @@ extern "C" rnnt_status_t rnnt_beam_reorder(const rnnt_state_t* states, int32_t n
         for (int j = 0; j < n_states; ++j) {
             const rnnt_state_t &d = states[i], &s = states[j];
             const uint64_t dn = extent(d, d.dst_stride, d.dst_batch, d.dst_beam, B, Ko);
+            if (i != j && d.dst == s.dst) return RNNT_INVALID_VALUE;
             if (overlaps(d.dst, dn, s.src,
                          extent(s, s.src_stride, s.src_batch, s.src_beam, B, K)))
                 return RNNT_INVALID_VALUE;

@@ -373,6 +373,11 @@ def test_reorder_refuses():
         rnnt_beam_reorder([x], p, out=[x])
     with pytest.raises(ValueError):
         rnnt_beam_reorder([x], p, out=[x[:, :, :1].expand(3, 4, 8)])
+    y = torch.empty_like(x)
+    with pytest.raises(N.RNNTError):                # one result for two states
+        rnnt_beam_reorder([x, x], p, out=[y, y])
+    a, b = rnnt_beam_reorder([x, x], p)             # one state twice
+    assert torch.equal(a, b) and a.data_ptr() != b.data_ptr()
     assert rnnt_beam_reorder([], p) == []
 
 
@@ -411,6 +416,65 @@ def test_streams_and_graphs():
             graph.replay()
             for a, b in zip(out, want):
                 assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on the device share nothing."""
+    jobs = []
+    for seed in (1, 2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        tokens = torch.randint(0, 900, (4, 1000), device="cuda", dtype=torch.int32, generator=g)
+        go = torch.randn(4, 1001, 64, device="cuda", generator=g)
+        x, scores = logits_of(3, 20, 30000, "f16", seed)
+        jobs.append((tokens, go, x, scores))
+
+    def run(job):
+        tokens, go, x, scores = job
+        return (rnnt_embed_grad(go, tokens, 900, start=0, check=False),
+                *rnnt_beam_select(x, scores, check=False))
+
+    want = [run(j) for j in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (st, job) in enumerate(zip(streams, jobs)):
+            with torch.cuda.stream(st):
+                got[i].append(run(job))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(r, want[i]))
+
+
+def test_far_offsets():
+    """Tables, logits and states whose last elements lie behind 2^31 elements."""
+    V, D = 1_100_000, 2048
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    w[-1], w[-2] = 3.0, 5.0
+    tokens = i32([[V - 1, V - 2, 0, -1]])
+    out = rnnt_embed(w, tokens, scale=2.0)
+    assert [float(out[0, i, 7]) for i in range(4)] == [6.0, 10.0, 0.0, 0.0]
+    del w
+    go = torch.ones(1, 4, D, dtype=torch.bfloat16, device="cuda")
+    for places in (go, torch.ones(1, 4000, D, dtype=torch.bfloat16, device="cuda")):
+        t = tokens if places is go else tokens.repeat(1, 1000)
+        g = rnnt_embed_grad(places, t, V)
+        n = places.shape[1] // 4
+        assert (g[[V - 1, V - 2, 0]] == n).all() and not g[1:V - 2].any()
+        del g
+    x = torch.zeros(33, 64, 1 << 20, dtype=torch.bfloat16, device="cuda")
+    x[32, 63, 1_000_001] = 8.0
+    x[32, 62, 17] = 7.0
+    scores = torch.zeros(33, 64, device="cuda")
+    s, tok, par = rnnt_beam_select(x, scores, 2)
+    assert tok[32].tolist() == [1_000_001, 17] and par[32].tolist() == [63, 62]
+    assert tok[5].tolist() == [0, 1] and par[5].tolist() == [0, 0]
+    del x
+    big = torch.zeros(2, 3, 1_000_000_007, dtype=torch.int8, device="cuda")
+    big[1, 2, -1] = 9
+    y, = rnnt_beam_reorder([big], i32([[0, 0, 1], [2, 1, 2]]))
+    assert y[1, :, -1].tolist() == [9, 0, 9] and not y[0].any()
 
 
 def test_training_step():
