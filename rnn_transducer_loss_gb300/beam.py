@@ -33,7 +33,7 @@ def rnnt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beam: int | Non
     :func:`rnnt_beam_reorder`); places left over get score -inf, token -1,
     parent -1.  ``check`` reads the device status word (one synchronisation) and
     raises on scores or logits that are NaN or +inf; without it a hypothesis
-    that holds one offers nothing.
+    that holds one offers nothing.  Not differentiable.
     """
     dt = _DT.get(logits.dtype)
     device = logits.device
@@ -139,6 +139,22 @@ def _plan(shape, strides, size, d, B, K, Ko):
     return new, out, None if 0 in new else _pack(_describe(shape, strides, out, size, d))
 
 
+def _apart(states, out):
+    """Raises where a result shares memory with a state or is given twice, as one C call does by
+    itself: for more states than it takes, of which an early one's result could be a late one's
+    source."""
+    def span(x):
+        at = x.data_ptr()
+        return at, at + x.element_size() * (1 + sum((n - 1) * a for n, a in zip(x.shape, x.stride())))
+
+    src = [span(x) for x in states if x.numel()]
+    dst = [span(y) for y in out if y.numel()]
+    if len({a for a, _ in dst}) < len(dst):
+        raise ValueError("out holds a tensor twice")
+    if any(a < d and c < b for a, b in dst for c, d in src):
+        raise ValueError("out must not share memory with states")
+
+
 def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, check: bool = True):
     """The states of the selected hypotheses: ``new[.., b, k, ..] = old[.., b, parents[b, k], ..]``.
 
@@ -152,9 +168,10 @@ def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, chec
     without it the results are new contiguous tensors.  Views are read with
     their strides: the filled part of a cache need not be copied out first.
     ``check`` reads the device status word (one synchronisation) and raises on
-    parents outside [-1, K); without it such a parent counts as -1.
+    parents outside [-1, K); without it such a parent counts as -1.  Not
+    differentiable.
     """
-    states = list(states)
+    states = [x.resolve_conj().resolve_neg() if x.is_conj() or x.is_neg() else x for x in states]
     if not states:
         return []
     device = states[0].device
@@ -177,6 +194,8 @@ def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, chec
         out = list(out)
         if len(out) != len(states):
             raise ValueError("out must have one tensor per state")
+        if len(out) > N.MAX_STATES:
+            _apart(states, out)
     results, rows = [], []
     for i, x in enumerate(states):
         if x.device != device:
@@ -189,6 +208,8 @@ def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, chec
             y = out[i]
             if y.device != device or y.dtype != x.dtype or y.shape != new:
                 raise ValueError(f"out must be {x.dtype} {new} on {device}")
+            if y.is_conj() or y.is_neg():
+                raise ValueError("out must not be a conjugate or negative view")
             if any(n > 1 and a == 0 for n, a in zip(new, y.stride())):
                 raise ValueError("out must not be an expanded tensor")
             if packed is not None:

@@ -381,6 +381,30 @@ def test_reorder_refuses():
     assert rnnt_beam_reorder([], p) == []
 
 
+def test_reorder_many_refuses():
+    """More states than one launch takes: an early result must not be a late one's source."""
+    x = [torch.randn(2, 3, 5, device="cuda") for _ in range(20)]
+    y = [torch.empty_like(t) for t in x]
+    p = i32([[2, 1, 0], [0, 0, -1]])
+    for a, b in zip(x, rnnt_beam_reorder(x, p, out=y)):
+        assert torch.equal(b, plain_reorder(a, p, 0))
+    for bad in (y[:1] + y[2:] + y[:1], [x[18]] + y[1:], x):
+        with pytest.raises(ValueError):
+            rnnt_beam_reorder(x, p, out=bad)
+
+
+def test_reorder_lazy_views():
+    """Conjugate and negative views, whose memory holds other values than they do."""
+    z = torch.randn(2, 3, 5, device="cuda", dtype=torch.complex64)
+    p = i32([[2, 1, 0], [0, 0, 1]])
+    a, b = rnnt_beam_reorder([z.conj(), z.conj().imag], p)
+    rows = torch.arange(2, device="cuda")[:, None]
+    assert torch.equal(a, z.conj().resolve_conj()[rows, p.long()])
+    assert torch.equal(b, -z.imag[rows, p.long()])
+    with pytest.raises(ValueError):
+        rnnt_beam_reorder([z], p, out=[torch.empty_like(z).conj()])
+
+
 def test_streams_and_graphs():
     """Another stream than the tensors' first one; two graphs, replayed in turn with new inputs."""
     w = torch.randn(60, 32, device="cuda")
