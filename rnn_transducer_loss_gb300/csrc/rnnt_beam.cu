@@ -43,6 +43,7 @@ constexpr int kRowThreads = 128;           // of k_rows: 8 CTAs an SM hold 1024 
                                            // threads, 4 CTAs: a second wave, 32 against 25 us)
 constexpr int kClusterThreads = 128;       // of k_search
 constexpr int kMaxCluster = 16;
+constexpr int kClusterBytes = 32 << 10;    // of a row that a CTA of a cluster takes, at most
 constexpr float kLog2e = 1.44269504f;      // log2 e to 2^-26
 constexpr float kRescale = 16.0f;
 constexpr float kMostRef = 1e30f;          // larger references: computed again by exact_lse
@@ -55,8 +56,11 @@ constexpr float kTermError = 2.4e-7f + 6 * 6e-8f;
 constexpr float kExponentError = 5.2e-8f;          // 1.25 * 2^-24 * ln 2
 constexpr float kRescaleError = 1e-6f;
 constexpr int kMaxLists = 128;             // splits of a batch item's rows
-constexpr int kSlots = 8;                  // of tiles, whose maxima a thread keeps
 constexpr int kBuf = 1024;                 // elements ranked at a time: > 3 TH (best_of_row)
+// Slots of tiles, whose maxima a thread keeps: a slot that reaches the bound is read once more as a
+// whole.  Blocks with fewer than 4 vectors a thread have one tile.  (64 x 16 rows of 200000
+// bfloat16: 96 us with 8 slots, 89 with 16, 87 with 32; no difference up to 50000.)
+template <int NV, int MOST> constexpr int kSlots = NV == 4 ? MOST : 1;
 
 struct SelectParams {
     const char* logits;
@@ -208,19 +212,29 @@ __device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, 16>& v, float2*
         y[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
-// Largest element of a vector (NaN is passed over).
-__device__ __forceinline__ float vec_max(const Pack<float, 16>& v) {
-    return fmaxf(fmaxf(v.e[0], v.e[1]), fmaxf(v.e[2], v.e[3]));
+// Largest element of a tile's vectors (NaN is passed over).
+template <int NV>
+__device__ __forceinline__ float tile_max(const Pack<float, 16> (&v)[NV]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        m = fmaxf(m, fmaxf(fmaxf(v[i].e[0], v[i].e[1]), fmaxf(v[i].e[2], v[i].e[3])));
+    return m;
 }
-__device__ __forceinline__ float vec_max(const Pack<__half, 16>& v) {
-    const __half2* h = reinterpret_cast<const __half2*>(&v.raw);
-    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
-}
-__device__ __forceinline__ float vec_max(const Pack<__nv_bfloat16, 16>& v) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v.raw);
-    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
+template <typename T, int NV>
+__device__ __forceinline__ float tile_max(const Pack<T, 16> (&v)[NV]) {
+    using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+    T2 m[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const T2* h = reinterpret_cast<const T2*>(&v[i].raw);
+        m[i] = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    }
+#pragma unroll
+    for (int o = NV / 2; o; o /= 2)
+#pragma unroll
+        for (int i = 0; i < o; ++i) m[i] = __hmax2(m[i], m[i + o]);
+    return fmaxf(__low2float(m[0]), __high2float(m[0]));
 }
 
 __device__ __forceinline__ uint64_t key_of(float x, int element) {
@@ -324,22 +338,26 @@ __device__ __noinline__ void best_of_row(const SelectParams& p, uint32_t row, in
     __syncthreads();
 }
 
-template <int TH>
+template <int TH, int SLOTS>
 struct RowShared {
-    uint64_t buf[kBuf], best[RNNT_MAX_BEAM];       // best: the split's list
+    union {
+        float tops[SLOTS][TH];            // each thread's maxima of the slots
+        uint64_t buf[kBuf];               // keys to be ranked, once the tops have been read
+    };
+    uint64_t best[RNNT_MAX_BEAM];         // the split's list
     float4 stat;
     Pair wsum[(TH / 32)];
     float wref[(TH / 32)], wleast[(TH / 32)], wover[(TH / 32)];
-    float tops[kSlots][TH];
-    int hit[kSlots * TH];                 // slots to be read once more
+    uint16_t hit[kBuf];                   // slots to be read once more: each has an element that is
+                                          // ranked, so more of them are a crowd
     int hits, count, bads, rescales;
 };
 
 // Leaves the split's statistics and list (zeros behind its end) in sh, behind a barrier; returns
 // false, at once, for a beam that offers no logits.
-template <typename T, int NV, bool FUSED, int TH>
+template <typename T, int NV, bool FUSED, int TH, int SLOTS>
 __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, int split,
-                                         RowShared<TH>& sh) {
+                                         RowShared<TH, SLOTS>& sh) {
     constexpr int E = 16 / (int)sizeof(T);
     constexpr int kTileVecs = TH * NV;
     auto& buf = sh.buf;
@@ -376,18 +394,16 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
     float most = odd_x;                            // the thread's maximum
     bool bad = !FUSED && !(odd_x < INFINITY), rescaled = false;
     int shift_slot = 0;                            // tiles of a slot: 1 << shift_slot
-    while ((vecs - 1) / kTileVecs >> shift_slot >= kSlots) ++shift_slot;
+    while ((vecs - 1) / kTileVecs >> shift_slot >= SLOTS) ++shift_slot;
     float slot_top = -INFINITY;
     for (int t0 = 0; t0 < vecs || t0 == 0; t0 += kTileVecs) {
         if (t0 + kTileVecs < vecs) load_tile(next, t0 + kTileVecs);
-        float top = -INFINITY;
+        float top = tile_max(v);
+        if (!FUSED) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            top = fmaxf(top, vec_max(v[i]));
-            if (!FUSED) {
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < E; ++e) bad |= !(to_f32(v[i].e[e]) < INFINITY);
-            }
         }
         most = fmaxf(most, top);
         slot_top = fmaxf(slot_top, top);
@@ -474,7 +490,7 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
         int to = 0;
         if (lane == 0) to = atomicAdd(&hits, __popc(who));
         to = __shfl_sync(0xffffffffu, to, 0) + __popc(who & ((1u << lane) - 1));
-        if (reaches) hit[to] = t * TH + tid;
+        if (reaches && to < kBuf) hit[to] = (uint16_t)(t * TH + tid);
     }
     float at = ref;                                // the largest of the threads' references
     if (FUSED) {
@@ -506,7 +522,7 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
     __syncthreads();
     // Those slots' vectors once more: their elements that reach the bound.
     const int per = NV << shift_slot;              // vectors of a slot
-    for (int i = tid; i < hits * per; i += TH) {
+    for (int i = tid; i < min(hits, kBuf) * per; i += TH) {
         const int slot = hit[i / per];
         const int j = slot / TH * span + i % per * TH + slot % TH;
         const Pack<T, 16> w = sp.at(j);
@@ -531,7 +547,7 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
         if (to < kBuf) buf[to] = key_of(odd_x, odd);
     }
     __syncthreads();
-    const bool crowd = count > kBuf;
+    const bool crowd = hits > kBuf || count > kBuf;
     if (warp == (TH / 32) - 1) {                   // the keys are ranked by the first ones
         Pair total{0.0f, 0.0f};
         float over = 0.0f, err = 0.0f;
@@ -564,13 +580,14 @@ __device__ __forceinline__ bool row_pass(const SelectParams& p, uint32_t row, in
     return true;
 }
 
+
 template <typename T, int NV, bool FUSED>
 __global__ void __launch_bounds__(kRowThreads, NV == 1 ? 12 : 8) k_rows(const SelectParams p) {
-    __shared__ RowShared<kRowThreads> sh;
+    __shared__ RowShared<kRowThreads, kSlots<NV, 32>> sh;
     let_next_start();
     const uint32_t row = blockIdx.x / (uint32_t)p.splits;
     const int split = (int)(blockIdx.x - row * (uint32_t)p.splits);
-    if (!row_pass<T, NV, FUSED, kRowThreads>(p, row, split, sh)) return;
+    if (!row_pass<T, NV, FUSED>(p, row, split, sh)) return;
     uint64_t* list = p.list + (int64_t)blockIdx.x * p.n;
     if (threadIdx.x < p.n) list[threadIdx.x] = sh.best[threadIdx.x];
     if (threadIdx.x == 0) p.stat[blockIdx.x] = sh.stat;
@@ -914,9 +931,10 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
 // A cluster takes a batch item: each CTA streams a row and leaves its list and statistics in the
 // first CTA's shared memory, which picks; where that wants exact log-sum-exps, each CTA
 // computes its own row's.  One launch and no workspace.
+template <int NV>
 struct ClusterShared {
     union {
-        RowShared<kClusterThreads> rows;
+        RowShared<kClusterThreads, kSlots<NV, kClusterBytes / 16 / (4 * kClusterThreads)>> rows;
         PickShared pick;
     };
     float4 stat[kMaxCluster];
@@ -926,14 +944,15 @@ template <typename T, int NV, bool FUSED>
 __global__ void __launch_bounds__(kClusterThreads, 8) k_search(const SelectParams p) {
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) char search_space[];
-    ClusterShared& sh = *reinterpret_cast<ClusterShared*>(search_space);
-    uint64_t* lists = reinterpret_cast<uint64_t*>(search_space + sizeof(ClusterShared));
+    using Shared = ClusterShared<NV>;
+    Shared& sh = *reinterpret_cast<Shared*>(search_space);
+    uint64_t* lists = reinterpret_cast<uint64_t*>(search_space + sizeof(Shared));
     const int rank = (int)cluster.block_rank();
     const uint32_t b = blockIdx.x / (uint32_t)p.K;
     cluster.barrier_arrive();                          // that every CTA has started:
-    ClusterShared& first = *cluster.map_shared_rank(&sh, 0);
+    Shared& first = *cluster.map_shared_rank(&sh, 0);
     uint64_t* to_lists = cluster.map_shared_rank(lists, 0);
-    const bool reads = row_pass<T, NV, FUSED, kClusterThreads>(p, b * p.K + rank, 0, sh.rows);
+    const bool reads = row_pass<T, NV, FUSED>(p, b * p.K + rank, 0, sh.rows);
     cluster.barrier_wait();                            // here it is to be known
     if (reads) {
         if (threadIdx.x < p.n) to_lists[rank * p.n + threadIdx.x] = sh.rows.best[threadIdx.x];
@@ -965,7 +984,6 @@ struct SelectLayout {
     int32_t splits, split_vecs, n;
     int32_t cluster;                       // CTAs of an item's cluster, or 0: two launches
 };
-constexpr int64_t kClusterBytes = 32 << 10;
 SelectLayout select_layout(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt) {
     SelectLayout L{};
     const int es = elem_size(dt), E = 16 / es;
@@ -1012,7 +1030,7 @@ bool launch_select(const SelectParams& p, int cluster, cudaStream_t st) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)(p.B * cluster));
         cfg.blockDim = dim3(kClusterThreads);
-        cfg.dynamicSmemBytes = sizeof(ClusterShared) + 2 * sizeof(uint64_t) * p.K * p.n;
+        cfg.dynamicSmemBytes = sizeof(ClusterShared<NV>) + 2 * sizeof(uint64_t) * p.K * p.n;
         cfg.stream = st;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1050,7 +1068,7 @@ bool raise_limits() {
                    cudaSuccess;
     };
     const size_t lists = 2 * sizeof(uint64_t) * kMaxCluster * RNNT_MAX_BEAM;
-    const size_t most = sizeof(ClusterShared) + lists;
+    const size_t most = sizeof(ClusterShared<4>) + lists;
     return raise(k_pick<T>, 2 * sizeof(uint64_t) * kMaxLists * RNNT_MAX_BEAM) &&
            raise(k_search<T, 1, true>, most) && raise(k_search<T, 1, false>, most) &&
            raise(k_search<T, 2, true>, most) && raise(k_search<T, 2, false>, most) &&
