@@ -58,10 +58,11 @@ def rnnt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beam: int | Non
             raise ValueError(f"finished must be bool or uint8 ({B}, {K}) on {device}")
         finished = finished.contiguous()
     scores = scores.contiguous()
-    # one allocation: tokens, parents and (as they are) the scores
-    out = torch.empty((3, B, beam), dtype=_I32, device=device)
-    tokens, parents, out_scores = out.unbind(0)
-    out_scores = out_scores.view(_F32)
+    # three allocations: the code of the second and third is in the caches, while that of the views
+    # that would share one is not (7 us instead of 11)
+    out_scores = torch.empty((B, beam), dtype=_F32, device=device)
+    tokens = torch.empty((B, beam), dtype=_I32, device=device)
+    parents = torch.empty((B, beam), dtype=_I32, device=device)
     if not B:
         return out_scores, tokens, parents
     item, row, step = logits.stride()
@@ -71,10 +72,10 @@ def rnnt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beam: int | Non
     nbytes = N.rnnt_beam_workspace_size(B, K, V, beam, dt)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     status = status_word(device) if check else None
-    at, each = out.data_ptr(), 4 * B * beam
     call("rnnt_beam_select", device, N.load().rnnt_beam_select, logits.data_ptr(), dt, B, K, V,
          item, row, scores.data_ptr(), None if finished is None else finished.data_ptr(), beam,
-         1 if fused_log_softmax else 0, at + 2 * each, at, at + each, ws.data_ptr() if nbytes else None, nbytes,
+         1 if fused_log_softmax else 0, out_scores.data_ptr(), tokens.data_ptr(),
+         parents.data_ptr(), ws.data_ptr() if nbytes else None, nbytes,
          None if status is None else status.data_ptr())
     if check:
         finish("rnnt_beam_select", status, "finite scores or -inf, logits below +inf and not NaN")
@@ -120,9 +121,10 @@ def _pack(rows):
 
 
 @lru_cache(maxsize=1024)
-def _plan(shape, strides, size, d, B, K, Ko):
-    """(shape of a new result, its strides, packed rows or None if there are none) of a state by
-    its layout; raises if it is no state of (B, K)."""
+def _plan(shape, strides, dtype, d, B, K, Ko):
+    """(shape of a new result, packed rows or None if there are none) of a state by its layout;
+    raises if it is no state of (B, K)."""
+    shape = tuple(shape)
     if d < 0:
         d += len(shape)
     if not 0 <= d < len(shape) - 1:
@@ -136,7 +138,7 @@ def _plan(shape, strides, size, d, B, K, Ko):
         out.append(n)
         n *= max(m, 1)
     out = tuple(reversed(out))
-    return new, out, None if 0 in new else _pack(_describe(shape, strides, out, size, d))
+    return new, None if 0 in new else _pack(_describe(shape, strides, out, dtype.itemsize, d))
 
 
 def _apart(states, out):
@@ -171,7 +173,7 @@ def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, chec
     parents outside [-1, K); without it such a parent counts as -1.  Not
     differentiable.
     """
-    states = [x.resolve_conj().resolve_neg() if x.is_conj() or x.is_neg() else x for x in states]
+    states = list(states)
     if not states:
         return []
     device = states[0].device
@@ -185,7 +187,7 @@ def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, chec
     dims = [batch_dim] * len(states) if isinstance(batch_dim, int) else batch_dim
     if len(dims) != len(states):
         raise ValueError("batch_dim must be one number, or one per state")
-    first = tuple(states[0].shape)
+    first = states[0].shape
     d = dims[0] + len(first) if dims[0] < 0 else dims[0]
     if not 0 <= d < len(first) - 1:
         raise ValueError("batch_dim must leave a beam axis behind it")
@@ -200,21 +202,23 @@ def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, chec
     for i, x in enumerate(states):
         if x.device != device:
             raise ValueError(f"states must be on {device}")
-        shape, strides, size = tuple(x.shape), x.stride(), x.element_size()
-        new, _, packed = _plan(shape, strides, size, dims[i], B, K, Ko)
+        if x.is_conj() or x.is_neg():
+            states[i] = x = x.resolve_conj().resolve_neg()
+        dtype = x.dtype
+        new, packed = _plan(x.shape, x.stride(), dtype, dims[i], B, K, Ko)
         if out is None:
-            y = torch.empty(new, dtype=x.dtype, device=device)
+            y = torch.empty(new, dtype=dtype, device=device)
         else:
             y = out[i]
-            if y.device != device or y.dtype != x.dtype or y.shape != new:
-                raise ValueError(f"out must be {x.dtype} {new} on {device}")
+            if y.device != device or y.dtype != dtype or y.shape != new:
+                raise ValueError(f"out must be {dtype} {new} on {device}")
             if y.is_conj() or y.is_neg():
                 raise ValueError("out must not be a conjugate or negative view")
             if any(n > 1 and a == 0 for n, a in zip(new, y.stride())):
                 raise ValueError("out must not be an expanded tensor")
             if packed is not None:
-                d = dims[i] + len(shape) if dims[i] < 0 else dims[i]
-                packed = _pack(_describe(shape, strides, y.stride(), size, d))
+                d = dims[i] + x.dim() if dims[i] < 0 else dims[i]
+                packed = _pack(_describe(tuple(x.shape), x.stride(), y.stride(), x.element_size(), d))
         results.append(y)
         if packed is not None:
             rows.append(_POINTERS.pack(x.data_ptr(), y.data_ptr()) + packed)
