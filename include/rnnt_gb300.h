@@ -383,7 +383,7 @@ rnnt_status_t rnnt_embed(const void *weight, rnnt_dtype_t dt, int32_t V, int32_t
                          rnnt_stream_t stream);
 
 /* rnnt_embed_grad_workspace_size -- bytes of device scratch of rnnt_embed_grad:
- * 0 up to 2048 places, else about 16 + D/4 bytes per place. */
+ * 0 up to 4096 places, else about 16 + D/4 bytes per place. */
 rnnt_status_t rnnt_embed_grad_workspace_size(int32_t B, int32_t S, int32_t has_start, int32_t V,
                                              int32_t D, size_t *bytes);
 

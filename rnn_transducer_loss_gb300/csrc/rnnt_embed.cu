@@ -536,57 +536,96 @@ __global__ void __launch_bounds__(kSumThreads, 12) k_sum(const SumParams p) {
     }
 }
 
-// The long ids' partial sums, tile after tile.  A CTA takes an id and a slice of columns; its
-// groups of threads add stretches of the id's tiles, which are then added in order.  Bound by the
-// longest id's chain of additions: 10 us by itself, less behind k_sum's end, where the longest of
-// the long ids has 85 tiles; with one stretch an id, 62.
-constexpr int kJoinThreads = 128;
+// The long ids' partial sums, tile after tile.  A CTA takes every gridDim.x-th id and a slice of
+// columns.  Ids of up to kShortRun further tiles are a warp's each; the others are the whole
+// CTA's, one by one: its groups of threads add stretches of the id's tiles, which are then added
+// in order.  Bound by the longest id's chain of additions: 9 us by itself, less behind k_sum's
+// end, where the longest of the long ids has 85 tiles; with one stretch an id, 62.  One id at all
+// of 65472 places of 512 float16, 2045 tiles: 82 us for the whole gradient (128 with CTAs of 128
+// threads).
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kShortRun = 12;
 template <typename T, int UB>
 __global__ void __launch_bounds__(kJoinThreads) k_join(const SumParams p) {
     constexpr int E = UB / (int)sizeof(T);
     __shared__ float partly[kJoinThreads * E];
+    __shared__ int runs[kJoinWarps];
+    __shared__ bool is_long[kJoinWarps];
     const int group = min(p.group, 32), groups = kJoinThreads / group;
-    const int g = threadIdx.x / group, lane = threadIdx.x & 31;
+    const int g = threadIdx.x / group, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_previous();
     const int64_t n = *p.count;
     const int heavy = *p.heavy;
-    for (int which = blockIdx.x; which < heavy; which += gridDim.x) {
-        const int64_t t = p.heavy[1 + which];
-        const int id = p.sorted[(t + 1) * kTile - 1].x;
-        // Tiles t + 1 .. t + m hold more of it: the first that ends with another id is the last.
-        __shared__ int runs[kJoinThreads / 32];
-        int64_t m = 0;
-        for (;;) {
-            const int64_t at = (t + 1 + m + threadIdx.x + 1) * kTile;      // the tile behind
+    for (int64_t first = blockIdx.x; first < heavy; first += (int64_t)gridDim.x * kJoinWarps) {
+        const int64_t own = first + (int64_t)gridDim.x * warp;
+        bool many = false;
+        if (own < heavy) {
+            const int64_t t = p.heavy[1 + own];
+            const int id = p.sorted[(t + 1) * kTile - 1].x;
+            // Tiles t + 1 .. t + m hold more of it: the first that ends with another id is the last.
+            const int64_t at = (t + 2 + lane) * kTile;             // the tile behind
             const unsigned go = __ballot_sync(0xffffffffu, at < n && p.sorted[at].x == id);
-            __syncthreads();
-            if (lane == 0) runs[threadIdx.x / 32] = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
-            __syncthreads();
-            int run = 0;
-            for (int w = 0; w < kJoinThreads / 32 && run == 32 * w; ++w) run += runs[w];
-            m += run < kJoinThreads ? run + 1 : run;
-            if (run < kJoinThreads) break;
-        }
-        const int64_t each = (m + groups - 1) / groups;          // a group's stretch
-        for (int u0 = blockIdx.y * group; u0 < p.nunits; u0 += gridDim.y * group) {
-            const int unit = u0 + (threadIdx.x & (group - 1));
-            float acc[E] = {};
-            if (unit < p.nunits) {
+            const int m = go == 0xffffffffu ? 33 : __ffs(~go);
+            many = m > kShortRun;
+            for (int unit = blockIdx.y * 32 + lane; !many && unit < p.nunits; unit += gridDim.y * 32) {
                 const float* part = p.partial + (t + 1) * 2 * p.D + unit * E;
-                if (g == 0) add_sums<E>(part - p.D, acc);        // of tile t, slot 1
-                const int64_t end = min(m, (g + 1) * each);
-#pragma unroll 8
-                for (int64_t i = g * each; i < end; ++i) add_sums<E>(part + i * 2 * p.D, acc);
-            }
-            __syncthreads();
+                float acc[E] = {};
+                add_sums<E>(part - p.D, acc);                      // of tile t, slot 1
+                for (int i0 = 0; i0 < m; i0 += 4) {
+                    float next[4][E] = {};
 #pragma unroll
-            for (int e = 0; e < E; ++e) partly[threadIdx.x * E + e] = acc[e];
-            __syncthreads();
-            if (g == 0 && unit < p.nunits) {
-                for (int i = 1; i < groups; ++i)
+                    for (int i = 0; i < 4; ++i)
+                        if (i0 + i < m) add_sums<E>(part + (i0 + i) * 2 * (int64_t)p.D, next[i]);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += partly[(i * group + threadIdx.x) * E + e];
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < E; ++e) acc[e] += next[i][e];
+                }
                 store_unit<T, UB>(p.grad_weight, id, p.nunits, unit, acc, p.scale);
+            }
+        }
+        __syncthreads();
+        if (lane == 0) is_long[warp] = many;
+        __syncthreads();
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (!is_long[w]) continue;
+            const int64_t t = p.heavy[1 + first + (int64_t)gridDim.x * w];
+            const int id = p.sorted[(t + 1) * kTile - 1].x;
+            int64_t m = 0;
+            for (;;) {
+                const int64_t at = (t + 2 + m + threadIdx.x) * kTile;
+                const unsigned go = __ballot_sync(0xffffffffu, at < n && p.sorted[at].x == id);
+                __syncthreads();
+                if (lane == 0) runs[warp] = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
+                __syncthreads();
+                int run = 0;
+                for (int i = 0; i < kJoinWarps && run == 32 * i; ++i) run += runs[i];
+                m += run < kJoinThreads ? run + 1 : run;
+                if (run < kJoinThreads) break;
+            }
+            const int64_t each = (m + groups - 1) / groups;        // a group's stretch
+            for (int u0 = blockIdx.y * group; u0 < p.nunits; u0 += gridDim.y * group) {
+                const int unit = u0 + (threadIdx.x & (group - 1));
+                float acc[E] = {};
+                if (unit < p.nunits) {
+                    const float* part = p.partial + (t + 1) * 2 * p.D + unit * E;
+                    if (g == 0) add_sums<E>(part - p.D, acc);
+                    const int64_t end = min(m, (g + 1) * each);
+#pragma unroll 8
+                    for (int64_t i = g * each; i < end; ++i) add_sums<E>(part + i * 2 * p.D, acc);
+                }
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < E; ++e) partly[threadIdx.x * E + e] = acc[e];
+                __syncthreads();
+                if (g == 0 && unit < p.nunits) {
+                    for (int i = 1; i < groups; ++i)
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            acc[e] += partly[(i * group + threadIdx.x) * E + e];
+                    store_unit<T, UB>(p.grad_weight, id, p.nunits, unit, acc, p.scale);
+                }
             }
         }
     }
@@ -594,109 +633,206 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const SumParams p) {
 
 // ------------------------------------------------- gradient: few places, one launch
 // With up to kFewPlaces places every CTA looks at all of them.  It takes a range of ids and a
-// slice of 32 units of columns: it collects the places of its ids, sorts them (id, then
-// place) in shared memory, gives each warp an equal stretch of them to add, joins the sums
-// of ids that cross stretches in order, and zeroes the rows of ids without places.  Bound by
-// latency (the sort's barriers, a stretch's loads): 1312 places of 29 ids x 301 float32 take 8 us in
-// a graph; sort, sums and join by three launches took 17.
-constexpr int kFewPlaces = 2048;
-constexpr int kFewBits = 11;              // of a place in a key; the rest is the id's number
-constexpr int kFewThreads = 256;
-constexpr int kFewWarps = kFewThreads / 32;
+// slice of columns: it collects the places of its ids, sorts them by id (stable) in shared
+// memory, gives each group of kFewLanes threads an equal stretch of them to add, joins the sums
+// of ids that cross stretches in order, and zeroes the rows of ids without places.
+//
+// Latency bounds it, and where one id has most places the CTAs that own it: 1312 places of 29
+// ids x 301 float32 take 6.7 us in a graph; 2032 places of 512 float16, evenly over 1024 ids, 6.4, all
+// of one id 14.5.  Sort, sums and join by three launches took 17 for the first, and take 17 to 20
+// for 4096 places, where this takes 8 to 23.  A bitonic sort in the place of the ballots took 5000
+// cycles for 23 keys and 46000 for 4080 (18 us of 41).  Slices of 8 units: 1 us slower for even ids, 1
+// to 4 faster for one id; of 32: 1 us faster and 5 to 10 slower.
+constexpr int kFewPlaces = 4096;
+constexpr int kFewBits = 12;              // of a place in a key; the rest is the id's number
+constexpr int kFewThreads = 512;
+constexpr int kFewLanes = 16;             // units of a CTA's slice of columns
+constexpr int kFewGroups = kFewThreads / kFewLanes;
 constexpr int kFewIds = 4096;             // ids of a CTA, at most
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewDigit = 6;              // bits of a digit, at most
+constexpr int kFewItems = kFewPlaces / kFewThreads;
+constexpr int kFewStride = kFewWarps + 1; // of a digit's counts: lanes' digits lie in different banks
 
 struct FewParams {
     Places pl;
     const char* grad_out;
     char* grad_weight;
-    int32_t N, ids, nunits;
+    int32_t N, ids, nunits, slices;
+    int32_t passes, bits;      // of the sort: digits of `bits` bits
     float scale;
     int32_t* status;
 };
 
+// A ring of rows, as k_sum's (before it, every other pass's keys); each group's sum of an id that
+// began in an earlier stretch; the keys.
 template <typename T, int UB>
-__global__ void __launch_bounds__(kFewThreads) k_few(const FewParams p) {
+struct FewShared {
+    union {
+        typename Unit<UB>::type ring[kRing][kFewThreads];
+        uint32_t other[kFewPlaces];
+    };
+    float partly[kFewGroups][kFewLanes * (UB / (int)sizeof(T))];
+    uint32_t key[kFewPlaces];
+    uint32_t present[kFewIds / 32];
+    int counts[kFewStride << kFewDigit];      // [digit][warp]: counts, then starts
+    int sums[kFewWarps];
+};
+
+template <typename T, int UB>
+__global__ void __launch_bounds__(kFewThreads, 2) k_few(const FewParams p) {
     using U = typename Unit<UB>::type;
     constexpr int E = UB / (int)sizeof(T);
-    __shared__ uint32_t key[kFewPlaces];
-    __shared__ uint32_t present[kFewIds / 32];
-    __shared__ float partly[2][kFewWarps][32 * E];     // begun in an earlier stretch / goes on
-    __shared__ int count;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int v0 = blockIdx.x * p.ids, ids = min(p.ids, p.pl.V - v0);
-    const int unit = blockIdx.y * 32 + lane;
+    extern __shared__ __align__(16) char few_space[];
+    auto& sh = *reinterpret_cast<FewShared<T, UB>*>(few_space);
+    auto& key = sh.key;
+    auto& present = sh.present;
+    auto& partly = sh.partly;
+    auto& ring = sh.ring;
+    const int tid = threadIdx.x, lane = tid % kFewLanes, group = tid / kFewLanes;
+    const int warp = tid / 32, in_warp = tid & 31;
+    const unsigned below = (1u << in_warp) - 1;
+    const int range = (int)(blockIdx.x / (unsigned)p.slices);
+    const int v0 = range * p.ids, ids = min(p.ids, p.pl.V - v0);
+    const int unit = (int)(blockIdx.x - (unsigned)(range * p.slices)) * kFewLanes + lane;
     for (int i = tid; i < (ids + 31) / 32; i += kFewThreads) present[i] = 0;
-    if (tid == 0) count = 0;
-    __syncthreads();
+    // The places of the CTA's ids, in order; the last pass is to end in `key`.
+    int n = 0;
     for (int c = 0; c < p.N; c += 4 * kFewThreads) {
+        uint32_t* to = p.passes & 1 ? sh.other : key;
         uint32_t place[4];
         int id[4];
+        unsigned who[4];
         bool bad = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) place[i] = c + i * kFewThreads + tid;
+        for (int i = 0; i < 4; ++i) place[i] = c + (warp * 4 + i) * 32 + in_warp;
         place_ids<4>(p.pl, place, p.N, id, bad);
         if (bad && p.status) *p.status = RNNT_INVALID_VALUE;
+        int mine = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int mine = id[i] - v0;
-            if (id[i] >= 0 && mine >= 0 && mine < ids) {
-                key[atomicAdd(&count, 1)] = (uint32_t)mine << kFewBits | place[i];
-                atomicOr(&present[mine >> 5], 1u << (mine & 31));
-            }
+            who[i] = __ballot_sync(0xffffffffu, id[i] >= v0 && id[i] - v0 < ids);
+            mine += __popc(who[i]);
         }
+        if (in_warp == 0) sh.sums[warp] = mine;
+        __syncthreads();
+        const int of_warp = in_warp < kFewWarps ? sh.sums[in_warp] : 0;
+        int at = n + __reduce_add_sync(0xffffffffu, in_warp < warp ? of_warp : 0);
+        n += __reduce_add_sync(0xffffffffu, of_warp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (who[i] >> in_warp & 1)
+                to[at + __popc(who[i] & below)] = (uint32_t)(id[i] - v0) << kFewBits | place[i];
+            at += __popc(who[i]);
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    const int n = count;
-    // bitonic sort of the next power of two
-    int size = 1;
-    while (size < n) size *= 2;
-    for (int i = n + tid; i < size; i += kFewThreads) key[i] = 0xffffffffu;
-    for (int k = 2; k <= size; k *= 2)
-        for (int o = k / 2; o; o /= 2) {
-            __syncthreads();
-            for (int i = tid; i < size / 2; i += kFewThreads) {
-                const int a = (i & ~(o - 1)) << 1 | (i & (o - 1)), b = a + o;
-                const uint32_t x = key[a], y = key[b];
-                if ((x > y) == ((a & k) == 0)) {
-                    key[a] = y;
-                    key[b] = x;
-                }
+    // Stable radix sort by id.  A warp's keys are adjacent, each one's rank among them by ballots.
+    const int per = (n + kFewThreads - 1) / kFewThreads;         // keys of a lane
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const bool back = (p.passes - pass) & 1;
+        const uint32_t* from = back ? sh.other : key;
+        uint32_t* to = back ? key : sh.other;
+        const int shift = kFewBits + pass * p.bits, bins = 1 << p.bits;
+        for (int i = tid; i < bins * kFewStride; i += kFewThreads) sh.counts[i] = 0;
+        __syncthreads();
+        uint32_t k[kFewItems];
+        int ahead[kFewItems];
+#pragma unroll
+        for (int s = 0; s < kFewItems; ++s) {
+            if (s >= per) break;
+            const int i = (warp * per + s) * 32 + in_warp;
+            k[s] = i < n ? from[i] : 0;
+            const int d = (int)(k[s] >> shift) & (bins - 1);
+            unsigned same = __ballot_sync(0xffffffffu, i < n);
+            for (int bit = 0; bit < p.bits; ++bit) {
+                const bool one = d >> bit & 1;
+                const unsigned ones = __ballot_sync(0xffffffffu, one);
+                same &= one ? ones : ~ones;
             }
+            int* count = &sh.counts[d * kFewStride + warp];
+            const int before = *count;
+            ahead[s] = i < n ? before + __popc(same & below) : -1;
+            __syncwarp();
+            if (i < n && in_warp == __ffs(same) - 1) *count = before + __popc(same);
+            __syncwarp();
         }
-    __syncthreads();
-    // A warp's stretch: ids that begin and end in it are stored, the others' sums kept.
-    const int each = (n + kFewWarps - 1) / kFewWarps;
-    const int lo = min(n, warp * each), hi = min(n, lo + each);
+        __syncthreads();
+        // Each count becomes the sum of those ahead of it, digit by digit and warp by warp: two a
+        // thread.
+        int* two = &sh.counts[tid / (kFewWarps / 2) * kFewStride + tid % (kFewWarps / 2) * 2];
+        const bool some = tid < bins * kFewWarps / 2;
+        const int x = some ? two[0] : 0, y = some ? two[1] : 0;
+        int upto = x + y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (in_warp >= o) upto += v;
+        }
+        if (in_warp == 31) sh.sums[warp] = upto;
+        __syncthreads();
+        const int of_warp = in_warp < kFewWarps ? sh.sums[in_warp] : 0;
+        upto += __reduce_add_sync(0xffffffffu, in_warp < warp ? of_warp : 0);
+        if (some) {
+            two[0] = upto - x - y;
+            two[1] = upto - y;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < kFewItems; ++s) {
+            if (s >= per) break;
+            if (ahead[s] >= 0)
+                to[sh.counts[((int)(k[s] >> shift) & (bins - 1)) * kFewStride + warp] + ahead[s]] = k[s];
+        }
+        __syncthreads();
+    }
+    for (int i = tid; i < n; i += kFewThreads) {
+        const int mine = (int)(key[i] >> kFewBits);
+        if (i == 0 || (int)(key[i - 1] >> kFewBits) != mine)
+            atomicOr(&present[mine >> 5], 1u << (mine & 31));
+    }
+    // A group's stretch: ids that begin and end in it are stored, the others' sums kept.
+    const int each = (n + kFewGroups - 1) / kFewGroups;
+    const int lo = min(n, group * each), hi = min(n, lo + each);
+    float acc[E] = {};                       // in the end, of the id that goes on behind hi
     if (unit < p.nunits && lo < hi) {
         const U* src = reinterpret_cast<const U*>(p.grad_out) + unit;
-        float acc[E] = {};
         int cur = (int)(key[lo] >> kFewBits);
         bool head = lo > 0 && (int)(key[lo - 1] >> kFewBits) == cur;
-        constexpr int kRows = 8;
-        for (int j = lo; j < hi; j += kRows) {
-            Pack<T, UB> v[kRows];
+        auto fetch = [&](int j) {
+            if (j < hi)
+                copy_unit<UB>(&ring[j & (kRing - 1)][tid],
+                              src + (int64_t)(key[j] & (kFewPlaces - 1)) * p.nunits);
+            copy_group();
+        };
 #pragma unroll
-            for (int i = 0; i < kRows; ++i)
-                if (j + i < hi)
-                    v[i].raw = __ldg(src + (int64_t)(key[j + i] & (kFewPlaces - 1)) * p.nunits);
+        for (int i = 0; i < kRing; ++i) fetch(lo + i);
+        auto take = [&](int j) {
+            copies_left<kRing - 1>();
+            Pack<T, UB> v;
+            v.raw = ring[j & (kRing - 1)][tid];
+            fetch(j + kRing);
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                if (j + i >= hi) break;
+            for (int e = 0; e < E; ++e) acc[e] += to_f32(v.e[e]);
+        };
+        for (int j = lo; j < hi; ++j) {
+            // eight rows of an id at a time while it goes on behind them, then one by one
+            for (; j + 8 < hi && (int)(key[j + 8] >> kFewBits) == cur; j += 8)
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += to_f32(v[i].e[e]);
-                const int next = j + i + 1 < n ? (int)(key[j + i + 1] >> kFewBits) : -1;
-                if (next != cur || j + i + 1 == hi) {
-                    if (head || next == cur) {
+                for (int i = 0; i < 8; ++i) take(j + i);
+            take(j);
+            const int next = j + 1 < n ? (int)(key[j + 1] >> kFewBits) : -1;
+            if (next != cur || (head && j + 1 == hi)) {
+                if (head) {
 #pragma unroll
-                        for (int e = 0; e < E; ++e) partly[head ? 0 : 1][warp][lane * E + e] = acc[e];
-                    } else {
-                        store_unit<T, UB>(p.grad_weight, v0 + cur, p.nunits, unit, acc, p.scale);
-                    }
-                    head = false;
-                    cur = next;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+                    for (int e = 0; e < E; ++e) partly[group][lane * E + e] = acc[e];
+                } else {
+                    store_unit<T, UB>(p.grad_weight, v0 + cur, p.nunits, unit, acc, p.scale);
                 }
+                head = false;
+                cur = next;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = 0.0f;
             }
         }
     }
@@ -705,21 +841,33 @@ __global__ void __launch_bounds__(kFewThreads) k_few(const FewParams p) {
         const int id = (int)(key[hi - 1] >> kFewBits);
         const bool begun = lo == 0 || (int)(key[lo - 1] >> kFewBits) != id;
         if (begun && (int)(key[hi] >> kFewBits) == id) {
-            float acc[E];
+            for (int w = group + 1; w * each < n && (int)(key[w * each] >> kFewBits) == id; ++w)
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = partly[1][warp][lane * E + e];
-            for (int w = warp + 1; w * each < n && (int)(key[w * each] >> kFewBits) == id; ++w)
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += partly[0][w][lane * E + e];
+                for (int e = 0; e < E; ++e) acc[e] += partly[w][lane * E + e];
             store_unit<T, UB>(p.grad_weight, v0 + id, p.nunits, unit, acc, p.scale);
         }
     }
     if (unit < p.nunits) {
         float zero[E] = {};
-        for (int r = warp; r < ids; r += kFewWarps)
+        for (int r = group; r < ids; r += kFewGroups)
             if (!(present[r >> 5] >> (r & 31) & 1))
                 store_unit<T, UB>(p.grad_weight, v0 + r, p.nunits, unit, zero, 1.0f);
     }
+}
+
+// k_few's limits, raised once per device.
+template <typename T, int UB>
+bool few_prepared() {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> done[kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return false;
+    if (done[dev].load(std::memory_order_acquire)) return true;
+    const bool ok = cudaFuncSetAttribute(k_few<T, UB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(FewShared<T, UB>)) == cudaSuccess;
+    if (ok) done[dev].store(true, std::memory_order_release);
+    else cudaGetLastError();
+    return ok;
 }
 
 // Calls f(T{}, unit) with the unit's width as a constant; units are never
@@ -892,16 +1040,27 @@ extern "C" rnnt_status_t rnnt_embed_grad(const void* grad_out, rnnt_dtype_t dt,
         f.nunits = (int32_t)nunits;
         f.scale = scale;
         f.status = status_dev;
-        const int64_t slices = (nunits + 31) / 32;
-        // four CTAs an SM, or one an id
-        const int64_t ctas = std::max<int64_t>(1, 152 * 4 / slices);
+        const int64_t slices = (nunits + kFewLanes - 1) / kFewLanes;
+        // two CTAs an SM, or one an id
+        const int64_t ctas = std::max<int64_t>(1, 152 * 2 / slices);
         f.ids = (int32_t)std::min<int64_t>(kFewIds, (V + ctas - 1) / ctas);
+        f.slices = (int32_t)slices;
+        int bits = 0;
+        while (1 << bits < f.ids) ++bits;
+        f.passes = (bits + kFewDigit - 1) / kFewDigit;
+        f.bits = f.passes ? (bits + f.passes - 1) / f.passes : 0;
+        const int64_t grid = ((int64_t)V + f.ids - 1) / f.ids * slices;
+        if (grid > INT32_MAX) return RNNT_INVALID_VALUE;
         if (!clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
+        bool ok = true;
         with_unit(dt, unit, [&](auto tag, auto ub) {
-            k_few<decltype(tag), decltype(ub)::value>
-                <<<dim3((unsigned)((V + f.ids - 1) / f.ids), (unsigned)slices), kFewThreads, 0, st>>>(f);
+            using T = decltype(tag);
+            constexpr int UB = decltype(ub)::value;
+            ok = few_prepared<T, UB>();
+            if (ok)
+                k_few<T, UB><<<(unsigned)grid, kFewThreads, sizeof(FewShared<T, UB>), st>>>(f);
         });
-        return launched();
+        return ok ? launched() : RNNT_LAUNCH_FAILED;
     }
 
     SortParams s{};

@@ -59,8 +59,10 @@ GRAD = EMBED + [
     (2, 1023, 3, 24, 1, False, 1.5),        # few ids, each of them over many tiles
     (1, 4000, 1, 5, None, False, 1.0),      # one id
     (9, 1000, 2500, 32, 0, True, 1.0),      # two digits, two blocks
-    (1, 2048, 700, 40, None, False, 1.0),   # the most places of the one-launch kernel
-    (1, 2049, 700, 40, None, False, 1.0),   # and one more
+    (1, 2048, 700, 40, None, False, 1.0), (1, 2049, 700, 40, None, False, 1.0),
+    (1, 4096, 700, 40, None, False, 1.0),   # the most places of the one-launch kernel
+    (1, 4097, 700, 40, None, False, 1.0),   # and one more
+    (1, 5000, 1, 5, None, False, 1.0),      # one id, over tiles
     (2, 1023, 1, 33, 0, False, 0.5), (7, 290, 9000, 260, 3, True, 2.0),
 ]
 

@@ -46,7 +46,7 @@ def embed_grad(**kw):
 
 @pytest.mark.parametrize("bad", [
     dict(grad_out=None), dict(grad_weight=None), dict(tokens=None),
-    dict(workspace=None, S=2000, tokens_stride=2000, grad_weight=1 << 24),
+    dict(workspace=None, S=2100, tokens_stride=2100, grad_weight=1 << 24),
     dict(dt=-1), dict(V=0), dict(D=0), dict(B=0), dict(S=0), dict(tokens_stride=4),
     dict(has_start=1, start=10), dict(scale=float("nan")), dict(workspace=(1 << 22) + 64),
     dict(grad_out=(1 << 20) + 1), dict(grad_weight=(1 << 20) + 64), dict(D=(1 << 20) + 1),
@@ -56,10 +56,10 @@ def test_embed_grad_refuses(bad):
 
 
 def test_embed_grad_workspace():
-    assert N.rnnt_embed_grad_workspace_size(2, 1024, 0, 10, 8) == 0       # 2048 places: none
-    n = N.rnnt_embed_grad_workspace_size(2, 2000, 0, 10, 8)
+    assert N.rnnt_embed_grad_workspace_size(2, 2048, 0, 10, 8) == 0       # 4096 places: none
+    n = N.rnnt_embed_grad_workspace_size(2, 2100, 0, 10, 8)
     assert n > 0 and n % 256 == 0
-    assert embed_grad(workspace_bytes=n - 1, S=2000, tokens_stride=2000, grad_weight=1 << 24) \
+    assert embed_grad(workspace_bytes=n - 1, S=2100, tokens_stride=2100, grad_weight=1 << 24) \
         == N.RNNT_WORKSPACE_TOO_SMALL
     big = N.rnnt_embed_grad_workspace_size(64, 1023, 1, 50000, 1024)
     assert 65536 * 16 <= big <= 65536 * (16 + 4 * 1024 // 8)
