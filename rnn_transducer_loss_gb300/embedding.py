@@ -159,7 +159,9 @@ def rnnt_embed(weight: torch.Tensor, tokens: torch.Tensor, lengths: torch.Tensor
     Each element is multiplied in float32 and rounded once.  ``check`` reads the
     device status word after the call (one synchronisation) and raises on tokens
     outside the vocabulary and lengths outside [0, S]; without it such a token
-    is padding and such a length the nearer bound.
+    is padding and such a length the nearer bound.  A backward pass is captured
+    into a CUDA graph with ``check=False`` and with no eager graph of the same
+    weight alive (autograd would make the capture wait for that one's stream).
     """
     if weight.requires_grad and torch.is_grad_enabled():
         return _Embed.apply(weight, tokens, lengths, start, float(scale), check)

@@ -449,8 +449,8 @@ def test_two_streams_at_once():
     jobs = []
     for seed in (1, 2):
         g = torch.Generator(device="cuda").manual_seed(seed)
-        tokens = torch.randint(0, 900, (4, 1000), device="cuda", dtype=torch.int32, generator=g)
-        go = torch.randn(4, 1001, 64, device="cuda", generator=g)
+        tokens = torch.randint(0, 900, (4, 1100), device="cuda", dtype=torch.int32, generator=g)
+        go = torch.randn(4, 1101, 64, device="cuda", generator=g)
         x, scores = logits_of(3, 20, 30000, "f16", seed)
         jobs.append((tokens, go, x, scores))
 
@@ -471,6 +471,35 @@ def test_two_streams_at_once():
     for i in range(2):
         for r in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(r, want[i]))
+
+
+@pytest.mark.parametrize("B", [2, 9])
+def test_captured_training(B):
+    """A forward and backward pass in a graph, by one launch and by three, replayed with new labels."""
+    g = torch.Generator(device="cuda").manual_seed(B)
+    w = torch.randn(300, 48, device="cuda", generator=g).requires_grad_()
+    tokens = torch.zeros(B, 600, device="cuda", dtype=torch.int32)
+    lengths = torch.full((B,), 600, device="cuda", dtype=torch.int32)
+    go = torch.randn(B, 601, 48, device="cuda", generator=g)
+
+    def step():
+        out = rnnt_embed(w, tokens, lengths, start=0, scale=3.0, check=False)
+        return out.detach(), torch.autograd.grad(out, w, go)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                            # nothing of it lives on: no eager graph of the same leaf
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for low in (600, 40, 0):
+        tokens.copy_(torch.randint(0, 300, tokens.shape, device="cuda", generator=g))
+        lengths.copy_(torch.randint(low, 601, lengths.shape, device="cuda", generator=g))
+        graph.replay()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
 
 
 def test_far_offsets():
