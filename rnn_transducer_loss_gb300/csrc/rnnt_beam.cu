@@ -709,10 +709,12 @@ __device__ __forceinline__ unsigned long long or_lanes(unsigned long long x) {
            __reduce_or_sync(0xffffffffu, (uint32_t)x);
 }
 
-// The beams of item b from their lists ([K * splits][n]) and statistics, in shared memory already
-// (behind the barrier here); leaves in sh.again the beams whose log-sum-exp is wanted exactly.
+// An item's beams from their scores, whether they are finished (or null), and their lists
+// ([K * splits][n]) and statistics, in shared memory already (behind the barrier here); leaves in
+// sh.again the beams whose log-sum-exp is wanted exactly.
 template <int THREADS>
-__device__ __forceinline__ void weigh(const SelectParams& p, uint32_t b, const uint64_t* lists,
+__device__ __forceinline__ void weigh(const SelectParams& p, const float* scores,
+                                      const uint8_t* finished, const uint64_t* lists,
                                       const float4* stat, PickShared& sh) {
     const int tid = threadIdx.x;
     if (tid == 0) sh.again = 0;
@@ -720,8 +722,8 @@ __device__ __forceinline__ void weigh(const SelectParams& p, uint32_t b, const u
     // A beam's log-sum-exp from its splits: by one thread, or a warp's lanes together.
     const int group = p.splits == 1 ? 1 : 32;
     for (int k = tid / group; k < p.K; k += THREADS / group) {
-        const float score = p.scores[b * p.K + k];
-        const bool done = p.finished && p.finished[b * p.K + k];
+        const float score = scores[k];
+        const bool done = finished && finished[k];
         const float4* st = stat + k * p.splits;
         const uint64_t* first = lists + k * p.splits * p.n;
         bool bad = !(score < INFINITY);
@@ -792,8 +794,9 @@ __device__ __forceinline__ void settle(const SelectParams& p, PickShared& sh, in
 }
 
 // The selection by the log-sum-exps at hand; leaves in sh.again the beams whose log-sum-exp it
-// wants exactly before it can be sure.  `values` is as large as the lists.
-template <int THREADS>
+// wants exactly before it can be sure.  `values` is as large as the lists, of which there are 32 L
+// at most.
+template <int THREADS, int L>
 __device__ __forceinline__ void choose(const SelectParams& p, const uint64_t* lists,
                                        uint64_t* values, PickShared& sh) {
     const int tid = threadIdx.x, lane = tid & 31;
@@ -812,7 +815,6 @@ __device__ __forceinline__ void choose(const SelectParams& p, const uint64_t* li
     }
     __syncthreads();
     if (tid < 32) {
-        constexpr int L = kMaxLists / 32;
         uint64_t head[L];
         int at[L];
 #pragma unroll
@@ -909,16 +911,22 @@ __device__ __forceinline__ void report(const SelectParams& p, uint32_t b, const 
 
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
-    wait_for_previous();
     extern __shared__ uint64_t lists[];                // [K * splits][n], twice
     __shared__ float4 stat[kMaxLists];
     __shared__ PickShared sh;
+    __shared__ float scores[RNNT_MAX_BEAM];
+    __shared__ uint8_t finished[RNNT_MAX_BEAM];
     const uint32_t b = blockIdx.x;
+    if (threadIdx.x < p.K) {                           // inputs: k_rows does not write them
+        scores[threadIdx.x] = p.scores[b * p.K + threadIdx.x];
+        finished[threadIdx.x] = p.finished && p.finished[b * p.K + threadIdx.x];
+    }
+    wait_for_previous();
     const int nlists = p.K * p.splits;
     const uint64_t* from = p.list + (int64_t)b * nlists * p.n;
     if (threadIdx.x < nlists) stat[threadIdx.x] = p.stat[(int64_t)b * nlists + threadIdx.x];
     for (int i = threadIdx.x; i < nlists * p.n; i += kPickThreads) lists[i] = from[i];
-    weigh<kPickThreads>(p, b, lists, stat, sh);
+    weigh<kPickThreads>(p, scores, finished, lists, stat, sh);
     for (int turn = 0; turn <= RNNT_MAX_BEAM; ++turn) {        // each settles a beam at least
         for (unsigned long long again = sh.again; again; again &= again - 1) {
             const int k = __ffsll((long long)again) - 1;
@@ -927,7 +935,8 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
             if (threadIdx.x == 0) settle(p, sh, k, l);
         }
         __syncthreads();
-        choose<kPickThreads>(p, lists, lists + nlists * p.n, sh);
+        if (nlists <= 32) choose<kPickThreads, 1>(p, lists, lists + nlists * p.n, sh);
+        else choose<kPickThreads, kMaxLists / 32>(p, lists, lists + nlists * p.n, sh);
         if (!sh.again) break;
     }
     report<kPickThreads>(p, b, lists, sh);
@@ -968,10 +977,13 @@ __global__ void __launch_bounds__(kClusterThreads, 8) k_search(const SelectParam
         if (threadIdx.x == 0) first.stat[rank] = sh.rows.stat;
     }
     cluster.sync();
-    if (rank == 0) weigh<kClusterThreads>(p, b, lists, sh.stat, sh.pick);
+    if (rank == 0)
+        weigh<kClusterThreads>(p, p.scores + b * p.K, p.finished ? p.finished + b * p.K : nullptr,
+                               lists, sh.stat, sh.pick);
     for (int turn = 0; turn <= kMaxCluster; ++turn) {          // each settles a beam at least
         if (rank == 0) {
-            if (turn || !sh.pick.again) choose<kClusterThreads>(p, lists, lists + p.K * p.n, sh.pick);
+            if (turn || !sh.pick.again)
+                choose<kClusterThreads, 1>(p, lists, lists + p.K * p.n, sh.pick);
         }
         if (!p.fused) break;                           // exact as it is
         cluster.sync();
