@@ -851,6 +851,7 @@ __device__ __forceinline__ void choose(const SelectParams& p, const uint64_t* li
                         head[q] = at[q] < p.n ? values[list * p.n + at[q]] : 0;
                     }
             }
+            __syncwarp();
         }
         __syncwarp();
         for (int r = lane; r < found; r += 32) sh.obeam[r] = (uint8_t)((sh.oid[r] >> 8) / p.splits);

@@ -213,6 +213,18 @@ def test_select_beams(K):
         check_select(x, scores, beam)
 
 
+@pytest.mark.parametrize("K", [1, 2, 17])
+@pytest.mark.parametrize("fused", [True, False])
+def test_select_small_vocabularies(K, fused):
+    """As many results as there are candidates, one less and one more, and lists of every length."""
+    for V in (1, 2, 3, 4, 5, 6, 7, 8, 9, 12, 17):
+        x, scores = logits_of(2, K, V, "f32", V + 100 * K)
+        if not fused:
+            x = torch.log_softmax(x, -1)
+        for beam in sorted({1, 2, max(V - 1, 1), V, V + 1, min(K * V, 64), min(K * V + 1, 64)}):
+            check_select(x, scores, beam, None, fused)
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("V", [31, 4099])
 def test_select_ties(dtype, V):
