@@ -41,7 +41,7 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 //     bound go through best_of_row instead, tile by tile.
 // Memory bounds it where rows are long (one read of the logits): 1024 rows of 200000 bfloat16, all
 // at once, take 87 us with k_pick (4.7 TB/s; the ex2 units are busy for 23 % of it, the issue slots
-// for 48 %), of 50000 28 us and 7 more for k_pick, of which 12 do not depend on the length:
+// for 48 %), of 50000 28 us and 6 more for k_pick, of which 13 do not depend on the length:
 // the first loads and, behind the stream, a chain of barriers (bound, second look, ranking).
 constexpr int kRowThreads = 128;           // of k_rows: 8 CTAs an SM hold 1024 rows at once (256
                                            // threads, 4 CTAs: a second wave, 32 against 28 us)
@@ -642,7 +642,7 @@ __device__ __forceinline__ Pair log_pair(Pair s) {
 // --------------------------------------------------------- the Ko best of all
 // One CTA per batch item.  Every (beam, split) list is in order, so the best candidate is among
 // the lists' heads: one warp holds them, up to 4 a lane, and takes Ko times the largest.  Latency
-// bounds it: 7 us behind k_rows for 64 items of 16 lists (5 less in the whole call with one warp's
+// bounds it: 6 us behind k_rows for 64 items of 16 lists (5 less in the whole call with one warp's
 // selection than with ranks by counting, which compares all candidates with all).
 //
 // The streamed sums leave a log-sum-exp off by error[k] (see kTermError).  Where the order of
@@ -947,9 +947,9 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
 // A cluster takes a batch item: each CTA streams a row and leaves its list and statistics in the
 // first CTA's shared memory, which picks; where that wants exact log-sum-exps, each CTA
 // computes its own row's.  One launch and no workspace.  Latency bounds it, a chain of the row's
-// barriers, two cluster barriers and one maximum of the heads a selected hypothesis: 8.3 us in a
-// graph for 1 x 4 x 1024 float16, 11.1 for 32 x 10 x 29 float32, 8.4 for 16 x 8 x 5000 float32
-// log-probabilities (by two launches 8.8, 11 and 11.2, and 6 us more of the host's time).
+// barriers, two cluster barriers and one maximum of the heads a selected hypothesis: 8.2 us in a
+// graph for 1 x 4 x 1024 float16, 10.5 for 32 x 10 x 29 float32, 8.0 for 16 x 8 x 5000 float32
+// log-probabilities (two launches: 3 us more for the last, and 5 us more of the host's time).
 template <int NV>
 struct ClusterShared {
     union {
@@ -1016,7 +1016,7 @@ SelectLayout select_layout(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt) 
     // A cluster's CTAs take a row each, whole, against splits over the whole device and a second
     // launch.  On the GPU they are level where rows are short (items of 4 and 16 rows of 5000
     // float16: 9.9 and 13.2 us against 9.7 and 14.1), and the one launch without a workspace
-    // costs the host 6 us less; long rows (of 50000: 15.3 and 19.5 against 9.5 and 15.4) are
+    // costs the host 5 us less; long rows (of 50000: 15.3 and 19.5 against 9.5 and 15.4) are
     // faster split, and their exact sums by k_pick's larger block.
     if (K <= kMaxCluster && (int64_t)V * es <= kClusterBytes) {
         L.cluster = K;
