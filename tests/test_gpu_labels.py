@@ -63,6 +63,9 @@ GRAD = EMBED + [
     (1, 4096, 700, 40, None, False, 1.0),   # the most places of the one-launch kernel
     (1, 4097, 700, 40, None, False, 1.0),   # and one more
     (1, 5000, 1, 5, None, False, 1.0),      # one id, over tiles
+    (5, 1000, 3, 24, 1, False, 1.5),        # few ids, each of them over many tiles
+    (9, 1000, 40, 301, None, False, 1.0),   # ids of 5 to 9 tiles, odd rows
+    (16, 290, 9000, 260, 3, True, 2.0),     # ids of one place or none
     (2, 1023, 1, 33, 0, False, 0.5), (7, 290, 9000, 260, 3, True, 2.0),
 ]
 
@@ -88,9 +91,10 @@ def test_embed_grad(case, dtype):
     assert torch.equal(got, again)
 
 
-@pytest.mark.parametrize("V,D,N", [(5_000_000, 2, 3000), (70, 4, 200_000), (9000, 4, 150_000)])
+@pytest.mark.parametrize("V,D,N", [(5_000_000, 2, 3000), (5_000_000, 2, 5000), (70, 4, 200_000), (9000, 4, 150_000)])
 def test_embed_grad_many(V, D, N):
-    """Three digits; more places than the sorting threads hold at a time."""
+    """Two digits of one launch's sort, three of the cluster's; more places than its threads hold at
+    a time."""
     g = torch.Generator(device="cuda").manual_seed(N)
     tokens = torch.randint(0, V, (1, N), device="cuda", dtype=torch.int32, generator=g)
     go = torch.randint(-8, 9, (1, N, D), device="cuda", generator=g).float()
