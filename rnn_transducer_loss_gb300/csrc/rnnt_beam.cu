@@ -27,9 +27,9 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 }
 
 // ------------------------------------------------------------- rows of logits
-// A row is cut into splits of whole aligned 16-byte vectors (the few elements ahead of them
-// and behind them go to threads of split 0 one by one); a CTA streams one split through
-// registers and writes
+// A row is cut into splits of whole aligned 16-byte vectors (the few elements ahead of them go to
+// threads of the first split one by one, those behind them to the last split's, so that the splits
+// are in the order of the tokens); a CTA streams one split through registers and writes
 //   - the sum of exp(x - r) over the split and its reference r.  r is the first tile's
 //     maximum and changes only when a thread meets a value more than 16 above it, so
 //     that a sum is (almost) never rescaled.
@@ -277,15 +277,17 @@ struct Split {
     }
 };
 
-// The element ahead of the row's whole vectors or behind them that is this thread's, or -1.
+// The element ahead of the row's whole vectors (of the first split) or behind them (of the last)
+// that is this thread's, or -1.
 template <typename T>
 __device__ __forceinline__ int odd_element(const SelectParams& p, uint32_t row, int split) {
     constexpr int E = 16 / (int)sizeof(T);
-    if (split || threadIdx.x >= 2 * E) return -1;
+    const bool front = threadIdx.x < E;
+    if (threadIdx.x >= 2 * E || split != (front ? 0 : p.splits - 1)) return -1;
     const int ahead = min(p.V, (int)(-(uintptr_t)row_of<T>(p, row) & 15) / (int)sizeof(T));
     const int behind = ahead + (p.V - ahead) / E * E;
-    const int at = threadIdx.x < E ? threadIdx.x : behind + threadIdx.x - E;
-    return at < (threadIdx.x < E ? ahead : p.V) ? at : -1;
+    const int at = front ? threadIdx.x : behind + threadIdx.x - E;
+    return at < (front ? ahead : p.V) ? at : -1;
 }
 
 // The n best of a split to best: every tile of TH vectors gives its elements above the
@@ -837,7 +839,8 @@ __device__ __forceinline__ void choose(const SelectParams& p, const uint64_t* li
             if (!hi) break;
             const uint32_t lo = __reduce_max_sync(
                 0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
-            // of equal values the lowest list: the lowest beam, and token
+            // of equal values the lowest list: the lowest beam, and token, as its lists are in
+            // the order of the tokens and each one's equal elements are
             const uint32_t list = __reduce_min_sync(
                 0xffffffffu, v == ((uint64_t)hi << 32 | lo) ? (uint32_t)(q0 * 32 + lane)
                                                             : 0xffffffffu);

@@ -1,0 +1,39 @@
+"""GPU: beam selection where it can go wrong: ties across the splits of a row."""
+import numpy as np
+import pytest
+import torch
+
+import label_ref as R
+from rnn_transducer_loss_gb300 import rnnt_beam_select
+
+pytestmark = pytest.mark.gpu
+DT = R.DTYPES
+
+
+def check(x, scores, beam, fused=True):
+    got = rnnt_beam_select(x, scores, beam, fused_log_softmax=fused)
+    want = R.select(R.f64(x), R.f64(scores), beam, None, fused)
+    np.testing.assert_array_equal(got[2].cpu().numpy(), want[2])
+    np.testing.assert_array_equal(got[1].cpu().numpy(), want[1])
+    s = R.f64(got[0])
+    left = np.isinf(want[0])
+    assert (s[left] == -np.inf).all()
+    assert (np.abs(s - want[0])[~left] <= R.score_bound(want[0], fused)[~left]).all()
+
+
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("B,K,V", [(1, 1, 20001), (1, 4, 50257), (2, 17, 1003), (3, 20, 4099)])
+def test_ties_across_splits(B, K, V, dtype, fused):
+    """Equal logits in different splits, among them the elements behind the last whole 16 bytes:
+    the lowest token first, also where the tie stands at the last place; misaligned rows too."""
+    x = torch.zeros(B, K, V + 9, dtype=DT[dtype], device="cuda")
+    scores = torch.full((B, K), -2.0, device="cuda")
+    scores[:, 0] = -1.0                             # one hypothesis ahead of equal ones
+    for skip in (0, 1, 5):
+        for at in ([V // 2, V - 1], [9, V // 2, 3 * V // 4, V - 1], [0, V - 2, V - 1]):
+            y = x[:, :, skip:skip + V]
+            y.zero_()
+            y[:, :, at] = 5.0
+            for beam in (1, len(at) - 1, len(at), len(at) + 3, 64):
+                check(y, scores, beam, fused)
