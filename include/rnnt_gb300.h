@@ -435,6 +435,9 @@ rnnt_status_t rnnt_beam_workspace_size(int32_t B, int32_t K, int32_t V, int32_t 
  *   finished       uint8 [B, K] (0 or not), or NULL: none.
  *   out_scores     float [B, Ko], best first; within 5e-6 of the value and one
  *                  float32 rounding (without fused_log_softmax: the rounding).
+ *                  A candidate beyond float32's range keeps its place in the
+ *                  order, its token and its parent, and its score is -inf
+ *                  (+inf above the range).
  *   out_tokens     int32 [B, Ko]: the selected output, -1 for a finished one.
  *   out_parents    int32 [B, Ko]: the hypothesis it extends.
  *                  Places left over when fewer than Ko candidates exist get

@@ -28,7 +28,9 @@ def rnnt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beam: int | Non
     itself alone, with its score unchanged and token -1, whatever its logits
     hold; one of score -inf offers nothing.  The order is that of the exact
     values to 40 bits (a returned score is within 5e-6 of its value and one
-    float32 rounding), ties go to the lowest hypothesis, then the lowest token.
+    float32 rounding; a candidate below float32's range keeps its place, its token
+    and its parent, and has score -inf), ties go to the lowest hypothesis, then the
+    lowest token.
     ``parents`` says which hypothesis each result extends (for
     :func:`rnnt_beam_reorder`); places left over get score -inf, token -1,
     parent -1.  ``check`` reads the device status word (one synchronisation) and

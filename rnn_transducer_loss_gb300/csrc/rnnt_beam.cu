@@ -136,9 +136,39 @@ __device__ __forceinline__ Pair add_loosely(Pair a, Pair b) {
 __device__ __forceinline__ uint64_t ordered(Pair a) {
     return (uint64_t)ordered(a.h) << 32 | ordered(a.l);
 }
+// The order of sums that float32 does not reach, given a quarter of each, |a| <= 3 2^126: as
+// different (their differences in more than 2^-50 of the value) as those of finite values, and in
+// keys that these leave: of bits that read as NaN.  Never 0.
+constexpr float kMost = 3.40282347e38f;                // the largest float32
+constexpr uint32_t kOrderedMost = 0xff7fffffu, kOrderedLeast = 0x00800000u;   // of kMost, -kMost
+__device__ __forceinline__ uint64_t ordered_beyond(Pair a) {
+    const uint64_t least = a.h < 0.0f ? (uint64_t)0x00bfffffu << 32        // ordered(-3 2^126)
+                                      : (uint64_t)0xfe800000u << 32;       // ordered(2^126)
+    const uint64_t base = a.h < 0.0f ? 1ull << 32 : (uint64_t)(kOrderedMost + 1) << 32;
+    return base + ((ordered(a) - least) >> 1);
+}
+// What is returned for a key: the value's float32 rounding.
+__device__ __forceinline__ float score_of(uint64_t key) {
+    const uint32_t o = (uint32_t)(key >> 32);
+    return o < kOrderedLeast ? -INFINITY : o > kOrderedMost ? INFINITY : unordered(o);
+}
+// NaN or infinite where a key is of a value beyond float32's range, whose step is more than any
+// log-sum-exp's error.
 __device__ __forceinline__ float difference(uint64_t a, uint64_t b) {
     return (unordered((uint32_t)(a >> 32)) - unordered((uint32_t)(b >> 32))) +
            (unordered((uint32_t)a) - unordered((uint32_t)b));
+}
+
+// The key of score + x - lse.  Where one of the steps passes float32's range (masks of the type's
+// lowest value in two steps of a search do), the sum is taken of quarters, which is exact.
+__device__ __noinline__ uint64_t key_of_far(float score, float x, Pair lse) {
+    const Pair q = add(two_sum(0.25f * score, 0.25f * x), Pair{-0.25f * lse.h, -0.25f * lse.l});
+    const Pair v{4.0f * q.h, 4.0f * q.l};
+    return fabsf(v.h) <= kMost ? ordered(v) : ordered_beyond(q);
+}
+__device__ __forceinline__ uint64_t key_of_sum(float score, float x, Pair lse) {
+    const Pair v = add(two_sum(score, x), Pair{-lse.h, -lse.l});
+    return fabsf(v.h) + fabsf(v.l) <= kMost ? ordered(v) : key_of_far(score, x, lse);   // not NaN
 }
 
 // Whether beam `row` offers its logits' candidates.
@@ -810,8 +840,7 @@ __device__ __forceinline__ void choose(const SelectParams& p, const uint64_t* li
         if (what == 2) {
             if (m == k * p.splits * p.n) v = ordered(Pair{sh.score[k], 0.0f});
         } else if (const uint64_t c = what == 1 ? lists[m] : 0) {
-            const Pair x = two_sum(sh.score[k], unordered((uint32_t)(c >> 32)));
-            v = ordered(add(x, Pair{-sh.lse[k].h, -sh.lse[k].l}));
+            v = key_of_sum(sh.score[k], unordered((uint32_t)(c >> 32)), sh.lse[k]);
         }
         values[m] = v;
     }
@@ -906,7 +935,7 @@ __device__ __forceinline__ void report(const SelectParams& p, uint32_t b, const 
     for (int r = threadIdx.x; r < p.Ko; r += THREADS) {
         const int64_t o = (int64_t)b * p.Ko + r;
         const int from = r < sh.found ? sh.obeam[r] : -1;
-        p.out_scores[o] = from < 0 ? -INFINITY : unordered((uint32_t)(sh.oval[r] >> 32));
+        p.out_scores[o] = from < 0 ? -INFINITY : score_of(sh.oval[r]);
         p.out_tokens[o] = from < 0 || sh.kind[from] == 2
                               ? -1 : (int)~(uint32_t)lists[(sh.oid[r] >> 8) * p.n + (sh.oid[r] & 255)];
         p.out_parents[o] = from;

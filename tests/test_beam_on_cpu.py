@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import beam_ref as BR
 import label_ref as R
 import on_cpu
 
@@ -54,3 +55,21 @@ def test_ties_across_splits(program, V, splits, dtype):
     x = torch.zeros(3, V, dtype=DT[dtype])          # nothing but ties, of hypotheses too
     x[1:, -3:] = 1.0
     check(program, x, [-1.0, -1.0, -1.0], 16, fused=False, splits=splits or 3)
+
+
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K,V,splits", [(4, 9, 0), (3, 700, 0), (4, 1003, 3), (18, 70, 0)])
+def test_beyond_float32(program, K, V, splits, dtype, fused):
+    """Scores and logits whose sums leave float32's range: the order is that of the values, which
+    come back as infinite; three steps on the scores that came back."""
+    for x, scores in BR.far_cases(DT[dtype], K, V, K):
+        for _ in range(3):
+            got = on_cpu.select(program, x, scores, K, None, fused, splits=splits)
+            want = BR.select(x.double().numpy(), scores, K, fused)
+            np.testing.assert_array_equal(got[2], want[2])
+            np.testing.assert_array_equal(got[1], want[1])
+            assert BR.score_error(got[0], want[0], fused) <= 0
+            bad = (scores == np.inf).any()
+            assert got[3] == (1 if bad else 0)
+            scores = got[0]
