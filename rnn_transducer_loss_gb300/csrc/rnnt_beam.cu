@@ -873,6 +873,11 @@ __device__ __forceinline__ void choose(const SelectParams& p, const uint64_t* li
             const uint32_t list = __reduce_min_sync(
                 0xffffffffu, v == ((uint64_t)hi << 32 | lo) ? (uint32_t)(q0 * 32 + lane)
                                                             : 0xffffffffu);
+            // No lane's, which cannot be: the same for the whole warp, and nothing is indexed by it.
+            if (list >= (uint32_t)nlists) {
+                if (lane == 0 && p.status) *p.status = RNNT_LAUNCH_FAILED;
+                break;
+            }
             if ((list & 31) == lane) {
                 sh.oval[found] = v;
                 sh.oid[found] = list << 8 | sel(at, q0);

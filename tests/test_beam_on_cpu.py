@@ -6,6 +6,7 @@ import torch
 import beam_ref as BR
 import label_ref as R
 import on_cpu
+from rnn_transducer_loss_gb300 import _native as N
 
 DT = R.DTYPES
 
@@ -73,3 +74,14 @@ def test_beyond_float32(program, K, V, splits, dtype, fused):
             bad = (scores == np.inf).any()
             assert got[3] == (1 if bad else 0)
             scores = got[0]
+
+
+@pytest.mark.parametrize("K,V,beam,splits", [(1, 5, 8, 0), (4, 40, 4, 0), (20, 70, 20, 0), (3, 515, 9, 3)])
+def test_selection_without_a_winner(program, K, V, beam, splits):
+    """The lists' best is always some lane's.  Were it none's, nothing may be indexed by it: the
+    places are left over and the status says so."""
+    x = torch.randn(K, V, generator=torch.Generator().manual_seed(V))
+    scores, tokens, parents, status = on_cpu.select(program, x, np.zeros(K), beam, splits=splits,
+                                                    plant=on_cpu.NO_MINIMUM)
+    assert status == N.RNNT_LAUNCH_FAILED
+    assert (scores == -np.inf).all() and (tokens == -1).all() and (parents == -1).all()
