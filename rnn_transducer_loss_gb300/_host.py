@@ -7,6 +7,7 @@ only to say what is wrong.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native as N
 
@@ -14,6 +15,12 @@ DTYPES = {torch.float32: N.RNNT_F32, torch.float16: N.RNNT_F16, torch.bfloat16: 
 
 current_device = torch._C._cuda_getDevice
 stream_of = torch._C._cuda_getCurrentRawStream      # of a device index, as an integer
+
+
+def differentiated(t):
+    """Whether autograd has to see a call on t: for its backward pass, or, where a forward-mode
+    level is open, for the error that a tangent meets (a call past autograd would drop it)."""
+    return t.requires_grad and torch.is_grad_enabled() or forward_ad._current_level >= 0
 
 
 def int32(name, t, device):

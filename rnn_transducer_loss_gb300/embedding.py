@@ -13,7 +13,7 @@ import torch
 
 from . import _native as N
 from ._host import DTYPES as _DT
-from ._host import call, finish, int32, status_word
+from ._host import call, differentiated, finish, int32, status_word
 
 _INT32 = torch.int32
 _WANTED = "tokens below the vocabulary size, lengths in [0, tokens.shape[1]]"
@@ -123,7 +123,7 @@ class _Embed(torch.autograd.Function):
         tokens, lengths = ctx.saved_tensors
         V, start, scale = ctx.args
         # what the device could object to, it objected to in the forward call
-        if grad_out.requires_grad and torch.is_grad_enabled():
+        if differentiated(grad_out):
             grad = _EmbedGrad.apply(grad_out, tokens, V, lengths, start, scale, False)
         else:
             grad = _gradient(grad_out, tokens, V, lengths, start, scale, False)
@@ -162,8 +162,9 @@ def rnnt_embed(weight: torch.Tensor, tokens: torch.Tensor, lengths: torch.Tensor
     is padding and such a length the nearer bound.  A backward pass is captured
     into a CUDA graph with ``check=False`` and with no eager graph of the same
     weight alive (autograd would make the capture wait for that one's stream).
+    Forward-mode derivatives raise.
     """
-    if weight.requires_grad and torch.is_grad_enabled():
+    if differentiated(weight):
         return _Embed.apply(weight, tokens, lengths, start, float(scale), check)
     return _forward(weight, tokens, lengths, start, float(scale), check)
 
@@ -177,9 +178,9 @@ def rnnt_embed_grad(grad_out: torch.Tensor, tokens: torch.Tensor, num_embeddings
     Rows of ids that do not occur are zero; ``grad_out`` at padding is not read.
     The places are sorted by id and added in float32 in an order that depends on
     the tokens alone: the same inputs give the same bits.  Differentiable with
-    respect to ``grad_out``.
+    respect to ``grad_out`` (in backward mode; forward-mode derivatives raise).
     """
-    if grad_out.requires_grad and torch.is_grad_enabled():
+    if differentiated(grad_out):
         return _EmbedGrad.apply(grad_out, tokens, int(num_embeddings), lengths, start,
                                 float(scale), check)
     return _gradient(grad_out, tokens, int(num_embeddings), lengths, start, float(scale), check)
