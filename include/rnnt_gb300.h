@@ -413,8 +413,9 @@ rnnt_status_t rnnt_embed_grad(const void *grad_out, rnnt_dtype_t dt, const int32
 #define RNNT_MAX_BEAM 64
 #define RNNT_MAX_BEAM_VOCAB (1 << 20)
 
-/* rnnt_beam_workspace_size -- bytes of device scratch of rnnt_beam_select; 0 for
- * up to 16 hypotheses with rows of up to 32 KB. */
+/* rnnt_beam_workspace_size -- bytes of device scratch of rnnt_beam_select on the
+ * current device; with rows of up to 32 KB, 0 for up to 8 hypotheses, and for
+ * up to 16 where the device runs clusters of 16 thread blocks (a GB300 does). */
 rnnt_status_t rnnt_beam_workspace_size(int32_t B, int32_t K, int32_t V, int32_t Ko,
                                        rnnt_dtype_t dt, size_t *bytes);
 

@@ -267,8 +267,8 @@ def rnnt_embed_grad(grad_out, dt, tokens, tokens_stride, lengths, B, S, has_star
                                   status_dev, stream)
 
 
-@functools.lru_cache(maxsize=256)
 def rnnt_beam_workspace_size(B, K, V, Ko, dt) -> int:
+    """Of the current device."""
     out = ctypes.c_size_t(0)
     rc = load().rnnt_beam_workspace_size(B, K, V, Ko, dt, ctypes.byref(out))
     if rc != RNNT_OK:

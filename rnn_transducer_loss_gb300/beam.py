@@ -14,6 +14,12 @@ from ._host import call, finish, int32, status_word
 _F32, _I32 = torch.float32, torch.int32
 
 
+@lru_cache(maxsize=256)
+def _workspace_size(B, K, V, beam, dt, index):
+    with torch.cuda.device(index):
+        return N.rnnt_beam_workspace_size(B, K, V, beam, dt)
+
+
 def rnnt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beam: int | None = None,
                      finished: torch.Tensor | None = None, fused_log_softmax: bool = True,
                      check: bool = True):
@@ -71,7 +77,7 @@ def rnnt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beam: int | Non
     if V > 1 and step != 1:
         logits = logits.contiguous()
         item, row, step = logits.stride()
-    nbytes = N.rnnt_beam_workspace_size(B, K, V, beam, dt)
+    nbytes = _workspace_size(B, K, V, beam, dt, device.index)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     status = status_word(device) if check else None
     call("rnnt_beam_select", device, N.load().rnnt_beam_select, logits.data_ptr(), dt, B, K, V,

@@ -46,7 +46,8 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 constexpr int kRowThreads = 128;           // of k_rows: 8 CTAs an SM hold 1024 rows at once (256
                                            // threads, 4 CTAs: a second wave, 32 against 28 us)
 constexpr int kClusterThreads = 128;       // of k_search
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 16;            // where the device runs clusters of so many blocks
+constexpr int kAnyCluster = 8;             // which every device runs
 constexpr int kClusterBytes = 32 << 10;    // of a row that a CTA of a cluster takes, at most
 constexpr float kLog2e = 1.44269504f;      // log2 e to 2^-26
 constexpr float kRescale = 16.0f;
@@ -1043,7 +1044,8 @@ struct SelectLayout {
     int32_t splits, split_vecs, n;
     int32_t cluster;                       // CTAs of an item's cluster, or 0: two launches
 };
-SelectLayout select_layout(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt) {
+// `widest`: the blocks of the largest cluster that the device runs.
+SelectLayout select_layout(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt, int widest) {
     SelectLayout L{};
     const int es = elem_size(dt), E = 16 / es;
     const int64_t vecs = std::max(1, V / E);                 // the most, whatever the alignment
@@ -1055,7 +1057,7 @@ SelectLayout select_layout(int32_t B, int32_t K, int32_t V, int32_t Ko, int dt) 
     // float16: 9.9 and 13.2 us against 9.7 and 14.1), and the one launch without a workspace
     // costs the host 5 us less; long rows (of 50000: 15.3 and 19.5 against 9.5 and 15.4) are
     // faster split, and their exact sums by k_pick's larger block.
-    if (K <= kMaxCluster && (int64_t)V * es <= kClusterBytes) {
+    if (K <= widest && (int64_t)V * es <= kClusterBytes) {
         L.cluster = K;
         return L;
     }
@@ -1143,6 +1145,50 @@ bool select_prepared() {
     if (ok) done[dev].store(true, std::memory_order_release);
     else cudaGetLastError();
     return ok;
+}
+
+// Blocks of the largest cluster that each of k_search's forms gets on the current device: 16, or
+// 8 where some does not fit (a part of a device, say) and where there is no device to ask. Asked
+// once per device, and only where K and V leave it open.
+template <typename T>
+bool widest_fits() {
+    const auto fits = [](auto kernel) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(kMaxCluster);
+        cfg.blockDim = dim3(kClusterThreads);
+        cfg.dynamicSmemBytes =
+            sizeof(ClusterShared<4>) + 2 * sizeof(uint64_t) * kMaxCluster * RNNT_MAX_BEAM;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kMaxCluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+    };
+    return fits(k_search<T, 1, true>) && fits(k_search<T, 1, false>) &&
+           fits(k_search<T, 2, true>) && fits(k_search<T, 2, false>) &&
+           fits(k_search<T, 4, true>) && fits(k_search<T, 4, false>);
+}
+int widest_cluster(int32_t K, int32_t V, int dt) {
+    if (K <= kAnyCluster || K > kMaxCluster || (int64_t)V * elem_size(dt) > kClusterBytes)
+        return kAnyCluster;
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices || !select_prepared()) {
+        cudaGetLastError();
+        return kAnyCluster;
+    }
+    int v = known[dev].load(std::memory_order_acquire);
+    if (!v) {
+        v = widest_fits<float>() && widest_fits<__half>() && widest_fits<__nv_bfloat16>()
+                ? kMaxCluster : kAnyCluster;
+        cudaGetLastError();
+        known[dev].store(v, std::memory_order_release);
+    }
+    return v;
 }
 
 // ------------------------------------------------------------------ reorder
@@ -1249,7 +1295,7 @@ uint64_t extent(const rnnt_state_t& s, const int64_t* stride, int64_t batch, int
 extern "C" rnnt_status_t rnnt_beam_workspace_size(int32_t B, int32_t K, int32_t V, int32_t Ko,
                                                   rnnt_dtype_t dt, size_t* bytes) {
     if (!bytes || !select_ok(B, K, V, Ko, dt)) return RNNT_INVALID_VALUE;
-    *bytes = select_layout(B, K, V, Ko, dt).total;
+    *bytes = select_layout(B, K, V, Ko, dt, widest_cluster(K, V, dt)).total;
     return RNNT_OK;
 }
 
@@ -1265,7 +1311,7 @@ extern "C" rnnt_status_t rnnt_beam_select(const void* logits, rnnt_dtype_t dt, i
         return RNNT_INVALID_VALUE;
     const int es = elem_size(dt);
     if (((uintptr_t)logits & (es - 1)) || ((uintptr_t)workspace & 255)) return RNNT_INVALID_VALUE;
-    const SelectLayout L = select_layout(B, K, V, Ko, dt);
+    const SelectLayout L = select_layout(B, K, V, Ko, dt, widest_cluster(K, V, dt));
     if (L.total && !workspace) return RNNT_INVALID_VALUE;
     if (workspace_bytes < L.total) return RNNT_WORKSPACE_TOO_SMALL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -49,7 +49,8 @@ def build(folder):
 
 def select(program, logits, scores, beam, finished=None, fused=True, splits=0, skip=0, plant=None):
     """(scores, tokens, parents, status) of one item: logits (K, V) of a torch type, scores (K,).
-    `splits`: of a row in the two-launch kernels, 0 for what the host chooses; `skip`: elements
+    `splits`: of a row in the two-launch kernels, 0 for what the host
+    chooses, -1 for what it does where no cluster has more than 8 blocks; `skip`: elements
     between a 16-byte boundary and the first row."""
     K, V = logits.shape
     dt = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}[logits.dtype]

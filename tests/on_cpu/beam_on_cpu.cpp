@@ -1,8 +1,8 @@
 // The selection's kernels, compiled from their source for the CPU (device.inc, cut out of
 // rnnt_beam.cu), on cases read from standard input: int32 header {dtype, K, V, Ko, fused, splits
-// (0: as the host chooses), skip, finished given, no minimum}, float scores[K], uint8 finished[K],
-// `skip` elements and the K * V logits.  Writes int32 {status, found a way out}, float scores[Ko],
-// int32 tokens[Ko], parents[Ko].
+// (0: as the host chooses, -1: as it does where the largest cluster has 8 blocks), skip, finished
+// given, no minimum}, float scores[K], uint8 finished[K], `skip` elements and the K * V logits.
+// Writes int32 {status, found a way out}, float scores[Ko], int32 tokens[Ko], parents[Ko].
 #include "cuda_on_cpu.h"
 
 #include "rnnt_gb300.h"
@@ -46,8 +46,9 @@ int main() {
             fread(finished.data(), 1, K, stdin) != (size_t)K ||
             fread(logits, 1, bytes, stdin) != bytes)
             return 2;
-        SelectLayout L = select_layout(1, K, V, Ko, dt);
-        if (splits) {
+        SelectLayout L =
+            select_layout(1, K, V, Ko, dt, splits < 0 ? kAnyCluster : kMaxCluster);
+        if (splits > 0) {
             const int vecs = std::max(1, V / (16 / (int)es));
             L.cluster = 0;
             L.split_vecs = (vecs + splits - 1) / splits;

@@ -85,3 +85,15 @@ def test_selection_without_a_winner(program, K, V, beam, splits):
                                                     plant=on_cpu.NO_MINIMUM)
     assert status == N.RNNT_LAUNCH_FAILED
     assert (scores == -np.inf).all() and (tokens == -1).all() and (parents == -1).all()
+
+
+@pytest.mark.parametrize("K", [8, 9, 16])
+def test_without_large_clusters(program, K):
+    """The two launches in the place of a cluster of more than 8 blocks: the same results."""
+    x = torch.randn(K, 301, generator=torch.Generator().manual_seed(K))
+    x[1] = x[0]
+    scores = np.repeat(-np.arange(K // 2 + 1), 2)[:K]
+    check(program, x, scores, 11, splits=-1)
+    for a, b in zip(on_cpu.select(program, x, scores, 11, splits=-1),
+                    on_cpu.select(program, x, scores, 11)):
+        np.testing.assert_array_equal(a, b)
