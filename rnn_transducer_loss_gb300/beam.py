@@ -65,6 +65,8 @@ def rnnt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beam: int | Non
                 or finished.device != device:
             raise ValueError(f"finished must be bool or uint8 ({B}, {K}) on {device}")
         finished = finished.contiguous()
+    if logits.is_neg() or scores.is_neg():  # their memory holds the negatives
+        logits, scores = logits.resolve_neg(), scores.resolve_neg()
     scores = scores.contiguous()
     # three allocations: the code of the second and third is in the caches, while that of the views
     # that would share one is not (7 us instead of 11)

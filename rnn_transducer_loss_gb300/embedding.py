@@ -64,6 +64,8 @@ def _forward(weight, tokens, lengths, start, scale, check):
     out = torch.empty((B, S + has, D), dtype=weight.dtype, device=device)
     if not B or not S + has:
         return out
+    if weight.is_neg():                     # its memory holds the negatives
+        weight = weight.resolve_neg()
     wrow, step = weight.stride()
     if D > 1 and step != 1 or V > 1 and wrow < D:
         weight, wrow = weight.contiguous(), D
@@ -95,6 +97,8 @@ def _gradient(grad_out, tokens, V, lengths, start, scale, check):
     D = grad_out.shape[2]
     if not B or not S + has or not D:
         return torch.zeros((V, D), dtype=grad_out.dtype, device=device)
+    if grad_out.is_neg():                   # its memory holds the negatives
+        grad_out = grad_out.resolve_neg()
     grad_out = grad_out.contiguous()
     if lengths is not None:
         lengths = lengths.contiguous()
