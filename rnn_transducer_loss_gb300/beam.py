@@ -176,7 +176,7 @@ def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, chec
     batch_dim 1).  ``parents`` (B, K') int32 is what
     :func:`rnnt_beam_select` returned; the results have K' in the place of K,
     and zeros where the parent is -1.  ``out`` gives tensors to write to (they
-    must not share memory with ``states``: keep two sets and swap them);
+    must not share memory with ``states`` or one another: keep two sets and swap them);
     without it the results are new contiguous tensors.  Views are read with
     their strides: the filled part of a cache need not be copied out first.
     ``check`` reads the device status word (one synchronisation) and raises on
@@ -240,6 +240,8 @@ def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, chec
         part = rows[i:i + N.MAX_STATES]
         call("rnnt_beam_reorder", device, N.load().rnnt_beam_reorder, b"".join(part), len(part),
              parents.data_ptr(), B, K, Ko, None if status is None or i else status.data_ptr())
+    if out is not None:                     # what autograd saved of them is no longer so
+        torch.autograd.graph.increment_version([y for y in results if not y.is_inference()])
     if status is not None:
         finish("rnnt_beam_reorder", status, f"parents in [-1, {K})")
     return results
