@@ -244,13 +244,6 @@ def rnnt_plan(B, rows, V, dt, targets_stride, fused_log_softmax, want_grad=True,
     return {"persistent": bool(plan.persistent), "launches": int(plan.launches)}
 
 
-def rnnt_embed(weight, dt, V, D, weight_stride, tokens, tokens_stride, lengths, B, S, has_start,
-               start, scale, out, status_dev, stream) -> int:
-    """Raw call; pointer arguments are integers (device addresses) or None."""
-    return load().rnnt_embed(weight, dt, V, D, weight_stride, tokens, tokens_stride, lengths, B, S,
-                             has_start, start, scale, out, status_dev, stream)
-
-
 @functools.lru_cache(maxsize=256)          # by the sizes alone
 def rnnt_embed_grad_workspace_size(B, S, has_start, V, D) -> int:
     out = ctypes.c_size_t(0)
@@ -258,13 +251,6 @@ def rnnt_embed_grad_workspace_size(B, S, has_start, V, D) -> int:
     if rc != RNNT_OK:
         raise RNNTError(rc, "rnnt_embed_grad_workspace_size")
     return out.value
-
-
-def rnnt_embed_grad(grad_out, dt, tokens, tokens_stride, lengths, B, S, has_start, start, V, D,
-                    scale, grad_weight, workspace, workspace_bytes, status_dev, stream) -> int:
-    return load().rnnt_embed_grad(grad_out, dt, tokens, tokens_stride, lengths, B, S, has_start,
-                                  start, V, D, scale, grad_weight, workspace, workspace_bytes,
-                                  status_dev, stream)
 
 
 def rnnt_beam_workspace_size(B, K, V, Ko, dt) -> int:
@@ -276,14 +262,10 @@ def rnnt_beam_workspace_size(B, K, V, Ko, dt) -> int:
     return out.value
 
 
-def rnnt_beam_select(logits, dt, B, K, V, batch_stride, beam_stride, scores, finished, Ko,
-                     fused_log_softmax, out_scores, out_tokens, out_parents, workspace,
-                     workspace_bytes, status_dev, stream) -> int:
-    return load().rnnt_beam_select(logits, dt, B, K, V, batch_stride, beam_stride, scores, finished,
-                                   Ko, fused_log_softmax, out_scores, out_tokens, out_parents,
-                                   workspace, workspace_bytes, status_dev, stream)
-
-
-def rnnt_beam_reorder(states, n_states, parents, B, K, Ko, status_dev, stream) -> int:
-    """states: a ctypes array of State (host memory)."""
-    return load().rnnt_beam_reorder(states, n_states, parents, B, K, Ko, status_dev, stream)
+def __getattr__(name):
+    """rnnt_embed, rnnt_embed_grad, rnnt_beam_select, rnnt_beam_reorder: the library's own functions,
+    with its arguments in its order (pointers as integers or None) and a status code as result."""
+    if name in ("rnnt_embed", "rnnt_embed_grad", "rnnt_beam_select", "rnnt_beam_reorder"):
+        fn = globals()[name] = getattr(load(), name)
+        return fn
+    raise AttributeError(name)

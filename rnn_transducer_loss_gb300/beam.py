@@ -82,7 +82,7 @@ def rnnt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beam: int | Non
     nbytes = _workspace_size(B, K, V, beam, dt, device.index)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     status = status_word(device) if check else None
-    call("rnnt_beam_select", device, N.load().rnnt_beam_select, logits.data_ptr(), dt, B, K, V,
+    call("rnnt_beam_select", device, N.rnnt_beam_select, logits.data_ptr(), dt, B, K, V,
          item, row, scores.data_ptr(), None if finished is None else finished.data_ptr(), beam,
          1 if fused_log_softmax else 0, out_scores.data_ptr(), tokens.data_ptr(),
          parents.data_ptr(), ws.data_ptr() if nbytes else None, nbytes,
@@ -238,7 +238,7 @@ def rnnt_beam_reorder(states, parents: torch.Tensor, batch_dim=0, out=None, chec
     status = status_word(device) if check else None
     for i in range(0, len(rows), N.MAX_STATES):
         part = rows[i:i + N.MAX_STATES]
-        call("rnnt_beam_reorder", device, N.load().rnnt_beam_reorder, b"".join(part), len(part),
+        call("rnnt_beam_reorder", device, N.rnnt_beam_reorder, b"".join(part), len(part),
              parents.data_ptr(), B, K, Ko, None if status is None or i else status.data_ptr())
     if out is not None:                     # what autograd saved of them is no longer so
         torch.autograd.graph.increment_version([y for y in results if not y.is_inference()])

@@ -72,7 +72,7 @@ def _forward(weight, tokens, lengths, start, scale, check):
     if lengths is not None:
         lengths = lengths.contiguous()
     status = status_word(device) if check else None
-    call("rnnt_embed", device, N.load().rnnt_embed, weight.data_ptr(), dt, V, D,
+    call("rnnt_embed", device, N.rnnt_embed, weight.data_ptr(), dt, V, D,
          wrow if wrow > D else D, tokens.data_ptr(), row,
          None if lengths is None else lengths.data_ptr(), B, S, has, first, scale, out.data_ptr(),
          None if status is None else status.data_ptr())
@@ -106,7 +106,7 @@ def _gradient(grad_out, tokens, V, lengths, start, scale, check):
     nbytes = N.rnnt_embed_grad_workspace_size(B, S, has, V, D)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     status = status_word(device) if check else None
-    call("rnnt_embed_grad", device, N.load().rnnt_embed_grad, grad_out.data_ptr(), dt,
+    call("rnnt_embed_grad", device, N.rnnt_embed_grad, grad_out.data_ptr(), dt,
          tokens.data_ptr(), row, None if lengths is None else lengths.data_ptr(), B, S, has, first,
          V, D, scale, grad.data_ptr(), ws.data_ptr() if nbytes else None, nbytes,
          None if status is None else status.data_ptr())

@@ -34,3 +34,12 @@ def test_workspace_without_large_clusters(K):
 def test_workspace(K, wanted):
     """On the whole device clusters of 16 blocks run."""
     assert (N.rnnt_beam_workspace_size(2, K, 30, 4, N.RNNT_F32) > 0) == wanted
+
+
+@pytest.mark.parametrize("name", ["rnnt_embed", "rnnt_embed_grad", "rnnt_beam_select",
+                                  "rnnt_beam_reorder"])
+def test_entry_points_are_the_library_s(name):
+    """What the package calls, and the tests of refusals with it, is the library's function itself."""
+    assert getattr(N, name) is getattr(N.load(), name)
+    with pytest.raises(AttributeError):
+        N.rnnt_no_such_name
