@@ -449,8 +449,8 @@ rnnt_status_t rnnt_beam_workspace_size(int32_t B, int32_t K, int32_t V, int32_t 
  *   status_dev     RNNT_INVALID_VALUE for a score of +inf or NaN, or a
  *                  hypothesis whose logits hold one; such a hypothesis offers
  *                  nothing.  RNNT_LAUNCH_FAILED for a selection that lost its
- *                  order on the device (none is known to): its remaining
- *                  places are left over.
+ *                  order on the device (none is known to): all its places
+ *                  are left over.
  */
 rnnt_status_t rnnt_beam_select(const void *logits, rnnt_dtype_t dt, int32_t B, int32_t K, int32_t V,
                                int64_t batch_stride, int64_t beam_stride, const float *scores,

@@ -856,6 +856,7 @@ __device__ __forceinline__ void choose(const SelectParams& p, const uint64_t* li
             head[q] = i < nlists ? values[i * p.n] : 0;
         }
         int found = 0;
+        bool lost = false;                         // the same for the whole warp
         for (; found < p.Ko; ++found) {
             uint64_t v = head[0];
             int q0 = 0;
@@ -874,12 +875,10 @@ __device__ __forceinline__ void choose(const SelectParams& p, const uint64_t* li
             const uint32_t list = __reduce_min_sync(
                 0xffffffffu, v == ((uint64_t)hi << 32 | lo) ? (uint32_t)(q0 * 32 + lane)
                                                             : 0xffffffffu);
-            // No lane's, which cannot be: the same for the whole warp, and nothing is indexed by it.
-            if (list >= (uint32_t)nlists) {
-                if (lane == 0 && p.status) *p.status = RNNT_LAUNCH_FAILED;
-                break;
-            }
-            if ((list & 31) == lane) {
+            // No lane's, which cannot be: nothing is indexed by it, and no result stays.
+            const bool some = list < (uint32_t)nlists;
+            lost |= !some;
+            if (some && (list & 31) == lane) {
                 sh.oval[found] = v;
                 sh.oid[found] = list << 8 | sel(at, q0);
 #pragma unroll
@@ -890,6 +889,10 @@ __device__ __forceinline__ void choose(const SelectParams& p, const uint64_t* li
                     }
             }
             __syncwarp();
+        }
+        if (lost) {
+            found = 0;
+            if (lane == 0 && p.status) *p.status = RNNT_LAUNCH_FAILED;
         }
         __syncwarp();
         for (int r = lane; r < found; r += 32) sh.obeam[r] = (uint8_t)((sh.oid[r] >> 8) / p.splits);
@@ -985,9 +988,9 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(const SelectParams p) {
 // A cluster takes a batch item: each CTA streams a row and leaves its list and statistics in the
 // first CTA's shared memory, which picks; where that wants exact log-sum-exps, each CTA
 // computes its own row's.  One launch and no workspace.  Latency bounds it, a chain of the row's
-// barriers, two cluster barriers and one maximum of the heads a selected hypothesis: 8.2 us in a
-// graph for 1 x 4 x 1024 float16, 10.5 for 32 x 10 x 29 float32, 8.0 for 16 x 8 x 5000 float32
-// log-probabilities (two launches: 3 us more for the last, and 5 us more of the host's time).
+// barriers, two cluster barriers and one maximum of the heads a selected hypothesis: 7.9 to 8.3 us
+// in a graph for 1 x 4 x 1024 float16 (from one GPU to another), 10.6 for 32 x 10 x 29 float32, 8.0
+// for 16 x 8 x 5000 float32 log-probabilities (two launches: 3 us more for the last, and 5 us more of the host's time).
 template <int NV>
 struct ClusterShared {
     union {

@@ -40,14 +40,14 @@ __device__ __forceinline__ void place_ids(const Places& p, const uint32_t* place
         b[i] = place[i] / P;
         j[i] = (int)(place[i] - b[i] * P) - p.first;
         n[i] = p.S;
-        // the start symbol's too: where S = 0 no other place sees a length
-        if (p.lengths && place[i] < end) n[i] = __ldg(p.lengths + b[i]);
+        // where S = 0 no place but the start symbol's sees a length
+        if (p.lengths && place[i] < end && (j[i] >= 0 || p.S == 0)) n[i] = __ldg(p.lengths + b[i]);
     }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
         bad |= n[i] < 0 || n[i] > p.S;
         id[i] = -1;
-        if (place[i] < end && (j[i] < 0 || j[i] < min(n[i], p.S)))
+        if (place[i] < end && j[i] < min(max(n[i], 0), p.S))
             id[i] = j[i] < 0 ? p.start : __ldg(p.tokens + (int64_t)b[i] * p.stride + j[i]);
     }
 #pragma unroll
