@@ -137,9 +137,9 @@ __device__ __forceinline__ Pair add_loosely(Pair a, Pair b) {
 __device__ __forceinline__ uint64_t ordered(Pair a) {
     return (uint64_t)ordered(a.h) << 32 | ordered(a.l);
 }
-// The order of sums that float32 does not reach, given a quarter of each, |a| <= 3 2^126: as
-// different (their differences in more than 2^-50 of the value) as those of finite values, and in
-// keys that these leave: of bits that read as NaN.  Never 0.
+// Keys of values beyond float32's range, in their order and outside the keys of finite values, from a
+// quarter of each (2^126 <= |a| <= 3 2^126).  They take the patterns that read as NaN, of which there
+// are half as many as such pairs: the last bit goes, of about 47.  Never 0.
 constexpr float kMost = 3.40282347e38f;                // the largest float32
 constexpr uint32_t kOrderedMost = 0xff7fffffu, kOrderedLeast = 0x00800000u;   // of kMost, -kMost
 __device__ __forceinline__ uint64_t ordered_beyond(Pair a) {
