@@ -494,6 +494,112 @@ rnnt_status_t rnnt_beam_reorder(const rnnt_state_t *states, int32_t n_states,
                                 const int32_t *parents, int32_t B, int32_t K, int32_t Ko,
                                 int32_t *status_dev, rnnt_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Learning from a teacher: the top logits of a teacher's lattice rows, the loss
+ * of a student against them.  No counterpart on the pages.  What is said of the
+ * label side above holds here as well.
+ */
+
+/* Most outputs kept of a teacher's row, and the largest vocabulary, of these operators. */
+#define RNNT_MAX_TOP 64
+#define RNNT_MAX_TOP_VOCAB (1 << 20)
+
+/*
+ * rnnt_top_logits -- of every row of V logits x the k largest with their ids, and
+ * what remains.
+ *
+ *   values[r], ids[r]   the k largest logits above -inf in descending order, equal
+ *                       ones by id; places left over get -inf and id -1.
+ *   rest[r]             log sum exp(x_j / temperature) over the outputs without a
+ *                       place; -inf where there is none.  A finite value below
+                       float32's range is its lowest.
+ *
+ *   logits         (rows, V) contiguous in dt.
+ *   logit_lengths, target_lengths
+ *                  int32 [B], or both NULL: every row counts.  With lengths the
+ *                  rows are those of the padded (B, max_T, max_U + 1, V) layout;
+ *                  a row outside its sequence is not read, and all its places
+ *                  are left over.  B, max_T and max_U are ignored without.
+ *   values         (rows, k) in dt;  ids int32 (rows, k);  rest float (rows).
+ *                  They must not overlap logits or one another.
+ *   status_dev     RNNT_INVALID_VALUE for a row that holds NaN or +inf (all its
+ *                  places are left over), or lengths outside the layout (taken
+ *                  as the nearer bound).
+ * 1 <= k <= min(V, RNNT_MAX_TOP), V <= RNNT_MAX_TOP_VOCAB, 1e-4 <= temperature <= 1e4.
+ */
+rnnt_status_t rnnt_top_logits(const void *logits, rnnt_dtype_t dt, int64_t rows, int32_t V,
+                              const int32_t *logit_lengths, const int32_t *target_lengths,
+                              int32_t B, int32_t max_T, int32_t max_U, int32_t k,
+                              double temperature, void *values, int32_t *ids, float *rest,
+                              int32_t *status_dev, rnnt_stream_t stream);
+
+/* rnnt_distill_workspace_size -- bytes of device scratch of rnnt_distill_loss: 4 per row
+ * and 16 per sample. */
+rnnt_status_t rnnt_distill_workspace_size(int32_t B, int64_t rows, size_t *bytes);
+
+/*
+ * rnnt_distill_loss -- the divergence of a student's lattice rows from a teacher's,
+ * summed over the rows of each sample, and its gradient.
+ *
+ * A row's teacher has up to k places, each a logit and the id of its output, and
+ * optionally a rest, the log-sum-exp of its remaining logits over the temperature
+ * tau.  p is the softmax over the places' logits / tau and the rest; q is the
+ * softmax of the student's logits x / tau, q_r its sum over the outputs without
+ * a place.
+ *
+ *   row      tau^2 * [ sum_k p_k log(p_k / q_id(k)) + p_r log(p_r / q_r) ], terms of
+ *            p = 0 being 0
+ *   loss[b]  weight * the sum over sample b's T_b * (U_b + 1) rows
+ *   grad     d loss_reduced / d x (of the sum for RNNT_RED_NONE): per row weight * tau
+ *            (/ B for the mean) times q_j - p_j for an output with a place, q_j (1 - p_r / q_r)
+ *            for another, q_j without a rest
+ *
+ * A row whose teacher holds nothing (no place above -inf, no rest above -inf) has loss 0
+ * and gradient 0, whatever its logits are.
+ *
+ *   logits         (rows, V) contiguous in dt, 16-byte aligned: the compact layout of
+ *                  rnnt_loss_fused, or the padded one, (B, max_T, max_U + 1, V), whose
+ *                  other rows are not read and get gradient 0.
+ *   teacher_logits (rows, k) in teacher_dt;  teacher_ids int32 (rows, k), a negative id
+ *                  being an empty place;  teacher_rest float (rows), or NULL: p is the
+ *                  softmax over the places alone.
+ *   logit_lengths, target_lengths   int32 [B], T_b >= 0, U_b >= 0.
+ *   loss           float [B];  loss_reduced float [1] or NULL: sum (SUM, NONE) or mean (MEAN).
+ *   grad           (rows, V) contiguous in dt, 16-byte aligned, or NULL: loss only.
+ *   workspace      rnnt_distill_workspace_size() bytes, 256-byte aligned.
+ *                  No output may overlap an input.
+ *   status_dev     RNNT_INVALID_VALUE for lengths out of range (taken as the nearer bound) or,
+ *                  in the compact layout, not adding up to rows (rows behind the last sample
+ *                  get gradient 0); an id >= V (its place counts as empty), an id twice in
+ *                  a row (the later places count as empty), a teacher's logit or rest that
+ *                  is NaN or +inf; logits that are NaN or +inf, or all -inf, in a row with a
+ *                  teacher (its loss and gradient are then NaN).
+ * 1 <= k <= RNNT_MAX_TOP, V <= RNNT_MAX_TOP_VOCAB, 1e-4 <= temperature <= 1e4, |weight| < 1e30.
+ */
+rnnt_status_t rnnt_distill_loss(const void *logits, rnnt_dtype_t dt, int64_t rows, int32_t V,
+                                const void *teacher_logits, rnnt_dtype_t teacher_dt,
+                                const int32_t *teacher_ids, const float *teacher_rest, int32_t k,
+                                const int32_t *logit_lengths, const int32_t *target_lengths,
+                                int32_t B, int32_t padded, int32_t max_T, int32_t max_U,
+                                double temperature, double weight, rnnt_reduction_t reduction,
+                                float *loss, float *loss_reduced, void *grad, void *workspace,
+                                size_t workspace_bytes, int32_t *status_dev,
+                                rnnt_stream_t stream);
+
+/*
+ * rnnt_distill_grad_scale -- multiplies a gradient of rnnt_distill_loss in place by upstream
+ * factors: factors[0], or with per_sample != 0 factors[b] for sample b's rows.  A
+ * factor of 1 leaves its rows as they are.
+ *
+ *   rows_each      rows of a sample of the padded layout, max_T * (max_U + 1); 0 for the
+ *                  compact one.
+ *   workspace      the one that the rnnt_distill_loss call used, unchanged since.
+ */
+rnnt_status_t rnnt_distill_grad_scale(void *grad, rnnt_dtype_t dt, int64_t rows, int32_t V,
+                                      int32_t B, int64_t rows_each, const void *workspace,
+                                      size_t workspace_bytes, const float *factors,
+                                      int32_t per_sample, rnnt_stream_t stream);
+
 /* Static English description of a status code. */
 const char *rnnt_status_string(rnnt_status_t status);
 

@@ -26,7 +26,8 @@ EXPORTS = ("rnnt_workspace_size", "rnnt_workspace_size_ex", "rnnt_loss_fused", "
            "rnnt_loss_fused_noalloc", "rnnt_selftest_wait_timeout", "rnnt_status_string",
            "rnnt_abi_version", "rnnt_plan", "rnnt_embed", "rnnt_embed_grad_workspace_size",
            "rnnt_embed_grad", "rnnt_beam_workspace_size", "rnnt_beam_select",
-           "rnnt_beam_reorder")
+           "rnnt_beam_reorder", "rnnt_top_logits", "rnnt_distill_workspace_size",
+           "rnnt_distill_loss", "rnnt_distill_grad_scale")
 
 
 MAX_BIG_BLANKS = 8                    # RNNT_MAX_BIG_BLANKS
@@ -66,6 +67,8 @@ class Plan(ctypes.Structure):
 MAX_BEAM = 64                         # RNNT_MAX_BEAM
 MAX_BEAM_VOCAB = 1 << 20              # RNNT_MAX_BEAM_VOCAB
 MAX_STATES = 16                       # RNNT_MAX_STATES
+MAX_TOP = 64                          # RNNT_MAX_TOP
+MAX_TOP_VOCAB = 1 << 20               # RNNT_MAX_TOP_VOCAB
 
 
 class State(ctypes.Structure):
@@ -138,6 +141,16 @@ def load() -> ctypes.CDLL:
     lib.rnnt_beam_select.restype = i32
     lib.rnnt_beam_reorder.argtypes = [P, i32, P, i32, i32, i32, P, P]
     lib.rnnt_beam_reorder.restype = i32
+    f64 = ctypes.c_double
+    lib.rnnt_top_logits.argtypes = [P, i32, i64, i32, P, P, i32, i32, i32, i32, f64, P, P, P, P, P]
+    lib.rnnt_top_logits.restype = i32
+    lib.rnnt_distill_workspace_size.argtypes = [i32, i64, ctypes.POINTER(sz)]
+    lib.rnnt_distill_workspace_size.restype = i32
+    lib.rnnt_distill_loss.argtypes = [P, i32, i64, i32, P, i32, P, P, i32, P, P, i32, i32, i32, i32,
+                                      f64, f64, i32, P, P, P, P, sz, P, P]
+    lib.rnnt_distill_loss.restype = i32
+    lib.rnnt_distill_grad_scale.argtypes = [P, i32, i64, i32, i32, i64, P, sz, P, i32, P]
+    lib.rnnt_distill_grad_scale.restype = i32
     _lib = lib
     return lib
 
@@ -262,10 +275,23 @@ def rnnt_beam_workspace_size(B, K, V, Ko, dt) -> int:
     return out.value
 
 
+@functools.lru_cache(maxsize=256)          # by the sizes alone
+def rnnt_distill_workspace_size(B, rows) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().rnnt_distill_workspace_size(B, rows, ctypes.byref(out))
+    if rc != RNNT_OK:
+        raise RNNTError(rc, "rnnt_distill_workspace_size")
+    return out.value
+
+
+# The library's own functions, with its arguments in its order (pointers as integers or None) and a
+# status code as result.
+_DIRECT = ("rnnt_embed", "rnnt_embed_grad", "rnnt_beam_select", "rnnt_beam_reorder",
+           "rnnt_top_logits", "rnnt_distill_loss", "rnnt_distill_grad_scale")
+
+
 def __getattr__(name):
-    """rnnt_embed, rnnt_embed_grad, rnnt_beam_select, rnnt_beam_reorder: the library's own functions,
-    with its arguments in its order (pointers as integers or None) and a status code as result."""
-    if name in ("rnnt_embed", "rnnt_embed_grad", "rnnt_beam_select", "rnnt_beam_reorder"):
+    if name in _DIRECT:
         fn = globals()[name] = getattr(load(), name)
         return fn
     raise AttributeError(name)

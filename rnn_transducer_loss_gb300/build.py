@@ -1,5 +1,5 @@
 """Build librnnt_gb300.so in-tree with nvcc for sm_103a (no CMake; one translation unit for
-the loss and one for each pair of label-side operators, compiled side by side)."""
+the loss and one for each pair of operators around it, compiled side by side)."""
 from __future__ import annotations
 
 import os
@@ -10,8 +10,9 @@ import time
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SRCS = [os.path.join(CSRC, f) for f in ("rnnt_gb300.cu", "rnnt_embed.cu", "rnnt_beam.cu")]
-DEPS = [os.path.join(CSRC, "rnnt_labels.cuh")]
+SRCS = [os.path.join(CSRC, f) for f in ("rnnt_gb300.cu", "rnnt_embed.cu", "rnnt_beam.cu",
+                                            "rnnt_distill.cu")]
+DEPS = [os.path.join(CSRC, f) for f in ("rnnt_labels.cuh", "rnnt_rows.cuh")]
 HDR = os.path.join(ROOT, "include", "rnnt_gb300.h")
 LIB = os.path.join(PKG, "librnnt_gb300.so")
 
