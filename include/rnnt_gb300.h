@@ -496,8 +496,8 @@ rnnt_status_t rnnt_beam_reorder(const rnnt_state_t *states, int32_t n_states,
 
 /* ------------------------------------------------------------------------
  * Learning from a teacher: the top logits of a teacher's lattice rows, the loss
- * of a student against them.  No counterpart on the pages.  What is said of the
- * label side above holds here as well.
+ * of a student against them, and the drawing of labels.  No counterpart on the
+ * pages.  What is said of the label side above holds here as well.
  */
 
 /* Most outputs kept of a teacher's row, and the largest vocabulary, of these operators. */
@@ -599,6 +599,39 @@ rnnt_status_t rnnt_distill_grad_scale(void *grad, rnnt_dtype_t dt, int64_t rows,
                                       int32_t B, int64_t rows_each, const void *workspace,
                                       size_t workspace_bytes, const float *factors,
                                       int32_t per_sample, rnnt_stream_t stream);
+
+/*
+ * rnnt_sample -- one step of drawing: of every hypothesis one extension.
+ *
+ * A hypothesis with logits x and a number u in [0, 1) draws as follows.  Outputs are ordered by
+ * logit (equal ones by id); with e_j = exp(x_j / temperature) those are kept that are among the
+ * first top_k, of these the shortest beginning whose sum of e is at least top_p of theirs, and of
+ * these the ones with e_j >= min_p * max e.  The token is the first kept id
+ * at which the running sum of e over the kept ids, in the order of the ids, is above u times
+ * their whole sum.  Outputs of logit -inf are never kept.  The sums decide as if held to 40 bits.
+ *
+ *   out_scores     scores + x_token - logsumexp(x) (scores + x_token without
+ *                  fused_log_softmax), at temperature 1 and over all outputs; within 5e-6 of
+ *                  the value and one float32 rounding.
+ *   out_tokens     the token.  A finished hypothesis keeps its score and gets token -1, whatever
+ *                  its logits hold; one of score -inf, or whose logits are all -inf, gets score
+ *                  -inf and token -1.
+ *
+ *   logits         (B, K, V) in dt: item b's hypothesis k starts at element
+ *                  b * batch_stride + k * beam_stride, its V logits adjacent.
+ *   scores, random float [B, K];  finished uint8 [B, K], or NULL: none.
+ *   top_k          >= 1, or 0: not used;  top_p in (0, 1], 1: not used;  min_p in [0, 1], 0: not
+ *                  used;  temperature in [1e-4, 1e4].
+ *   status_dev     RNNT_INVALID_VALUE for a score of NaN or +inf, a random number outside [0, 1),
+ *                  or logits that hold NaN or +inf; such a hypothesis gets score -inf and token -1.
+ * The outputs must not overlap the inputs or one another.  V <= RNNT_MAX_TOP_VOCAB.
+ */
+rnnt_status_t rnnt_sample(const void *logits, rnnt_dtype_t dt, int32_t B, int32_t K, int32_t V,
+                          int64_t batch_stride, int64_t beam_stride, const float *scores,
+                          const float *random, const uint8_t *finished, double temperature,
+                          int32_t top_k, double top_p, double min_p, int32_t fused_log_softmax,
+                          float *out_scores, int32_t *out_tokens, int32_t *status_dev,
+                          rnnt_stream_t stream);
 
 /* Static English description of a status code. */
 const char *rnnt_status_string(rnnt_status_t status);

@@ -1,7 +1,7 @@
 """rnn_transducer_loss_gb300: fused RNN-T (transducer) loss forward+backward for GB300,
 the label side of a transducer around it (label embedding and its gradient for
 training, beam selection and reordering of states for decoding), and learning
-from a teacher (its top logits, the distillation loss and gradient).
+from a teacher (its top logits, the distillation loss and gradient, drawn labels).
 
 The compute path is a C-ABI shared library (``librnnt_gb300.so``, declared in
 ``include/rnnt_gb300.h``) of hand-written CUDA kernels for sm_103a.  This
@@ -14,7 +14,7 @@ _FROM = {"rnnt_loss": "functional", "RNNTLoss": "functional",
          "rnnt_embed": "embedding", "rnnt_embed_grad": "embedding", "RNNTEmbedding": "embedding",
          "rnnt_beam_select": "beam", "rnnt_beam_reorder": "beam",
          "rnnt_top_logits": "distill", "rnnt_distill_loss": "distill",
-         "RNNTDistillLoss": "distill"}
+         "RNNTDistillLoss": "distill", "rnnt_sample": "sample"}
 __all__ = list(_FROM)
 
 

@@ -27,7 +27,7 @@ EXPORTS = ("rnnt_workspace_size", "rnnt_workspace_size_ex", "rnnt_loss_fused", "
            "rnnt_abi_version", "rnnt_plan", "rnnt_embed", "rnnt_embed_grad_workspace_size",
            "rnnt_embed_grad", "rnnt_beam_workspace_size", "rnnt_beam_select",
            "rnnt_beam_reorder", "rnnt_top_logits", "rnnt_distill_workspace_size",
-           "rnnt_distill_loss", "rnnt_distill_grad_scale")
+           "rnnt_distill_loss", "rnnt_distill_grad_scale", "rnnt_sample")
 
 
 MAX_BIG_BLANKS = 8                    # RNNT_MAX_BIG_BLANKS
@@ -151,6 +151,9 @@ def load() -> ctypes.CDLL:
     lib.rnnt_distill_loss.restype = i32
     lib.rnnt_distill_grad_scale.argtypes = [P, i32, i64, i32, i32, i64, P, sz, P, i32, P]
     lib.rnnt_distill_grad_scale.restype = i32
+    lib.rnnt_sample.argtypes = [P, i32, i32, i32, i32, i64, i64, P, P, P, f64, i32, f64, f64, i32,
+                                P, P, P, P]
+    lib.rnnt_sample.restype = i32
     _lib = lib
     return lib
 
@@ -287,7 +290,7 @@ def rnnt_distill_workspace_size(B, rows) -> int:
 # The library's own functions, with its arguments in its order (pointers as integers or None) and a
 # status code as result.
 _DIRECT = ("rnnt_embed", "rnnt_embed_grad", "rnnt_beam_select", "rnnt_beam_reorder",
-           "rnnt_top_logits", "rnnt_distill_loss", "rnnt_distill_grad_scale")
+           "rnnt_top_logits", "rnnt_distill_loss", "rnnt_distill_grad_scale", "rnnt_sample")
 
 
 def __getattr__(name):

@@ -11,7 +11,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SRCS = [os.path.join(CSRC, f) for f in ("rnnt_gb300.cu", "rnnt_embed.cu", "rnnt_beam.cu",
-                                            "rnnt_distill.cu")]
+                                            "rnnt_distill.cu", "rnnt_sample.cu")]
 DEPS = [os.path.join(CSRC, f) for f in ("rnnt_labels.cuh", "rnnt_rows.cuh")]
 HDR = os.path.join(ROOT, "include", "rnnt_gb300.h")
 LIB = os.path.join(PKG, "librnnt_gb300.so")
