@@ -21,7 +21,8 @@ using namespace rnnt_rows;
 namespace {
 
 constexpr float kMost = 3.40282347e38f;    // the largest float32: finite logits / tau stay finite
-constexpr int kMostRows = 152 * 16;        // blocks of a kernel that takes a row a block
+constexpr int kSMs = 152;
+constexpr int kMostRows = kSMs * 16;        // blocks of a kernel that takes a row a block
 
 // The lattice's rows: all of them (no lengths), or those of the sequences, compact or padded.
 struct Lattice {
@@ -45,6 +46,10 @@ struct Lattice {
     }
     // Whether a row of the padded layout belongs to a sequence.
     __device__ __forceinline__ bool inside(int64_t row) const {
+        if (rows <= INT32_MAX) {                           // 32-bit divisions
+            const uint32_t w = (uint32_t)max_U + 1, q = (uint32_t)row / w, b = q / (uint32_t)max_T;
+            return (int)(q - b * max_T) < T[b] && (int)((uint32_t)row - q * w) <= U[b];
+        }
         const int64_t w = (int64_t)max_U + 1, q = row / w;
         const int u = (int)(row - q * w), b = (int)(q / max_T), t = (int)(q - (int64_t)b * max_T);
         return t < T[b] && u <= U[b];
@@ -98,7 +103,7 @@ struct TopParams {
     const char* logits;
     Lattice lat;
     int32_t V, k;
-    float scale;                           // log2 e / tau
+    float scale, scale_low;                // log2 e / tau, in two parts
     float inv_tau;
     void* values;
     int32_t* ids;
@@ -196,13 +201,14 @@ __global__ void __launch_bounds__(kLongThreads) k_top_long(const TopParams p) {
                 // had no place
                 if (have == most) {
                     const float first = value_of(best[k]);
+                    const Exponent f(first, p.scale, p.scale_low);
                     float sum = 0.0f, equal = 0.0f;
                     for (int j = tid; j < r.n; j += TH) {
                         const Pack<T, 16> v = r.load(j);
 #pragma unroll
                         for (int e = 0; e < E; ++e) {
                             const float y = to_f32(v.e[e]);
-                            sum += y < first ? ex2((y - first) * p.scale) : 0.0f;
+                            sum += y < first ? f(y) : 0.0f;
                             equal += y == first ? 1.0f : 0.0f;
                         }
                     }
@@ -224,6 +230,212 @@ __global__ void __launch_bounds__(kLongThreads) k_top_long(const TopParams p) {
     }
 }
 
+// The stages of a group's ring, and what a group needs beside them.
+struct Ring {
+    int32_t stages;
+    uint32_t stage_bytes, group_bytes;
+};
+constexpr int kMostStages = 2;            // more cost blocks an SM: 3 and 4 measured slower
+
+template <int G>
+struct TopScratch {
+    static constexpr int BUF = G == 32 ? 128 : 512;        // elements that are ranked
+    uint64_t bar[kMostStages];
+    uint64_t buf[BUF], best[RNNT_MAX_TOP + 1];
+    typename Group<G>::Space space;
+    float bounds[G / 32];
+    int count;
+};
+
+// Sorted in descending order over the warp (bitonic).
+__device__ __forceinline__ float warp_sorted(float x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2) {
+#pragma unroll
+        for (int o = size / 2; o; o >>= 1) {
+            const float y = __shfl_xor_sync(kAll, x, o);
+            const bool larger = ((lane & o) == 0) == ((lane & size) == 0 || size == 32);
+            x = larger ? fmaxf(x, y) : fminf(x, y);
+        }
+    }
+    return x;
+}
+
+// The elements of a vector that are at least `least`, as bits.
+__device__ __forceinline__ uint32_t reaching(const Pack<float, 16>& v, float least) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m |= v.e[e] >= least ? 1u << e : 0u;
+    return m;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t reaching(const Pack<T, 16>& v, float least) {
+    using T2 = typename Two<T>::type;
+    const T one = from_f32<T>(least);                      // a value of the type
+    T2 two;
+    two.x = one, two.y = one;
+    const T2* h = reinterpret_cast<const T2*>(&v.raw);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m |= __hge2_mask(h[i], two) & (0x00020001u << (2 * i));
+    return (m | m >> 16) & 0xffu;
+}
+
+// Rows through a ring of shared memory, a group of threads each.  The k best of a row: the
+// largest maxima of its threads (of both halves of their vectors where k needs more than there are
+// threads in a warp) bound the k + 1-st best from below; the few elements that reach the bound are
+// ranked by counting.  They are then taken out of the row, which leaves the rest: its largest
+// element (the k + 1-st best, if it reached the bound) and the sum relative to it.
+template <typename T, int TH, int G>
+__global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) {
+    using Gr = Group<G>;
+    using Scratch = TopScratch<G>;
+    constexpr int WARPS = G / 32, E = 16 / (int)sizeof(T), GROUPS = TH / G;
+    extern __shared__ __align__(16) char space[];
+    char* const mine = space + (G == 32 ? threadIdx.x / G : 0) * ring.group_bytes;
+    Scratch& sh = *reinterpret_cast<Scratch*>(mine + ring.stages * ring.stage_bytes);
+    const int me = Gr::rank(), lane = me & 31, k = p.k;
+    const int64_t groups = (int64_t)gridDim.x * GROUPS;
+    const int64_t first_row = (int64_t)blockIdx.x * GROUPS + (G == 32 ? threadIdx.x / G : 0);
+    const auto live = [&](int64_t row) { return !p.lat.T || p.lat.inside(row); };
+    const auto staged = [&](int64_t row, int st) {
+        return Staged<T, G>(reinterpret_cast<const T*>(p.logits) + row * p.V, p.V,
+                            reinterpret_cast<uint4*>(mine + st * ring.stage_bytes), row == 0,
+                            row == p.lat.rows - 1);
+    };
+    if (blockIdx.x == 0 && p.lat.T) check_lengths<TH>(p.lat, p.status);
+    if (me == 0) {
+        for (int st = 0; st < ring.stages; ++st) mbar_init(&sh.bar[st]);
+        fence_mbar_init();
+        sh.count = 0;
+    }
+    Gr::sync();
+    if (me == 0)
+        for (int st = 0; st < ring.stages; ++st) {
+            const int64_t row = first_row + st * groups;
+            if (row < p.lat.rows && live(row)) staged(row, st).fetch(&sh.bar[st]);
+        }
+    int polls = kWaitPolls, st = 0;
+    uint32_t phases = 0;                                   // a bit a stage
+    for (int64_t row = first_row; row < p.lat.rows; row += groups) {
+        float rest = -INFINITY;
+        int have = 0;
+        if (live(row)) {
+            const Staged<T, G> x = staged(row, st);
+            mbar_wait(&sh.bar[st], phases >> st & 1, polls, p.status);
+            phases ^= 1u << st;
+            x.complete();
+            Pack<T, 16> m = all_minus_inf<T>();
+#pragma unroll 4
+            for (int j = me; j < x.r.n; j += G) m = larger(m, x.at(j));
+            float2 both = half_maxima(m);
+            const float top = Gr::max(max_nan(both.x, both.y), sh.space);
+            if (!(top < INFINITY)) {                       // NaN or +inf: the row is left empty
+                if (me == 0) invalid(p.status);
+            } else if (top > -INFINITY) {
+                const int c = min((k + WARPS) / WARPS, 64 / WARPS);    // a warp's share of k + 1
+                float bound;
+                if (c <= 32) {
+                    bound = __shfl_sync(kAll, warp_sorted(fmaxf(both.x, both.y)), c - 1);
+                } else {
+                    const int h = (c + 1) / 2 - 1;
+                    bound = fminf(__shfl_sync(kAll, warp_sorted(both.x), h),
+                                  __shfl_sync(kAll, warp_sorted(both.y), h));
+                }
+                if constexpr (G > 32) {
+                    if (lane == 0) sh.bounds[threadIdx.x >> 5] = bound;
+                    Gr::sync();
+#pragma unroll
+                    for (int w = 0; w < WARPS; ++w) bound = fminf(bound, sh.bounds[w]);
+                }
+                // -inf reaches no bound
+                bound = fmaxf(bound, sizeof(T) == 4 ? -kMost
+                                     : std::is_same_v<T, __half> ? -65504.0f : -3.38953139e38f);
+                for (int j = me; j < x.r.n; j += G) {
+                    uint32_t hits = reaching(x.at(j), bound);
+                    while (hits) {
+                        const int e = __ffs(hits) - 1, i = j * E + e - x.r.off;
+                        hits &= hits - 1;
+                        const int at = atomicAdd(&sh.count, 1);
+                        if (at < Scratch::BUF) sh.buf[at] = key_of(to_f32(x.element(i)), i);
+                    }
+                }
+                Gr::sync();
+                const int n = sh.count;
+                have = min(n, k);
+                if (n <= Scratch::BUF) {
+                    for (int i = me; i < n; i += G) {
+                        const uint64_t key = sh.buf[i];
+                        int rank = 0;
+                        for (int o = 0; o < n; ++o) rank += sh.buf[o] > key;
+                        if (rank <= k) sh.best[rank] = key;
+                    }
+                } else {                                   // a crowd: one by one
+                    uint64_t last = ~0ull;
+                    for (int i = 0; i <= k; ++i) {
+                        uint64_t next = 0;
+                        for (int j = me; j < x.r.n; j += G) {
+                            const Pack<T, 16> v = x.at(j);
+#pragma unroll
+                            for (int e = 0; e < E; ++e) {
+                                const uint64_t key = key_of(to_f32(v.e[e]), j * E + e - x.r.off);
+                                if (key < last && key > next) next = key;
+                            }
+                        }
+                        next = warp_largest(next);
+                        if constexpr (G > 32) {
+                            if (lane == 0) sh.buf[threadIdx.x >> 5] = next;
+                            Gr::sync();
+                            for (int w = 0; w < WARPS; ++w) next = max(next, sh.buf[w]);
+                            Gr::sync();
+                        }
+                        last = next;
+                        if (me == 0) sh.best[i] = last;
+                    }
+                }
+                Gr::sync();
+                if (me == 0) sh.count = 0;
+                for (int i = me; i < have; i += G)
+                    x.element(element_of(sh.best[i])) = from_f32<T>(-INFINITY);
+                Gr::sync();
+                float first = n > k ? value_of(sh.best[k]) : -INFINITY;
+                if (n == k && bound > -kMost) {
+                    Pack<T, 16> m = all_minus_inf<T>();
+                    for (int j = me; j < x.r.n; j += G) m = larger(m, x.at(j));
+                    both = half_maxima(m);
+                    first = Gr::max(max_nan(both.x, both.y), sh.space);
+                }
+                if (first > -INFINITY) {
+                    const Exponent f(first, p.scale, p.scale_low);
+                    float sum = 0.0f;
+#pragma unroll 4
+                    for (int j = me; j < x.r.n; j += G) {
+                        float2 e[E / 2];
+                        sum += terms_of(x.at(j), f, e);
+                    }
+                    sum = Gr::sum(sum, sh.space);
+                    rest = fmaxf(logf(sum) + first * p.inv_tau, -kMost);
+                }
+            }
+        }
+        for (int i = me; i < k; i += G) {
+            const uint64_t key = i < have ? sh.best[i] : 0;
+            reinterpret_cast<T*>(p.values)[row * k + i] =
+                from_f32<T>(i < have ? value_of(key) : -INFINITY);
+            p.ids[row * k + i] = i < have ? element_of(key) : -1;
+        }
+        if (me == 0) p.rest[row] = rest;
+        Gr::sync();                                        // the stage has been read
+        const int64_t next = row + ring.stages * groups;
+        if (me == 0 && next < p.lat.rows && live(next)) {
+            fence_proxy_async();
+            staged(next, st).fetch(&sh.bar[st]);
+        }
+        st = st + 1 == ring.stages ? 0 : st + 1;
+    }
+}
+
 // ------------------------------------------------------------- distillation
 struct DistillParams {
     const char* logits;
@@ -232,7 +444,7 @@ struct DistillParams {
     const float* rest;                     // or NULL
     Lattice lat;
     int32_t V, k, teacher_dt;
-    float scale;                           // log2 e / tau
+    float scale, scale_low;                // log2 e / tau, in two parts
     float inv_tau;
     float grad_scale;                      // tau * weight, over the batch for the mean
     double loss_scale;                     // tau^2 * weight
@@ -253,75 +465,157 @@ __device__ __forceinline__ float teacher_logit(const DistillParams& p, int64_t a
     return to_f32(reinterpret_cast<const __nv_bfloat16*>(p.teacher)[at]);
 }
 
-// A teacher's row, two places a lane of a warp.
+// Which of the warp's ids (of places 0 to 31, and 32 to 63) stand in a place before theirs: bits 0, 1.
+__device__ __noinline__ unsigned repeated(int id0, int id1) {
+    const int lane = threadIdx.x & 31;
+    unsigned again = 0;
+    for (int o = 0; o < 32; ++o) {
+        const int x = __shfl_sync(kAll, id0, o), y = __shfl_sync(kAll, id1, o);
+        if (id0 >= 0 && x == id0 && o < lane) again |= 1;
+        if (id1 >= 0 && (x == id1 || (y == id1 && o < lane))) again |= 2;
+    }
+    return again;
+}
+
+// A teacher's row, P places a lane of a warp.
+template <int P>
 struct Teacher {
-    int id[2];                             // -1: an empty place
-    float t[2];                            // logit / tau, -inf in an empty place
+    int id[P];                             // -1: an empty place
+    float t[P];                            // logit / tau, -inf in an empty place
     float rest;                            // -inf without one
-    bool given;                            // a rest
-    float p[2], log_p[2], p_rest, log_p_rest;
-    bool some;                             // whether anything is in it
+    float p[P], log_p[P], p_rest, log_p_rest;
 
     __device__ __forceinline__ void load(const DistillParams& a, int64_t row) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < P; ++q) {
             const int k = lane + 32 * q;
             id[q] = -1;
             t[q] = -INFINITY;
             if (k < a.k) {
                 id[q] = a.ids[row * a.k + k];
-                const float x = teacher_logit(a, row * a.k + k);
-                t[q] = x * a.inv_tau;
-                if (t[q] == -INFINITY && x != -INFINITY) t[q] = -kMost;
+                t[q] = teacher_logit(a, row * a.k + k);
             }
         }
-        given = a.rest != nullptr;
-        rest = given ? a.rest[row] : -INFINITY;
+        rest = a.rest ? a.rest[row] : -INFINITY;
     }
-    // Empties places without an output of the vocabulary; says what is not allowed.
+    // Logits / tau; empties places without an output of the vocabulary; says what is not allowed.
     __device__ __forceinline__ void check(const DistillParams& a) {
         bool bad = !(rest < INFINITY);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < P; ++q) {
             bad |= id[q] >= a.V;
             if ((unsigned)id[q] >= (unsigned)a.V) {
                 id[q] = -1;
                 t[q] = -INFINITY;
             }
+            const float x = t[q];
+            t[q] *= a.inv_tau;
+            if (t[q] == -INFINITY && x != -INFINITY) t[q] = -kMost;
             bad |= !(t[q] < INFINITY);
         }
         if (bad) invalid(a.status);
     }
     // Empties a place whose id stands in one before it.
-    __device__ __noinline__ void drop_repeated(const DistillParams& a) {
-        const int lane = threadIdx.x & 31;
-        const int id0 = id[0], id1 = id[1];
-        for (int o = 0; o < 32; ++o) {
-            const int x = __shfl_sync(kAll, id0, o), y = __shfl_sync(kAll, id1, o);
-            if (id0 >= 0 && o < lane && x == id0) id[0] = -1;
-            if (id1 >= 0 && (x == id1 || (o < lane && y == id1))) id[1] = -1;
-        }
+    __device__ __forceinline__ void drop_repeated(const DistillParams& a) {
+        const unsigned again = repeated(id[0], P > 1 ? id[P - 1] : -1);
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-            if (id[q] < 0) t[q] = -INFINITY;
+        for (int q = 0; q < P; ++q)
+            if (again >> q & 1) {
+                id[q] = -1;
+                t[q] = -INFINITY;
+            }
         invalid(a.status);
     }
+    // Whether anything is in it (NaN counts: the loss says so).
+    __device__ __forceinline__ bool some() const {
+        bool any = rest != -INFINITY;
+#pragma unroll
+        for (int q = 0; q < P; ++q) any |= t[q] != -INFINITY;
+        return __any_sync(kAll, any);
+    }
     __device__ __forceinline__ void softmax() {
-        const float top = warp_max(fmaxf(fmaxf(t[0], t[1]), rest));
-        some = top > -INFINITY;
+        float top = rest;
+#pragma unroll
+        for (int q = 0; q < P; ++q) top = fmaxf(top, t[q]);
+        top = warp_max(top);
         float sum = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) sum += t[q] == -INFINITY ? 0.0f : expf(t[q] - top);
+        for (int q = 0; q < P; ++q) sum += t[q] == -INFINITY ? 0.0f : expf(t[q] - top);
         sum = warp_sum(sum) + (rest == -INFINITY ? 0.0f : expf(rest - top));
         const float log_sum = logf(sum);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < P; ++q) {
             log_p[q] = (t[q] - top) - log_sum;
             p[q] = t[q] == -INFINITY ? 0.0f : expf(log_p[q]);
         }
         log_p_rest = (rest - top) - log_sum;
         p_rest = rest == -INFINITY ? 0.0f : expf(log_p_rest);
+    }
+};
+
+// What the places' logits give a row: the sum of their terms relative to the largest of them; then,
+// with the rest's, the row's sum, loss and the gradient's factors.
+template <int P>
+struct Places {
+    float at[P], e[P], top, sum;
+
+    // `scale` * the term of a place, less its probability, after finish().
+    __device__ __forceinline__ void terms(const DistillParams& a, const Teacher<P>& te) {
+        top = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < P; ++q) top = max_nan(top, at[q]);
+        top = warp_max_nan(top);
+        const Exponent f(top, a.scale, a.scale_low);
+        sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            e[q] = at[q] == -INFINITY ? 0.0f : f(at[q]);
+            sum += e[q];
+        }
+        sum = warp_sum(sum);
+    }
+};
+
+// The sum of a row whose outputs without a place have their largest at `outside` and a sum `left`
+// relative to it, and whose places have `top` and `sum`.
+struct Whole {
+    float base, outer, inner, total;       // 2^((outside - base) c), 2^((top - base) c)
+    __device__ __forceinline__ Whole(const DistillParams& a, float outside, float left, float top,
+                                     float sum) {
+        base = max_nan(outside, top);
+        const Exponent f(base, a.scale, a.scale_low);
+        outer = outside == -INFINITY ? 0.0f : f(outside);
+        inner = top == -INFINITY ? 0.0f : f(top);
+        total = left * outer + sum * inner;
+    }
+    __device__ __forceinline__ bool good() const { return total > 0.0f && total < INFINITY; }
+    // of the terms relative to `outside`
+    __device__ __forceinline__ float factor(const DistillParams& a, float left,
+                                            float p_rest) const {
+        float c = outer / total;
+        if (a.rest && left > 0.0f) c -= p_rest / left;
+        return c * a.grad_scale;
+    }
+    template <int P>
+    __device__ __forceinline__ float loss(const DistillParams& a, const Teacher<P>& te,
+                                          const Places<P>& pl, float outside, float left) const {
+        const float log_total = logf(total);
+        float kl = 0.0f;
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+            if (te.p[q] != 0.0f)
+                kl += te.p[q] * (te.log_p[q] - ((pl.at[q] - base) * a.inv_tau - log_total));
+        kl = warp_sum(kl);
+        if (te.p_rest != 0.0f)
+            kl += te.p_rest * (te.log_p_rest -
+                               (logf(left) + (outside - base) * a.inv_tau - log_total));
+        return kl;
+    }
+    template <int P>
+    __device__ __forceinline__ float place(const DistillParams& a, const Teacher<P>& te,
+                                           const Places<P>& pl, int q) const {
+        return (pl.e[q] * (inner / total) - te.p[q]) * a.grad_scale;
     }
 };
 
@@ -362,8 +656,8 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillPara
     for (int i = tid; i < (p.V + 31) / 32; i += TH) marks[i] = 0;
     const int64_t rows = p.lat.padded ? p.lat.rows : compact_rows<TH>(p.lat, space64);
     __syncthreads();
-    Teacher te;
-    float at[2];
+    Teacher<2> te;
+    Places<2> pl;
     for (int64_t row = blockIdx.x; row < p.lat.rows; row += gridDim.x) {
         const bool live = row < rows && (!p.lat.padded || p.lat.inside(row));
         if (warp == 0 && live) {
@@ -378,7 +672,8 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillPara
                 }
             if (__any_sync(kAll, again)) te.drop_repeated(p);
             te.softmax();
-            if (lane == 0) s_some = te.some;
+            const bool some = te.some();
+            if (lane == 0) s_some = some;
         }
         __syncthreads();
         if (!live || !s_some) {
@@ -408,14 +703,15 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillPara
             }
             if (m == -INFINITY) continue;
             if (!(m <= top)) {
-                sum = top == -INFINITY ? 0.0f : sum * ex2((top - m) * p.scale);
+                sum = top == -INFINITY ? 0.0f : sum * Exponent(m, p.scale, p.scale_low)(top);
                 top = m;
             }
+            const Exponent f(top, p.scale, p.scale_low);
 #pragma unroll
-            for (int e = 0; e < E; ++e) sum += ex2((y[e] - top) * p.scale);
+            for (int e = 0; e < E; ++e) sum += f(y[e]);
         }
         const float wtop = warp_max_nan(top);
-        sum = top == -INFINITY ? 0.0f : sum * ex2((top - wtop) * p.scale);
+        sum = top == -INFINITY ? 0.0f : sum * Exponent(wtop, p.scale, p.scale_low)(top);
         sum = warp_sum(sum);
         if (lane == 0) {
             tops[warp] = wtop;
@@ -423,65 +719,43 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillPara
         }
         __syncthreads();
         if (warp == 0) {
-            float m = -INFINITY;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                at[q] = te.id[q] >= 0 ? to_f32(r.x[te.id[q]]) : -INFINITY;
-                m = max_nan(m, at[q]);
-            }
-            const float wt = lane < WARPS ? tops[lane] : -INFINITY;
-            const float ws = lane < WARPS ? sums[lane] : 0.0f;
-            // the terms of the outputs without a place are relative to their own largest
-            // (relative to the whole row's they could vanish, with p_r > 0), the others to that of all
-            const float outside = warp_max_nan(wt), base = warp_max_nan(max_nan(m, wt));
-            const float left = warp_sum(wt == -INFINITY ? 0.0f : ws * ex2((wt - outside) * p.scale));
-            const float shift = outside == -INFINITY ? 0.0f : ex2((outside - base) * p.scale);
-            float e[2], mine = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                e[q] = te.id[q] >= 0 ? ex2((at[q] - base) * p.scale) : 0.0f;
-                mine += e[q];
-            }
-            const float total = left * shift + warp_sum(mine);
-            if (!(total > 0.0f && total < INFINITY)) invalid(p.status);    // NaN among them
-            const float log_total = logf(total);
-            float kl = 0.0f;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                if (te.p[q] != 0.0f)
-                    kl += te.p[q] *
-                          (te.log_p[q] - ((at[q] - base) * p.inv_tau - log_total));
-            kl = warp_sum(kl);
-            if (te.p_rest != 0.0f)
-                kl += te.p_rest * (te.log_p_rest - (logf(left) + (outside - base) * p.inv_tau -
-                                                    log_total));
-            const float inv = 1.0f / total;
+                pl.at[q] = te.id[q] >= 0 ? to_f32(r.x[te.id[q]]) : -INFINITY;
+            pl.terms(p, te);
+            const float wt = lane < WARPS ? tops[lane] : -INFINITY;
+            const float ws = lane < WARPS ? sums[lane] : 0.0f;
+            const float outside = warp_max_nan(wt);
+            const float left = warp_sum(
+                wt == -INFINITY ? 0.0f : ws * Exponent(outside, p.scale, p.scale_low)(wt));
+            const Whole w(p, outside, left, pl.top, pl.sum);
+            if (!w.good()) invalid(p.status);              // NaN among them
+            const float kl = w.loss(p, te, pl, outside, left);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) te.t[q] = e[q] * inv - te.p[q];    // of the places
-            float coef = shift * inv;
-            if (te.given && left > 0.0f) coef -= te.p_rest / left;
+            for (int q = 0; q < 2; ++q) te.t[q] = w.place(p, te, pl, q);
             if (lane == 0) {
-                p.row_loss[row] = kl;
+                p.row_loss[row] = w.good() ? kl : NAN;
                 s_base = outside == -INFINITY ? 0.0f : outside;
-                s_coef = coef * p.grad_scale;
+                s_coef = w.good() ? w.factor(p, left, te.p_rest) : NAN;
             }
         }
         __syncthreads();
         if (p.grad) {
-            const float base = s_base, coef = s_coef;
+            const Exponent f(s_base, p.scale, p.scale_low);
+            const float coef = s_coef;
             T* g = reinterpret_cast<T*>(p.grad) + row * p.V;
             for (int j = tid; j < r.n; j += TH) {
                 Pack<T, 16> v = r.load(j);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    v.e[e] = from_f32<T>(ex2((to_f32(v.e[e]) - base) * p.scale) * coef);
+                    v.e[e] = from_f32<T>(f(to_f32(v.e[e])) * coef);
                 r.store(g, j, v);
             }
             __syncthreads();
             if (warp == 0) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    if (te.id[q] >= 0) g[te.id[q]] = from_f32<T>(te.t[q] * p.grad_scale);
+                    if (te.id[q] >= 0) g[te.id[q]] = from_f32<T>(te.t[q]);
             }
         }
         if (warp == 0) {
@@ -490,6 +764,185 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillPara
                 if (te.id[q] >= 0) marks[te.id[q] >> 5] = 0;
         }
         __syncthreads();
+    }
+}
+
+template <int G>
+struct DistillScratch {
+    uint64_t bar[kMostStages];
+    typename Group<G>::Space space;
+    float top, sum, p_rest;                // of the places, for a block
+    int some;
+};
+
+// Rows through a ring of shared memory, a group of threads each, one read and one write.  The places'
+// logits are picked out of the staged row and -inf is left in their stead, so that what the threads
+// then read is the rest alone; its terms stay in registers from their sum to the gradient (NV vectors
+// a thread; NV = 0: rows too long for that are read from the stage again).  A group's first warp
+// looks after the teacher.
+template <typename T, int TH, int G, int NV, int P>
+__global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Ring ring) {
+    using Gr = Group<G>;
+    using Scratch = DistillScratch<G>;
+    using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+    constexpr int E = 16 / (int)sizeof(T), GROUPS = TH / G;
+    extern __shared__ __align__(16) char space[];
+    __shared__ int64_t space64[TH / 32];
+    char* const mine = space + (G == 32 ? threadIdx.x / G : 0) * ring.group_bytes;
+    Scratch& sh = *reinterpret_cast<Scratch*>(mine + ring.stages * ring.stage_bytes);
+    const int me = Gr::rank(), lane = me & 31;
+    const bool leads = G == 32 || threadIdx.x < 32;        // the teacher's warp
+    const int64_t groups = (int64_t)gridDim.x * GROUPS;
+    const int64_t first_row = (int64_t)blockIdx.x * GROUPS + (G == 32 ? threadIdx.x / G : 0);
+    let_next_start();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
+    const int64_t rows = p.lat.padded ? p.lat.rows : compact_rows<TH>(p.lat, space64);
+    const auto live = [&](int64_t row) {
+        return row < rows && (!p.lat.padded || p.lat.inside(row));
+    };
+    const auto staged = [&](int64_t row, int st) {
+        return Staged<T, G>(reinterpret_cast<const T*>(p.logits) + row * p.V, p.V,
+                            reinterpret_cast<uint4*>(mine + st * ring.stage_bytes), false,
+                            row == p.lat.rows - 1);
+    };
+    if (me == 0) {
+        for (int st = 0; st < ring.stages; ++st) mbar_init(&sh.bar[st]);
+        fence_mbar_init();
+    }
+    Gr::sync();
+    if (me == 0)
+        for (int st = 0; st < ring.stages; ++st) {
+            const int64_t row = first_row + st * groups;
+            if (live(row)) staged(row, st).fetch(&sh.bar[st]);
+        }
+    int polls = kWaitPolls, st = 0;
+    uint32_t phases = 0;                                   // a bit a stage
+    Teacher<P> te, ahead;
+    Places<P> pl;
+    bool now = live(first_row);
+    if (leads && now) ahead.load(p, first_row);
+    for (int64_t row = first_row; row < p.lat.rows; row += groups) {
+        const bool counts = now;
+        te = ahead;
+        now = live(row + groups);
+        if (leads && now) ahead.load(p, row + groups);     // one row ahead
+        T* const g = reinterpret_cast<T*>(p.grad) + row * p.V;
+        if (counts) {
+            const Staged<T, G> x = staged(row, st);
+            mbar_wait(&sh.bar[st], phases >> st & 1, polls, p.status);
+            phases ^= 1u << st;
+            x.complete();
+            bool some = true;
+            if (leads) {
+                te.check(p);
+#pragma unroll
+                for (int q = 0; q < P; ++q)
+                    pl.at[q] = te.id[q] >= 0 ? to_f32(x.element(te.id[q])) : -INFINITY;
+                __syncwarp();
+                // each place leaves its number; one that finds another's has its id in common
+#pragma unroll
+                for (int q = 0; q < P; ++q)
+                    if (te.id[q] >= 0)
+                        reinterpret_cast<volatile Bits&>(x.element(te.id[q])) =
+                            (Bits)(lane + 32 * q);
+                __syncwarp();
+                bool again = false;
+#pragma unroll
+                for (int q = 0; q < P; ++q)
+                    again |= te.id[q] >= 0 &&
+                             reinterpret_cast<volatile Bits&>(x.element(te.id[q])) !=
+                                 (Bits)(lane + 32 * q);
+                if (__any_sync(kAll, again)) {
+                    te.drop_repeated(p);
+#pragma unroll
+                    for (int q = 0; q < P; ++q)
+                        if (te.id[q] < 0) pl.at[q] = -INFINITY;
+                }
+#pragma unroll
+                for (int q = 0; q < P; ++q)
+                    if (te.id[q] >= 0) x.element(te.id[q]) = from_f32<T>(-INFINITY);
+                some = te.some();
+                if (G > 32 && lane == 0) sh.some = some;
+            }
+            Gr::sync();
+            if (G > 32) some = sh.some;
+            if (!some) {
+                if (p.grad) zero_row<T, G>(p, row);
+                if (me == 0) p.row_loss[row] = 0.0f;
+            } else {
+                Pack<T, 16> m = all_minus_inf<T>();
+#pragma unroll 4
+                for (int j = me; j < x.r.n; j += G) m = larger(m, x.at(j));
+                if (leads) {
+                    te.softmax();
+                    pl.terms(p, te);
+                    if (G > 32 && lane == 0) {
+                        sh.top = pl.top;
+                        sh.sum = pl.sum;
+                        sh.p_rest = te.p_rest;
+                    }
+                }
+                const float2 both = half_maxima(m);
+                const float outside = Gr::max(max_nan(both.x, both.y), sh.space);
+                const Exponent f(outside == -INFINITY ? 0.0f : outside, p.scale, p.scale_low);
+                float2 e[NV ? NV : 1][E / 2];
+                float left = 0.0f;
+                if constexpr (NV > 0) {
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+                        if (me + i * G < x.r.n) left += terms_of(x.at(me + i * G), f, e[i]);
+                } else {
+                    for (int j = me; j < x.r.n; j += G) left += terms_of(x.at(j), f, e[0]);
+                }
+                left = Gr::sum(left, sh.space);
+                const float top = G > 32 ? sh.top : pl.top, sum = G > 32 ? sh.sum : pl.sum;
+                const Whole w(p, outside, left, top, sum);
+                if (p.grad) {
+                    const float c = w.good() ? w.factor(p, left, G > 32 ? sh.p_rest : te.p_rest) : NAN;
+                    const float2 c2 = make_float2(c, c);
+                    const auto put = [&](int j, float2 (&y)[E / 2]) {
+                        Pack<T, 16> v;
+#pragma unroll
+                        for (int i = 0; i < E / 2; ++i) y[i] = mul2(y[i], c2);
+                        pack(v, y);
+                        x.r.store(g, j, v);
+                    };
+                    if constexpr (NV > 0) {
+#pragma unroll
+                        for (int i = 0; i < NV; ++i)
+                            if (me + i * G < x.r.n) put(me + i * G, e[i]);
+                    } else {
+                        for (int j = me; j < x.r.n; j += G) {
+                            terms_of(x.at(j), f, e[0]);
+                            put(j, e[0]);
+                        }
+                    }
+                }
+                if (leads) {
+                    if (!w.good()) invalid(p.status);      // NaN among them
+                    const float kl = w.loss(p, te, pl, outside, left);
+                    if (lane == 0) p.row_loss[row] = w.good() ? kl : NAN;
+                }
+                if (p.grad) {
+                    Gr::sync();                            // behind the rest's stores
+                    if (leads) {
+#pragma unroll
+                        for (int q = 0; q < P; ++q)
+                            if (te.id[q] >= 0) g[te.id[q]] = from_f32<T>(w.place(p, te, pl, q));
+                    }
+                }
+            }
+        } else {
+            if (p.grad) zero_row<T, G>(p, row);
+            if (me == 0) p.row_loss[row] = 0.0f;
+        }
+        Gr::sync();                                        // the stage has been read
+        const int64_t next = row + ring.stages * groups;
+        if (me == 0 && live(next)) {
+            fence_proxy_async();
+            staged(next, st).fetch(&sh.bar[st]);
+        }
+        st = st + 1 == ring.stages ? 0 : st + 1;
     }
 }
 
@@ -626,6 +1079,94 @@ DistillLayout distill_layout(int32_t B, int64_t rows) {
     return L;
 }
 
+// How rows of V elements are taken: by a warp or a block, through how many stages.
+constexpr int kWarpThreads = 256;          // of blocks whose warps take a row each
+constexpr int kBlockThreads = 256;         // of blocks that take a row each
+constexpr size_t kShared = 226 << 10;      // of a block, at most (1 KB is left for what is static)
+struct Shape {
+    int group;                             // 32, kBlockThreads, or 0: the kernels of long rows
+    Ring ring;
+    size_t shared;
+    int64_t blocks;
+};
+Shape shape_of(const void* logits, int64_t rows, int32_t V, int es, size_t warp_scratch,
+               size_t block_scratch) {
+    Shape s{};
+    // at any alignment where rows are not whole units
+    const size_t row = (size_t)V * es, units =
+        row % 16 || ((uintptr_t)logits & 15) ? (row + 30) / 16 * 16 : row;
+    const bool warp = units <= 4096;
+    const int groups = warp ? kWarpThreads / 32 : 1;
+    const size_t scratch = ((warp ? warp_scratch : block_scratch) + 15) & ~size_t(15);
+    int stages = kMostStages;
+    while (stages > 1 && groups * (stages * units + scratch) > kShared / 2) --stages;
+    if (groups * (stages * units + scratch) > kShared) return s;
+    s.group = warp ? 32 : kBlockThreads;
+    s.ring.stages = stages;
+    s.ring.stage_bytes = (uint32_t)units;
+    s.ring.group_bytes = (uint32_t)(stages * units + scratch);
+    s.shared = (size_t)groups * s.ring.group_bytes;
+    s.blocks = (rows + groups - 1) / groups;
+    return s;
+}
+// One wave of blocks, each taking its rows in turn.
+template <typename K>
+unsigned grid_of(const Shape& s, K kernel, int threads) {
+    int per_sm = 1;
+    if (s.blocks > kSMs &&
+        (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, s.shared) !=
+             cudaSuccess || per_sm < 1)) {
+        cudaGetLastError();
+        per_sm = 1;
+    }
+    return (unsigned)std::min<int64_t>(s.blocks, (int64_t)kSMs * per_sm);
+}
+
+template <typename T>
+bool raise_top() {
+    const auto raise = [](auto kernel) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)kShared) == cudaSuccess;
+    };
+    return raise(k_top<T, kWarpThreads, 32>) && raise(k_top<T, kBlockThreads, kBlockThreads>);
+}
+// Calls f(k_distill's form for rows of n vectors and k places).
+template <typename T, typename F>
+auto distill_form(int group, int n, int k, F&& f) {
+    const auto by_places = [&](auto g, auto nv) {
+        constexpr int G = decltype(g)::value, NV = decltype(nv)::value;
+        constexpr int TH = G == 32 ? kWarpThreads : G;
+        return k <= 32 ? f(k_distill<T, TH, G, NV, 1>, TH) : f(k_distill<T, TH, G, NV, 2>, TH);
+    };
+    using std::integral_constant;
+    if (group == 32) {
+        constexpr integral_constant<int, 32> g{};
+        if (n <= 32) return by_places(g, integral_constant<int, 1>{});
+        if (n <= 128) return by_places(g, integral_constant<int, 4>{});
+        return by_places(g, integral_constant<int, 8>{});
+    }
+    constexpr integral_constant<int, kBlockThreads> g{};
+    constexpr int most = sizeof(T) == 4 ? 8 : 4;           // vectors in 32 registers
+    if (n <= most * kBlockThreads) return by_places(g, integral_constant<int, most>{});
+    return by_places(g, integral_constant<int, 0>{});
+}
+template <typename T>
+bool raise_distill() {
+    bool ok = true;
+    for (int k : {1, 64})
+        for (int n : {1, 100, 200})
+            ok &= distill_form<T>(32, n, k, [](auto kernel, int) {
+                return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            (int)kShared) == cudaSuccess;
+            });
+    for (int k : {1, 64})
+        for (int n : {1, 1 << 20})
+            ok &= distill_form<T>(kBlockThreads, n, k, [](auto kernel, int) {
+                return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            (int)kShared) == cudaSuccess;
+            });
+    return ok;
+}
 bool distill_prepared() {
     static std::atomic<bool> done[64];
     return prepared_once(done, [] {
@@ -633,7 +1174,10 @@ bool distill_prepared() {
             return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         RNNT_MAX_TOP_VOCAB / 8) == cudaSuccess;
         };
-        return raise(k_distill_long<float>) && raise(k_distill_long<__half>) &&
+        return raise_top<float>() && raise_top<__half>() && raise_top<__nv_bfloat16>() &&
+               raise_distill<float>() && raise_distill<__half>() &&
+               raise_distill<__nv_bfloat16>() &&
+               raise(k_distill_long<float>) && raise(k_distill_long<__half>) &&
                raise(k_distill_long<__nv_bfloat16>);
     });
 }
@@ -667,16 +1211,24 @@ extern "C" rnnt_status_t rnnt_top_logits(const void* logits, rnnt_dtype_t dt, in
     p.logits = static_cast<const char*>(logits);
     p.V = V;
     p.k = k;
-    p.scale = (float)(kLog2e / temperature);
+    parts_below(kLog2e / temperature, p.scale, p.scale_low);
     p.inv_tau = (float)(1.0 / temperature);
     p.values = values;
     p.ids = ids;
     p.rest = rest;
     p.status = status_dev;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (!clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
+    if (!distill_prepared() || !clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
     with_type(dt, [&](auto t) {
-        k_top_long<decltype(t)><<<row_grid(rows), kLongThreads, 0, st>>>(p);
+        using T = decltype(t);
+        const Shape s = shape_of(logits, rows, V, es, sizeof(TopScratch<32>), sizeof(TopScratch<kBlockThreads>));
+        const auto launch = [&](auto kernel, int threads) {
+            kernel<<<grid_of(s, kernel, threads), threads, s.shared, st>>>(p, s.ring);
+        };
+        if (s.group == 32) launch(k_top<T, kWarpThreads, 32>, kWarpThreads);
+        else if (s.group) launch(k_top<T, kBlockThreads, kBlockThreads>, kBlockThreads);
+        else
+            k_top_long<T><<<row_grid(rows), kLongThreads, 0, st>>>(p);
     });
     return launched();
 }
@@ -735,7 +1287,7 @@ extern "C" rnnt_status_t rnnt_distill_loss(
     p.rest = teacher_rest;
     p.V = V;
     p.k = k;
-    p.scale = (float)(kLog2e / temperature);
+    parts_below(kLog2e / temperature, p.scale, p.scale_low);
     p.inv_tau = (float)(1.0 / temperature);
     p.mean = reduction == RNNT_RED_MEAN;
     p.grad_scale = (float)(temperature * weight / (p.mean ? B : 1));
@@ -751,8 +1303,16 @@ extern "C" rnnt_status_t rnnt_distill_loss(
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!distill_prepared() || !clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
     with_type(dt, [&](auto t) {
-        k_distill_long<decltype(t)>
-            <<<row_grid(rows), kLongThreads, (size_t)(V + 31) / 32 * 4, st>>>(p);
+        using T = decltype(t);
+        const Shape s = shape_of(logits, rows, V, es, sizeof(DistillScratch<32>),
+                                 sizeof(DistillScratch<kBlockThreads>));
+        if (s.group)
+            distill_form<T>(s.group, (int)(s.ring.stage_bytes / 16), k, [&](auto kernel, int th) {
+                kernel<<<grid_of(s, kernel, th), th, s.shared, st>>>(p, s.ring);
+                return 0;
+            });
+        else
+            k_distill_long<T><<<row_grid(rows), kLongThreads, (size_t)(V + 31) / 32 * 4, st>>>(p);
     });
     if (launched() != RNNT_OK) return RNNT_LAUNCH_FAILED;
     if (!launch_after(k_distill_sum, dim3((unsigned)B), kSumThreads, 0, st, p)) {

@@ -3,6 +3,7 @@
 // reductions of a warp and of a block.
 #pragma once
 #include <atomic>
+#include <cmath>
 
 #include "rnnt_labels.cuh"
 
@@ -106,6 +107,262 @@ struct Row {
             }
         }
     }
+};
+
+// ------------------------------------------------------ packed arithmetic
+// Two float32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d)
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d)
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d)
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return reinterpret_cast<float2&>(d);
+}
+// The elements of a vector, two by two, and back (rounded to the type).
+__device__ __forceinline__ void unpack(const Pack<float, 16>& v, float2 (&y)[2]) {
+    y[0] = make_float2(v.e[0], v.e[1]);
+    y[1] = make_float2(v.e[2], v.e[3]);
+}
+__device__ __forceinline__ void unpack(const Pack<__half, 16>& v, float2 (&y)[4]) {
+    const __half2* h = reinterpret_cast<const __half2*>(&v.raw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __half22float2(h[i]);
+}
+__device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, 16>& v, float2 (&y)[4]) {
+    const uint32_t w[4] = {v.raw.x, v.raw.y, v.raw.z, v.raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void pack(Pack<float, 16>& v, const float2 (&y)[2]) {
+    v.e[0] = y[0].x, v.e[1] = y[0].y, v.e[2] = y[1].x, v.e[3] = y[1].y;
+}
+__device__ __forceinline__ void pack(Pack<__half, 16>& v, const float2 (&y)[4]) {
+    __half2* h = reinterpret_cast<__half2*>(&v.raw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __float22half2_rn(y[i]);
+}
+__device__ __forceinline__ void pack(Pack<__nv_bfloat16, 16>& v, const float2 (&y)[4]) {
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v.raw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __float22bfloat162_rn(y[i]);
+}
+// The larger of two vectors' elements, and the largest element of one; NaN where there is one.
+__device__ __forceinline__ Pack<float, 16> larger(const Pack<float, 16>& a, const Pack<float, 16>& b) {
+    Pack<float, 16> m;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m.e[e] = max_nan(a.e[e], b.e[e]);
+    return m;
+}
+template <typename T> struct Two;
+template <> struct Two<__half> { using type = __half2; };
+template <> struct Two<__nv_bfloat16> { using type = __nv_bfloat162; };
+template <typename T>
+__device__ __forceinline__ Pack<T, 16> larger(const Pack<T, 16>& a, const Pack<T, 16>& b) {
+    using T2 = typename Two<T>::type;
+    const T2 *x = reinterpret_cast<const T2*>(&a.raw), *y = reinterpret_cast<const T2*>(&b.raw);
+    Pack<T, 16> m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<T2*>(&m.raw)[i] = __hmax2_nan(x[i], y[i]);
+    return m;
+}
+// Of the first and of the second half of a vector's elements.
+__device__ __forceinline__ float2 half_maxima(const Pack<float, 16>& m) {
+    return make_float2(max_nan(m.e[0], m.e[1]), max_nan(m.e[2], m.e[3]));
+}
+template <typename T>
+__device__ __forceinline__ float2 half_maxima(const Pack<T, 16>& m) {
+    using T2 = typename Two<T>::type;
+    const T2* h = reinterpret_cast<const T2*>(&m.raw);
+    const T2 a = __hmax2_nan(h[0], h[1]), b = __hmax2_nan(h[2], h[3]);
+    return make_float2(max_nan(__low2float(a), __high2float(a)),
+                       max_nan(__low2float(b), __high2float(b)));
+}
+template <typename T>
+__device__ __forceinline__ Pack<T, 16> all_minus_inf() {
+    Pack<T, 16> v;
+#pragma unroll
+    for (int e = 0; e < 16 / (int)sizeof(T); ++e) v.e[e] = from_f32<T>(-INFINITY);
+    return v;
+}
+
+// 2^((y - ref) c), c in two parts: rounded to one float32 it would shift all of a row's terms by up
+// to 6e-8 of their exponent the same way, and with them the sum's logarithm.  Both parts are above 0,
+// so that y = -inf gives 0.
+inline void parts_below(double c, float& hi, float& lo) {
+    hi = (float)c;
+    if ((double)hi >= c) hi = std::nextafter(hi, 0.0f);
+    lo = (float)(c - (double)hi);
+}
+struct Exponent {
+    float2 ref, hi, lo;                    // -ref, c
+    __device__ __forceinline__ Exponent(float at, float h, float l)
+        : ref(make_float2(-at, -at)), hi(make_float2(h, h)), lo(make_float2(l, l)) {}
+    __device__ __forceinline__ float2 operator()(float2 y) const {
+        const float2 d = add2(y, ref), t = fma2(d, hi, mul2(d, lo));
+        return make_float2(ex2(t.x), ex2(t.y));
+    }
+    __device__ __forceinline__ float operator()(float y) const {
+        const float d = y + ref.x;
+        return ex2(__fmaf_rn(d, hi.x, d * lo.x));
+    }
+};
+// The terms of a vector and their sum, as a tree.
+template <typename T, int H>
+__device__ __forceinline__ float terms_of(const Pack<T, 16>& v, const Exponent& f, float2 (&e)[H]) {
+    unpack(v, e);
+#pragma unroll
+    for (int i = 0; i < H; ++i) e[i] = f(e[i]);
+    if constexpr (H == 4) {
+        const float2 s = add2(add2(e[0], e[1]), add2(e[2], e[3]));
+        return s.x + s.y;
+    } else {
+        const float2 s = add2(e[0], e[1]);
+        return s.x + s.y;
+    }
+}
+
+// ------------------------------------------------------------ groups of threads
+// A row is taken by a group: a warp, or a whole block of G threads.
+template <int G>
+struct Group {
+    static constexpr int WARPS = G / 32;
+    struct Space { float f[2 * WARPS]; };  // of a block; a warp needs none
+    __device__ static __forceinline__ int rank() { return G == 32 ? threadIdx.x & 31 : threadIdx.x; }
+    __device__ static __forceinline__ void sync() {
+        if constexpr (G == 32) __syncwarp();
+        else __syncthreads();
+    }
+    __device__ static __forceinline__ float max(float x, Space& s) {
+        x = warp_max_nan(x);
+        if constexpr (G > 32) {
+            if ((threadIdx.x & 31) == 0) s.f[threadIdx.x >> 5] = x;
+            __syncthreads();
+            x = s.f[0];
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w) x = max_nan(x, s.f[w]);
+        }
+        return x;
+    }
+    // Needs a barrier between two of one kind.
+    __device__ static __forceinline__ float sum(float x, Space& s) {
+        x = warp_sum(x);
+        if constexpr (G > 32) {
+            if ((threadIdx.x & 31) == 0) s.f[WARPS + (threadIdx.x >> 5)] = x;
+            __syncthreads();
+            x = s.f[WARPS];
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w) x += s.f[WARPS + w];
+        }
+        return x;
+    }
+};
+
+// ------------------------------------------------ rows through shared memory
+// Every group has a ring of stages; a row comes by one bulk copy of the whole units it lies in,
+// announced at the stage's mbarrier, and is laid out in the stage as in memory.  Units that
+// reach past the tensor's ends are not copied: their elements are loaded one by one.
+constexpr int kWaitPolls = 1 << 22;        // then a wait gives up
+
+__device__ __forceinline__ uint32_t shared_at(const void* p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void mbar_init(uint64_t* bar) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_at(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_mbar_init() {
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void fence_proxy_async() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_at(bar)),
+                 "r"(bytes) : "memory");
+    if (bytes)
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+            ::"r"(shared_at(dst)), "l"(src), "r"(bytes), "r"(shared_at(bar)) : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                 "r"(shared_at(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// A wait that gives up reports it, and later ones of the thread poll once: the kernel ends soon.
+__device__ __forceinline__ void mbar_wait(uint64_t* bar, uint32_t parity, int& polls,
+                                          int32_t* status) {
+    for (int i = 0; i < polls; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred q;\n mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n"
+            " selp.b32 %0, 1, 0, q;\n}"
+            : "=r"(ok) : "r"(shared_at(bar)), "r"(parity) : "memory");
+        if (ok) return;
+    }
+    polls = 1;
+    if (status) *status = RNNT_TIMEOUT;
+}
+
+// A row in a stage: vectors as Row has them.
+template <typename T, int G>
+struct Staged {
+    static constexpr int E = 16 / (int)sizeof(T);
+    Row<T> r;
+    uint4* s;
+    int lo, hi;                            // the vectors that the copy brings
+
+    __device__ __forceinline__ Staged(const T* x, int V, uint4* stage, bool first, bool last)
+        : r(x, V), s(stage) {
+        lo = first && r.off ? 1 : 0;
+        hi = last && (r.off + V) % E ? r.n - 1 : r.n;
+    }
+    __device__ __forceinline__ void fetch(uint64_t* bar) const {       // by one thread
+        const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;
+        bulk_load(s + lo, reinterpret_cast<const uint4*>(r.x - r.off) + lo, bytes, bar);
+    }
+    // After the copy has arrived: what it did not bring, and -inf in place of what is not the row's.
+    __device__ __forceinline__ void complete() const {
+        if (r.off == 0 && r.V % E == 0) return;
+        const int i = Group<G>::rank();
+        T* e = reinterpret_cast<T*>(s);
+        if (i < 2 * E) {
+            const int at = i < E ? i : (r.n - 1) * E + i - E, el = at - r.off;
+            if (i < E || r.n > 1) {
+                if ((unsigned)el >= (unsigned)r.V) e[at] = from_f32<T>(-INFINITY);
+                else if (i < E ? lo > 0 || hi <= lo : hi < r.n) e[at] = r.x[el];
+            }
+        }
+        Group<G>::sync();
+    }
+    __device__ __forceinline__ Pack<T, 16> at(int j) const {
+        Pack<T, 16> v;
+        v.raw = s[j];
+        return v;
+    }
+    __device__ __forceinline__ T& element(int i) const { return reinterpret_cast<T*>(s)[r.off + i]; }
 };
 
 // Device-side memory limits of kernels, raised once per device by `raise()`.
