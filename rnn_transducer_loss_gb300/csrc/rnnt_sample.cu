@@ -7,8 +7,9 @@
 // so what is kept is what reaches one key (value and id).  The token is the first kept id at
 // which the running sum of e, by id, exceeds u times the kept sum.
 //
-// Whether a sum reaches a border decides a whole number, so sums are taken as if held to 40 bits: in
-// pairs of floats, of exponentials that are pairs of floats themselves.
+// Whether a sum reaches a border decides a whole number, so sums are taken as if held to 40 bits:
+// fast ones, of float32 exponentials, come with a bound of their error, and where a border is nearer
+// than that they are taken again in pairs of floats, of exponentials that are pairs themselves.
 #include <cmath>
 
 #include "rnnt_rows.cuh"
@@ -90,6 +91,10 @@ struct SampleParams {
     const float* random;
     const uint8_t* finished;
     int32_t B, K, V, top_k, fused;
+    int32_t unit_tau;                      // temperature 1
+    float scale, scale_low;                // log2 e / tau, in two parts
+    float one, one_low;                    // log2 e
+    float bin_scale;                       // bins of a logit's unit
     Pair inv_tau, top_p;                   // top_p.h >= 1: not used
     double min_gap;                        // tau log min_p, or -inf
     float* out_scores;
@@ -108,117 +113,430 @@ constexpr uint64_t kFinite = (uint64_t)0x00800000u << kIdBits;   // the least ke
 // A mass that is kept is above 0 however far it lies: u = 0 draws the first id.
 constexpr float kLeastMass = 1.17549435e-38f;
 
+// Fast sums are of float32 terms, added as trees of a vector's and then as pairs.  A term is off by at
+// most kTerm and kStep for each of its exponent's binary orders (ex2.approx 2^-22, three additions;
+// the roundings of x - top and of the exponent), relative; the mean order over a row is at most
+// log2 V - log2 sum (its entropy is at most log2 V), which bounds a sum's error.  Of many terms the
+// errors do not all point one way: by Hoeffding's inequality sums of independent ones exceed 8
+// times the root of the squares' sum with a chance below 2e-14; kBias is what ex2.approx may be off
+// on average.  A border nearer to a sum than that is decided on sums of pairs.
+constexpr float kTerm = 4.2e-7f, kStep = 8.3e-8f, kBias = 2e-8f;
+__device__ __forceinline__ float error_of(float sum, int V) {      // absolute; terms are at most 1
+    const float worst = sum * (kTerm + kStep * fmaxf(__log2f((float)V) - __log2f(sum), 0.0f));
+    return fminf(worst, 8.0f * kTerm * sqrtf(sum) + kBias * sum);
+}
+__device__ __forceinline__ Pair add_loosely(Pair a, float b) {     // of sums of positive terms
+    const Pair s = two_sum(a.h, b);
+    return {s.h, __fadd_rn(s.l, a.l)};
+}
+__device__ __forceinline__ float difference(Pair a, Pair b) {
+    return __fadd_rn(__fsub_rn(a.h, b.h), __fsub_rn(a.l, b.l));
+}
+
+constexpr int kBins = 1024;
+constexpr float kBinsPerOrder = 32.0f;     // of the first histogram: bins of 2^(1/32)
+constexpr int kList = 512;                 // elements that are put in order
+
 template <int TH>
 struct Shared {
     static constexpr int WARPS = TH / 32;
-    Pair pairs[WARPS], prefix[WARPS + 1];
+    union {
+        uint32_t bins[kBins];
+        uint64_t order[kList];
+    };
+    uint64_t list[kList];
+    uint32_t groups[32];                   // sums of 32 bins each
+    Pair pairs[2][WARPS], prefix[WARPS + 1];
     float floats[WARPS];
     int ints[WARPS];
-    int token, found;
+    unsigned long long low, high;          // keys
+    uint32_t before;
+    int bin, count, token, found, kept;
+    bool unsure;
 };
 
-template <typename T, int TH>
+// A draw by a block of TH threads; the row lies in shared memory (HERE) or is read from the cache.
+template <typename T, int TH, bool HERE>
 struct Draw {
     static constexpr int E = 16 / (int)sizeof(T), WARPS = TH / 32;
     const SampleParams& p;
     Shared<TH>& sh;
     const Row<T> r;
+    uint4* const here;
     float top;
+    bool unsure;                           // of the last result: the fast sums leave it open
 
-    __device__ __forceinline__ Draw(const SampleParams& a, Shared<TH>& s, const T* x)
-        : p(a), sh(s), r(x, a.V), top(0.0f) {}
+    __device__ __forceinline__ Draw(const SampleParams& a, Shared<TH>& s, const T* x, uint4* stage)
+        : p(a), sh(s), r(x, a.V), here(stage), top(0.0f), unsure(false) {}
 
+    __device__ __forceinline__ Pack<T, 16> at(int j) const {
+        if constexpr (HERE) {
+            Pack<T, 16> v;
+            v.raw = here[j];
+            return v;
+        } else {
+            return r.load(j);
+        }
+    }
+    __device__ __forceinline__ int id_of(int j, int e) const { return j * E + e - r.off; }
+
+    // ---- masses: of pairs (exact), or float32
     __device__ __forceinline__ Pair mass(float x) const {
         const Pair d = two_sum(x, -top);
         const Pair e = exp_pair(mul(d, p.inv_tau));
         return e.h >= kLeastMass ? e : Pair{kLeastMass, 0.0f};
     }
-    __device__ __forceinline__ Pair sum(Pair s) {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s = add(s, shuffled(s, o));
-        if (lane == 0) sh.pairs[threadIdx.x >> 5] = s;
-        __syncthreads();
-        s = lane < WARPS ? sh.pairs[lane] : Pair{0.0f, 0.0f};
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s = add(s, shuffled(s, o));
-        __syncthreads();
-        return s;
+    __device__ __forceinline__ float fast_mass(float x) const {
+        return fmaxf(Exponent(top, p.scale, p.scale_low)(x), kLeastMass);
     }
-    // Of the elements whose keys are at least `least`.
-    __device__ __noinline__ Pair mass_from(uint64_t least) {
+    // What is kept: keys from `least` on.
+    struct Floor {
+        uint64_t least;
+        float value;
+        __device__ __forceinline__ explicit Floor(uint64_t key)
+            : least(key), value(unordered((uint32_t)(key >> kIdBits))) {}
+        __device__ __forceinline__ bool keeps(float x, int id) const {
+            return x > value || (x == value && short_key(x, id) >= least);
+        }
+    };
+    __device__ __forceinline__ float largest(const Pack<T, 16>& v) const {
+        const float2 m = half_maxima(v);
+        return fmaxf(m.x, m.y);
+    }
+    template <bool EXACT>
+    __device__ __forceinline__ Pair mass_of_vector(int j, const Floor& f) const {
+        const Pack<T, 16> v = at(j);
         Pair s{0.0f, 0.0f};
-        for (int j = threadIdx.x; j < r.n; j += TH) {
-            const Pack<T, 16> v = r.load(j);
+        if (!(largest(v) >= f.value)) return s;
+        if constexpr (EXACT) {
 #pragma unroll 1
             for (int e = 0; e < E; ++e) {
                 const float x = to_f32(v.e[e]);
-                if (short_key(x, j * E + e - r.off) >= least && x > -INFINITY) s = add(s, mass(x));
+                if (f.keeps(x, id_of(j, e))) s = add(s, mass(x));
             }
-        }
-        return sum(s);
-    }
-    __device__ __noinline__ int count_from(uint64_t least) {
-        int n = 0;
-        for (int j = threadIdx.x; j < r.n; j += TH) {
-            const Pack<T, 16> v = r.load(j);
+        } else {
+            float t[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float x = to_f32(v.e[e]);
-                n += short_key(x, j * E + e - r.off) >= least && x > -INFINITY;
+                t[e] = f.keeps(x, id_of(j, e)) ? fast_mass(x) : 0.0f;
+            }
+#pragma unroll
+            for (int o = E / 2; o; o /= 2)
+#pragma unroll
+                for (int e = 0; e < o; ++e) t[e] += t[e + o];
+            s.h = t[0];
+        }
+        return s;
+    }
+
+    // ---- over the block
+    __device__ __forceinline__ void sum2(Pair& a, Pair& b) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            a = add(a, shuffled(a, o));
+            b = add(b, shuffled(b, o));
+        }
+        if (lane == 0) {
+            sh.pairs[0][threadIdx.x >> 5] = a;
+            sh.pairs[1][threadIdx.x >> 5] = b;
+        }
+        __syncthreads();
+        a = sh.pairs[0][0];
+        b = sh.pairs[1][0];
+#pragma unroll 1
+        for (int w = 1; w < WARPS; ++w) {
+            a = add(a, sh.pairs[0][w]);
+            b = add(b, sh.pairs[1][w]);
+        }
+        __syncthreads();
+    }
+    // Sums of pairs over the keys from `least` and from `above` on.
+    __device__ __noinline__ void exact_sums(uint64_t least, uint64_t above, Pair& whole,
+                                            Pair& upper) {
+        const Floor f(least);
+        Pair a{0.0f, 0.0f}, b{0.0f, 0.0f};
+        for (int j = threadIdx.x; j < r.n; j += TH) {
+            const Pack<T, 16> v = at(j);
+            if (!(largest(v) >= f.value)) continue;
+#pragma unroll 1
+            for (int e = 0; e < E; ++e) {
+                const float x = to_f32(v.e[e]);
+                if (!f.keeps(x, id_of(j, e))) continue;
+                const Pair m = mass(x);
+                a = add(a, m);
+                if (short_key(x, id_of(j, e)) >= above) b = add(b, m);
             }
         }
-        n = __reduce_add_sync(kAll, n);
-        if ((threadIdx.x & 31) == 0) sh.ints[threadIdx.x >> 5] = n;
-        __syncthreads();
-        n = __reduce_add_sync(kAll, (threadIdx.x & 31) < WARPS ? sh.ints[threadIdx.x & 31] : 0);
-        __syncthreads();
-        return n;
+        sum2(a, b);
+        whole = a;
+        upper = b;
     }
-    // The least key of the first k: fewer than k lie above it.
-    __device__ __noinline__ uint64_t floor_of_count(int k) {
-        uint64_t lo = kFinite, hi = short_key(top, 0);
-        while (lo < hi) {
-            const uint64_t mid = lo + (hi - lo) / 2;
-            if (count_from(mid + 1) < k) hi = mid;
-            else lo = mid + 1;
-        }
-        return lo;
-    }
-    // The least key, from `least` on, above which lies less than the target.
-    __device__ __noinline__ uint64_t floor_of_mass(uint64_t least, Pair target) {
+    // The least key, from `least` on, above which lies less than the target: by bisection.
+    __device__ __noinline__ uint64_t bisect(uint64_t least, Pair target) {
         uint64_t lo = least, hi = short_key(top, 0);
         while (lo < hi) {
             const uint64_t mid = lo + (hi - lo) / 2;
-            if (less(mass_from(mid + 1), target)) hi = mid;
+            Pair whole, upper;
+            exact_sums(mid + 1, mid + 1, whole, upper);
+            if (less(whole, target)) hi = mid;
             else lo = mid + 1;
         }
         return lo;
     }
+
+    // ---- the first histogram's bins: by the exponent
+    __device__ __forceinline__ int bin_of(float x) const {
+        return (int)fminf((top - x) * p.bin_scale, (float)(kBins - 1));
+    }
+    // The bin at whose end `target` is reached (the last filled one if it is not), and what is in
+    // those before it.
+    __device__ __forceinline__ void find_bin(uint32_t target) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        for (int g = warp; g < kBins / 32; g += WARPS) {
+            const uint32_t n = __reduce_add_sync(kAll, sh.bins[g * 32 + lane]);
+            if (lane == 0) sh.groups[g] = n;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const auto find = [&](uint32_t mine, uint32_t& before) {   // the lane that reaches it
+                uint32_t run = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const uint32_t y = __shfl_up_sync(kAll, run, o);
+                    if (lane >= o) run += y;
+                }
+                const unsigned at = __ballot_sync(kAll, mine && before + run >= target);
+                const unsigned some = __ballot_sync(kAll, mine != 0);
+                const int g = at ? __ffs(at) - 1 : some ? 31 - __clz(some) : 0;
+                before += __shfl_sync(kAll, run - mine, g);
+                return g;
+            };
+            uint32_t before = 0;
+            const int g = find(sh.groups[lane], before);
+            const int b = g * 32 + find(sh.bins[g * 32 + lane], before);
+            if (lane == 0) {
+                sh.bin = b;
+                sh.before = before;
+            }
+        }
+        __syncthreads();
+    }
+
+    // Puts a list in order that holds the border of `count` elements (MASS: of `target`, by fast
+    // sums) among the keys from `least` on; returns its length, and in `above` (MASS) the sum of
+    // the masses above the list or (else) `before`, the number of elements above it.
+    // Each turn counts the elements of a range by bins and takes the bin in which the
+    // border lies for the next range, until it holds few enough: first by their
+    // exponents, then by the bits of their keys, which are all different.
+    template <bool MASS>
+    __device__ __noinline__ int list_at(uint64_t least, uint32_t count, float target, float whole,
+                                        Pair& above, uint32_t& before) {
+        const Floor f(least);
+        uint64_t low = 0, high = ~0ull;    // the range; whole at first
+        int shift = -1;                    // of keys to bins; -1: by exponents
+        uint32_t base = 0;                 // elements above the range
+        float mass_above = 0.0f, mass_in = whole;
+        above = Pair{0.0f, 0.0f};
+        for (int turn = 0; turn < 12; ++turn) {
+            for (int i = threadIdx.x; i < kBins; i += TH) sh.bins[i] = 0;
+            if (threadIdx.x == 0) {
+                sh.count = 0;
+                sh.low = ~0ull;
+                sh.high = 0;
+            }
+            __syncthreads();
+            const float unit = MASS ? 2147483648.0f / mass_in : 0.0f;
+            const auto bin = [&](float x, uint64_t key) {
+                return shift < 0 ? bin_of(x) : (int)((high - key) >> shift);
+            };
+            for (int j = threadIdx.x; j < r.n; j += TH) {
+                const Pack<T, 16> v = at(j);
+                if (!(largest(v) >= f.value)) continue;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float x = to_f32(v.e[e]);
+                    const int id = id_of(j, e);
+                    if (!f.keeps(x, id)) continue;
+                    const uint64_t key = short_key(x, id);
+                    if (key < low || key > high) continue;
+                    atomicAdd(&sh.bins[bin(x, key)],
+                              MASS ? __float2uint_rn(fminf(fast_mass(x) * unit, 2147483648.0f)) : 1u);
+                }
+            }
+            __syncthreads();
+            find_bin(MASS ? (uint32_t)fminf(fmaxf((target - mass_above) * unit, 1.0f), 4.0e9f)
+                          : count - base);
+            const int b = sh.bin;
+            Pair over{0.0f, 0.0f}, in{0.0f, 0.0f};
+            uint64_t mine_low = ~0ull, mine_high = 0;
+            for (int j = threadIdx.x; j < r.n; j += TH) {
+                const Pack<T, 16> v = at(j);
+                if (!(largest(v) >= f.value)) continue;
+                float t = 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float x = to_f32(v.e[e]);
+                    const int id = id_of(j, e);
+                    if (!f.keeps(x, id)) continue;
+                    const uint64_t key = short_key(x, id);
+                    if (key < low) continue;
+                    const int at_bin = key > high ? -1 : bin(x, key);
+                    if (at_bin > b) continue;
+                    const float m = MASS ? fast_mass(x) : 0.0f;
+                    if (at_bin < b) {
+                        t += m;
+                        continue;
+                    }
+                    if (MASS) in = add_loosely(in, m);
+                    const int i = atomicAdd(&sh.count, 1);
+                    if (i < kList) sh.list[i] = key;
+                    mine_low = key < mine_low ? key : mine_low;
+                    mine_high = key > mine_high ? key : mine_high;
+                }
+                if (MASS) over = add_loosely(over, t);
+            }
+            if (mine_high) {
+                atomicMin(&sh.low, (unsigned long long)mine_low);
+                atomicMax(&sh.high, (unsigned long long)mine_high);
+            }
+            if (MASS) sum2(over, in);
+            else __syncthreads();
+            const int n = sh.count;
+            above = over;
+            if (!MASS) base += sh.before;
+            if (n <= kList) {
+                for (int i = threadIdx.x; i < n; i += TH) {
+                    const uint64_t key = sh.list[i];
+                    int rank = 0;
+                    for (int o = 0; o < n; ++o) rank += sh.list[o] > key;
+                    sh.order[rank] = key;              // where the bins were
+                }
+                __syncthreads();
+                before = base;
+                return n;
+            }
+            low = sh.low;
+            high = sh.high;
+            mass_above = over.h;
+            mass_in = in.h;
+            shift = 0;
+            while ((high - low) >> shift >= kBins) ++shift;
+            __syncthreads();
+        }
+        before = base;
+        return 0;                          // not reached: a turn leaves 1/1024 of a range of 52 bits
+    }
+
+    // The least key of the first k.
+    __device__ __forceinline__ uint64_t floor_of_count(int k) {
+        Pair above;
+        uint32_t before;
+        const int n = list_at<false>(kFinite, (uint32_t)k, 0.0f, 0.0f, above, before);
+        const int at = min(k - 1 - (int)before, n - 1);    // fewer than k finite ones: the last
+        const uint64_t key = at >= 0 ? sh.order[at] : kFinite;
+        __syncthreads();
+        return key;
+    }
+
+    // How many of the list's n elements are kept: those before which, with what is above the list,
+    // less than the target lies.  -1: the border is not in the list.
+    template <bool EXACT>
+    __device__ __noinline__ int kept_of_list(int n, Pair above, Pair target, float error) {
+        const int lane = threadIdx.x & 31;
+        if (threadIdx.x < 32) {
+            constexpr int EACH = kList / 32;
+            Pair s{0.0f, 0.0f};
+            const int i0 = lane * EACH;
+            for (int i = i0; i < min(n, i0 + EACH); ++i) {
+                const float x = unordered((uint32_t)(sh.order[i] >> kIdBits));
+                s = add(s, EXACT ? mass(x) : Pair{fast_mass(x), 0.0f});
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const Pair y = shuffled_up(s, o);
+                if (lane >= o) s = add(s, y);
+            }
+            Pair run = shuffled_up(s, 1);
+            run = lane ? add(above, run) : above;
+            int kept = 0;
+            bool close = false;
+            for (int i = i0; i < min(n, i0 + EACH); ++i) {
+                kept += less(run, target);
+                close |= fabsf(difference(run, target)) <= error;
+                const float x = unordered((uint32_t)(sh.order[i] >> kIdBits));
+                run = add(run, EXACT ? mass(x) : Pair{fast_mass(x), 0.0f});
+            }
+            // behind the list's end
+            const Pair end = add(above, Pair{__shfl_sync(kAll, s.h, 31), __shfl_sync(kAll, s.l, 31)});
+            kept = __reduce_add_sync(kAll, kept);
+            if (kept == 0 && !less(above, target)) kept = -1;
+            if (less(end, target)) kept = -1;
+            close |= fabsf(difference(end, target)) <= error;
+            close = __any_sync(kAll, close);
+            if (lane == 0) {
+                sh.kept = kept;
+                sh.unsure = close;
+            }
+        }
+        __syncthreads();
+        const int kept = sh.kept;
+        unsure = sh.unsure || kept < 0;
+        __syncthreads();
+        return kept;
+    }
+    // The least key of the first ones, from `least` on, whose masses reach top_p of theirs.
+    __device__ __forceinline__ uint64_t floor_of_mass(uint64_t least, Pair whole) {
+        Pair above;
+        uint32_t before;
+        Pair target = mul(whole, p.top_p);
+        const int n = list_at<true>(least, 0, target.h, whole.h, above, before);
+        int kept = kept_of_list<false>(n, above, target, 2.0f * error_of(whole.h, p.V));
+        if (unsure && n) {
+            // the sums again, to 40 bits, over the same list
+            Pair exact, upper;
+            exact_sums(least, sh.order[0] + 1, exact, upper);
+            target = mul(exact, p.top_p);
+            kept = kept_of_list<true>(n, upper, target, 0.0f);
+        }
+        // a border outside the list (the histogram's masses are rounded): by bisection
+        const uint64_t key = kept > 0 && n ? sh.order[kept - 1] : 0;
+        __syncthreads();
+        return key ? key : bisect(least, target);
+    }
+
     // The first id of a key from `least` on at which the running sum exceeds u of the whole.
     // A warp takes a piece of the row; the one in whose piece the border lies goes through it.
+    template <bool EXACT>
     __device__ __noinline__ int token_from(uint64_t least, float u) {
+        const Floor f(least);
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const int each = (r.n + WARPS - 1) / WARPS, j0 = warp * each, j1 = min(r.n, j0 + each);
+        const int each = (r.n + WARPS - 1) / WARPS, j0 = min(r.n, warp * each);
+        const int j1 = min(r.n, j0 + each);
         Pair s{0.0f, 0.0f};
-        for (int j = j0 + lane; j < j1; j += 32) s = add(s, mass_of_vector(j, least));
+        for (int j = j0 + lane; j < j1; j += 32)
+            s = EXACT ? add(s, mass_of_vector<true>(j, f))
+                      : add_loosely(s, mass_of_vector<false>(j, f).h);
 #pragma unroll
         for (int o = 16; o; o >>= 1) s = add(s, shuffled(s, o));
-        if (lane == 0) sh.pairs[warp] = s;
-        if (threadIdx.x == 0) sh.found = WARPS;
+        if (lane == 0) sh.pairs[0][warp] = s;
         __syncthreads();
         if (threadIdx.x == 0) {
             Pair run{0.0f, 0.0f};
             int last = 0;
+#pragma unroll 1
             for (int w = 0; w < WARPS; ++w) {
                 sh.prefix[w] = run;
-                run = add(run, sh.pairs[w]);
-                if (sh.pairs[w].h > 0.0f) last = w;
+                run = add(run, sh.pairs[0][w]);
+                if (sh.pairs[0][w].h > 0.0f) last = w;
             }
             const Pair border = mul(run, Pair{u, 0.0f});
             sh.prefix[WARPS] = border;
+            sh.floats[0] = EXACT ? 0.0f : 2.0f * error_of(run.h, p.V);
             int w = 0;                     // the first piece at whose end the border is passed
-            while (w < last && !less(border, add(sh.prefix[w], sh.pairs[w]))) ++w;
+#pragma unroll 1
+            while (w < last && !less(border, add(sh.prefix[w], sh.pairs[0][w]))) ++w;
             sh.found = w;
         }
         __syncthreads();
@@ -226,8 +544,9 @@ struct Draw {
             const Pair border = sh.prefix[WARPS];
             Pair run = sh.prefix[warp];
             int token = -1;
+            Pair before = run, after = run;                // of the token
             for (int j = j0; j < j1; j += 32) {
-                Pair s = j + lane < j1 ? mass_of_vector(j + lane, least) : Pair{0.0f, 0.0f};
+                Pair s = j + lane < j1 ? mass_of_vector<EXACT>(j + lane, f) : Pair{0.0f, 0.0f};
                 const Pair mine = s;
 #pragma unroll
                 for (int o = 1; o < 32; o *= 2) {
@@ -237,45 +556,47 @@ struct Draw {
                 const Pair end = add(run, s);
                 const unsigned some = __ballot_sync(kAll, mine.h > 0.0f);
                 const unsigned past = __ballot_sync(kAll, mine.h > 0.0f && less(border, end));
-                // the vector that passes the border, or (where the sums' last bits differ) the last
-                // that holds a kept element so far
-                const int at = past ? __ffs(past) - 1 : 31 - __clz(some);
                 if (some) {
-                    Pair before = shuffled_up(s, 1);
-                    before = lane ? add(run, before) : run;
+                    // the vector that passes the border, or (where the sums' last bits differ)
+                    // the last that holds a kept element so far
+                    const int at_lane = past ? __ffs(past) - 1 : 31 - __clz(some);
+                    Pair upto = shuffled_up(s, 1);
+                    upto = lane ? add(run, upto) : run;
                     int got = -1;
-                    if (lane == at) {
-                        const Pack<T, 16> v = r.load(j + lane);
+                    Pair ahead = upto;
+                    if (lane == at_lane) {
+                        const Pack<T, 16> v = at(j + lane);
 #pragma unroll 1
                         for (int e = 0; e < E; ++e) {
                             const float x = to_f32(v.e[e]);
-                            const int id = (j + lane) * E + e - r.off;
-                            if (x > -INFINITY && short_key(x, id) >= least) {
-                                got = id;
-                                before = add(before, mass(x));
-                                if (past && less(border, before)) break;
-                            }
+                            if (!f.keeps(x, id_of(j + lane, e))) continue;
+                            got = id_of(j + lane, e);
+                            ahead = upto;
+                            upto = add(upto, EXACT ? mass(x) : Pair{fast_mass(x), 0.0f});
+                            if (past && less(border, upto)) break;
                         }
                     }
-                    token = __shfl_sync(kAll, got, at);
+                    token = __shfl_sync(kAll, got, at_lane);
+                    before = Pair{__shfl_sync(kAll, ahead.h, at_lane), __shfl_sync(kAll, ahead.l, at_lane)};
+                    after = Pair{__shfl_sync(kAll, upto.h, at_lane), __shfl_sync(kAll, upto.l, at_lane)};
                 }
                 if (past) break;
                 run = Pair{__shfl_sync(kAll, end.h, 31), __shfl_sync(kAll, end.l, 31)};
             }
-            if (lane == 0) sh.token = token;
+            if (lane == 0) {
+                // certain where nothing is kept before the token, and on its other side as u < 1
+                const float error = sh.floats[0];
+                const bool low = before.h > 0.0f && difference(border, before) <= error;
+                const bool high = difference(after, border) <= error;
+                sh.token = token;
+                sh.unsure = low || high;
+            }
         }
         __syncthreads();
-        return sh.token;
-    }
-    __device__ __noinline__ Pair mass_of_vector(int j, uint64_t least) {
-        const Pack<T, 16> v = r.load(j);
-        Pair s{0.0f, 0.0f};
-#pragma unroll 1
-        for (int e = 0; e < E; ++e) {
-            const float x = to_f32(v.e[e]);
-            if (x > -INFINITY && short_key(x, j * E + e - r.off) >= least) s = add(s, mass(x));
-        }
-        return s;
+        unsure = sh.unsure;
+        const int token = sh.token;
+        __syncthreads();
+        return token;
     }
 };
 
@@ -287,9 +608,10 @@ __device__ __forceinline__ float score_of(float score, float x, float top, float
     return add(add(two_sum(x, -top), Pair{-lse, 0.0f}), Pair{score, 0.0f}).h;
 }
 
-template <typename T, int TH>
+template <typename T, int TH, bool HERE>
 __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
     constexpr int E = 16 / (int)sizeof(T), WARPS = TH / 32;
+    extern __shared__ uint4 stage[];
     __shared__ Shared<TH> sh;
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const int b = row / p.K, k = row - b * p.K;
@@ -301,48 +623,65 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
     if (bad) out = -INFINITY;
     if (!bad && !finished && score > -INFINITY) {
         const T* x = reinterpret_cast<const T*>(p.logits + b * p.batch_stride + k * p.beam_stride);
-        Draw<T, TH> d(p, sh, x);
-        float m = -INFINITY;
-        for (int j = tid; j < d.r.n; j += TH) {
-            const Pack<T, 16> v = d.r.load(j);
+        Draw<T, TH, HERE> d(p, sh, x, stage);
+        Pack<T, 16> most = all_minus_inf<T>();
+        for (int j0 = tid; j0 < d.r.n; j0 += 4 * TH) {     // four loads in flight
+            Pack<T, 16> v[4];
 #pragma unroll
-            for (int e = 0; e < E; ++e) m = max_nan(m, to_f32(v.e[e]));
+            for (int i = 0; i < 4; ++i)
+                v[i] = j0 + i * TH < d.r.n ? d.r.load(j0 + i * TH) : all_minus_inf<T>();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                most = larger(most, v[i]);
+                if (HERE && j0 + i * TH < d.r.n) stage[j0 + i * TH] = v[i].raw;
+            }
         }
-        m = warp_max_nan(m);
+        const float2 both = half_maxima(most);
+        float m = warp_max_nan(max_nan(both.x, both.y));
         if (lane == 0) sh.floats[tid >> 5] = m;
         __syncthreads();
         m = warp_max_nan(lane < WARPS ? sh.floats[lane] : -INFINITY);
-        __syncthreads();
         bad = !(m < INFINITY);
         if (!bad && m > -INFINITY) {
             d.top = m;
-            float lse = 0.0f;
-            if (p.fused) {
-                Pair s{0.0f, 0.0f};
+            // the whole row's sums at the temperature and at 1, where they are wanted
+            const bool at_tau = p.top_p.h < 1.0f || (p.fused && p.unit_tau);
+            const bool at_one = p.fused && !p.unit_tau;
+            Pair s{0.0f, 0.0f}, s1{0.0f, 0.0f};
+            if (at_tau || at_one) {
+                const Exponent f(m, p.scale, p.scale_low), f1(m, p.one, p.one_low);
                 for (int j = tid; j < d.r.n; j += TH) {
-                    const Pack<T, 16> v = d.r.load(j);
-                    float part = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) part += ex2((to_f32(v.e[e]) - m) * (float)kLog2e);
-                    s = add(s, Pair{part, 0.0f});
+                    const Pack<T, 16> v = d.at(j);
+                    float2 e[E / 2];
+                    if (at_tau) s = add_loosely(s, terms_of(v, f, e));
+                    if (at_one) s1 = add_loosely(s1, terms_of(v, f1, e));
                 }
-                lse = logf(d.sum(s).h);
+                d.sum2(s, s1);
             }
+            const float lse = p.fused ? logf(p.unit_tau ? s.h : s1.h) : 0.0f;
             uint64_t least = kFinite;
             if (p.top_k && p.top_k < p.V) least = d.floor_of_count(p.top_k);
-            uint64_t floor = least;
-            if (p.top_p.h < 1.0f) floor = d.floor_of_mass(least, mul(d.mass_from(least), p.top_p));
+            uint64_t by_gap = 0;
             if (p.min_gap > -INFINITY) {
                 // the least float32 that is not below top + tau log min_p
-                const double border = (double)m + p.min_gap;
-                const float f = __double2float_ru(border);
-                if (f > -INFINITY) {
-                    const uint64_t by_gap = (uint64_t)ordered(f) << kIdBits;
-                    floor = by_gap > floor ? by_gap : floor;
-                }
+                const float f = __double2float_ru((double)m + p.min_gap);
+                if (f > -INFINITY) by_gap = (uint64_t)ordered(f) << kIdBits;
             }
-            token = d.token_from(floor, u);
-            out = score_of(score, to_f32(x[token]), m, lse, p.fused);
+            uint64_t floor = least;
+            if (p.top_p.h < 1.0f) {
+                if (least != kFinite) {                    // of what top_k has left
+                    const typename Draw<T, TH, HERE>::Floor f(least);
+                    s = s1 = Pair{0.0f, 0.0f};
+                    for (int j = tid; j < d.r.n; j += TH)
+                        s = add_loosely(s, d.template mass_of_vector<false>(j, f).h);
+                    d.sum2(s, s1);
+                }
+                floor = d.floor_of_mass(least, s);
+            }
+            floor = by_gap > floor ? by_gap : floor;
+            token = d.template token_from<false>(floor, u);
+            if (d.unsure) token = d.template token_from<true>(floor, u);
+            if (token >= 0) out = score_of(score, to_f32(x[token]), m, lse, p.fused);
         }
     }
     if (tid == 0) {
@@ -352,11 +691,27 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
     }
 }
 
+constexpr size_t kHere = 200 << 10;        // bytes of a row that a block holds in shared memory
+
 template <typename T>
 void launch_sample(const SampleParams& p, cudaStream_t st) {
     const unsigned rows = (unsigned)(p.B * p.K);
-    if ((int64_t)p.V * (int64_t)sizeof(T) <= 16 << 10) k_sample<T, 128><<<rows, 128, 0, st>>>(p);
-    else k_sample<T, 1024><<<rows, 1024, 0, st>>>(p);
+    const size_t bytes = ((size_t)p.V * sizeof(T) + 30) / 16 * 16;         // at any alignment
+    if (bytes <= 4 << 10) k_sample<T, 128, true><<<rows, 128, bytes, st>>>(p);
+    else if (bytes <= 32 << 10) k_sample<T, 256, true><<<rows, 256, bytes, st>>>(p);
+    else if (bytes <= kHere) k_sample<T, 512, true><<<rows, 512, bytes, st>>>(p);
+    else k_sample<T, 512, false><<<rows, 512, 0, st>>>(p);
+}
+template <typename T>
+bool raise_sample() {
+    return cudaFuncSetAttribute(k_sample<T, 512, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)kHere) == cudaSuccess;
+}
+bool sample_prepared() {
+    static std::atomic<bool> done[64];
+    return prepared_once(done, [] {
+        return raise_sample<float>() && raise_sample<__half>() && raise_sample<__nv_bfloat16>();
+    });
 }
 
 }  // namespace
@@ -400,6 +755,10 @@ extern "C" rnnt_status_t rnnt_sample(const void* logits, rnnt_dtype_t dt, int32_
     p.V = V;
     p.top_k = top_k;
     p.fused = fused_log_softmax != 0;
+    p.unit_tau = temperature == 1.0;
+    parts_below(kLog2e / temperature, p.scale, p.scale_low);
+    parts_below(kLog2e, p.one, p.one_low);
+    p.bin_scale = (float)(kLog2e / temperature) * kBinsPerOrder;
     p.inv_tau = pair_of(1.0 / temperature);
     p.top_p = top_p < 1.0 ? pair_of(top_p) : Pair{2.0f, 0.0f};
     p.min_gap = min_p > 0.0 ? temperature * std::log(min_p) : -INFINITY;
@@ -407,7 +766,7 @@ extern "C" rnnt_status_t rnnt_sample(const void* logits, rnnt_dtype_t dt, int32_
     p.out_tokens = out_tokens;
     p.status = status_dev;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (!clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
+    if (!sample_prepared() || !clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
     with_type(dt, [&](auto t) { launch_sample<decltype(t)>(p, st); });
     return launched();
 }
