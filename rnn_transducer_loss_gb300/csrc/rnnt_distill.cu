@@ -247,41 +247,6 @@ struct TopScratch {
     int count;
 };
 
-// Sorted in descending order over the warp (bitonic).
-__device__ __forceinline__ float warp_sorted(float x) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int size = 2; size <= 32; size *= 2) {
-#pragma unroll
-        for (int o = size / 2; o; o >>= 1) {
-            const float y = __shfl_xor_sync(kAll, x, o);
-            const bool larger = ((lane & o) == 0) == ((lane & size) == 0 || size == 32);
-            x = larger ? fmaxf(x, y) : fminf(x, y);
-        }
-    }
-    return x;
-}
-
-// The elements of a vector that are at least `least`, as bits.
-__device__ __forceinline__ uint32_t reaching(const Pack<float, 16>& v, float least) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m |= v.e[e] >= least ? 1u << e : 0u;
-    return m;
-}
-template <typename T>
-__device__ __forceinline__ uint32_t reaching(const Pack<T, 16>& v, float least) {
-    using T2 = typename Two<T>::type;
-    const T one = from_f32<T>(least);                      // a value of the type
-    T2 two;
-    two.x = one, two.y = one;
-    const T2* h = reinterpret_cast<const T2*>(&v.raw);
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m |= __hge2_mask(h[i], two) & (0x00020001u << (2 * i));
-    return (m | m >> 16) & 0xffu;
-}
-
 // Rows through a ring of shared memory, a group of threads each.  The k best of a row: the
 // largest maxima of its threads (of both halves of their vectors where k needs more than there are
 // threads in a warp) bound the k + 1-st best from below; the few elements that reach the bound are
@@ -350,10 +315,10 @@ __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) 
                     for (int w = 0; w < WARPS; ++w) bound = fminf(bound, sh.bounds[w]);
                 }
                 // -inf reaches no bound
-                bound = fmaxf(bound, sizeof(T) == 4 ? -kMost
-                                     : std::is_same_v<T, __half> ? -65504.0f : -3.38953139e38f);
+                bound = fmaxf(bound, lowest<T>());
+                const T at_least = from_f32<T>(bound);     // a value of the type
                 for (int j = me; j < x.r.n; j += G) {
-                    uint32_t hits = reaching(x.at(j), bound);
+                    uint32_t hits = reaching(x.at(j), at_least);
                     while (hits) {
                         const int e = __ffs(hits) - 1, i = j * E + e - x.r.off;
                         hits &= hits - 1;
@@ -400,7 +365,7 @@ __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) 
                     x.element(element_of(sh.best[i])) = from_f32<T>(-INFINITY);
                 Gr::sync();
                 float first = n > k ? value_of(sh.best[k]) : -INFINITY;
-                if (n == k && bound > -kMost) {
+                if (n == k && bound > lowest<T>()) {
                     Pack<T, 16> m = all_minus_inf<T>();
                     for (int j = me; j < x.r.n; j += G) m = larger(m, x.at(j));
                     both = half_maxima(m);
@@ -946,6 +911,271 @@ __global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Rin
     }
 }
 
+// ------------------------------------------------------------------ short rows
+// A warp takes 32 consecutive rows, which are one aligned piece of memory whatever V is, through its
+// part of shared memory, and a thread each of them: no reductions, no idle lanes.
+struct ShortBatch {
+    int32_t stage_bytes, warp_bytes;       // of a warp: the rows; with what is behind them
+};
+constexpr int kShortThreads = 128;
+constexpr int kShortRow = 512;             // bytes of a row, at most
+
+// A thread's row in shared memory.  Its elements are gone through from `start` on, which turns with
+// the thread so that a warp's accesses lie in different banks where V is even.
+template <typename T>
+struct ShortRow {
+    using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+    static constexpr Bits kTaken = (Bits)~0u;              // a NaN; rows with one are left out before
+    T* s;
+    int V, start;
+    __device__ __forceinline__ ShortRow(T* rows, int size) : V(size) {
+        const int lane = threadIdx.x & 31;
+        s = rows + lane * V;
+        start = sizeof(T) == 4 ? (V % 2 ? 0 : lane) : (V % 4 ? 0 : 2 * lane);
+        start %= V;
+    }
+    __device__ __forceinline__ Bits& bits(int i) const { return reinterpret_cast<Bits*>(s)[i]; }
+    template <typename F>
+    __device__ __forceinline__ void each(F&& f) const {
+#pragma unroll 4
+        for (int i = start; i < V; ++i) f(i, s[i]);
+#pragma unroll 4
+        for (int i = 0; i < start; ++i) f(i, s[i]);
+    }
+};
+
+// Brings `n` rows from row0 on; all lanes call it.
+template <typename T>
+__device__ __forceinline__ void fetch_short(const char* logits, int64_t row0, int n, int V, T* stage,
+                                            uint64_t* bar, uint32_t& phase, int& polls,
+                                            int32_t* status) {
+    const int lane = threadIdx.x & 31;
+    const T* x = reinterpret_cast<const T*>(logits) + row0 * V;
+    const uint32_t bytes = (uint32_t)(n * V) * (uint32_t)sizeof(T), whole = bytes & ~15u;
+    if (lane == 0) {
+        fence_proxy_async();
+        bulk_load(stage, x, whole, bar);
+    }
+    const int i = (int)(whole / sizeof(T)) + lane;         // behind the last whole unit
+    if (i < n * V) stage[i] = x[i];
+    mbar_wait(bar, phase, polls, status);
+    phase ^= 1;
+    __syncwarp();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kShortThreads) k_top_short(const TopParams p, const ShortBatch sb) {
+    extern __shared__ __align__(16) char space[];
+    __shared__ uint64_t bars[kShortThreads / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = p.k;
+    char* const mine = space + warp * sb.warp_bytes;
+    T* const stage = reinterpret_cast<T*>(mine);
+    T* const values = reinterpret_cast<T*>(mine + sb.stage_bytes);
+    int32_t* const ids = reinterpret_cast<int32_t*>(mine + sb.stage_bytes + 128 * k);
+    uint64_t* const bar = &bars[warp];
+    if (blockIdx.x == 0 && p.lat.T) check_lengths<kShortThreads>(p.lat, p.status);
+    if (lane == 0) {
+        mbar_init(bar);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    int polls = kWaitPolls;
+    uint32_t phase = 0;
+    const int64_t step = (int64_t)gridDim.x * (kShortThreads / 32) * 32;
+    for (int64_t row0 = ((int64_t)blockIdx.x * (kShortThreads / 32) + warp) * 32; row0 < p.lat.rows;
+         row0 += step) {
+        const int n = (int)min((int64_t)32, p.lat.rows - row0);
+        fetch_short(p.logits, row0, n, p.V, stage, bar, phase, polls, p.status);
+        const ShortRow<T> r(stage, p.V);
+        float rest = -INFINITY;
+        int have = 0;
+        const int64_t row = row0 + lane;
+        if (lane < n && (!p.lat.T || p.lat.inside(row))) {
+            float top = -INFINITY;
+            r.each([&](int, T x) { top = max_nan(top, to_f32(x)); });
+            if (!(top < INFINITY)) {                       // NaN or +inf: the row is left empty
+                invalid(p.status);
+            } else {
+                float best = -INFINITY;
+                for (int q = 0; q <= k; ++q) {             // the last is the largest of the rest
+                    best = -INFINITY;
+                    int at = p.V;
+                    r.each([&](int i, T x) {
+                        const float y = to_f32(x);
+                        if (y > best || (y == best && i < at)) {
+                            best = y;
+                            at = i;
+                        }
+                    });
+                    if (best == -INFINITY || q == k) break;
+                    values[lane * k + q] = from_f32<T>(best);
+                    ids[lane * k + q] = at;
+                    have = q + 1;
+                    r.s[at] = from_f32<T>(-INFINITY);
+                }
+                if (best > -INFINITY) {
+                    const Exponent f(best, p.scale, p.scale_low);
+                    float sum = 0.0f;
+                    r.each([&](int, T x) { sum += f(to_f32(x)); });
+                    rest = fmaxf(logf(sum) + best * p.inv_tau, -kMost);
+                }
+            }
+        }
+        if (lane < n) {
+            for (int q = have; q < k; ++q) {
+                values[lane * k + q] = from_f32<T>(-INFINITY);
+                ids[lane * k + q] = -1;
+            }
+            p.rest[row] = rest;
+        }
+        __syncwarp();
+        for (int i = lane; i < n * k; i += 32) {
+            reinterpret_cast<T*>(p.values)[row0 * k + i] = values[i];
+            p.ids[row0 * k + i] = ids[i];
+        }
+        __syncwarp();
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillParams p,
+                                                                 const ShortBatch sb) {
+    extern __shared__ __align__(16) char space[];
+    __shared__ uint64_t bars[kShortThreads / 32];
+    __shared__ int64_t space64[kShortThreads / 32];
+    using Bits = typename ShortRow<T>::Bits;
+    constexpr Bits kTaken = ShortRow<T>::kTaken;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    char* const mine = space + warp * sb.warp_bytes;
+    T* const stage = reinterpret_cast<T*>(mine);
+    float* const ats = reinterpret_cast<float*>(mine + sb.stage_bytes);    // [k][32]
+    uint64_t* const bar = &bars[warp];
+    let_next_start();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
+    const int64_t rows = p.lat.padded ? p.lat.rows : compact_rows<kShortThreads>(p.lat, space64);
+    if (lane == 0) {
+        mbar_init(bar);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    int polls = kWaitPolls;
+    uint32_t phase = 0;
+    const int64_t step = (int64_t)gridDim.x * (kShortThreads / 32) * 32;
+    for (int64_t row0 = ((int64_t)blockIdx.x * (kShortThreads / 32) + warp) * 32; row0 < p.lat.rows;
+         row0 += step) {
+        const int n = (int)min((int64_t)32, p.lat.rows - row0);
+        fetch_short(p.logits, row0, n, p.V, stage, bar, phase, polls, p.status);
+        const ShortRow<T> r(stage, p.V);
+        const int64_t row = row0 + lane, first = row * p.k;
+        float loss = 0.0f, c = 0.0f, inner = 0.0f, outside = -INFINITY, weight = 0.0f;
+        float t_top = -INFINITY, top = -INFINITY;
+        bool some = false;
+        if (lane < n && row < rows && (!p.lat.padded || p.lat.inside(row))) {
+            bool bad = false;
+            float most = -INFINITY;
+            r.each([&](int, T x) { most = max_nan(most, to_f32(x)); });
+            const bool fine = most < INFINITY;
+            // the places: their logits are put aside, and what they leave is marked; +inf: an empty one
+            for (int q = 0; q < p.k; ++q) {
+                const int id = p.ids[first + q];
+                float at = INFINITY;
+                bad |= id >= p.V;
+                if ((unsigned)id < (unsigned)p.V) {
+                    if (r.bits(id) == kTaken && fine) {
+                        bad = true;                        // an id again
+                    } else {
+                        const float x = teacher_logit(p, first + q);
+                        float t = x * p.inv_tau;
+                        if (t == -INFINITY && x != -INFINITY) t = -kMost;
+                        bad |= !(t < INFINITY);
+                        at = fine ? to_f32(r.s[id]) : -INFINITY;
+                        r.bits(id) = kTaken;
+                        t_top = max_nan(t_top, t);
+                        top = fmaxf(top, at);
+                    }
+                }
+                ats[q * 32 + lane] = at;
+            }
+            const float rest = p.rest ? p.rest[row] : -INFINITY;
+            bad |= !(rest < INFINITY);
+            t_top = max_nan(t_top, rest);
+            some = t_top != -INFINITY;                     // NaN counts
+            if (some) {
+                r.each([&](int i, T x) {
+                    if (r.bits(i) != kTaken) outside = fmaxf(outside, to_f32(x));
+                });
+                const Exponent f(outside == -INFINITY ? 0.0f : outside, p.scale, p.scale_low);
+                float left = 0.0f;
+                r.each([&](int i, T x) { left += r.bits(i) != kTaken ? f(to_f32(x)) : 0.0f; });
+                const Exponent g(top, p.scale, p.scale_low);
+                float sum = 0.0f, w_sum = 0.0f, w_log = 0.0f;
+                for (int q = 0; q < p.k; ++q) {
+                    const float at = ats[q * 32 + lane];
+                    if (at == INFINITY) continue;
+                    sum += at == -INFINITY ? 0.0f : g(at);
+                    const float x = teacher_logit(p, first + q);
+                    if (x == -INFINITY) continue;
+                    const float t = fmaxf(x * p.inv_tau, -kMost) - t_top, w = x != x ? x : expf(t);
+                    w_sum += w;
+                    if (w != 0.0f)
+                        w_log += at == -INFINITY ? INFINITY : w * (t - (at - top) * p.inv_tau);
+                }
+                const float w_rest = rest == -INFINITY ? 0.0f : expf(rest - t_top);
+                const Whole w(p, outside, left, top, sum);
+                const bool good = fine && w.good();
+                bad |= !good;
+                const float all = w_sum + w_rest, ratio = logf(w.total / all);
+                float kl = w_sum == 0.0f ? 0.0f
+                                         : w_log + w_sum * (ratio - (top - w.base) * p.inv_tau);
+                if (w_rest != 0.0f)
+                    kl += w_rest * ((rest - t_top) - (outside - w.base) * p.inv_tau + ratio -
+                                    logf(left));
+                loss = good ? kl / all : NAN;
+                c = good ? w.factor(p, left, w_rest / all) : NAN;
+                inner = good ? w.inner / w.total : NAN;
+                weight = 1.0f / all;
+            }
+            if (bad) invalid(p.status);
+        }
+        if (lane < n) p.row_loss[row] = loss;
+        if (!p.grad) {
+            __syncwarp();
+            continue;
+        }
+        if (lane < n && some) {
+            const Exponent f(outside == -INFINITY ? 0.0f : outside, p.scale, p.scale_low);
+            const Exponent g(top, p.scale, p.scale_low);
+            r.each([&](int i, T x) {
+                if (r.bits(i) != kTaken || c != c) r.s[i] = from_f32<T>(f(to_f32(x)) * c);
+            });
+            for (int q = 0; q < p.k; ++q) {
+                const float at = ats[q * 32 + lane];
+                if (at == INFINITY) continue;
+                const float x = teacher_logit(p, first + q);
+                const float t = fmaxf(x * p.inv_tau, -kMost) - t_top;
+                const float prob = x == -INFINITY ? 0.0f : (x != x ? x : expf(t)) * weight;
+                const float e = at == -INFINITY ? 0.0f : g(at);
+                r.s[p.ids[first + q]] = from_f32<T>((e * inner - prob) * p.grad_scale);
+            }
+        } else if (lane < n) {
+            for (int i = 0; i < p.V; ++i) r.s[i] = from_f32<T>(0.0f);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        T* const y = reinterpret_cast<T*>(p.grad) + row0 * p.V;
+        const uint32_t bytes = (uint32_t)(n * p.V) * (uint32_t)sizeof(T), whole = bytes & ~15u;
+        const int i = (int)(whole / sizeof(T)) + lane;     // behind the last whole unit
+        if (i < n * p.V) y[i] = stage[i];
+        if (lane == 0) {
+            if (whole) bulk_store(y, stage, whole);
+            bulk_commit();
+            bulk_wait_read<0>();                           // the stage is free again
+        }
+        __syncwarp();
+    }
+    if (lane == 0) bulk_wait_all();
+}
+
 // A block a sample: its rows' losses, added in float64 in an order that depends on the lengths
 // alone; the last block adds the samples.  The compact layout's row offsets stay in the workspace
 // for the gradient's scaling.
@@ -1122,13 +1352,32 @@ unsigned grid_of(const Shape& s, K kernel, int threads) {
     return (unsigned)std::min<int64_t>(s.blocks, (int64_t)kSMs * per_sm);
 }
 
+// Rows that are short enough for a thread each.
+bool short_rows(const void* logits, int32_t V, int es) {
+    return (size_t)V * es <= kShortRow && ((uintptr_t)logits & 15) == 0;
+}
+ShortBatch short_batch(int32_t V, int es, size_t behind) {
+    ShortBatch sb;
+    sb.stage_bytes = 32 * V * es;
+    sb.warp_bytes = (int32_t)(((size_t)sb.stage_bytes + behind + 127) & ~size_t(127));
+    return sb;
+}
+template <typename K>
+unsigned short_grid(K kernel, int64_t rows, size_t shared) {
+    Shape s{};
+    s.shared = shared;
+    s.blocks = (rows + kShortThreads - 1) / kShortThreads;
+    return grid_of(s, kernel, kShortThreads);
+}
+
 template <typename T>
 bool raise_top() {
     const auto raise = [](auto kernel) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)kShared) == cudaSuccess;
     };
-    return raise(k_top<T, kWarpThreads, 32>) && raise(k_top<T, kBlockThreads, kBlockThreads>);
+    return raise(k_top<T, kWarpThreads, 32>) && raise(k_top<T, kBlockThreads, kBlockThreads>) &&
+           raise(k_top_short<T>) && raise(k_distill_short<T>);
 }
 // Calls f(k_distill's form for rows of n vectors and k places).
 template <typename T, typename F>
@@ -1221,6 +1470,14 @@ extern "C" rnnt_status_t rnnt_top_logits(const void* logits, rnnt_dtype_t dt, in
     if (!distill_prepared() || !clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
     with_type(dt, [&](auto t) {
         using T = decltype(t);
+        // the best are taken one by one, in k + 1 looks at the row
+        if (short_rows(logits, V, es) && (k + 1) * V <= 2048) {
+            const ShortBatch sb = short_batch(V, es, (size_t)256 * k);
+            const size_t shared = (size_t)sb.warp_bytes * (kShortThreads / 32);
+            k_top_short<T><<<short_grid(k_top_short<T>, rows, shared), kShortThreads, shared, st>>>(
+                p, sb);
+            return;
+        }
         const Shape s = shape_of(logits, rows, V, es, sizeof(TopScratch<32>), sizeof(TopScratch<kBlockThreads>));
         const auto launch = [&](auto kernel, int threads) {
             kernel<<<grid_of(s, kernel, threads), threads, s.shared, st>>>(p, s.ring);
@@ -1304,6 +1561,13 @@ extern "C" rnnt_status_t rnnt_distill_loss(
     if (!distill_prepared() || !clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
     with_type(dt, [&](auto t) {
         using T = decltype(t);
+        if (short_rows(logits, V, es)) {
+            const ShortBatch sb = short_batch(V, es, (size_t)128 * k);
+            const size_t shared = (size_t)sb.warp_bytes * (kShortThreads / 32);
+            k_distill_short<T>
+                <<<short_grid(k_distill_short<T>, rows, shared), kShortThreads, shared, st>>>(p, sb);
+            return;
+        }
         const Shape s = shape_of(logits, rows, V, es, sizeof(DistillScratch<32>),
                                  sizeof(DistillScratch<kBlockThreads>));
         if (s.group)

@@ -693,6 +693,20 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
 
 constexpr size_t kHere = 200 << 10;        // bytes of a row that a block holds in shared memory
 
+void fill_params(SampleParams& p, int32_t V, double temperature, int32_t top_k, double top_p,
+                 double min_p, bool fused) {
+    p.V = V;
+    p.top_k = top_k;
+    p.fused = fused;
+    p.unit_tau = temperature == 1.0;
+    parts_below(kLog2e / temperature, p.scale, p.scale_low);
+    parts_below(kLog2e, p.one, p.one_low);
+    p.bin_scale = (float)(kLog2e / temperature) * kBinsPerOrder;
+    p.inv_tau = pair_of(1.0 / temperature);
+    p.top_p = top_p < 1.0 ? pair_of(top_p) : Pair{2.0f, 0.0f};
+    p.min_gap = min_p > 0.0 ? temperature * std::log(min_p) : -INFINITY;
+}
+
 template <typename T>
 void launch_sample(const SampleParams& p, cudaStream_t st) {
     const unsigned rows = (unsigned)(p.B * p.K);
@@ -752,16 +766,7 @@ extern "C" rnnt_status_t rnnt_sample(const void* logits, rnnt_dtype_t dt, int32_
     p.finished = finished;
     p.B = B;
     p.K = K;
-    p.V = V;
-    p.top_k = top_k;
-    p.fused = fused_log_softmax != 0;
-    p.unit_tau = temperature == 1.0;
-    parts_below(kLog2e / temperature, p.scale, p.scale_low);
-    parts_below(kLog2e, p.one, p.one_low);
-    p.bin_scale = (float)(kLog2e / temperature) * kBinsPerOrder;
-    p.inv_tau = pair_of(1.0 / temperature);
-    p.top_p = top_p < 1.0 ? pair_of(top_p) : Pair{2.0f, 0.0f};
-    p.min_gap = min_p > 0.0 ? temperature * std::log(min_p) : -INFINITY;
+    fill_params(p, V, temperature, top_k, top_p, min_p, fused_log_softmax != 0);
     p.out_scores = out_scores;
     p.out_tokens = out_tokens;
     p.status = status_dev;
