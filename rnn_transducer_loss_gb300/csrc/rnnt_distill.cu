@@ -237,25 +237,70 @@ struct Ring {
 };
 constexpr int kMostStages = 2;            // more cost blocks an SM: 3 and 4 measured slower
 
-template <int G>
+// Keys of a row's elements in the order of their values, the lower element first where they are equal:
+// in 32 bits where a value has 16 and a row at most 65536.
+template <typename T, int G>
+struct Keys {
+    static constexpr bool kShort = sizeof(T) == 2 && G == 32;
+    using Key = std::conditional_t<kShort, uint32_t, uint64_t>;
+    __device__ static __forceinline__ Key of(T x, int element) {
+        if constexpr (kShort) {
+            uint32_t b = reinterpret_cast<const uint16_t&>(x);
+            b = b == 0x8000u ? 0u : b;                     // -0 counts as 0
+            return (b ^ (b >> 15 ? 0xffffu : 0x8000u)) << 16 | (uint32_t)(0xffff - element);
+        } else {
+            return key_of(to_f32(x), element);
+        }
+    }
+    __device__ static __forceinline__ float value(Key key) {
+        if constexpr (kShort) {
+            const uint32_t o = key >> 16;
+            const uint16_t b = (uint16_t)(o ^ (o >> 15 ? 0x8000u : 0xffffu));
+            return to_f32(reinterpret_cast<const T&>(b));
+        } else {
+            return value_of(key);
+        }
+    }
+    __device__ static __forceinline__ int element(Key key) {
+        if constexpr (kShort) return 0xffff - (int)(key & 0xffffu);
+        else return element_of(key);
+    }
+};
+
+template <typename T, int G>
 struct TopScratch {
     static constexpr int BUF = G == 32 ? 128 : 512;        // elements that are ranked
+    using Key = typename Keys<T, G>::Key;
     uint64_t bar[kMostStages];
-    uint64_t buf[BUF], best[RNNT_MAX_TOP + 1];
+    __align__(16) Key buf[BUF + 4];
+    Key best[RNNT_MAX_TOP + 1];
     typename Group<G>::Space space;
     float bounds[G / 32];
     int count;
 };
+
+// The c-th largest of the warp's values.
+__device__ __forceinline__ float warp_cth(float x, int c) {
+    if (c > 12) return __shfl_sync(kAll, warp_sorted(x), c - 1);
+    for (int n = 0;;) {
+        const float m = warp_max(x);
+        n += __popc(__ballot_sync(kAll, x == m));
+        if (n >= c) return m;
+        x = x == m ? -INFINITY : x;
+    }
+}
 
 // Rows through a ring of shared memory, a group of threads each.  The k best of a row: the
 // largest maxima of its threads (of both halves of their vectors where k needs more than there are
 // threads in a warp) bound the k + 1-st best from below; the few elements that reach the bound are
 // ranked by counting.  They are then taken out of the row, which leaves the rest: its largest
 // element (the k + 1-st best, if it reached the bound) and the sum relative to it.
-template <typename T, int TH, int G>
+template <typename T, int TH, int G, bool WHOLE>
 __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) {
     using Gr = Group<G>;
-    using Scratch = TopScratch<G>;
+    using Scratch = TopScratch<T, G>;
+    using K = Keys<T, G>;
+    using Key = typename K::Key;
     constexpr int WARPS = G / 32, E = 16 / (int)sizeof(T), GROUPS = TH / G;
     extern __shared__ __align__(16) char space[];
     char* const mine = space + (G == 32 ? threadIdx.x / G : 0) * ring.group_bytes;
@@ -265,9 +310,9 @@ __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) 
     const int64_t first_row = (int64_t)blockIdx.x * GROUPS + (G == 32 ? threadIdx.x / G : 0);
     const auto live = [&](int64_t row) { return !p.lat.T || p.lat.inside(row); };
     const auto staged = [&](int64_t row, int st) {
-        return Staged<T, G>(reinterpret_cast<const T*>(p.logits) + row * p.V, p.V,
-                            reinterpret_cast<uint4*>(mine + st * ring.stage_bytes), row == 0,
-                            row == p.lat.rows - 1);
+        return Staged<T, G, WHOLE>(reinterpret_cast<const T*>(p.logits) + row * p.V, p.V,
+                                   reinterpret_cast<uint4*>(mine + st * ring.stage_bytes),
+                                   row == 0, row == p.lat.rows - 1);
     };
     if (blockIdx.x == 0 && p.lat.T) check_lengths<TH>(p.lat, p.status);
     if (me == 0) {
@@ -287,7 +332,7 @@ __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) 
         float rest = -INFINITY;
         int have = 0;
         if (live(row)) {
-            const Staged<T, G> x = staged(row, st);
+            const Staged<T, G, WHOLE> x = staged(row, st);
             mbar_wait(&sh.bar[st], phases >> st & 1, polls, p.status);
             phases ^= 1u << st;
             x.complete();
@@ -302,11 +347,10 @@ __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) 
                 const int c = min((k + WARPS) / WARPS, 64 / WARPS);    // a warp's share of k + 1
                 float bound;
                 if (c <= 32) {
-                    bound = __shfl_sync(kAll, warp_sorted(fmaxf(both.x, both.y)), c - 1);
+                    bound = warp_cth(fmaxf(both.x, both.y), c);
                 } else {
-                    const int h = (c + 1) / 2 - 1;
-                    bound = fminf(__shfl_sync(kAll, warp_sorted(both.x), h),
-                                  __shfl_sync(kAll, warp_sorted(both.y), h));
+                    const int h = (c + 1) / 2;
+                    bound = fminf(warp_cth(both.x, h), warp_cth(both.y, h));
                 }
                 if constexpr (G > 32) {
                     if (lane == 0) sh.bounds[threadIdx.x >> 5] = bound;
@@ -317,34 +361,65 @@ __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) 
                 // -inf reaches no bound
                 bound = fmaxf(bound, lowest<T>());
                 const T at_least = from_f32<T>(bound);     // a value of the type
-                for (int j = me; j < x.r.n; j += G) {
-                    uint32_t hits = reaching(x.at(j), at_least);
-                    while (hits) {
-                        const int e = __ffs(hits) - 1, i = j * E + e - x.r.off;
-                        hits &= hits - 1;
-                        const int at = atomicAdd(&sh.count, 1);
-                        if (at < Scratch::BUF) sh.buf[at] = key_of(to_f32(x.element(i)), i);
+                int n = 0;
+                constexpr int B = 32 / E;                  // vectors whose elements have a bit each
+                for (int j0 = 0; j0 < x.r.n; j0 += B * G) {
+                    uint32_t hits = 0;
+#pragma unroll
+                    for (int i = 0; i < B; ++i)
+                        if (j0 + me + i * G < x.r.n)
+                            hits |= reaching(x.at(j0 + me + i * G), at_least) << (i * E);
+                    if constexpr (G == 32) {
+                        for (unsigned some; (some = __ballot_sync(kAll, hits != 0)) != 0;) {
+                            const int at = n + __popc(some & ((1u << lane) - 1u));
+                            if (hits) {
+                                const int bit = __ffs(hits) - 1;
+                                const int i = (j0 + me + bit / E * G) * E + bit % E - x.r.off;
+                                if (at < Scratch::BUF) sh.buf[at] = K::of(x.element(i), i);
+                            }
+                            hits &= hits - 1;
+                            n += __popc(some);
+                        }
+                    } else {
+                        while (hits) {
+                            const int bit = __ffs(hits) - 1;
+                            const int i = (j0 + me + bit / E * G) * E + bit % E - x.r.off;
+                            hits &= hits - 1;
+                            const int at = atomicAdd(&sh.count, 1);
+                            if (at < Scratch::BUF) sh.buf[at] = K::of(x.element(i), i);
+                        }
                     }
                 }
+                if constexpr (G == 32) {
+                    if (lane < 4 && n <= Scratch::BUF) sh.buf[n + lane] = 0;   // to fours
+                }
                 Gr::sync();
-                const int n = sh.count;
+                if constexpr (G > 32) n = sh.count;
                 have = min(n, k);
                 if (n <= Scratch::BUF) {
                     for (int i = me; i < n; i += G) {
-                        const uint64_t key = sh.buf[i];
+                        const Key key = sh.buf[i];
                         int rank = 0;
-                        for (int o = 0; o < n; ++o) rank += sh.buf[o] > key;
+                        if constexpr (K::kShort) {
+                            for (int o = 0; o < n; o += 4) {
+                                const uint4 four = *reinterpret_cast<const uint4*>(&sh.buf[o]);
+                                rank += (four.x > key) + (four.y > key) + (four.z > key) +
+                                        (four.w > key);
+                            }
+                        } else {
+                            for (int o = 0; o < n; ++o) rank += sh.buf[o] > key;
+                        }
                         if (rank <= k) sh.best[rank] = key;
                     }
                 } else {                                   // a crowd: one by one
-                    uint64_t last = ~0ull;
+                    Key last = (Key)~0ull;
                     for (int i = 0; i <= k; ++i) {
-                        uint64_t next = 0;
+                        Key next = 0;
                         for (int j = me; j < x.r.n; j += G) {
                             const Pack<T, 16> v = x.at(j);
 #pragma unroll
                             for (int e = 0; e < E; ++e) {
-                                const uint64_t key = key_of(to_f32(v.e[e]), j * E + e - x.r.off);
+                                const Key key = K::of(v.e[e], max(j * E + e - x.r.off, 0));
                                 if (key < last && key > next) next = key;
                             }
                         }
@@ -360,11 +435,11 @@ __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) 
                     }
                 }
                 Gr::sync();
-                if (me == 0) sh.count = 0;
+                if (G > 32 && me == 0) sh.count = 0;
                 for (int i = me; i < have; i += G)
-                    x.element(element_of(sh.best[i])) = from_f32<T>(-INFINITY);
+                    x.element(K::element(sh.best[i])) = from_f32<T>(-INFINITY);
                 Gr::sync();
-                float first = n > k ? value_of(sh.best[k]) : -INFINITY;
+                float first = n > k ? K::value(sh.best[k]) : -INFINITY;
                 if (n == k && bound > lowest<T>()) {
                     Pack<T, 16> m = all_minus_inf<T>();
                     for (int j = me; j < x.r.n; j += G) m = larger(m, x.at(j));
@@ -384,11 +459,12 @@ __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) 
                 }
             }
         }
+        const int64_t out = row * k;
         for (int i = me; i < k; i += G) {
-            const uint64_t key = i < have ? sh.best[i] : 0;
-            reinterpret_cast<T*>(p.values)[row * k + i] =
-                from_f32<T>(i < have ? value_of(key) : -INFINITY);
-            p.ids[row * k + i] = i < have ? element_of(key) : -1;
+            const Key key = i < have ? sh.best[i] : 0;
+            reinterpret_cast<T*>(p.values)[out + i] =
+                from_f32<T>(i < have ? K::value(key) : -INFINITY);
+            p.ids[out + i] = i < have ? K::element(key) : -1;
         }
         if (me == 0) p.rest[row] = rest;
         Gr::sync();                                        // the stage has been read
@@ -442,13 +518,14 @@ __device__ __noinline__ unsigned repeated(int id0, int id1) {
     return again;
 }
 
+constexpr float kLog2eLow = (float)(kLog2e - (double)(float)kLog2e);
+
 // A teacher's row, P places a lane of a warp.
 template <int P>
 struct Teacher {
     int id[P];                             // -1: an empty place
     float t[P];                            // logit / tau, -inf in an empty place
     float rest;                            // -inf without one
-    float p[P], log_p[P], p_rest, log_p_rest;
 
     __device__ __forceinline__ void load(const DistillParams& a, int64_t row) {
         const int lane = threadIdx.x & 31;
@@ -499,46 +576,46 @@ struct Teacher {
         for (int q = 0; q < P; ++q) any |= t[q] != -INFINITY;
         return __any_sync(kAll, any);
     }
-    __device__ __forceinline__ void softmax() {
-        float top = rest;
-#pragma unroll
-        for (int q = 0; q < P; ++q) top = fmaxf(top, t[q]);
-        top = warp_max(top);
-        float sum = 0.0f;
-#pragma unroll
-        for (int q = 0; q < P; ++q) sum += t[q] == -INFINITY ? 0.0f : expf(t[q] - top);
-        sum = warp_sum(sum) + (rest == -INFINITY ? 0.0f : expf(rest - top));
-        const float log_sum = logf(sum);
-#pragma unroll
-        for (int q = 0; q < P; ++q) {
-            log_p[q] = (t[q] - top) - log_sum;
-            p[q] = t[q] == -INFINITY ? 0.0f : expf(log_p[q]);
-        }
-        log_p_rest = (rest - top) - log_sum;
-        p_rest = rest == -INFINITY ? 0.0f : expf(log_p_rest);
-    }
 };
 
-// What the places' logits give a row: the sum of their terms relative to the largest of them; then,
-// with the rest's, the row's sum, loss and the gradient's factors.
+// A row's places, relative to the largest of their teacher's logits (`t_top`, with the rest) and of
+// their student's (`top`): w = exp(t - t_top), e = exp((x - top) / tau).  With W = the sum of
+// all w, S that of e, and the row's sum total = left * outer + S * inner relative to `base`,
+//   sum of p log (p / q) over the places
+//     = [ sum w (t - t_top - (x - top) / tau) + (sum w) (log (total / W) - (top - base) / tau) ] / W,
+// so that one exchange over the warp gives all sums.
 template <int P>
 struct Places {
-    float at[P], e[P], top, sum;
+    float at[P], w[P], e[P], t_top, top, w_rest;
+    float w_sum, w_log, sum;               // of this lane's, then of the warp's
 
-    // `scale` * the term of a place, less its probability, after finish().
     __device__ __forceinline__ void terms(const DistillParams& a, const Teacher<P>& te) {
-        top = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < P; ++q) top = max_nan(top, at[q]);
-        top = warp_max_nan(top);
-        const Exponent f(top, a.scale, a.scale_low);
-        sum = 0.0f;
+        float m = -INFINITY, x = -INFINITY;
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            e[q] = at[q] == -INFINITY ? 0.0f : f(at[q]);
-            sum += e[q];
+            m = max_nan(m, te.t[q]);
+            x = max_nan(x, at[q]);
         }
-        sum = warp_sum(sum);
+        t_top = max_nan(warp_max_nan(m), te.rest);
+        top = warp_max_nan(x);
+        const Exponent f(top, a.scale, a.scale_low), g(t_top, (float)kLog2e, kLog2eLow);
+        w_rest = te.rest == -INFINITY ? 0.0f : g(te.rest);
+        w_sum = w_log = sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            w[q] = te.t[q] == -INFINITY ? 0.0f : g(te.t[q]);
+            e[q] = at[q] == -INFINITY ? 0.0f : f(at[q]);
+            w_sum += w[q];
+            sum += e[q];
+            if (w[q] != 0.0f)
+                w_log += at[q] == -INFINITY
+                             ? INFINITY
+                             : w[q] * ((te.t[q] - t_top) - (at[q] - top) * a.inv_tau);
+        }
+    }
+    __device__ __forceinline__ void finish(float& left) {              // left: a fourth sum
+        const float4 s = warp_sum4(w_sum, w_log, sum, left);
+        w_sum = s.x, w_log = s.y, sum = s.z, left = s.w;
     }
 };
 
@@ -558,29 +635,30 @@ struct Whole {
     // of the terms relative to `outside`
     __device__ __forceinline__ float factor(const DistillParams& a, float left,
                                             float p_rest) const {
-        float c = outer / total;
-        if (a.rest && left > 0.0f) c -= p_rest / left;
+        float c = outer * reciprocal(total);
+        if (a.rest && left > 0.0f) c -= p_rest * reciprocal(left);
         return c * a.grad_scale;
     }
+    // The row's divergence, of the warp's sums (the same in all lanes).
     template <int P>
-    __device__ __forceinline__ float loss(const DistillParams& a, const Teacher<P>& te,
-                                          const Places<P>& pl, float outside, float left) const {
-        const float log_total = logf(total);
-        float kl = 0.0f;
-#pragma unroll
-        for (int q = 0; q < P; ++q)
-            if (te.p[q] != 0.0f)
-                kl += te.p[q] * (te.log_p[q] - ((pl.at[q] - base) * a.inv_tau - log_total));
-        kl = warp_sum(kl);
-        if (te.p_rest != 0.0f)
-            kl += te.p_rest * (te.log_p_rest -
-                               (logf(left) + (outside - base) * a.inv_tau - log_total));
-        return kl;
+    __device__ __forceinline__ float loss(const DistillParams& a, const Places<P>& pl, float rest,
+                                          float outside, float left) const {
+        // the two logarithms by two lanes
+        const float all = pl.w_sum + pl.w_rest;
+        const float mine = logf((threadIdx.x & 1) ? left : total / all);
+        const float ratio = __shfl_sync(kAll, mine, 0), log_left = __shfl_sync(kAll, mine, 1);
+        float kl = pl.w_sum == 0.0f
+                       ? 0.0f
+                       : pl.w_log + pl.w_sum * (ratio - (pl.top - base) * a.inv_tau);
+        if (pl.w_rest != 0.0f)
+            kl += pl.w_rest * ((rest - pl.t_top) - (outside - base) * a.inv_tau + ratio - log_left);
+        return kl / all;
     }
     template <int P>
-    __device__ __forceinline__ float place(const DistillParams& a, const Teacher<P>& te,
-                                           const Places<P>& pl, int q) const {
-        return (pl.e[q] * (inner / total) - te.p[q]) * a.grad_scale;
+    __device__ __forceinline__ float place(const DistillParams& a, const Places<P>& pl,
+                                           int q) const {
+        return (pl.e[q] * (inner * reciprocal(total)) -
+                pl.w[q] * reciprocal(pl.w_sum + pl.w_rest)) * a.grad_scale;
     }
 };
 
@@ -636,7 +714,6 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillPara
                     again |= (atomicOr(&marks[te.id[q] >> 5], bit) & bit) != 0;
                 }
             if (__any_sync(kAll, again)) te.drop_repeated(p);
-            te.softmax();
             const bool some = te.some();
             if (lane == 0) s_some = some;
         }
@@ -691,17 +768,17 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillPara
             const float wt = lane < WARPS ? tops[lane] : -INFINITY;
             const float ws = lane < WARPS ? sums[lane] : 0.0f;
             const float outside = warp_max_nan(wt);
-            const float left = warp_sum(
-                wt == -INFINITY ? 0.0f : ws * Exponent(outside, p.scale, p.scale_low)(wt));
+            float left = wt == -INFINITY ? 0.0f : ws * Exponent(outside, p.scale, p.scale_low)(wt);
+            pl.finish(left);
             const Whole w(p, outside, left, pl.top, pl.sum);
             if (!w.good()) invalid(p.status);              // NaN among them
-            const float kl = w.loss(p, te, pl, outside, left);
+            const float kl = w.loss(p, pl, te.rest, outside, left);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) te.t[q] = w.place(p, te, pl, q);
+            for (int q = 0; q < 2; ++q) te.t[q] = w.place(p, pl, q);
             if (lane == 0) {
                 p.row_loss[row] = w.good() ? kl : NAN;
                 s_base = outside == -INFINITY ? 0.0f : outside;
-                s_coef = w.good() ? w.factor(p, left, te.p_rest) : NAN;
+                s_coef = w.good() ? w.factor(p, left, pl.w_rest / (pl.w_sum + pl.w_rest)) : NAN;
             }
         }
         __syncthreads();
@@ -745,7 +822,7 @@ struct DistillScratch {
 // then read is the rest alone; its terms stay in registers from their sum to the gradient (NV vectors
 // a thread; NV = 0: rows too long for that are read from the stage again).  A group's first warp
 // looks after the teacher.
-template <typename T, int TH, int G, int NV, int P>
+template <typename T, int TH, int G, int NV, int P, bool WHOLE>
 __global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Ring ring) {
     using Gr = Group<G>;
     using Scratch = DistillScratch<G>;
@@ -766,7 +843,7 @@ __global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Rin
         return row < rows && (!p.lat.padded || p.lat.inside(row));
     };
     const auto staged = [&](int64_t row, int st) {
-        return Staged<T, G>(reinterpret_cast<const T*>(p.logits) + row * p.V, p.V,
+        return Staged<T, G, WHOLE>(reinterpret_cast<const T*>(p.logits) + row * p.V, p.V,
                             reinterpret_cast<uint4*>(mine + st * ring.stage_bytes), false,
                             row == p.lat.rows - 1);
     };
@@ -793,7 +870,7 @@ __global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Rin
         if (leads && now) ahead.load(p, row + groups);     // one row ahead
         T* const g = reinterpret_cast<T*>(p.grad) + row * p.V;
         if (counts) {
-            const Staged<T, G> x = staged(row, st);
+            const Staged<T, G, WHOLE> x = staged(row, st);
             mbar_wait(&sh.bar[st], phases >> st & 1, polls, p.status);
             phases ^= 1u << st;
             x.complete();
@@ -839,12 +916,15 @@ __global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Rin
 #pragma unroll 4
                 for (int j = me; j < x.r.n; j += G) m = larger(m, x.at(j));
                 if (leads) {
-                    te.softmax();
                     pl.terms(p, te);
-                    if (G > 32 && lane == 0) {
-                        sh.top = pl.top;
-                        sh.sum = pl.sum;
-                        sh.p_rest = te.p_rest;
+                    if constexpr (G > 32) {
+                        float none = 0.0f;
+                        pl.finish(none);
+                        if (lane == 0) {
+                            sh.top = pl.top;
+                            sh.sum = pl.sum;
+                            sh.p_rest = pl.w_rest / (pl.w_sum + pl.w_rest);
+                        }
                     }
                 }
                 const float2 both = half_maxima(m);
@@ -859,11 +939,14 @@ __global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Rin
                 } else {
                     for (int j = me; j < x.r.n; j += G) left += terms_of(x.at(j), f, e[0]);
                 }
-                left = Gr::sum(left, sh.space);
+                if constexpr (G > 32) left = Gr::sum(left, sh.space);
+                else pl.finish(left);
                 const float top = G > 32 ? sh.top : pl.top, sum = G > 32 ? sh.sum : pl.sum;
                 const Whole w(p, outside, left, top, sum);
                 if (p.grad) {
-                    const float c = w.good() ? w.factor(p, left, G > 32 ? sh.p_rest : te.p_rest) : NAN;
+                    const float c = w.good() ? w.factor(p, left,
+                                                       G > 32 ? sh.p_rest
+                                                              : pl.w_rest / (pl.w_sum + pl.w_rest)) : NAN;
                     const float2 c2 = make_float2(c, c);
                     const auto put = [&](int j, float2 (&y)[E / 2]) {
                         Pack<T, 16> v;
@@ -885,7 +968,7 @@ __global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Rin
                 }
                 if (leads) {
                     if (!w.good()) invalid(p.status);      // NaN among them
-                    const float kl = w.loss(p, te, pl, outside, left);
+                    const float kl = w.loss(p, pl, te.rest, outside, left);
                     if (lane == 0) p.row_loss[row] = w.good() ? kl : NAN;
                 }
                 if (p.grad) {
@@ -893,7 +976,7 @@ __global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Rin
                     if (leads) {
 #pragma unroll
                         for (int q = 0; q < P; ++q)
-                            if (te.id[q] >= 0) g[te.id[q]] = from_f32<T>(w.place(p, te, pl, q));
+                            if (te.id[q] >= 0) g[te.id[q]] = from_f32<T>(w.place(p, pl, q));
                     }
                 }
             }
@@ -1376,16 +1459,22 @@ bool raise_top() {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)kShared) == cudaSuccess;
     };
-    return raise(k_top<T, kWarpThreads, 32>) && raise(k_top<T, kBlockThreads, kBlockThreads>) &&
+    return raise(k_top<T, kWarpThreads, 32, true>) && raise(k_top<T, kWarpThreads, 32, false>) &&
+           raise(k_top<T, kBlockThreads, kBlockThreads, true>) &&
+           raise(k_top<T, kBlockThreads, kBlockThreads, false>) &&
            raise(k_top_short<T>) && raise(k_distill_short<T>);
 }
 // Calls f(k_distill's form for rows of n vectors and k places).
 template <typename T, typename F>
-auto distill_form(int group, int n, int k, F&& f) {
+auto distill_form(int group, int n, int k, bool whole, F&& f) {
     const auto by_places = [&](auto g, auto nv) {
         constexpr int G = decltype(g)::value, NV = decltype(nv)::value;
         constexpr int TH = G == 32 ? kWarpThreads : G;
-        return k <= 32 ? f(k_distill<T, TH, G, NV, 1>, TH) : f(k_distill<T, TH, G, NV, 2>, TH);
+        if (whole)
+            return k <= 32 ? f(k_distill<T, TH, G, NV, 1, true>, TH)
+                           : f(k_distill<T, TH, G, NV, 2, true>, TH);
+        return k <= 32 ? f(k_distill<T, TH, G, NV, 1, false>, TH)
+                       : f(k_distill<T, TH, G, NV, 2, false>, TH);
     };
     using std::integral_constant;
     if (group == 32) {
@@ -1402,18 +1491,15 @@ auto distill_form(int group, int n, int k, F&& f) {
 template <typename T>
 bool raise_distill() {
     bool ok = true;
-    for (int k : {1, 64})
-        for (int n : {1, 100, 200})
-            ok &= distill_form<T>(32, n, k, [](auto kernel, int) {
-                return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            (int)kShared) == cudaSuccess;
-            });
-    for (int k : {1, 64})
-        for (int n : {1, 1 << 20})
-            ok &= distill_form<T>(kBlockThreads, n, k, [](auto kernel, int) {
-                return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            (int)kShared) == cudaSuccess;
-            });
+    const auto raise = [](auto kernel, int) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)kShared) == cudaSuccess;
+    };
+    for (bool whole : {false, true})
+        for (int k : {1, 64}) {
+            for (int n : {1, 100, 200}) ok &= distill_form<T>(32, n, k, whole, raise);
+            for (int n : {1, 1 << 20}) ok &= distill_form<T>(kBlockThreads, n, k, whole, raise);
+        }
     return ok;
 }
 bool distill_prepared() {
@@ -1478,12 +1564,17 @@ extern "C" rnnt_status_t rnnt_top_logits(const void* logits, rnnt_dtype_t dt, in
                 p, sb);
             return;
         }
-        const Shape s = shape_of(logits, rows, V, es, sizeof(TopScratch<32>), sizeof(TopScratch<kBlockThreads>));
+        const Shape s = shape_of(logits, rows, V, es, sizeof(TopScratch<T, 32>),
+                                 sizeof(TopScratch<T, kBlockThreads>));
         const auto launch = [&](auto kernel, int threads) {
             kernel<<<grid_of(s, kernel, threads), threads, s.shared, st>>>(p, s.ring);
         };
-        if (s.group == 32) launch(k_top<T, kWarpThreads, 32>, kWarpThreads);
-        else if (s.group) launch(k_top<T, kBlockThreads, kBlockThreads>, kBlockThreads);
+        const bool whole = (size_t)V * es % 16 == 0 && ((uintptr_t)logits & 15) == 0;
+        if (s.group == 32 && whole) launch(k_top<T, kWarpThreads, 32, true>, kWarpThreads);
+        else if (s.group == 32) launch(k_top<T, kWarpThreads, 32, false>, kWarpThreads);
+        else if (s.group && whole)
+            launch(k_top<T, kBlockThreads, kBlockThreads, true>, kBlockThreads);
+        else if (s.group) launch(k_top<T, kBlockThreads, kBlockThreads, false>, kBlockThreads);
         else
             k_top_long<T><<<row_grid(rows), kLongThreads, 0, st>>>(p);
     });
@@ -1571,10 +1662,11 @@ extern "C" rnnt_status_t rnnt_distill_loss(
         const Shape s = shape_of(logits, rows, V, es, sizeof(DistillScratch<32>),
                                  sizeof(DistillScratch<kBlockThreads>));
         if (s.group)
-            distill_form<T>(s.group, (int)(s.ring.stage_bytes / 16), k, [&](auto kernel, int th) {
-                kernel<<<grid_of(s, kernel, th), th, s.shared, st>>>(p, s.ring);
-                return 0;
-            });
+            distill_form<T>(s.group, (int)(s.ring.stage_bytes / 16), k, (size_t)V * es % 16 == 0,
+                            [&](auto kernel, int th) {
+                                kernel<<<grid_of(s, kernel, th), th, s.shared, st>>>(p, s.ring);
+                                return 0;
+                            });
         else
             k_distill_long<T><<<row_grid(rows), kLongThreads, (size_t)(V + 31) / 32 * 4, st>>>(p);
     });

@@ -47,14 +47,32 @@ __device__ __forceinline__ V warp_sum(V x) {
     return x;
 }
 __device__ __forceinline__ float warp_max(float x) {           // NaN is passed over
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, o));
-    return x;
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Four sums at once: half of the values go with each half of the lanes, so 6 exchanges instead of 20.
+__device__ __forceinline__ float4 warp_sum4(float a, float b, float c, float d) {
+    const int lane = threadIdx.x & 31;
+    const bool up = lane & 16, right = lane & 8;
+    float x = (up ? c : a) + __shfl_xor_sync(kAll, up ? a : c, 16);
+    float y = (up ? d : b) + __shfl_xor_sync(kAll, up ? b : d, 16);
+    x = (right ? y : x) + __shfl_xor_sync(kAll, right ? x : y, 8);
+    x += __shfl_xor_sync(kAll, x, 4);
+    x += __shfl_xor_sync(kAll, x, 2);
+    x += __shfl_xor_sync(kAll, x, 1);
+    return make_float4(__shfl_sync(kAll, x, 0), __shfl_sync(kAll, x, 8), __shfl_sync(kAll, x, 16),
+                       __shfl_sync(kAll, x, 24));
+}
+__device__ __forceinline__ float reciprocal(float x) {          // to one step
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ float warp_max_nan(float x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x = max_nan(x, __shfl_xor_sync(kAll, x, o));
-    return x;
+    float y;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
 }
 template <typename Key>
 __device__ __forceinline__ Key warp_largest(Key x) {
@@ -84,18 +102,19 @@ __device__ __forceinline__ float warp_sorted(float x) {
 // A row of V elements from x on, as the 16-byte units of memory it lies in: element e of vector j is
 // x[j * E + e - off].  What of the first and the last unit is not the row's reads as -inf and
 // is neither loaded nor stored.
-template <typename T>
+// WHOLE: every row is made of whole units.
+template <typename T, bool WHOLE = false>
 struct Row {
     static constexpr int E = 16 / (int)sizeof(T);
     const T* x;
     int V, off, n;
 
     __device__ __forceinline__ Row(const T* row, int size) : x(row), V(size) {
-        off = (int)((uintptr_t)row & 15) / (int)sizeof(T);
+        off = WHOLE ? 0 : (int)((uintptr_t)row & 15) / (int)sizeof(T);
         n = (off + V + E - 1) / E;
     }
     __device__ __forceinline__ bool whole(int j) const {
-        return j * E >= off && (j + 1) * E <= off + V;
+        return WHOLE || (j * E >= off && (j + 1) * E <= off + V);
     }
     __device__ __forceinline__ Pack<T, 16> load(int j) const {
         Pack<T, 16> v;
@@ -379,17 +398,17 @@ __device__ __forceinline__ void mbar_wait(uint64_t* bar, uint32_t parity, int& p
 }
 
 // A row in a stage: vectors as Row has them.
-template <typename T, int G>
+template <typename T, int G, bool WHOLE = false>
 struct Staged {
     static constexpr int E = 16 / (int)sizeof(T);
-    Row<T> r;
+    Row<T, WHOLE> r;
     uint4* s;
     int lo, hi;                            // the vectors that the copy brings
 
     __device__ __forceinline__ Staged(const T* x, int V, uint4* stage, bool first, bool last)
         : r(x, V), s(stage) {
-        lo = first && r.off ? 1 : 0;
-        hi = last && (r.off + V) % E ? r.n - 1 : r.n;
+        lo = !WHOLE && first && r.off ? 1 : 0;
+        hi = !WHOLE && last && (r.off + V) % E ? r.n - 1 : r.n;
     }
     __device__ __forceinline__ void fetch(uint64_t* bar) const {       // by one thread
         const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;
@@ -397,7 +416,7 @@ struct Staged {
     }
     // After the copy has arrived: what it did not bring, and -inf in place of what is not the row's.
     __device__ __forceinline__ void complete() const {
-        if (r.off == 0 && r.V % E == 0) return;
+        if (WHOLE || (r.off == 0 && r.V % E == 0)) return;
         const int i = Group<G>::rank();
         T* e = reinterpret_cast<T*>(s);
         if (i < 2 * E) {
