@@ -114,16 +114,17 @@ constexpr uint64_t kFinite = (uint64_t)0x00800000u << kIdBits;   // the least ke
 constexpr float kLeastMass = 1.17549435e-38f;
 
 // Fast sums are of float32 terms, added as trees of a vector's and then as pairs.  A term is off by at
-// most kTerm and kStep for each of its exponent's binary orders (ex2.approx 2^-22, three additions;
-// the roundings of x - top and of the exponent), relative; the mean order over a row is at most
-// log2 V - log2 sum (its entropy is at most log2 V), which bounds a sum's error.  Of many terms the
-// errors do not all point one way: by Hoeffding's inequality sums of independent ones exceed 8
-// times the root of the squares' sum with a chance below 2e-14; kBias is what ex2.approx may be off
-// on average.  A border nearer to a sum than that is decided on sums of pairs.
-constexpr float kTerm = 4.2e-7f, kStep = 8.3e-8f, kBias = 2e-8f;
-__device__ __forceinline__ float error_of(float sum, int V) {      // absolute; terms are at most 1
+// most kTerm and kStep for each of its exponent's binary orders (ex2.approx by 1.0e-7 from its mean, which
+// all terms share; three additions; the roundings of x - top and of the exponent), relative; the
+// mean order over a row is at most log2 V - log2 sum (its entropy is at most log2 V), which bounds a
+// sum's error.  Of many terms the errors do not all point one way: by Hoeffding's inequality a sum
+// of independent ones exceeds 6 times the root of the terms' squares' sum with a chance below 4e-8;
+// kBias is what ex2.approx's mean over a 64th of an order is off, at most.  A border nearer to a sum
+// than that is decided on sums of pairs.
+constexpr float kTerm = 3e-7f, kStep = 8.3e-8f, kBias = 3e-8f;
+__device__ __forceinline__ float error_of(float sum, float squares, int V) {   // absolute
     const float worst = sum * (kTerm + kStep * fmaxf(__log2f((float)V) - __log2f(sum), 0.0f));
-    return fminf(worst, 8.0f * kTerm * sqrtf(sum) + kBias * sum);
+    return fminf(worst, 6.0f * kTerm * sqrtf(fminf(squares, sum)) + kBias * sum);
 }
 __device__ __forceinline__ Pair add_loosely(Pair a, float b) {     // of sums of positive terms
     const Pair s = two_sum(a.h, b);
@@ -155,6 +156,27 @@ struct Shared {
     bool unsure;
 };
 
+// What is kept: values above `value`, and equal ones up to an id.
+template <typename T>
+struct Floor {
+    T value;
+    int last;
+    __device__ __forceinline__ explicit Floor(uint64_t key) {
+        const float f = unordered((uint32_t)(key >> kIdBits));
+        value = not_below<T>(fmaxf(f, lowest<T>()));
+        last = (1 << kIdBits) - 1 -
+               (to_f32(value) == f ? (int)(key & ((1 << kIdBits) - 1)) : 0);
+    }
+    // The kept elements of a vector whose first has this id.
+    __device__ __forceinline__ uint32_t kept(const Pack<T, 16>& v, int id) const {
+        const uint32_t ge = reaching(v, value);
+        if (!ge) return 0;
+        const int more = last - id;        // ids up to last
+        const uint32_t ids = more < 0 ? 0u : more > 30 ? ~0u : (2u << more) - 1u;
+        return ge & (ids | reaching<true>(v, value));
+    }
+};
+
 // A draw by a block of TH threads; the row lies in shared memory (HERE) or is read from the cache.
 template <typename T, int TH, bool HERE>
 struct Draw {
@@ -165,9 +187,11 @@ struct Draw {
     uint4* const here;
     float top;
     bool unsure;                           // of the last result: the fast sums leave it open
+    float squares;                         // the sum of the terms' squares
 
     __device__ __forceinline__ Draw(const SampleParams& a, Shared<TH>& s, const T* x, uint4* stage)
-        : p(a), sh(s), r(x, a.V), here(stage), top(0.0f), unsure(false) {}
+        : p(a), sh(s), r(x, a.V), here(stage), top(0.0f), unsure(false),
+          squares(INFINITY) {}
 
     __device__ __forceinline__ Pack<T, 16> at(int j) const {
         if constexpr (HERE) {
@@ -189,45 +213,36 @@ struct Draw {
     __device__ __forceinline__ float fast_mass(float x) const {
         return fmaxf(Exponent(top, p.scale, p.scale_low)(x), kLeastMass);
     }
-    // What is kept: keys from `least` on.
-    struct Floor {
-        uint64_t least;
-        float value;
-        __device__ __forceinline__ explicit Floor(uint64_t key)
-            : least(key), value(unordered((uint32_t)(key >> kIdBits))) {}
-        __device__ __forceinline__ bool keeps(float x, int id) const {
-            return x > value || (x == value && short_key(x, id) >= least);
-        }
-    };
-    __device__ __forceinline__ float largest(const Pack<T, 16>& v) const {
-        const float2 m = half_maxima(v);
-        return fmaxf(m.x, m.y);
-    }
     template <bool EXACT>
-    __device__ __forceinline__ Pair mass_of_vector(int j, const Floor& f) const {
-        const Pack<T, 16> v = at(j);
+    __device__ __forceinline__ Pair masses(const Pack<T, 16>& v, uint32_t kept) const {
         Pair s{0.0f, 0.0f};
-        if (!(largest(v) >= f.value)) return s;
         if constexpr (EXACT) {
-#pragma unroll 1
-            for (int e = 0; e < E; ++e) {
-                const float x = to_f32(v.e[e]);
-                if (f.keeps(x, id_of(j, e))) s = add(s, mass(x));
-            }
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (kept >> e & 1) s = add(s, mass(to_f32(v.e[e])));
         } else {
-            float t[E];
+            const Exponent f(top, p.scale, p.scale_low);
+            float2 e[E / 2];
+            unpack(v, e);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float x = to_f32(v.e[e]);
-                t[e] = f.keeps(x, id_of(j, e)) ? fast_mass(x) : 0.0f;
+            for (int i = 0; i < E / 2; ++i) {
+                e[i] = f(e[i]);
+                e[i].x = kept >> (2 * i) & 1 ? fmaxf(e[i].x, kLeastMass) : 0.0f;
+                e[i].y = kept >> (2 * i + 1) & 1 ? fmaxf(e[i].y, kLeastMass) : 0.0f;
             }
 #pragma unroll
-            for (int o = E / 2; o; o /= 2)
+            for (int o = E / 4; o; o /= 2)
 #pragma unroll
-                for (int e = 0; e < o; ++e) t[e] += t[e + o];
-            s.h = t[0];
+                for (int i = 0; i < o; ++i) e[i] = add2(e[i], e[i + o]);
+            s.h = e[0].x + e[0].y;
         }
         return s;
+    }
+    template <bool EXACT>
+    __device__ __forceinline__ Pair mass_of_vector(int j, const Floor<T>& f) const {
+        const Pack<T, 16> v = at(j);
+        const uint32_t kept = f.kept(v, id_of(j, 0));
+        return kept ? masses<EXACT>(v, kept) : Pair{0.0f, 0.0f};
     }
 
     // ---- over the block
@@ -255,18 +270,18 @@ struct Draw {
     // Sums of pairs over the keys from `least` and from `above` on.
     __device__ __noinline__ void exact_sums(uint64_t least, uint64_t above, Pair& whole,
                                             Pair& upper) {
-        const Floor f(least);
+        const Floor<T> f(least), g(above);
         Pair a{0.0f, 0.0f}, b{0.0f, 0.0f};
         for (int j = threadIdx.x; j < r.n; j += TH) {
             const Pack<T, 16> v = at(j);
-            if (!(largest(v) >= f.value)) continue;
-#pragma unroll 1
+            const uint32_t kept = f.kept(v, id_of(j, 0)), over = g.kept(v, id_of(j, 0));
+            if (!kept) continue;
+#pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float x = to_f32(v.e[e]);
-                if (!f.keeps(x, id_of(j, e))) continue;
-                const Pair m = mass(x);
+                if (!(kept >> e & 1)) continue;
+                const Pair m = mass(to_f32(v.e[e]));
                 a = add(a, m);
-                if (short_key(x, id_of(j, e)) >= above) b = add(b, m);
+                if (over >> e & 1) b = add(b, m);
             }
         }
         sum2(a, b);
@@ -333,7 +348,7 @@ struct Draw {
     template <bool MASS>
     __device__ __noinline__ int list_at(uint64_t least, uint32_t count, float target, float whole,
                                         Pair& above, uint32_t& before) {
-        const Floor f(least);
+        const Floor<T> f(least);
         uint64_t low = 0, high = ~0ull;    // the range; whole at first
         int shift = -1;                    // of keys to bins; -1: by exponents
         uint32_t base = 0;                 // elements above the range
@@ -353,14 +368,17 @@ struct Draw {
             };
             for (int j = threadIdx.x; j < r.n; j += TH) {
                 const Pack<T, 16> v = at(j);
-                if (!(largest(v) >= f.value)) continue;
+                const uint32_t kept = f.kept(v, id_of(j, 0));
+                if (!kept) continue;
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
+                    if (!(kept >> e & 1)) continue;
                     const float x = to_f32(v.e[e]);
-                    const int id = id_of(j, e);
-                    if (!f.keeps(x, id)) continue;
-                    const uint64_t key = short_key(x, id);
-                    if (key < low || key > high) continue;
+                    uint64_t key = 0;
+                    if (shift >= 0) {
+                        key = short_key(x, id_of(j, e));
+                        if (key < low || key > high) continue;
+                    }
                     atomicAdd(&sh.bins[bin(x, key)],
                               MASS ? __float2uint_rn(fminf(fast_mass(x) * unit, 2147483648.0f)) : 1u);
                 }
@@ -373,29 +391,31 @@ struct Draw {
             uint64_t mine_low = ~0ull, mine_high = 0;
             for (int j = threadIdx.x; j < r.n; j += TH) {
                 const Pack<T, 16> v = at(j);
-                if (!(largest(v) >= f.value)) continue;
-                float t = 0.0f;
+                const uint32_t kept = f.kept(v, id_of(j, 0));
+                if (!kept) continue;
+                uint32_t higher = 0;       // of those, the ones above the bin
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
+                    if (!(kept >> e & 1)) continue;
                     const float x = to_f32(v.e[e]);
-                    const int id = id_of(j, e);
-                    if (!f.keeps(x, id)) continue;
-                    const uint64_t key = short_key(x, id);
-                    if (key < low) continue;
-                    const int at_bin = key > high ? -1 : bin(x, key);
-                    if (at_bin > b) continue;
-                    const float m = MASS ? fast_mass(x) : 0.0f;
-                    if (at_bin < b) {
-                        t += m;
-                        continue;
+                    uint64_t key = 0;
+                    int at_bin;
+                    if (shift < 0) {
+                        at_bin = bin_of(x);
+                    } else {
+                        key = short_key(x, id_of(j, e));
+                        at_bin = key > high ? -1 : key < low ? kBins : bin(x, key);
                     }
-                    if (MASS) in = add_loosely(in, m);
+                    higher |= at_bin < b ? 1u << e : 0u;
+                    if (at_bin != b) continue;
+                    key = short_key(x, id_of(j, e));
+                    if (MASS) in = add_loosely(in, fast_mass(x));
                     const int i = atomicAdd(&sh.count, 1);
                     if (i < kList) sh.list[i] = key;
                     mine_low = key < mine_low ? key : mine_low;
                     mine_high = key > mine_high ? key : mine_high;
                 }
-                if (MASS) over = add_loosely(over, t);
+                if (MASS && higher) over = add_loosely(over, masses<false>(v, higher).h);
             }
             if (mine_high) {
                 atomicMin(&sh.low, (unsigned long long)mine_low);
@@ -492,7 +512,7 @@ struct Draw {
         uint32_t before;
         Pair target = mul(whole, p.top_p);
         const int n = list_at<true>(least, 0, target.h, whole.h, above, before);
-        int kept = kept_of_list<false>(n, above, target, 2.0f * error_of(whole.h, p.V));
+        int kept = kept_of_list<false>(n, above, target, 2.0f * error_of(whole.h, squares, p.V));
         if (unsure && n) {
             // the sums again, to 40 bits, over the same list
             Pair exact, upper;
@@ -510,7 +530,7 @@ struct Draw {
     // A warp takes a piece of the row; the one in whose piece the border lies goes through it.
     template <bool EXACT>
     __device__ __noinline__ int token_from(uint64_t least, float u) {
-        const Floor f(least);
+        const Floor<T> f(least);
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const int each = (r.n + WARPS - 1) / WARPS, j0 = min(r.n, warp * each);
         const int j1 = min(r.n, j0 + each);
@@ -533,7 +553,7 @@ struct Draw {
             }
             const Pair border = mul(run, Pair{u, 0.0f});
             sh.prefix[WARPS] = border;
-            sh.floats[0] = EXACT ? 0.0f : 2.0f * error_of(run.h, p.V);
+            sh.floats[0] = EXACT ? 0.0f : 2.0f * error_of(run.h, squares, p.V);
             int w = 0;                     // the first piece at whose end the border is passed
 #pragma unroll 1
             while (w < last && !less(border, add(sh.prefix[w], sh.pairs[0][w]))) ++w;
@@ -566,14 +586,16 @@ struct Draw {
                     Pair ahead = upto;
                     if (lane == at_lane) {
                         const Pack<T, 16> v = at(j + lane);
-#pragma unroll 1
+                        const uint32_t kept = f.kept(v, id_of(j + lane, 0));
+                        bool open = true;
+#pragma unroll
                         for (int e = 0; e < E; ++e) {
+                            if (!open || !(kept >> e & 1)) continue;
                             const float x = to_f32(v.e[e]);
-                            if (!f.keeps(x, id_of(j + lane, e))) continue;
                             got = id_of(j + lane, e);
                             ahead = upto;
                             upto = add(upto, EXACT ? mass(x) : Pair{fast_mass(x), 0.0f});
-                            if (past && less(border, upto)) break;
+                            if (past && less(border, upto)) open = false;
                         }
                     }
                     token = __shfl_sync(kAll, got, at_lane);
@@ -650,13 +672,24 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
             Pair s{0.0f, 0.0f}, s1{0.0f, 0.0f};
             if (at_tau || at_one) {
                 const Exponent f(m, p.scale, p.scale_low), f1(m, p.one, p.one_low);
+                float2 squares = make_float2(0.0f, 0.0f);
                 for (int j = tid; j < d.r.n; j += TH) {
                     const Pack<T, 16> v = d.at(j);
                     float2 e[E / 2];
-                    if (at_tau) s = add_loosely(s, terms_of(v, f, e));
                     if (at_one) s1 = add_loosely(s1, terms_of(v, f1, e));
+                    if (at_tau) {
+                        s = add_loosely(s, terms_of(v, f, e));
+#pragma unroll
+                        for (int i = 0; i < E / 2; ++i) squares = fma2(e[i], e[i], squares);
+                    }
                 }
                 d.sum2(s, s1);
+                if (at_tau) {
+                    const float sq = warp_sum(squares.x + squares.y);
+                    if (lane == 0) sh.floats[tid >> 5] = sq;
+                    __syncthreads();
+                    d.squares = warp_sum(lane < WARPS ? sh.floats[lane] : 0.0f);
+                }
             }
             const float lse = p.fused ? logf(p.unit_tau ? s.h : s1.h) : 0.0f;
             uint64_t least = kFinite;
@@ -670,7 +703,7 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
             uint64_t floor = least;
             if (p.top_p.h < 1.0f) {
                 if (least != kFinite) {                    // of what top_k has left
-                    const typename Draw<T, TH, HERE>::Floor f(least);
+                    const Floor<T> f(least);
                     s = s1 = Pair{0.0f, 0.0f};
                     for (int j = tid; j < d.r.n; j += TH)
                         s = add_loosely(s, d.template mass_of_vector<false>(j, f).h);

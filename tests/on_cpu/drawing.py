@@ -29,6 +29,9 @@ def device_source():
 
     body("float ex2", "std::exp2(x)")
     body("float max_nan", "a != a ? a : b != b ? b : a > b ? a : b")
+    body("float warp_max", "warp_reduced(x, [](float a, float b) { return fmaxf(a, b); })")
+    body("float warp_max_nan", "warp_reduced(x, max_nan)")
+    body("float reciprocal", "1.0f / x")
     body("float2 fma2", "make_float2(std::fma(a.x, b.x, c.x), std::fma(a.y, b.y, c.y))")
     body("float2 mul2", "make_float2(a.x * b.x, a.y * b.y)")
     body("float2 add2", "make_float2(a.x + b.x, a.y + b.y)")

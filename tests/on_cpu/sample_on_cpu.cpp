@@ -18,6 +18,13 @@ inline uint32_t __reduce_add_sync(unsigned, uint32_t x) {
         return s;
     });
 }
+template <class F> float warp_reduced(float x, F f) {
+    return from_bits<float>(warp_op(bits_of(x), [&](uint64_t* v) {
+        float m = from_bits<float>(v[0]);
+        for (int i = 1; i < 32; ++i) m = f(m, from_bits<float>(v[i]));
+        return bits_of(m);
+    }));
+}
 inline bool __any_sync(unsigned m, bool p) { return __ballot_sync(m, p) != 0; }
 inline int __clz(unsigned x) { return x ? __builtin_clz(x) : 32; }
 inline uint32_t atomicAdd(uint32_t* p, uint32_t x) { const uint32_t o = *p; *p += x; return o; }
