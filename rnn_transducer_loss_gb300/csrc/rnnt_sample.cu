@@ -147,12 +147,12 @@ struct Shared {
     };
     uint64_t list[kList];
     uint32_t groups[32];                   // sums of 32 bins each
-    Pair pairs[2][WARPS], prefix[WARPS + 1];
-    float floats[WARPS];
+    Pair pairs[2][WARPS];
+    float floats[2][WARPS];
     int ints[WARPS];
     unsigned long long low, high;          // keys
     uint32_t before;
-    int bin, count, token, found, kept;
+    int bin, count, token, kept;
     bool unsure;
 };
 
@@ -181,17 +181,19 @@ struct Floor {
 template <typename T, int TH, bool HERE>
 struct Draw {
     static constexpr int E = 16 / (int)sizeof(T), WARPS = TH / 32;
-    const SampleParams& p;
     Shared<TH>& sh;
     const Row<T> r;
     uint4* const here;
+    const float scale, scale_low, bin_scale;
+    const Pair inv_tau, top_p;
     float top;
-    bool unsure;                           // of the last result: the fast sums leave it open
     float squares;                         // the sum of the terms' squares
+    bool unsure;                           // of the last result: the fast sums leave it open
 
-    __device__ __forceinline__ Draw(const SampleParams& a, Shared<TH>& s, const T* x, uint4* stage)
-        : p(a), sh(s), r(x, a.V), here(stage), top(0.0f), unsure(false),
-          squares(INFINITY) {}
+    __device__ __forceinline__ Draw(const SampleParams& p, Shared<TH>& s, const T* x, uint4* stage)
+        : sh(s), r(x, p.V), here(stage), scale(p.scale), scale_low(p.scale_low),
+          bin_scale(p.bin_scale), inv_tau(p.inv_tau), top_p(p.top_p), top(0.0f), squares(INFINITY),
+          unsure(false) {}
 
     __device__ __forceinline__ Pack<T, 16> at(int j) const {
         if constexpr (HERE) {
@@ -207,11 +209,11 @@ struct Draw {
     // ---- masses: of pairs (exact), or float32
     __device__ __forceinline__ Pair mass(float x) const {
         const Pair d = two_sum(x, -top);
-        const Pair e = exp_pair(mul(d, p.inv_tau));
+        const Pair e = exp_pair(mul(d, inv_tau));
         return e.h >= kLeastMass ? e : Pair{kLeastMass, 0.0f};
     }
     __device__ __forceinline__ float fast_mass(float x) const {
-        return fmaxf(Exponent(top, p.scale, p.scale_low)(x), kLeastMass);
+        return fmaxf(Exponent(top, scale, scale_low)(x), kLeastMass);
     }
     template <bool EXACT>
     __device__ __forceinline__ Pair masses(const Pack<T, 16>& v, uint32_t kept) const {
@@ -221,7 +223,7 @@ struct Draw {
             for (int e = 0; e < E; ++e)
                 if (kept >> e & 1) s = add(s, mass(to_f32(v.e[e])));
         } else {
-            const Exponent f(top, p.scale, p.scale_low);
+            const Exponent f(top, scale, scale_low);
             float2 e[E / 2];
             unpack(v, e);
 #pragma unroll
@@ -258,18 +260,24 @@ struct Draw {
             sh.pairs[1][threadIdx.x >> 5] = b;
         }
         __syncthreads();
-        a = sh.pairs[0][0];
-        b = sh.pairs[1][0];
-#pragma unroll 1
-        for (int w = 1; w < WARPS; ++w) {
-            a = add(a, sh.pairs[0][w]);
-            b = add(b, sh.pairs[1][w]);
+        a = lane < WARPS ? sh.pairs[0][lane] : Pair{0.0f, 0.0f};
+        b = lane < WARPS ? sh.pairs[1][lane] : Pair{0.0f, 0.0f};
+#pragma unroll
+        for (int o = WARPS / 2; o; o >>= 1) {
+            a = add(a, shuffled(a, o));
+            b = add(b, shuffled(b, o));
         }
+        a = Pair{__shfl_sync(kAll, a.h, 0), __shfl_sync(kAll, a.l, 0)};
+        b = Pair{__shfl_sync(kAll, b.h, 0), __shfl_sync(kAll, b.l, 0)};
         __syncthreads();
     }
     // Sums of pairs over the keys from `least` and from `above` on.
     __device__ __noinline__ void exact_sums(uint64_t least, uint64_t above, Pair& whole,
-                                            Pair& upper) {
+                                            Pair& upper) const {
+        Draw(*this).exact_sums_of(least, above, whole, upper);     // a copy, for registers
+    }
+    __device__ __forceinline__ void exact_sums_of(uint64_t least, uint64_t above, Pair& whole,
+                                                  Pair& upper) {
         const Floor<T> f(least), g(above);
         Pair a{0.0f, 0.0f}, b{0.0f, 0.0f};
         for (int j = threadIdx.x; j < r.n; j += TH) {
@@ -303,7 +311,7 @@ struct Draw {
 
     // ---- the first histogram's bins: by the exponent
     __device__ __forceinline__ int bin_of(float x) const {
-        return (int)fminf((top - x) * p.bin_scale, (float)(kBins - 1));
+        return (int)fminf((top - x) * bin_scale, (float)(kBins - 1));
     }
     // The bin at whose end `target` is reached (the last filled one if it is not), and what is in
     // those before it.
@@ -345,9 +353,15 @@ struct Draw {
     // Each turn counts the elements of a range by bins and takes the bin in which the
     // border lies for the next range, until it holds few enough: first by their
     // exponents, then by the bits of their keys, which are all different.
+    // With `few` the whole range is tried as a list first.
     template <bool MASS>
-    __device__ __noinline__ int list_at(uint64_t least, uint32_t count, float target, float whole,
-                                        Pair& above, uint32_t& before) {
+    __device__ __noinline__ int list_at(bool few, uint64_t least, uint32_t count, float target,
+                                        float whole, Pair& above, uint32_t& before) const {
+        return Draw(*this).template list_of<MASS>(few, least, count, target, whole, above, before);
+    }
+    template <bool MASS>
+    __device__ __forceinline__ int list_of(bool few, uint64_t least, uint32_t count, float target,
+                                           float whole, Pair& above, uint32_t& before) {
         const Floor<T> f(least);
         uint64_t low = 0, high = ~0ull;    // the range; whole at first
         int shift = -1;                    // of keys to bins; -1: by exponents
@@ -355,7 +369,9 @@ struct Draw {
         float mass_above = 0.0f, mass_in = whole;
         above = Pair{0.0f, 0.0f};
         for (int turn = 0; turn < 12; ++turn) {
-            for (int i = threadIdx.x; i < kBins; i += TH) sh.bins[i] = 0;
+            const bool binned = !few || turn;
+            if (binned)
+                for (int i = threadIdx.x; i < kBins; i += TH) sh.bins[i] = 0;
             if (threadIdx.x == 0) {
                 sh.count = 0;
                 sh.low = ~0ull;
@@ -366,7 +382,7 @@ struct Draw {
             const auto bin = [&](float x, uint64_t key) {
                 return shift < 0 ? bin_of(x) : (int)((high - key) >> shift);
             };
-            for (int j = threadIdx.x; j < r.n; j += TH) {
+            for (int j = binned ? (int)threadIdx.x : r.n; j < r.n; j += TH) {
                 const Pack<T, 16> v = at(j);
                 const uint32_t kept = f.kept(v, id_of(j, 0));
                 if (!kept) continue;
@@ -383,10 +399,12 @@ struct Draw {
                               MASS ? __float2uint_rn(fminf(fast_mass(x) * unit, 2147483648.0f)) : 1u);
                 }
             }
-            __syncthreads();
-            find_bin(MASS ? (uint32_t)fminf(fmaxf((target - mass_above) * unit, 1.0f), 4.0e9f)
-                          : count - base);
-            const int b = sh.bin;
+            if (binned) {
+                __syncthreads();
+                find_bin(MASS ? (uint32_t)fminf(fmaxf((target - mass_above) * unit, 1.0f), 4.0e9f)
+                              : count - base);
+            }
+            const int b = binned ? sh.bin : kBins;
             Pair over{0.0f, 0.0f}, in{0.0f, 0.0f};
             uint64_t mine_low = ~0ull, mine_high = 0;
             for (int j = threadIdx.x; j < r.n; j += TH) {
@@ -399,8 +417,9 @@ struct Draw {
                     if (!(kept >> e & 1)) continue;
                     const float x = to_f32(v.e[e]);
                     uint64_t key = 0;
-                    int at_bin;
-                    if (shift < 0) {
+                    int at_bin = kBins;
+                    if (!binned) {
+                    } else if (shift < 0) {
                         at_bin = bin_of(x);
                     } else {
                         key = short_key(x, id_of(j, e));
@@ -417,7 +436,7 @@ struct Draw {
                 }
                 if (MASS && higher) over = add_loosely(over, masses<false>(v, higher).h);
             }
-            if (mine_high) {
+            if (binned && mine_high) {
                 atomicMin(&sh.low, (unsigned long long)mine_low);
                 atomicMax(&sh.high, (unsigned long long)mine_high);
             }
@@ -425,11 +444,12 @@ struct Draw {
             else __syncthreads();
             const int n = sh.count;
             above = over;
-            if (!MASS) base += sh.before;
+            if (!MASS && binned) base += sh.before;
             if (n <= kList) {
                 for (int i = threadIdx.x; i < n; i += TH) {
                     const uint64_t key = sh.list[i];
                     int rank = 0;
+#pragma unroll 2
                     for (int o = 0; o < n; ++o) rank += sh.list[o] > key;
                     sh.order[rank] = key;              // where the bins were
                 }
@@ -437,23 +457,28 @@ struct Draw {
                 before = base;
                 return n;
             }
-            low = sh.low;
-            high = sh.high;
-            mass_above = over.h;
-            mass_in = in.h;
-            shift = 0;
-            while ((high - low) >> shift >= kBins) ++shift;
+            if (binned) {
+                low = sh.low;
+                high = sh.high;
+                mass_above = over.h;
+                mass_in = in.h;
+                shift = 0;
+                while ((high - low) >> shift >= kBins) ++shift;
+            }
             __syncthreads();
         }
         before = base;
         return 0;                          // not reached: a turn leaves 1/1024 of a range of 52 bits
     }
 
-    // The least key of the first k.
-    __device__ __forceinline__ uint64_t floor_of_count(int k) {
+    // The least key of the first k; `bound`: a value that k elements reach, or -inf.
+    __device__ __forceinline__ uint64_t floor_of_count(int k, float bound) {
         Pair above;
         uint32_t before;
-        const int n = list_at<false>(kFinite, (uint32_t)k, 0.0f, 0.0f, above, before);
+        const bool bounded = bound > -INFINITY;
+        const int n = list_at<false>(bounded || r.V <= kList,
+                                     bounded ? (uint64_t)ordered(bound) << kIdBits : kFinite,
+                                     (uint32_t)k, 0.0f, 0.0f, above, before);
         const int at = min(k - 1 - (int)before, n - 1);    // fewer than k finite ones: the last
         const uint64_t key = at >= 0 ? sh.order[at] : kFinite;
         __syncthreads();
@@ -461,15 +486,21 @@ struct Draw {
     }
 
     // How many of the list's n elements are kept: those before which, with what is above the list,
-    // less than the target lies.  -1: the border is not in the list.
+    // less than the target lies.  -1: less than the target lies before its end, -2: more before its begin.
     template <bool EXACT>
     __device__ __noinline__ int kept_of_list(int n, Pair above, Pair target, float error) {
+        Draw d(*this);
+        const int kept = d.template kept_of<EXACT>(n, above, target, error);
+        unsure = d.unsure;
+        return kept;
+    }
+    template <bool EXACT>
+    __device__ __forceinline__ int kept_of(int n, Pair above, Pair target, float error) {
         const int lane = threadIdx.x & 31;
         if (threadIdx.x < 32) {
-            constexpr int EACH = kList / 32;
+            const int each = (n + 31) / 32, i0 = min(n, lane * each), i1 = min(n, i0 + each);
             Pair s{0.0f, 0.0f};
-            const int i0 = lane * EACH;
-            for (int i = i0; i < min(n, i0 + EACH); ++i) {
+            for (int i = i0; i < i1; ++i) {
                 const float x = unordered((uint32_t)(sh.order[i] >> kIdBits));
                 s = add(s, EXACT ? mass(x) : Pair{fast_mass(x), 0.0f});
             }
@@ -482,7 +513,7 @@ struct Draw {
             run = lane ? add(above, run) : above;
             int kept = 0;
             bool close = false;
-            for (int i = i0; i < min(n, i0 + EACH); ++i) {
+            for (int i = i0; i < i1; ++i) {
                 kept += less(run, target);
                 close |= fabsf(difference(run, target)) <= error;
                 const float x = unordered((uint32_t)(sh.order[i] >> kIdBits));
@@ -491,8 +522,8 @@ struct Draw {
             // behind the list's end
             const Pair end = add(above, Pair{__shfl_sync(kAll, s.h, 31), __shfl_sync(kAll, s.l, 31)});
             kept = __reduce_add_sync(kAll, kept);
-            if (kept == 0 && !less(above, target)) kept = -1;
             if (less(end, target)) kept = -1;
+            else if (!less(above, target)) kept = -2;
             close |= fabsf(difference(end, target)) <= error;
             close = __any_sync(kAll, close);
             if (lane == 0) {
@@ -502,34 +533,44 @@ struct Draw {
         }
         __syncthreads();
         const int kept = sh.kept;
-        unsure = sh.unsure || kept < 0;
+        unsure = sh.unsure;
         __syncthreads();
         return kept;
     }
-    // The least key of the first ones, from `least` on, whose masses reach top_p of theirs.
-    __device__ __forceinline__ uint64_t floor_of_mass(uint64_t least, Pair whole) {
+    // The least key of the first ones, from `least` on, whose masses reach top_p of theirs (`whole`), or
+    // `from` if that is higher; `few`: no more than a list holds are there.
+    __device__ __forceinline__ uint64_t floor_of_mass(bool few, uint64_t least, uint64_t from,
+                                                      Pair whole) {
         Pair above;
         uint32_t before;
-        Pair target = mul(whole, p.top_p);
-        const int n = list_at<true>(least, 0, target.h, whole.h, above, before);
-        int kept = kept_of_list<false>(n, above, target, 2.0f * error_of(whole.h, squares, p.V));
+        Pair target = mul(whole, top_p);
+        const int n = list_at<true>(few, from, 0, target.h, whole.h, above, before);
+        int kept = kept_of_list<false>(n, above, target, 2.0f * error_of(whole.h, squares, r.V));
         if (unsure && n) {
             // the sums again, to 40 bits, over the same list
             Pair exact, upper;
             exact_sums(least, sh.order[0] + 1, exact, upper);
-            target = mul(exact, p.top_p);
+            target = mul(exact, top_p);
             kept = kept_of_list<true>(n, upper, target, 0.0f);
         }
-        // a border outside the list (the histogram's masses are rounded): by bisection
-        const uint64_t key = kept > 0 && n ? sh.order[kept - 1] : 0;
+        uint64_t key = kept > 0 && n ? sh.order[kept - 1] : 0;
+        // all from `from` on, or a border outside the list, found by the histogram's rounded masses
+        if (!key && kept == -1 && few) key = from;
         __syncthreads();
-        return key ? key : bisect(least, target);
+        return key ? key : bisect(from, target);
     }
 
     // The first id of a key from `least` on at which the running sum exceeds u of the whole.
     // A warp takes a piece of the row; the one in whose piece the border lies goes through it.
     template <bool EXACT>
     __device__ __noinline__ int token_from(uint64_t least, float u) {
+        Draw d(*this);
+        const int token = d.template token_of<EXACT>(least, u);
+        unsure = d.unsure;
+        return token;
+    }
+    template <bool EXACT>
+    __device__ __forceinline__ int token_of(uint64_t least, float u) {
         const Floor<T> f(least);
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const int each = (r.n + WARPS - 1) / WARPS, j0 = min(r.n, warp * each);
@@ -542,27 +583,26 @@ struct Draw {
         for (int o = 16; o; o >>= 1) s = add(s, shuffled(s, o));
         if (lane == 0) sh.pairs[0][warp] = s;
         __syncthreads();
-        if (threadIdx.x == 0) {
-            Pair run{0.0f, 0.0f};
-            int last = 0;
-#pragma unroll 1
-            for (int w = 0; w < WARPS; ++w) {
-                sh.prefix[w] = run;
-                run = add(run, sh.pairs[0][w]);
-                if (sh.pairs[0][w].h > 0.0f) last = w;
-            }
-            const Pair border = mul(run, Pair{u, 0.0f});
-            sh.prefix[WARPS] = border;
-            sh.floats[0] = EXACT ? 0.0f : 2.0f * error_of(run.h, squares, p.V);
-            int w = 0;                     // the first piece at whose end the border is passed
-#pragma unroll 1
-            while (w < last && !less(border, add(sh.prefix[w], sh.pairs[0][w]))) ++w;
-            sh.found = w;
+        // every warp adds up the pieces before each, by its lanes
+        const Pair piece = lane < WARPS ? sh.pairs[0][lane] : Pair{0.0f, 0.0f};
+        Pair upto_piece = piece;
+#pragma unroll
+        for (int o = 1; o < WARPS; o *= 2) {
+            const Pair y = shuffled_up(upto_piece, o);
+            if (lane >= o) upto_piece = add(upto_piece, y);
         }
-        __syncthreads();
-        if (warp == sh.found) {
-            const Pair border = sh.prefix[WARPS];
-            Pair run = sh.prefix[warp];
+        const Pair whole{__shfl_sync(kAll, upto_piece.h, WARPS - 1),
+                         __shfl_sync(kAll, upto_piece.l, WARPS - 1)};
+        const Pair border = mul(whole, Pair{u, 0.0f});
+        const float error = EXACT ? 0.0f : 2.0f * error_of(whole.h, squares, r.V);
+        // the first piece at whose end the border is passed, else the last with a mass
+        const unsigned filled = __ballot_sync(kAll, piece.h > 0.0f);
+        const unsigned passed = __ballot_sync(kAll, piece.h > 0.0f && less(border, upto_piece));
+        const int found = passed ? __ffs(passed) - 1 : filled ? 31 - __clz(filled) : 0;
+        const int ahead_of = max(found - 1, 0);
+        Pair run{__shfl_sync(kAll, upto_piece.h, ahead_of), __shfl_sync(kAll, upto_piece.l, ahead_of)};
+        if (found == 0) run = Pair{0.0f, 0.0f};
+        if (warp == found) {
             int token = -1;
             Pair before = run, after = run;                // of the token
             for (int j = j0; j < j1; j += 32) {
@@ -607,7 +647,6 @@ struct Draw {
             }
             if (lane == 0) {
                 // certain where nothing is kept before the token, and on its other side as u < 1
-                const float error = sh.floats[0];
                 const bool low = before.h > 0.0f && difference(border, before) <= error;
                 const bool high = difference(after, border) <= error;
                 sh.token = token;
@@ -659,10 +698,11 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
             }
         }
         const float2 both = half_maxima(most);
-        float m = warp_max_nan(max_nan(both.x, both.y));
-        if (lane == 0) sh.floats[tid >> 5] = m;
+        const float mine = max_nan(both.x, both.y);        // the thread's largest
+        float m = warp_max_nan(mine);
+        if (lane == 0) sh.floats[0][tid >> 5] = m;
         __syncthreads();
-        m = warp_max_nan(lane < WARPS ? sh.floats[lane] : -INFINITY);
+        m = warp_max_nan(lane < WARPS ? sh.floats[0][lane] : -INFINITY);
         bad = !(m < INFINITY);
         if (!bad && m > -INFINITY) {
             d.top = m;
@@ -686,14 +726,28 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
                 d.sum2(s, s1);
                 if (at_tau) {
                     const float sq = warp_sum(squares.x + squares.y);
-                    if (lane == 0) sh.floats[tid >> 5] = sq;
+                    if (lane == 0) sh.floats[1][tid >> 5] = sq;
                     __syncthreads();
-                    d.squares = warp_sum(lane < WARPS ? sh.floats[lane] : 0.0f);
+                    d.squares = warp_sum(lane < WARPS ? sh.floats[1][lane] : 0.0f);
                 }
             }
             const float lse = p.fused ? logf(p.unit_tau ? s.h : s1.h) : 0.0f;
             uint64_t least = kFinite;
-            if (p.top_k && p.top_k < p.V) least = d.floor_of_count(p.top_k);
+            const bool some_k = p.top_k && p.top_k < p.V;
+            if (some_k) {
+                // of every warp's threads' largest elements its share of top_k, the least of them: a
+                // bound that so many elements reach
+                const int c = (p.top_k + WARPS - 1) / WARPS;
+                float bound = -INFINITY;
+                if (c <= 32) {
+                    const float cth = __shfl_sync(kAll, warp_sorted(mine), c - 1);
+                    __syncthreads();
+                    if (lane == 0) sh.floats[0][tid >> 5] = -cth;
+                    __syncthreads();
+                    bound = -warp_max(lane < WARPS ? sh.floats[0][lane] : -INFINITY);
+                }
+                least = d.floor_of_count(p.top_k, bound);
+            }
             uint64_t by_gap = 0;
             if (p.min_gap > -INFINITY) {
                 // the least float32 that is not below top + tau log min_p
@@ -702,14 +756,36 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
             }
             uint64_t floor = least;
             if (p.top_p.h < 1.0f) {
-                if (least != kFinite) {                    // of what top_k has left
+                const uint64_t from = by_gap > least ? by_gap : least;
+                bool few = p.V <= kList || (some_k && p.top_k <= kList);
+                if (some_k) {                              // of what top_k has left
                     const Floor<T> f(least);
                     s = s1 = Pair{0.0f, 0.0f};
                     for (int j = tid; j < d.r.n; j += TH)
                         s = add_loosely(s, d.template mass_of_vector<false>(j, f).h);
                     d.sum2(s, s1);
                 }
-                floor = d.floor_of_mass(least, s);
+                bool within = true;                        // the border lies above `from`
+                if (from > least) {
+                    const Floor<T> f(from);
+                    Pair upper{0.0f, 0.0f};
+                    s1 = Pair{0.0f, 0.0f};
+                    int n = 0;
+                    for (int j = tid; j < d.r.n; j += TH) {
+                        const Pack<T, 16> v = d.at(j);
+                        const uint32_t kept = f.kept(v, d.id_of(j, 0));
+                        if (!kept) continue;
+                        upper = add_loosely(upper, d.template masses<false>(v, kept).h);
+                        n += __popc(kept);
+                    }
+                    s1.h = (float)n;
+                    d.sum2(upper, s1);
+                    few |= s1.h <= (float)kList;
+                    // where that is open, by what the exact sums say of the whole list, or of all
+                    within = !(difference(mul(s, p.top_p), upper) >
+                               2.0f * error_of(s.h, d.squares, p.V));
+                }
+                floor = within ? d.floor_of_mass(few, least, from, s) : from;
             }
             floor = by_gap > floor ? by_gap : floor;
             token = d.template token_from<false>(floor, u);
