@@ -57,7 +57,8 @@ inline Pair pair_of(double x) {
 // Waite's reduction: ln 2 in three parts, the first with few bits so that n times it is exact),
 // e^(g/16) - 1 by its Taylor series and four times (1 + q)^2 - 1.
 __device__ __forceinline__ Pair exp_pair(Pair d) {
-    if (!(d.h > -86.0f)) return {0.0f, 0.0f};
+    const bool some = d.h > -86.0f;
+    if (!some) d = Pair{0.0f, 0.0f};
     const float n = rintf(d.h * (float)kLog2e);
     constexpr double ln2 = 0.69314718055994530942;
     constexpr float ln2a = 11356.0f / 16384.0f;            // 14 bits: n * ln2a is exact
@@ -79,7 +80,7 @@ __device__ __forceinline__ Pair exp_pair(Pair d) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) q = add(Pair{2.0f * q.h, 2.0f * q.l}, mul(q, q));
     const Pair e = add(Pair{1.0f, 0.0f}, q);
-    const float s = __int_as_float(((int)n + 127) << 23);  // n >= -125
+    const float s = some ? __int_as_float(((int)n + 127) << 23) : 0.0f;    // n >= -125
     return {e.h * s, e.l * s};
 }
 
@@ -145,12 +146,16 @@ struct Shared {
         uint32_t bins[kBins];
         uint64_t order[kList];
     };
-    uint64_t list[kList];
+    union {
+        uint64_t list[kList];
+        Pair masses[kList];
+    };
     uint32_t groups[32];                   // sums of 32 bins each
     Pair pairs[2][WARPS];
     float floats[2][WARPS];
     int ints[WARPS];
     unsigned long long low, high;          // keys
+    uint64_t bar;                          // of the row's copy
     uint32_t before;
     int bin, count, token, kept;
     bool unsure;
@@ -215,13 +220,33 @@ struct Draw {
     __device__ __forceinline__ float fast_mass(float x) const {
         return fmaxf(Exponent(top, scale, scale_low)(x), kLeastMass);
     }
+    // One copy of the code: it is seldom run, and then mostly waits to be fetched.
+    __device__ __noinline__ Pair exact_masses(uint4 raw, uint32_t kept) const {
+        Pair s{0.0f, 0.0f};
+        uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll 1
+        for (int i = 0; i < 4 && kept; ++i) {              // a word's elements side by side
+            float x, y = -INFINITY;
+            if constexpr (sizeof(T) == 4) {
+                x = __uint_as_float(w[0]);
+            } else {
+                const uint16_t a = (uint16_t)w[0], b = (uint16_t)(w[0] >> 16);
+                x = to_f32(reinterpret_cast<const T&>(a));
+                y = to_f32(reinterpret_cast<const T&>(b));
+            }
+            const Pair m = mass(x), n = sizeof(T) == 4 ? Pair{0.0f, 0.0f} : mass(y);
+            s = add(s, add(kept & 1 ? m : Pair{0.0f, 0.0f},
+                           sizeof(T) == 2 && (kept & 2) ? n : Pair{0.0f, 0.0f}));
+            kept >>= sizeof(T) == 4 ? 1 : 2;
+            w[0] = w[1], w[1] = w[2], w[2] = w[3];
+        }
+        return s;
+    }
     template <bool EXACT>
     __device__ __forceinline__ Pair masses(const Pack<T, 16>& v, uint32_t kept) const {
         Pair s{0.0f, 0.0f};
         if constexpr (EXACT) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (kept >> e & 1) s = add(s, mass(to_f32(v.e[e])));
+            s = exact_masses(v.raw, kept);
         } else {
             const Exponent f(top, scale, scale_low);
             float2 e[E / 2];
@@ -282,18 +307,14 @@ struct Draw {
         Pair a{0.0f, 0.0f}, b{0.0f, 0.0f};
         for (int j = threadIdx.x; j < r.n; j += TH) {
             const Pack<T, 16> v = at(j);
-            const uint32_t kept = f.kept(v, id_of(j, 0)), over = g.kept(v, id_of(j, 0));
+            const uint32_t kept = f.kept(v, id_of(j, 0));
             if (!kept) continue;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (!(kept >> e & 1)) continue;
-                const Pair m = mass(to_f32(v.e[e]));
-                a = add(a, m);
-                if (over >> e & 1) b = add(b, m);
-            }
+            const uint32_t over = g.kept(v, id_of(j, 0));  // of those: above >= least
+            if (over) b = add(b, masses<true>(v, over));
+            if (kept != over) a = add(a, masses<true>(v, kept ^ over));
         }
         sum2(a, b);
-        whole = a;
+        whole = add(a, b);
         upper = b;
     }
     // The least key, from `least` on, above which lies less than the target: by bisection.
@@ -497,13 +518,15 @@ struct Draw {
     template <bool EXACT>
     __device__ __forceinline__ int kept_of(int n, Pair above, Pair target, float error) {
         const int lane = threadIdx.x & 31;
+        for (int i = threadIdx.x; i < n; i += TH) {        // in the place of the unordered list
+            const float x = unordered((uint32_t)(sh.order[i] >> kIdBits));
+            sh.masses[i] = EXACT ? mass(x) : Pair{fast_mass(x), 0.0f};
+        }
+        __syncthreads();
         if (threadIdx.x < 32) {
             const int each = (n + 31) / 32, i0 = min(n, lane * each), i1 = min(n, i0 + each);
             Pair s{0.0f, 0.0f};
-            for (int i = i0; i < i1; ++i) {
-                const float x = unordered((uint32_t)(sh.order[i] >> kIdBits));
-                s = add(s, EXACT ? mass(x) : Pair{fast_mass(x), 0.0f});
-            }
+            for (int i = i0; i < i1; ++i) s = add(s, sh.masses[i]);
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
                 const Pair y = shuffled_up(s, o);
@@ -516,8 +539,7 @@ struct Draw {
             for (int i = i0; i < i1; ++i) {
                 kept += less(run, target);
                 close |= fabsf(difference(run, target)) <= error;
-                const float x = unordered((uint32_t)(sh.order[i] >> kIdBits));
-                run = add(run, EXACT ? mass(x) : Pair{fast_mass(x), 0.0f});
+                run = add(run, sh.masses[i]);
             }
             // behind the list's end
             const Pair end = add(above, Pair{__shfl_sync(kAll, s.h, 31), __shfl_sync(kAll, s.l, 31)});
@@ -608,40 +630,39 @@ struct Draw {
             for (int j = j0; j < j1; j += 32) {
                 Pair s = j + lane < j1 ? mass_of_vector<EXACT>(j + lane, f) : Pair{0.0f, 0.0f};
                 const Pair mine = s;
+                const unsigned some = __ballot_sync(kAll, mine.h > 0.0f);
+                if (!some) continue;
 #pragma unroll
                 for (int o = 1; o < 32; o *= 2) {
                     const Pair y = shuffled_up(s, o);
                     if (lane >= o) s = add(s, y);
                 }
                 const Pair end = add(run, s);
-                const unsigned some = __ballot_sync(kAll, mine.h > 0.0f);
                 const unsigned past = __ballot_sync(kAll, mine.h > 0.0f && less(border, end));
-                if (some) {
-                    // the vector that passes the border, or (where the sums' last bits differ)
-                    // the last that holds a kept element so far
-                    const int at_lane = past ? __ffs(past) - 1 : 31 - __clz(some);
-                    Pair upto = shuffled_up(s, 1);
-                    upto = lane ? add(run, upto) : run;
-                    int got = -1;
-                    Pair ahead = upto;
-                    if (lane == at_lane) {
-                        const Pack<T, 16> v = at(j + lane);
-                        const uint32_t kept = f.kept(v, id_of(j + lane, 0));
-                        bool open = true;
+                // the vector that passes the border, or (where the sums' last bits differ)
+                // the last that holds a kept element so far
+                const int at_lane = past ? __ffs(past) - 1 : 31 - __clz(some);
+                Pair upto = shuffled_up(s, 1);
+                upto = lane ? add(run, upto) : run;
+                int got = -1;
+                Pair ahead = upto;
+                if (lane == at_lane) {
+                    const Pack<T, 16> v = at(j + lane);
+                    const uint32_t kept = f.kept(v, id_of(j + lane, 0));
+                    bool open = true;
 #pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            if (!open || !(kept >> e & 1)) continue;
-                            const float x = to_f32(v.e[e]);
-                            got = id_of(j + lane, e);
-                            ahead = upto;
-                            upto = add(upto, EXACT ? mass(x) : Pair{fast_mass(x), 0.0f});
-                            if (past && less(border, upto)) open = false;
-                        }
+                    for (int e = 0; e < E; ++e) {
+                        if (!open || !(kept >> e & 1)) continue;
+                        const float x = to_f32(v.e[e]);
+                        got = id_of(j + lane, e);
+                        ahead = upto;
+                        upto = add(upto, EXACT ? mass(x) : Pair{fast_mass(x), 0.0f});
+                        if (past && less(border, upto)) open = false;
                     }
-                    token = __shfl_sync(kAll, got, at_lane);
-                    before = Pair{__shfl_sync(kAll, ahead.h, at_lane), __shfl_sync(kAll, ahead.l, at_lane)};
-                    after = Pair{__shfl_sync(kAll, upto.h, at_lane), __shfl_sync(kAll, upto.l, at_lane)};
                 }
+                token = __shfl_sync(kAll, got, at_lane);
+                before = Pair{__shfl_sync(kAll, ahead.h, at_lane), __shfl_sync(kAll, ahead.l, at_lane)};
+                after = Pair{__shfl_sync(kAll, upto.h, at_lane), __shfl_sync(kAll, upto.l, at_lane)};
                 if (past) break;
                 run = Pair{__shfl_sync(kAll, end.h, 31), __shfl_sync(kAll, end.l, 31)};
             }
@@ -686,16 +707,23 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
         const T* x = reinterpret_cast<const T*>(p.logits + b * p.batch_stride + k * p.beam_stride);
         Draw<T, TH, HERE> d(p, sh, x, stage);
         Pack<T, 16> most = all_minus_inf<T>();
-        for (int j0 = tid; j0 < d.r.n; j0 += 4 * TH) {     // four loads in flight
-            Pack<T, 16> v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = j0 + i * TH < d.r.n ? d.r.load(j0 + i * TH) : all_minus_inf<T>();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                most = larger(most, v[i]);
-                if (HERE && j0 + i * TH < d.r.n) stage[j0 + i * TH] = v[i].raw;
+        if constexpr (HERE) {
+            // one bulk copy; the units it shares with what is not the row's element by element
+            const Staged<T, TH> row_here(x, p.V, stage, true, true);
+            if (tid == 0) {
+                mbar_init(&sh.bar);
+                fence_mbar_init();
+                row_here.fetch(&sh.bar);
             }
+            __syncthreads();                               // the barrier is there
+            int polls = kWaitPolls;
+            mbar_wait(&sh.bar, 0, polls, p.status);
+            row_here.complete();
+#pragma unroll 4
+            for (int j = tid; j < d.r.n; j += TH) most = larger(most, row_here.at(j));
+        } else {
+#pragma unroll 4
+            for (int j = tid; j < d.r.n; j += TH) most = larger(most, d.r.load(j));
         }
         const float2 both = half_maxima(most);
         const float mine = max_nan(both.x, both.y);        // the thread's largest

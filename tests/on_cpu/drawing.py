@@ -16,7 +16,9 @@ def device_source():
     """What the kernel needs of rnnt_rows.cuh, and rnnt_sample.cu up to its launches; inline assembly
     as C++."""
     rows = open(os.path.join(B.CSRC, "rnnt_rows.cuh")).read()
-    rows = rows[rows.index("constexpr unsigned kAll"):rows.index("// ------------------------------------------------------------ groups of threads")]
+    rows = rows[rows.index("constexpr unsigned kAll"):rows.index("// Device-side memory limits")]
+    rows = re.sub(r"__device__ __forceinline__ uint32_t shared_at.*?(?=// A row in a stage)",
+                  "", rows, flags=re.S)        # copies: in the harness
     s = open(os.path.join(B.CSRC, "rnnt_sample.cu")).read()
     s = rows + s[s.index("// ------------------------------------------------------------ pairs of floats"):
                  s.index("template <typename T>\nvoid launch_sample")]

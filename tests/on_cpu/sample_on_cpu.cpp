@@ -67,6 +67,14 @@ template <class T2> unsigned __hgt2_mask(T2 a, T2 b) {
     return (to_f32(a.x) > to_f32(b.x) ? 0xffffu : 0u) | (to_f32(a.y) > to_f32(b.y) ? 0xffff0000u : 0u);
 }
 
+inline void mbar_init(uint64_t*) {}
+inline void fence_mbar_init() {}
+inline void mbar_wait(uint64_t*, uint32_t, int&, int32_t*) {}
+inline void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t*) {
+    if ((uintptr_t)to % 16 || (uintptr_t)from % 16 || bytes % 16) abort();
+    memcpy(to, from, bytes);
+}
+
 #include "sample_device.inc"
 
 template <typename T, int TH, bool HERE> bool draw(const SampleParams& p) {
