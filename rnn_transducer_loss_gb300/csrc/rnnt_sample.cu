@@ -53,35 +53,49 @@ inline Pair pair_of(double x) {
     return {h, (float)(x - (double)h)};
 }
 
-// exp(d) for d <= 0, relative error below 2^-40 down to e^-60: with d = n ln 2 + g (Cody and
-// Waite's reduction: ln 2 in three parts, the first with few bits so that n times it is exact),
-// e^(g/16) - 1 by its Taylor series and four times (1 + q)^2 - 1.
-__device__ __forceinline__ Pair exp_pair(Pair d) {
-    const bool some = d.h > -86.0f;
-    if (!some) d = Pair{0.0f, 0.0f};
-    const float n = rintf(d.h * (float)kLog2e);
+// 2^(i / 16) as pairs.
+__device__ const float2 kRoots[16] = {
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f},
+    {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f},
+    {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}, {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f},
+    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f},
+    {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f},
+    {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}, {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f},
+    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f},
+    {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}};
+// 2^(d c) for d <= 0, relative error below 2^-40 down to 2^-120: d c = n + i / 16 + g, and 2^g = e^z,
+// z = g ln 2, by its Taylor series (|z| < 0.0217: the first two terms in pairs, what follows is
+// below 2e-6).  About 50 operations.
+__device__ __forceinline__ Pair exp2_pair(Pair d, Pair c) {
+    float th = __fmul_rn(d.h, c.h);
+    const bool some = th > -120.0f;
+    if (!some) {
+        d = Pair{0.0f, 0.0f};
+        th = 0.0f;
+    }
+    const float tl = __fadd_rn(__fmaf_rn(d.h, c.h, -th),
+                               __fmaf_rn(d.h, c.l, __fmul_rn(d.l, c.h)));
+    const float at = rintf(th * 16.0f);                    // in sixteenths
+    const int k = (int)at, n = k >> 4;                     // rounded down
+    const float gh = __fmaf_rn(at, -0.0625f, th);          // exact
     constexpr double ln2 = 0.69314718055994530942;
-    constexpr float ln2a = 11356.0f / 16384.0f;            // 14 bits: n * ln2a is exact
-    constexpr float ln2b = (float)(ln2 - (double)ln2a);
-    constexpr float ln2c = (float)(ln2 - (double)ln2a - (double)ln2b);
-    const Pair a = two_sum(__fmaf_rn(-n, ln2a, d.h), d.l);
-    const float p = __fmul_rn(n, ln2b);
-    const float pl = __fadd_rn(__fmaf_rn(n, ln2b, -p), __fmul_rn(n, ln2c));
-    Pair g = add(a, Pair{-p, -pl});
-    g = Pair{g.h * 0.0625f, g.l * 0.0625f};                // |g| < 0.0217
-    const Pair g2 = mul(g, g);
-    float tail = __fmaf_rn(g.h, 1.0f / 5040.0f, 1.0f / 720.0f);
-    tail = __fmaf_rn(tail, g.h, 1.0f / 120.0f);
-    tail = __fmaf_rn(tail, g.h, 1.0f / 24.0f);
-    tail = tail * g.h * g.h * g2.h;                        // g^4/24 + ...: below 1e-8
-    const Pair g3 = mul(g2, g);
-    const Pair sixth{1.0f / 6.0f, (float)(1.0 / 6.0 - (double)(1.0f / 6.0f))};
-    Pair q = add(g, add(Pair{0.5f * g2.h, 0.5f * g2.l}, add(mul(g3, sixth), Pair{tail, 0.0f})));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q = add(Pair{2.0f * q.h, 2.0f * q.l}, mul(q, q));
-    const Pair e = add(Pair{1.0f, 0.0f}, q);
-    const float s = some ? __int_as_float(((int)n + 127) << 23) : 0.0f;    // n >= -125
-    return {e.h * s, e.l * s};
+    constexpr float lh = (float)ln2, ll = (float)(ln2 - (double)lh);
+    const float zh = __fmul_rn(gh, lh);
+    const float zl = __fadd_rn(__fmaf_rn(gh, lh, -zh), __fmaf_rn(gh, ll, __fmul_rn(tl, lh)));
+    const float qh = __fmul_rn(zh, zh);                    // z^2
+    const float ql = __fmaf_rn(2.0f * zh, zl, __fmaf_rn(zh, zh, -qh));
+    float tail = __fmaf_rn(zh, 1.0f / 120.0f, 1.0f / 24.0f);
+    tail = __fmaf_rn(tail, zh, 1.0f / 6.0f);
+    tail = __fmul_rn(tail, __fmul_rn(qh, zh));
+    const Pair q = fast_two_sum(zh, 0.5f * qh);
+    const float low = __fadd_rn(q.l, __fadd_rn(__fmaf_rn(0.5f, ql, zl), tail));
+    const float2 r = __ldg(&kRoots[k & 15]);
+    const float ph = __fmul_rn(r.x, q.h);
+    const float pl = __fadd_rn(__fmaf_rn(r.x, q.h, -ph), __fmaf_rn(r.x, low, __fmul_rn(r.y, q.h)));
+    const Pair e = fast_two_sum(r.x, ph);
+    const Pair f = fast_two_sum(e.h, __fadd_rn(e.l, __fadd_rn(r.y, pl)));
+    const float s = some ? __int_as_float((n + 127) << 23) : 0.0f;     // n >= -120
+    return {f.h * s, f.l * s};
 }
 
 // --------------------------------------------------------------------- rows
@@ -96,7 +110,7 @@ struct SampleParams {
     float scale, scale_low;                // log2 e / tau, in two parts
     float one, one_low;                    // log2 e
     float bin_scale;                       // bins of a logit's unit
-    Pair inv_tau, top_p;                   // top_p.h >= 1: not used
+    Pair exact_scale, top_p;               // log2 e / tau; top_p.h >= 1: not used
     double min_gap;                        // tau log min_p, or -inf
     float* out_scores;
     int32_t* out_tokens;
@@ -148,7 +162,7 @@ struct Shared {
     };
     union {
         uint64_t list[kList];
-        Pair masses[kList];
+        Pair masses[kList + 32];
     };
     uint32_t groups[32];                   // sums of 32 bins each
     Pair pairs[2][WARPS];
@@ -190,14 +204,14 @@ struct Draw {
     const Row<T> r;
     uint4* const here;
     const float scale, scale_low, bin_scale;
-    const Pair inv_tau, top_p;
+    const Pair exact_scale, top_p;
     float top;
     float squares;                         // the sum of the terms' squares
     bool unsure;                           // of the last result: the fast sums leave it open
 
     __device__ __forceinline__ Draw(const SampleParams& p, Shared<TH>& s, const T* x, uint4* stage)
         : sh(s), r(x, p.V), here(stage), scale(p.scale), scale_low(p.scale_low),
-          bin_scale(p.bin_scale), inv_tau(p.inv_tau), top_p(p.top_p), top(0.0f), squares(INFINITY),
+          bin_scale(p.bin_scale), exact_scale(p.exact_scale), top_p(p.top_p), top(0.0f), squares(INFINITY),
           unsure(false) {}
 
     __device__ __forceinline__ Pack<T, 16> at(int j) const {
@@ -213,8 +227,7 @@ struct Draw {
 
     // ---- masses: of pairs (exact), or float32
     __device__ __forceinline__ Pair mass(float x) const {
-        const Pair d = two_sum(x, -top);
-        const Pair e = exp_pair(mul(d, inv_tau));
+        const Pair e = exp2_pair(two_sum(x, -top), exact_scale);
         return e.h >= kLeastMass ? e : Pair{kLeastMass, 0.0f};
     }
     __device__ __forceinline__ float fast_mass(float x) const {
@@ -250,6 +263,10 @@ struct Draw {
         } else {
             const Exponent f(top, scale, scale_low);
             float2 e[E / 2];
+            if (kept == (1u << E) - 1u) {
+                s.h = fmaxf(terms_of(v, f, e), kLeastMass);
+                return s;
+            }
             unpack(v, e);
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) {
@@ -624,49 +641,79 @@ struct Draw {
         const int ahead_of = max(found - 1, 0);
         Pair run{__shfl_sync(kAll, upto_piece.h, ahead_of), __shfl_sync(kAll, upto_piece.l, ahead_of)};
         if (found == 0) run = Pair{0.0f, 0.0f};
-        if (warp == found) {
-            int token = -1;
-            Pair before = run, after = run;                // of the token
-            for (int j = j0; j < j1; j += 32) {
-                Pair s = j + lane < j1 ? mass_of_vector<EXACT>(j + lane, f) : Pair{0.0f, 0.0f};
-                const Pair mine = s;
-                const unsigned some = __ballot_sync(kAll, mine.h > 0.0f);
-                if (!some) continue;
+        // the piece again, in steps of 32 vectors that all warps share; every warp then looks for the
+        // step with the border
+        const int k0 = min(r.n, found * each), k1 = min(r.n, k0 + each);
+        const int steps = (k1 - k0 + 31) / 32;             // up to kList + 1
+        for (int i = warp; i < steps; i += WARPS) {
+            const int j = k0 + i * 32 + lane;
+            Pair m = j < k1 ? mass_of_vector<EXACT>(j, f) : Pair{0.0f, 0.0f};
 #pragma unroll
-                for (int o = 1; o < 32; o *= 2) {
-                    const Pair y = shuffled_up(s, o);
-                    if (lane >= o) s = add(s, y);
-                }
-                const Pair end = add(run, s);
-                const unsigned past = __ballot_sync(kAll, mine.h > 0.0f && less(border, end));
-                // the vector that passes the border, or (where the sums' last bits differ)
-                // the last that holds a kept element so far
-                const int at_lane = past ? __ffs(past) - 1 : 31 - __clz(some);
-                Pair upto = shuffled_up(s, 1);
-                upto = lane ? add(run, upto) : run;
-                int got = -1;
-                Pair ahead = upto;
-                if (lane == at_lane) {
-                    const Pack<T, 16> v = at(j + lane);
-                    const uint32_t kept = f.kept(v, id_of(j + lane, 0));
-                    bool open = true;
+            for (int o = 16; o; o >>= 1) m = add(m, shuffled(m, o));
+            if (lane == 0) sh.masses[i] = m;
+        }
+        __syncthreads();
+        const auto reached = [&](Pair mine, Pair upto, unsigned& past) {   // by which lane
+            past = __ballot_sync(kAll, mine.h > 0.0f && less(border, upto));
+            const unsigned some = __ballot_sync(kAll, mine.h > 0.0f);
+            return past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
+        };
+        const auto scanned = [&](Pair m) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        if (!open || !(kept >> e & 1)) continue;
-                        const float x = to_f32(v.e[e]);
-                        got = id_of(j + lane, e);
-                        ahead = upto;
-                        upto = add(upto, EXACT ? mass(x) : Pair{fast_mass(x), 0.0f});
-                        if (past && less(border, upto)) open = false;
-                    }
-                }
-                token = __shfl_sync(kAll, got, at_lane);
-                before = Pair{__shfl_sync(kAll, ahead.h, at_lane), __shfl_sync(kAll, ahead.l, at_lane)};
-                after = Pair{__shfl_sync(kAll, upto.h, at_lane), __shfl_sync(kAll, upto.l, at_lane)};
-                if (past) break;
-                run = Pair{__shfl_sync(kAll, end.h, 31), __shfl_sync(kAll, end.l, 31)};
+            for (int o = 1; o < 32; o *= 2) {
+                const Pair y = shuffled_up(m, o);
+                if (lane >= o) m = add(m, y);
             }
-            if (lane == 0) {
+            return m;
+        };
+        const auto from_lane = [&](Pair m, int l) {
+            return Pair{__shfl_sync(kAll, m.h, l), __shfl_sync(kAll, m.l, l)};
+        };
+        const auto ahead = [&](Pair upto) {                // of what the lane before has reached
+            const Pair y = shuffled_up(upto, 1);
+            return lane ? add(run, y) : run;
+        };
+        int step = 0;
+        {
+            const int some = (steps + 31) / 32, i0 = min(steps, lane * some), i1 = min(steps, i0 + some);
+            Pair m{0.0f, 0.0f};
+            for (int i = i0; i < i1; ++i) m = add(m, sh.masses[i]);
+            const Pair upto = scanned(m);
+            unsigned past;
+            const int l = reached(m, add(run, upto), past);
+            Pair at_step = ahead(upto), next = at_step;
+            for (int i = i0; i < i1; ++i) {
+                const Pair t = sh.masses[i];
+                if (!(t.h > 0.0f)) continue;
+                step = i;
+                at_step = next;
+                next = add(next, t);
+                if (past && less(border, next)) break;
+            }
+            step = __shfl_sync(kAll, step, l);
+            run = from_lane(at_step, l);
+        }
+        if (warp == step % WARPS) {
+            const int j = k0 + step * 32 + lane;
+            const Pair m = j < k1 ? mass_of_vector<EXACT>(j, f) : Pair{0.0f, 0.0f};
+            const Pair upto = scanned(m);
+            unsigned past;
+            const int l = reached(m, add(run, upto), past);
+            Pair before = ahead(upto), after = before;     // of the token
+            if (lane == l) {
+                int token = -1;
+                const Pack<T, 16> v = at(min(j, r.n - 1));
+                const uint32_t kept = j < k1 ? f.kept(v, id_of(j, 0)) : 0u;
+                bool open = true;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    if (!open || !(kept >> e & 1)) continue;
+                    const float x = to_f32(v.e[e]);
+                    token = id_of(j, e);
+                    before = after;
+                    after = add(after, EXACT ? mass(x) : Pair{fast_mass(x), 0.0f});
+                    if (past && less(border, after)) open = false;
+                }
                 // certain where nothing is kept before the token, and on its other side as u < 1
                 const bool low = before.h > 0.0f && difference(border, before) <= error;
                 const bool high = difference(after, border) <= error;
@@ -839,7 +886,7 @@ void fill_params(SampleParams& p, int32_t V, double temperature, int32_t top_k, 
     parts_below(kLog2e / temperature, p.scale, p.scale_low);
     parts_below(kLog2e, p.one, p.one_low);
     p.bin_scale = (float)(kLog2e / temperature) * kBinsPerOrder;
-    p.inv_tau = pair_of(1.0 / temperature);
+    p.exact_scale = pair_of(kLog2e / temperature);
     p.top_p = top_p < 1.0 ? pair_of(top_p) : Pair{2.0f, 0.0f};
     p.min_gap = min_p > 0.0 ? temperature * std::log(min_p) : -INFINITY;
 }
