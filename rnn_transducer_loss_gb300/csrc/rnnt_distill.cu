@@ -56,6 +56,31 @@ struct Lattice {
     }
 };
 
+// Whether the rows first, first + step, ... count: rows below `rows` and, in the padded layout, inside
+// their sequence.  A warp's lanes look 32 rows up at a time, up to 64 rows ahead.
+struct Window {
+    uint32_t now, later;
+    int32_t i;
+    __device__ static __forceinline__ uint32_t look(const Lattice& lat, int64_t first, int64_t step,
+                                                    int64_t rows) {
+        const int64_t row = first + (threadIdx.x & 31) * step;
+        return __ballot_sync(kAll, row < rows && (!lat.T || !lat.padded || lat.inside(row)));
+    }
+    __device__ __forceinline__ Window(const Lattice& lat, int64_t first, int64_t step, int64_t rows)
+        : now(look(lat, first, step, rows)), later(look(lat, first + 32 * step, step, rows)), i(0) {}
+    // Of the row `ahead` (below 32) behind the present one.
+    __device__ __forceinline__ bool operator[](int ahead) const {
+        return __funnelshift_r(now, later, i) >> ahead & 1;
+    }
+    __device__ __forceinline__ void advance(const Lattice& lat, int64_t next, int64_t step,
+                                            int64_t rows) {
+        if (++i < 32) return;
+        i = 0;
+        now = later;
+        later = look(lat, next + 32 * step, step, rows);
+    }
+};
+
 // ------------------------------------------------------------------ blocks
 template <int TH>
 __device__ __forceinline__ uint64_t block_largest(uint64_t x, uint64_t* space) {
@@ -296,7 +321,7 @@ __device__ __forceinline__ float warp_cth(float x, int c) {
 // ranked by counting.  They are then taken out of the row, which leaves the rest: its largest
 // element (the k + 1-st best, if it reached the bound) and the sum relative to it.
 template <typename T, int TH, int G, bool WHOLE>
-__global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) {
+__global__ void __launch_bounds__(TH, 5) k_top(const TopParams p, const Ring ring) {
     using Gr = Group<G>;
     using Scratch = TopScratch<T, G>;
     using K = Keys<T, G>;
@@ -308,7 +333,6 @@ __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) 
     const int me = Gr::rank(), lane = me & 31, k = p.k;
     const int64_t groups = (int64_t)gridDim.x * GROUPS;
     const int64_t first_row = (int64_t)blockIdx.x * GROUPS + (G == 32 ? threadIdx.x / G : 0);
-    const auto live = [&](int64_t row) { return !p.lat.T || p.lat.inside(row); };
     const auto staged = [&](int64_t row, int st) {
         return Staged<T, G, WHOLE>(reinterpret_cast<const T*>(p.logits) + row * p.V, p.V,
                                    reinterpret_cast<uint4*>(mine + st * ring.stage_bytes),
@@ -321,17 +345,16 @@ __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) 
         sh.count = 0;
     }
     Gr::sync();
+    Window live(p.lat, first_row, groups, p.lat.rows);
     if (me == 0)
-        for (int st = 0; st < ring.stages; ++st) {
-            const int64_t row = first_row + st * groups;
-            if (row < p.lat.rows && live(row)) staged(row, st).fetch(&sh.bar[st]);
-        }
+        for (int st = 0; st < ring.stages; ++st)
+            if (live[st]) staged(first_row + st * groups, st).fetch(&sh.bar[st]);
     int polls = kWaitPolls, st = 0;
     uint32_t phases = 0;                                   // a bit a stage
     for (int64_t row = first_row; row < p.lat.rows; row += groups) {
         float rest = -INFINITY;
         int have = 0;
-        if (live(row)) {
+        if (live[0]) {
             const Staged<T, G, WHOLE> x = staged(row, st);
             mbar_wait(&sh.bar[st], phases >> st & 1, polls, p.status);
             phases ^= 1u << st;
@@ -468,11 +491,11 @@ __global__ void __launch_bounds__(TH) k_top(const TopParams p, const Ring ring) 
         }
         if (me == 0) p.rest[row] = rest;
         Gr::sync();                                        // the stage has been read
-        const int64_t next = row + ring.stages * groups;
-        if (me == 0 && next < p.lat.rows && live(next)) {
+        if (me == 0 && live[ring.stages]) {
             fence_proxy_async();
-            staged(next, st).fetch(&sh.bar[st]);
+            staged(row + ring.stages * groups, st).fetch(&sh.bar[st]);
         }
+        live.advance(p.lat, row + groups, groups, p.lat.rows);
         st = st + 1 == ring.stages ? 0 : st + 1;
     }
 }
@@ -823,7 +846,8 @@ struct DistillScratch {
 // a thread; NV = 0: rows too long for that are read from the stage again).  A group's first warp
 // looks after the teacher.
 template <typename T, int TH, int G, int NV, int P, bool WHOLE>
-__global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Ring ring) {
+__global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 || NV == 1 ? 4 : 3)
+    k_distill(const DistillParams p, const Ring ring) {
     using Gr = Group<G>;
     using Scratch = DistillScratch<G>;
     using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
@@ -839,9 +863,6 @@ __global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Rin
     let_next_start();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
     const int64_t rows = p.lat.padded ? p.lat.rows : compact_rows<TH>(p.lat, space64);
-    const auto live = [&](int64_t row) {
-        return row < rows && (!p.lat.padded || p.lat.inside(row));
-    };
     const auto staged = [&](int64_t row, int st) {
         return Staged<T, G, WHOLE>(reinterpret_cast<const T*>(p.logits) + row * p.V, p.V,
                             reinterpret_cast<uint4*>(mine + st * ring.stage_bytes), false,
@@ -852,22 +873,19 @@ __global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Rin
         fence_mbar_init();
     }
     Gr::sync();
+    Window live(p.lat, first_row, groups, rows);
     if (me == 0)
-        for (int st = 0; st < ring.stages; ++st) {
-            const int64_t row = first_row + st * groups;
-            if (live(row)) staged(row, st).fetch(&sh.bar[st]);
-        }
+        for (int st = 0; st < ring.stages; ++st)
+            if (live[st]) staged(first_row + st * groups, st).fetch(&sh.bar[st]);
     int polls = kWaitPolls, st = 0;
     uint32_t phases = 0;                                   // a bit a stage
     Teacher<P> te, ahead;
     Places<P> pl;
-    bool now = live(first_row);
-    if (leads && now) ahead.load(p, first_row);
+    if (leads && live[0]) ahead.load(p, first_row);
     for (int64_t row = first_row; row < p.lat.rows; row += groups) {
-        const bool counts = now;
+        const bool counts = live[0];
         te = ahead;
-        now = live(row + groups);
-        if (leads && now) ahead.load(p, row + groups);     // one row ahead
+        if (leads && live[1]) ahead.load(p, row + groups); // one row ahead
         T* const g = reinterpret_cast<T*>(p.grad) + row * p.V;
         if (counts) {
             const Staged<T, G, WHOLE> x = staged(row, st);
@@ -985,11 +1003,11 @@ __global__ void __launch_bounds__(TH) k_distill(const DistillParams p, const Rin
             if (me == 0) p.row_loss[row] = 0.0f;
         }
         Gr::sync();                                        // the stage has been read
-        const int64_t next = row + ring.stages * groups;
-        if (me == 0 && live(next)) {
+        if (me == 0 && live[ring.stages]) {
             fence_proxy_async();
-            staged(next, st).fetch(&sh.bar[st]);
+            staged(row + ring.stages * groups, st).fetch(&sh.bar[st]);
         }
+        live.advance(p.lat, row + groups, groups, rows);
         st = st + 1 == ring.stages ? 0 : st + 1;
     }
 }
