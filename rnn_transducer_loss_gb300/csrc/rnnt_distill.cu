@@ -541,7 +541,6 @@ __device__ __noinline__ unsigned repeated(int id0, int id1) {
     return again;
 }
 
-constexpr float kLog2eLow = (float)(kLog2e - (double)(float)kLog2e);
 
 // A teacher's row, P places a lane of a warp.
 template <int P>
@@ -550,7 +549,7 @@ struct Teacher {
     float t[P];                            // logit / tau, -inf in an empty place
     float rest;                            // -inf without one
 
-    __device__ __forceinline__ void load(const DistillParams& a, int64_t row) {
+    __device__ __forceinline__ void load(const DistillParams& a, int64_t row, int64_t place0) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int q = 0; q < P; ++q) {
@@ -558,8 +557,8 @@ struct Teacher {
             id[q] = -1;
             t[q] = -INFINITY;
             if (k < a.k) {
-                id[q] = a.ids[row * a.k + k];
-                t[q] = teacher_logit(a, row * a.k + k);
+                id[q] = a.ids[place0 + k];
+                t[q] = teacher_logit(a, place0 + k);
             }
         }
         rest = a.rest ? a.rest[row] : -INFINITY;
@@ -621,13 +620,14 @@ struct Places {
         }
         t_top = max_nan(warp_max_nan(m), te.rest);
         top = warp_max_nan(x);
-        const Exponent f(top, a.scale, a.scale_low), g(t_top, (float)kLog2e, kLog2eLow);
-        w_rest = te.rest == -INFINITY ? 0.0f : g(te.rest);
+        // few terms, of which the largest is exactly 1: by expf, which ex2.approx's corrected mean is
+        // not good enough for
+        w_rest = te.rest == -INFINITY ? 0.0f : expf(te.rest - t_top);
         w_sum = w_log = sum = 0.0f;
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            w[q] = te.t[q] == -INFINITY ? 0.0f : g(te.t[q]);
-            e[q] = at[q] == -INFINITY ? 0.0f : f(at[q]);
+            w[q] = te.t[q] == -INFINITY ? 0.0f : expf(te.t[q] - t_top);
+            e[q] = at[q] == -INFINITY ? 0.0f : expf((at[q] - top) * a.inv_tau);
             w_sum += w[q];
             sum += e[q];
             if (w[q] != 0.0f)
@@ -649,9 +649,8 @@ struct Whole {
     __device__ __forceinline__ Whole(const DistillParams& a, float outside, float left, float top,
                                      float sum) {
         base = max_nan(outside, top);
-        const Exponent f(base, a.scale, a.scale_low);
-        outer = outside == -INFINITY ? 0.0f : f(outside);
-        inner = top == -INFINITY ? 0.0f : f(top);
+        outer = outside == -INFINITY ? 0.0f : expf((outside - base) * a.inv_tau);
+        inner = top == -INFINITY ? 0.0f : expf((top - base) * a.inv_tau);
         total = left * outer + sum * inner;
     }
     __device__ __forceinline__ bool good() const { return total > 0.0f && total < INFINITY; }
@@ -667,15 +666,15 @@ struct Whole {
     __device__ __forceinline__ float loss(const DistillParams& a, const Places<P>& pl, float rest,
                                           float outside, float left) const {
         // the two logarithms by two lanes
-        const float all = pl.w_sum + pl.w_rest;
-        const float mine = logf((threadIdx.x & 1) ? left : total / all);
+        const float inv_all = reciprocal(pl.w_sum + pl.w_rest);
+        const float mine = logf((threadIdx.x & 1) ? left : total * inv_all);
         const float ratio = __shfl_sync(kAll, mine, 0), log_left = __shfl_sync(kAll, mine, 1);
         float kl = pl.w_sum == 0.0f
                        ? 0.0f
                        : pl.w_log + pl.w_sum * (ratio - (pl.top - base) * a.inv_tau);
         if (pl.w_rest != 0.0f)
             kl += pl.w_rest * ((rest - pl.t_top) - (outside - base) * a.inv_tau + ratio - log_left);
-        return kl / all;
+        return kl * inv_all;
     }
     template <int P>
     __device__ __forceinline__ float place(const DistillParams& a, const Places<P>& pl,
@@ -727,7 +726,7 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillPara
     for (int64_t row = blockIdx.x; row < p.lat.rows; row += gridDim.x) {
         const bool live = row < rows && (!p.lat.padded || p.lat.inside(row));
         if (warp == 0 && live) {
-            te.load(p, row);
+            te.load(p, row, row * p.k);
             te.check(p);
             bool again = false;
 #pragma unroll
@@ -881,11 +880,14 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
     uint32_t phases = 0;                                   // a bit a stage
     Teacher<P> te, ahead;
     Places<P> pl;
-    if (leads && live[0]) ahead.load(p, first_row);
+    int64_t place0 = first_row * p.k;                      // of the row's places
+    const int64_t place_step = groups * p.k;
+    if (leads && live[0]) ahead.load(p, first_row, place0);
     for (int64_t row = first_row; row < p.lat.rows; row += groups) {
         const bool counts = live[0];
         te = ahead;
-        if (leads && live[1]) ahead.load(p, row + groups); // one row ahead
+        place0 += place_step;
+        if (leads && live[1]) ahead.load(p, row + groups, place0);     // one row ahead
         T* const g = reinterpret_cast<T*>(p.grad) + row * p.V;
         if (counts) {
             const Staged<T, G, WHOLE> x = staged(row, st);
@@ -941,7 +943,7 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
                         if (lane == 0) {
                             sh.top = pl.top;
                             sh.sum = pl.sum;
-                            sh.p_rest = pl.w_rest / (pl.w_sum + pl.w_rest);
+                            sh.p_rest = pl.w_rest * reciprocal(pl.w_sum + pl.w_rest);
                         }
                     }
                 }
@@ -964,7 +966,7 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
                 if (p.grad) {
                     const float c = w.good() ? w.factor(p, left,
                                                        G > 32 ? sh.p_rest
-                                                              : pl.w_rest / (pl.w_sum + pl.w_rest)) : NAN;
+                                                              : pl.w_rest * reciprocal(pl.w_sum + pl.w_rest)) : NAN;
                     const float2 c2 = make_float2(c, c);
                     const auto put = [&](int j, float2 (&y)[E / 2]) {
                         Pack<T, 16> v;
@@ -1208,12 +1210,11 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
                 const Exponent f(outside == -INFINITY ? 0.0f : outside, p.scale, p.scale_low);
                 float left = 0.0f;
                 r.each([&](int i, T x) { left += r.bits(i) != kTaken ? f(to_f32(x)) : 0.0f; });
-                const Exponent g(top, p.scale, p.scale_low);
                 float sum = 0.0f, w_sum = 0.0f, w_log = 0.0f;
                 for (int q = 0; q < p.k; ++q) {
                     const float at = ats[q * 32 + lane];
                     if (at == INFINITY) continue;
-                    sum += at == -INFINITY ? 0.0f : g(at);
+                    sum += at == -INFINITY ? 0.0f : expf((at - top) * p.inv_tau);
                     const float x = teacher_logit(p, first + q);
                     if (x == -INFINITY) continue;
                     const float t = fmaxf(x * p.inv_tau, -kMost) - t_top, w = x != x ? x : expf(t);
@@ -1245,7 +1246,6 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
         }
         if (lane < n && some) {
             const Exponent f(outside == -INFINITY ? 0.0f : outside, p.scale, p.scale_low);
-            const Exponent g(top, p.scale, p.scale_low);
             r.each([&](int i, T x) {
                 if (r.bits(i) != kTaken || c != c) r.s[i] = from_f32<T>(f(to_f32(x)) * c);
             });
@@ -1255,7 +1255,7 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
                 const float x = teacher_logit(p, first + q);
                 const float t = fmaxf(x * p.inv_tau, -kMost) - t_top;
                 const float prob = x == -INFINITY ? 0.0f : (x != x ? x : expf(t)) * weight;
-                const float e = at == -INFINITY ? 0.0f : g(at);
+                const float e = at == -INFINITY ? 0.0f : expf((at - top) * p.inv_tau);
                 r.s[p.ids[first + q]] = from_f32<T>((e * inner - prob) * p.grad_scale);
             }
         } else if (lane < n) {
