@@ -533,8 +533,8 @@ rnnt_status_t rnnt_top_logits(const void *logits, rnnt_dtype_t dt, int64_t rows,
                               double temperature, void *values, int32_t *ids, float *rest,
                               int32_t *status_dev, rnnt_stream_t stream);
 
-/* rnnt_distill_workspace_size -- bytes of device scratch of rnnt_distill_loss: 4 per row
- * and 16 per sample. */
+/* rnnt_distill_workspace_size -- bytes of device scratch of rnnt_distill_loss: 4 per row,
+ * 8 per sample, and 8 per part of a sample's sum (64 of them at most). */
 rnnt_status_t rnnt_distill_workspace_size(int32_t B, int64_t rows, size_t *bytes);
 
 /*

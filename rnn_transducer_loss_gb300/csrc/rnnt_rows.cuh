@@ -274,9 +274,9 @@ inline void parts_below(double c, float& hi, float& lo) {
     if ((double)hi >= c) hi = std::nextafter(hi, 0.0f);
     lo = (float)(c - (double)hi);
 }
-// ex2.approx comes out low on average (by 5.1e-8 over the exponents of one order, by 3e-8 over the sums of
-// rows of normal logits); kLow, in the exponent, makes up for that, so that logarithms of sums of
-// many terms are off by no more than 1e-8 on average.
+// ex2.approx comes out low on average: by 2e-8 for exponents above -1, by 5e-8 below (measured over 2^20
+// of them an order).  kLow, in the exponent, makes up for 3e-8, which leaves logarithms of sums off
+// by 1e-8 on average, for rows of normal logits at temperatures of 1 to 4.
 constexpr float kLow = 4.4e-8f;
 struct Exponent {
     float2 ref, hi, lo;                    // -ref, c
