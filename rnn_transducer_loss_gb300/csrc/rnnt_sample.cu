@@ -197,6 +197,10 @@ struct Floor {
 };
 
 // A draw by a block of TH threads; the row lies in shared memory (HERE) or is read from the cache.
+// Blocks of 128, 256 and 512 threads for rows of up to 4 KB, 32 KB and beyond.  Latency bounds short
+// rows (4 of 1024 float16 with top_k 40: 8.9 us, one chain of barriers); issue slots and barriers long
+// ones, of which two fit an SM: 1024 rows of 50000 bfloat16 take 100 us unfiltered, 145 with
+// top_p 0.9 and min_p 0.002, 66 where few elements are kept.
 template <typename T, int TH, bool HERE>
 struct Draw {
     static constexpr int E = 16 / (int)sizeof(T), WARPS = TH / 32;
