@@ -135,7 +135,8 @@ constexpr float kLeastMass = 1.17549435e-38f;
 // sum's error.  Of many terms the errors do not all point one way: by Hoeffding's inequality a sum
 // of independent ones exceeds 6 times the root of the terms' squares' sum with a chance below 4e-8;
 // kBias is what ex2.approx's mean over a 64th of an order is off, at most.  A border nearer to a sum
-// than that is decided on sums of pairs.
+// than that is decided on sums of pairs (by the bound, in one row of 25 of 50000 outputs with top_p
+// 0.9; a row then takes 10 to 30 us more).
 constexpr float kTerm = 3e-7f, kStep = 8.3e-8f, kBias = 3e-8f;
 __device__ __forceinline__ float error_of(float sum, float squares, int V) {   // absolute
     const float worst = sum * (kTerm + kStep * fmaxf(__log2f((float)V) - __log2f(sum), 0.0f));
