@@ -590,18 +590,25 @@ struct Draw {
         Pair target = mul(whole, top_p);
         const int n = list_at<true>(few, from, 0, target.h, whole.h, above, before);
         int kept = kept_of_list<false>(n, above, target, 2.0f * error_of(whole.h, squares, r.V));
-        if (unsure && n) {
+        const bool again = unsure && n;
+        Pair exact, upper;
+        if (again) {
             // the sums again, to 40 bits, over the same list
-            Pair exact, upper;
             exact_sums(least, sh.order[0] + 1, exact, upper);
             target = mul(exact, top_p);
             kept = kept_of_list<true>(n, upper, target, 0.0f);
         }
         uint64_t key = kept > 0 && n ? sh.order[kept - 1] : 0;
-        // all from `from` on, or a border outside the list, found by the histogram's rounded masses
-        if (!key && kept == -1 && few) key = from;
+        if (!key && kept == -1 && few) key = from;         // all from `from` on
         __syncthreads();
-        return key ? key : bisect(from, target);
+        if (key) return key;
+        // a border outside the list, which the histogram's rounded masses did not place: the bisection
+        // compares sums of pairs, so its target has to be one
+        if (!again) {
+            exact_sums(least, least, exact, upper);
+            target = mul(exact, top_p);
+        }
+        return bisect(from, target);
     }
 
     // The first id of a key from `least` on at which the running sum exceeds u of the whole.
