@@ -128,19 +128,32 @@ constexpr uint64_t kFinite = (uint64_t)0x00800000u << kIdBits;   // the least ke
 // A mass that is kept is above 0 however far it lies: u = 0 draws the first id.
 constexpr float kLeastMass = 1.17549435e-38f;
 
-// Fast sums are of float32 terms, added as trees of a vector's and then as pairs.  A term is off by at
-// most kTerm and kStep for each of its exponent's binary orders (ex2.approx by 1.0e-7 from its mean, which
-// all terms share; three additions; the roundings of x - top and of the exponent), relative; the
-// mean order over a row is at most log2 V - log2 sum (its entropy is at most log2 V), which bounds a
-// sum's error.  Of many terms the errors do not all point one way: by Hoeffding's inequality a sum
-// of independent ones exceeds 6 times the root of the terms' squares' sum with a chance below 4e-8;
-// kBias is what ex2.approx's mean over a 64th of an order is off, at most.  A border nearer to a sum
-// than that is decided on sums of pairs (by the bound, in one row of 25 of 50000 outputs with top_p
-// 0.9; a row then takes 10 to 30 us more).
-constexpr float kTerm = 3e-7f, kStep = 8.3e-8f, kBias = 3e-8f;
-__device__ __forceinline__ float error_of(float sum, float squares, int V) {   // absolute
-    const float worst = sum * (kTerm + kStep * fmaxf(__log2f((float)V) - __log2f(sum), 0.0f));
-    return fminf(worst, 6.0f * kTerm * sqrtf(fminf(squares, sum)) + kBias * sum);
+// Fast sums are of float32 terms, added as trees of a vector's and then as pairs.  A border is u of a
+// whole sum W, and a running sum R beside it is compared with u W.  A term is a function of its logit:
+// relative to a factor that all share (and that cancels) it is off by at most kTerm and kStep for each
+// of its exponent's binary orders.  ex2.approx is off by -1.44e-7 to 1.05e-7 (all float32 from -126 to 0,
+// against exp2 in float64), so by 1.25e-7 from the middle; x - top and the exponent are rounded once each.
+// The term counts 1 - u times in R - u W where it is in R, and -u times where it is not; the terms of R
+// have a mean order of at most log2 V - log2 R (their entropy is at most log2 V), the others likewise.
+// With R = u W and c = u (1 - u) that is
+//   |error of R - u W| <= W [ c (2 kTerm + kStep (2 (log2 V - log2 W) - log2 c)) + kSum ],
+// kSum for the pairs' own additions (below 2^-30 for the longest rows).  A vector's tree is off by
+// kAdd of its sum, in R and in W alike where both add the same trees.  Nothing is assumed of how the
+// errors are spread: equal logits share theirs, and 16-bit rows are full of them.  A border nearer
+// to a sum than the bound is decided on sums of pairs: of 50000 normal logits (bfloat16) one row in 11 with
+// top_p 0.9, one in 38 without filters; a row then takes 10 to 30 us more.
+constexpr float kTerm = 1.27e-7f, kStep = 8.3e-8f, kSum = 2e-9f;
+template <typename T>
+constexpr float kAdd = (sizeof(T) == 4 ? 2.0f : 3.0f) * 5.97e-8f;              // additions, one after another
+__device__ __forceinline__ float error_at(float u, float sum, int V, float term) {     // absolute
+    const float c = fmaxf(u * (1.0f - u), 1e-12f);
+    return sum * (c * (2.0f * term +
+                       kStep * (2.0f * (__log2f((float)V) - __log2f(sum)) - __log2f(c))) + kSum);
+}
+// Where R and W add different trees: of a list's elements, one by one, and of the row's vectors.
+template <typename T>
+__device__ __forceinline__ float error_of_list(float u, float sum, int V) {
+    return error_at(u, sum, V, kTerm) + 2.0f * u * kAdd<T> * sum;
 }
 __device__ __forceinline__ Pair add_loosely(Pair a, float b) {     // of sums of positive terms
     const Pair s = two_sum(a.h, b);
@@ -167,7 +180,7 @@ struct Shared {
     };
     uint32_t groups[32];                   // sums of 32 bins each
     Pair pairs[2][WARPS];
-    float floats[2][WARPS];
+    float floats[WARPS];
     int ints[WARPS];
     unsigned long long low, high;          // keys
     uint64_t bar;                          // of the row's copy
@@ -211,13 +224,11 @@ struct Draw {
     const float scale, scale_low, bin_scale;
     const Pair exact_scale, top_p;
     float top;
-    float squares;                         // the sum of the terms' squares
     bool unsure;                           // of the last result: the fast sums leave it open
 
     __device__ __forceinline__ Draw(const SampleParams& p, Shared<TH>& s, const T* x, uint4* stage)
         : sh(s), r(x, p.V), here(stage), scale(p.scale), scale_low(p.scale_low),
-          bin_scale(p.bin_scale), exact_scale(p.exact_scale), top_p(p.top_p), top(0.0f), squares(INFINITY),
-          unsure(false) {}
+          bin_scale(p.bin_scale), exact_scale(p.exact_scale), top_p(p.top_p), top(0.0f), unsure(false) {}
 
     __device__ __forceinline__ Pack<T, 16> at(int j) const {
         if constexpr (HERE) {
@@ -589,7 +600,7 @@ struct Draw {
         uint32_t before;
         Pair target = mul(whole, top_p);
         const int n = list_at<true>(few, from, 0, target.h, whole.h, above, before);
-        int kept = kept_of_list<false>(n, above, target, 2.0f * error_of(whole.h, squares, r.V));
+        int kept = kept_of_list<false>(n, above, target, error_of_list<T>(top_p.h, whole.h, r.V));
         const bool again = unsure && n;
         Pair exact, upper;
         if (again) {
@@ -645,7 +656,7 @@ struct Draw {
         const Pair whole{__shfl_sync(kAll, upto_piece.h, WARPS - 1),
                          __shfl_sync(kAll, upto_piece.l, WARPS - 1)};
         const Pair border = mul(whole, Pair{u, 0.0f});
-        const float error = EXACT ? 0.0f : 2.0f * error_of(whole.h, squares, r.V);
+        const float error = EXACT ? 0.0f : error_at(u, whole.h, r.V, kTerm + kAdd<T>);
         // the first piece at whose end the border is passed, else the last with a mass
         const unsigned filled = __ballot_sync(kAll, piece.h > 0.0f);
         const unsigned passed = __ballot_sync(kAll, piece.h > 0.0f && less(border, upto_piece));
@@ -727,8 +738,10 @@ struct Draw {
                     if (past && less(border, after)) open = false;
                 }
                 // certain where nothing is kept before the token, and on its other side as u < 1
-                const bool low = before.h > 0.0f && difference(border, before) <= error;
-                const bool high = difference(after, border) <= error;
+                // (the elements of this vector are added one by one here, as a tree in the whole)
+                const float near = error + (EXACT ? 0.0f : kAdd<T> * m.h);
+                const bool low = before.h > 0.0f && difference(border, before) <= near;
+                const bool high = difference(after, border) <= near;
                 sh.token = token;
                 sh.unsure = low || high;
             }
@@ -787,9 +800,9 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
         const float2 both = half_maxima(most);
         const float mine = max_nan(both.x, both.y);        // the thread's largest
         float m = warp_max_nan(mine);
-        if (lane == 0) sh.floats[0][tid >> 5] = m;
+        if (lane == 0) sh.floats[tid >> 5] = m;
         __syncthreads();
-        m = warp_max_nan(lane < WARPS ? sh.floats[0][lane] : -INFINITY);
+        m = warp_max_nan(lane < WARPS ? sh.floats[lane] : -INFINITY);
         bad = !(m < INFINITY);
         if (!bad && m > -INFINITY) {
             d.top = m;
@@ -799,24 +812,13 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
             Pair s{0.0f, 0.0f}, s1{0.0f, 0.0f};
             if (at_tau || at_one) {
                 const Exponent f(m, p.scale, p.scale_low), f1(m, p.one, p.one_low);
-                float2 squares = make_float2(0.0f, 0.0f);
                 for (int j = tid; j < d.r.n; j += TH) {
                     const Pack<T, 16> v = d.at(j);
                     float2 e[E / 2];
                     if (at_one) s1 = add_loosely(s1, terms_of(v, f1, e));
-                    if (at_tau) {
-                        s = add_loosely(s, terms_of(v, f, e));
-#pragma unroll
-                        for (int i = 0; i < E / 2; ++i) squares = fma2(e[i], e[i], squares);
-                    }
+                    if (at_tau) s = add_loosely(s, terms_of(v, f, e));
                 }
                 d.sum2(s, s1);
-                if (at_tau) {
-                    const float sq = warp_sum(squares.x + squares.y);
-                    if (lane == 0) sh.floats[1][tid >> 5] = sq;
-                    __syncthreads();
-                    d.squares = warp_sum(lane < WARPS ? sh.floats[1][lane] : 0.0f);
-                }
             }
             const float lse = p.fused ? logf(p.unit_tau ? s.h : s1.h) : 0.0f;
             uint64_t least = kFinite;
@@ -829,9 +831,9 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
                 if (c <= 32) {
                     const float cth = __shfl_sync(kAll, warp_sorted(mine), c - 1);
                     __syncthreads();
-                    if (lane == 0) sh.floats[0][tid >> 5] = -cth;
+                    if (lane == 0) sh.floats[tid >> 5] = -cth;
                     __syncthreads();
-                    bound = -warp_max(lane < WARPS ? sh.floats[0][lane] : -INFINITY);
+                    bound = -warp_max(lane < WARPS ? sh.floats[lane] : -INFINITY);
                 }
                 least = d.floor_of_count(p.top_k, bound);
             }
@@ -870,7 +872,7 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
                     few |= s1.h <= (float)kList;
                     // where that is open, by what the exact sums say of the whole list, or of all
                     within = !(difference(mul(s, p.top_p), upper) >
-                               2.0f * error_of(s.h, d.squares, p.V));
+                               error_of_list<T>(p.top_p.h, s.h, p.V));
                 }
                 floor = within ? d.floor_of_mass(few, least, from, s) : from;
             }

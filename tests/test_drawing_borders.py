@@ -41,3 +41,49 @@ def test_border_in_a_crowd(program):
     x = torch.full((100000,), -22.3)
     x[:4] = torch.tensor([0.0, -0.37, -0.91, -0.53])
     check(program, x, [MOST], dict(top_p=0.999995), threads=512, here=False)
+
+
+def few_values(V, values, dtype):
+    """A row of few values, the larger ones first: all terms of a value share one error."""
+    x = torch.empty(V)
+    for i, v in enumerate(sorted(values, reverse=True)):
+        x[i * V // len(values):] = v
+    return x.to(dtype)
+
+
+def beside(sums, whole, seed, n):
+    """float32 numbers at and next to some of the running sums' shares of the whole."""
+    at = np.random.default_rng(seed).integers(0, len(sums) - 1, size=n)
+    u = (sums[at] / whole).astype(np.float32)
+    u = np.concatenate([u, np.nextafter(u, np.float32(0)), np.nextafter(u, np.float32(1))])
+    return u[u < 1]
+
+
+VALUES = [(-0.9375, 0.0), (-6.5625, -5.625, 0.0), (-3.03125, -2.0, -1.046875, -0.09765625)]
+
+
+def test_draw_in_equal_logits(program):
+    """25000 equal terms on either side of a step: their errors add up."""
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.full((50000,), -6.5625)
+        x[25000:], x[-1] = -5.625, 0.0
+        check(program, x.to(dtype), [0.2791885435581207], dict())
+
+
+@pytest.mark.parametrize("values", VALUES, ids=str)
+def test_draws_beside_running_sums(program, values):
+    for V, dtype in ((29, torch.float32), (203, torch.bfloat16), (1001, torch.float16), (20011, torch.bfloat16)):
+        x = few_values(V, values, dtype)
+        sums = np.cumsum(np.exp(x.double().numpy()))
+        check(program, x, beside(sums, sums[-1], V, 3), dict())
+
+
+@pytest.mark.parametrize("values", VALUES, ids=str)
+def test_top_p_beside_running_sums(program, values):
+    """The last id drawn is the last one kept."""
+    for V, places in ((29, (0, 5, 13, 26, 27)), (1001, (3, 250, 499, 750, 998)), (5003, (1200, 2500, 4100))):
+        x = few_values(V, values, torch.bfloat16)
+        sums = np.cumsum(np.exp(x.double().numpy()))
+        for at in places:
+            for off in (-2e-8, -3e-9, 3e-9, 2e-8):
+                check(program, x, [MOST], dict(top_p=sums[at] / sums[-1] + off))
