@@ -1309,13 +1309,14 @@ __global__ void __launch_bounds__(kSumThreads) k_distill_sum(const DistillParams
     const int64_t n = p.lat.of_sequence(b, t, u, ok);
     int64_t first = 0;
     if (!p.lat.padded) {
+        const int64_t most = p.lat.rows + 1;               // so that one too many shows in the sum
         for (int i = tid; i < b; i += TH) {
             int t0, u0;
             bool ok0;
-            first += min(p.lat.of_sequence(i, t0, u0, ok0), p.lat.rows);
+            first += min(p.lat.of_sequence(i, t0, u0, ok0), most);
         }
         first = block_sum<TH>(first, space64);
-        const int64_t end = first + min(n, p.lat.rows);
+        const int64_t end = first + min(n, most);
         if (b == p.lat.B - 1) ok &= end == p.lat.rows;
         if (tid == 0 && part == 0) {
             p.first_row[b] = first;

@@ -1,0 +1,33 @@
+"""GPU: the distillation loss and a teacher's top logits at the edges of what may be called."""
+import numpy as np
+import pytest
+import torch
+
+import distill_ref as R
+import label_ref as L
+from rnn_transducer_loss_gb300 import rnnt_distill_loss, rnnt_top_logits
+
+pytestmark = pytest.mark.gpu
+DT = L.DTYPES
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+@pytest.mark.parametrize("V", [29, 1024, 5000])
+def test_one_sample_longer_than_the_rows(V):
+    """Lengths of more rows than there are, in one sample: refused, and without the check cut at the rows."""
+    x = torch.randn(6, V, device="cuda", generator=gen(1))
+    values, ids, rest = rnnt_top_logits(x + 1, 4)
+    whole = rnnt_distill_loss(x, values, ids, i32([6]), i32([0]), rest, reduction="sum")
+    for t, u in (([7], [0]), ([7, 0], [0, 0]), ([0, 7], [0, 0]), ([2], [3]), ([2 ** 31 - 1], [2 ** 31 - 2]),
+                 ([0, 2 ** 31 - 1, 0], [0, 0, 5])):
+        with pytest.raises(ValueError, match="T_b"):
+            rnnt_distill_loss(x, values, ids, i32(t), i32(u), rest)
+        got = rnnt_distill_loss(x, values, ids, i32(t), i32(u), rest, reduction="sum", check=False)
+        assert torch.equal(got, whole)
