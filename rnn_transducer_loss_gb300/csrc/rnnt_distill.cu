@@ -338,10 +338,12 @@ __global__ void __launch_bounds__(TH, 5) k_top(const TopParams p, const Ring rin
     const int me = Gr::rank(), lane = me & 31, k = p.k;
     const int64_t groups = (int64_t)gridDim.x * GROUPS;
     const int64_t first_row = (int64_t)blockIdx.x * GROUPS + (G == 32 ? threadIdx.x / G : 0);
+    const T* const logits = reinterpret_cast<const T*>(p.logits);
+    const T* const end = logits + p.lat.rows * p.V;
     const auto staged = [&](int64_t row, int st) {
-        return Staged<T, G, WHOLE>(reinterpret_cast<const T*>(p.logits) + row * p.V, p.V,
-                                   reinterpret_cast<uint4*>(mine + st * ring.stage_bytes),
-                                   row == 0, row == p.lat.rows - 1);
+        return Staged<T, G, WHOLE>(logits + row * p.V, p.V,
+                                   reinterpret_cast<uint4*>(mine + st * ring.stage_bytes), logits,
+                                   end);
     };
     if (blockIdx.x == 0 && p.lat.T) check_lengths<TH>(p.lat, p.status);
     if (me == 0) {
@@ -873,10 +875,12 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
     let_next_start();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
     const int64_t rows = p.lat.padded ? p.lat.rows : compact_rows<TH>(p.lat, space64);
+    const T* const logits = reinterpret_cast<const T*>(p.logits);
+    const T* const end = logits + p.lat.rows * p.V;
     const auto staged = [&](int64_t row, int st) {
-        return Staged<T, G, WHOLE>(reinterpret_cast<const T*>(p.logits) + row * p.V, p.V,
-                            reinterpret_cast<uint4*>(mine + st * ring.stage_bytes), false,
-                            row == p.lat.rows - 1);
+        return Staged<T, G, WHOLE>(logits + row * p.V, p.V,
+                                   reinterpret_cast<uint4*>(mine + st * ring.stage_bytes), logits,
+                                   end);
     };
     if (me == 0) {
         for (int st = 0; st < ring.stages; ++st) mbar_init(&sh.bar[st]);

@@ -406,10 +406,12 @@ struct Staged {
     uint4* s;
     int lo, hi;                            // the vectors that the copy brings
 
-    __device__ __forceinline__ Staged(const T* x, int V, uint4* stage, bool first, bool last)
+    // begin, end: of the tensor.  Rows shorter than a unit share its first and last one.
+    __device__ __forceinline__ Staged(const T* x, int V, uint4* stage, const T* begin, const T* end)
         : r(x, V), s(stage) {
-        lo = !WHOLE && first && r.off ? 1 : 0;
-        hi = !WHOLE && last && (r.off + V) % E ? r.n - 1 : r.n;
+        const uintptr_t at = (uintptr_t)x - r.off * sizeof(T);
+        lo = !WHOLE && at < (uintptr_t)begin ? 1 : 0;
+        hi = !WHOLE && at + (uintptr_t)r.n * 16 > (uintptr_t)end ? r.n - 1 : r.n;
     }
     __device__ __forceinline__ void fetch(uint64_t* bar) const {       // by one thread
         const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;

@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(TH) k_sample(const SampleParams p) {
         Pack<T, 16> most = all_minus_inf<T>();
         if constexpr (HERE) {
             // one bulk copy; the units it shares with what is not the row's element by element
-            const Staged<T, TH> row_here(x, p.V, stage, true, true);
+            const Staged<T, TH> row_here(x, p.V, stage, x, x + p.V);
             if (tid == 0) {
                 mbar_init(&sh.bar);
                 fence_mbar_init();

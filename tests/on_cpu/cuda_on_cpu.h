@@ -128,7 +128,7 @@ inline bool run_blocks(int ctas, int threads, unsigned first, size_t dynamic,
         }
     }
     for (size_t left = fibers.size(); left;) {
-        uint64_t before = left + cl.all.turn;
+        uint64_t before = (uint64_t)cl.all.turn - left;      // every step makes it larger
         for (auto& c : cl.ctas) {
             before += c.all.turn;
             for (auto& w : c.warps) before += w.meet.turn;
@@ -138,7 +138,7 @@ inline bool run_blocks(int ctas, int threads, unsigned first, size_t dynamic,
             run(f);
             left -= f.done;
         }
-        uint64_t after = left + cl.all.turn;
+        uint64_t after = (uint64_t)cl.all.turn - left;
         for (auto& c : cl.ctas) {
             after += c.all.turn;
             for (auto& w : c.warps) after += w.meet.turn;

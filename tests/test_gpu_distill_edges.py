@@ -31,3 +31,16 @@ def test_one_sample_longer_than_the_rows(V):
             rnnt_distill_loss(x, values, ids, i32(t), i32(u), rest)
         got = rnnt_distill_loss(x, values, ids, i32(t), i32(u), rest, reduction="sum", check=False)
         assert torch.equal(got, whole)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("V", [1, 2, 3, 5])
+def test_top_of_rows_shorter_than_a_unit(V, dtype):
+    """Unaligned rows of which several lie in one 16-byte unit: as from an aligned copy."""
+    for skip in (1, 3, 7):
+        for rows in (1, 2, 50):
+            big = torch.randn(rows * V + 16, device="cuda", generator=gen(V)).to(DT[dtype])
+            x = big[skip:skip + rows * V].view(rows, V)
+            for k in {1, V}:
+                for a, b in zip(rnnt_top_logits(x, k), rnnt_top_logits(x.clone(), k)):
+                    assert torch.equal(a, b) or torch.allclose(a, b, rtol=4 * L.U32, atol=4 * L.U32)
