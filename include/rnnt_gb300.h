@@ -518,8 +518,8 @@ rnnt_status_t rnnt_beam_reorder(const rnnt_state_t *states, int32_t n_states,
  *   logit_lengths, target_lengths
  *                  int32 [B], or both NULL: every row counts.  With lengths the
  *                  rows are those of the padded (B, max_T, max_U + 1, V) layout;
- *                  a row outside its sequence is not read, and all its places
- *                  are left over.  B, max_T and max_U are ignored without.
+ *                  what a row outside its sequence holds is not used, and all its
+ *                  places are left over.  B, max_T and max_U are ignored without.
  *   values         (rows, k) in dt;  ids int32 (rows, k);  rest float (rows).
  *                  They must not overlap logits or one another.
  *   status_dev     RNNT_INVALID_VALUE for a row that holds NaN or +inf (all its
@@ -558,8 +558,8 @@ rnnt_status_t rnnt_distill_workspace_size(int32_t B, int64_t rows, size_t *bytes
  * and gradient 0, whatever its logits are.
  *
  *   logits         (rows, V) contiguous in dt, 16-byte aligned: the compact layout of
- *                  rnnt_loss_fused, or the padded one, (B, max_T, max_U + 1, V), whose
- *                  other rows are not read and get gradient 0.
+ *                  rnnt_loss_fused, or the padded one, (B, max_T, max_U + 1, V).  What
+ *                  other rows hold is not used, and their gradient is 0.
  *   teacher_logits (rows, k) in teacher_dt;  teacher_ids int32 (rows, k), a negative id
  *                  being an empty place;  teacher_rest float (rows), or NULL: p is the
  *                  softmax over the places alone.

@@ -1031,7 +1031,8 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
 
 // ------------------------------------------------------------------ short rows
 // A warp takes 32 consecutive rows, which are one aligned piece of memory whatever V is, through its
-// part of shared memory, and a thread each of them: no reductions, no idle lanes.  172000 rows of
+// part of shared memory (unless none of them counts), and a thread each of them: no reductions, no idle
+// lanes.  172000 rows of
 // 29 float32 with 8 places take 24 us with the gradient (a warp a row: 150); 1.7 TB/s, bound by
 // latency: a thread's looks at its row follow one another.
 struct ShortBatch {
@@ -1105,12 +1106,14 @@ __global__ void __launch_bounds__(kShortThreads) k_top_short(const TopParams p, 
     for (int64_t row0 = ((int64_t)blockIdx.x * (kShortThreads / 32) + warp) * 32; row0 < p.lat.rows;
          row0 += step) {
         const int n = (int)min((int64_t)32, p.lat.rows - row0);
-        fetch_short(p.logits, row0, n, p.V, stage, bar, phase, polls, p.status);
+        const int64_t row = row0 + lane;
+        const bool counts = lane < n && (!p.lat.T || p.lat.inside(row));
+        if (__any_sync(kAll, counts))
+            fetch_short(p.logits, row0, n, p.V, stage, bar, phase, polls, p.status);
         const ShortRow<T> r(stage, p.V);
         float rest = -INFINITY;
         int have = 0;
-        const int64_t row = row0 + lane;
-        if (lane < n && (!p.lat.T || p.lat.inside(row))) {
+        if (counts) {
             float top = -INFINITY;
             r.each([&](int, T x) { top = max_nan(top, to_f32(x)); });
             if (!(top < INFINITY)) {                       // NaN or +inf: the row is left empty
@@ -1184,13 +1187,15 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
     for (int64_t row0 = ((int64_t)blockIdx.x * (kShortThreads / 32) + warp) * 32; row0 < p.lat.rows;
          row0 += step) {
         const int n = (int)min((int64_t)32, p.lat.rows - row0);
-        fetch_short(p.logits, row0, n, p.V, stage, bar, phase, polls, p.status);
-        const ShortRow<T> r(stage, p.V);
         const int64_t row = row0 + lane, first = row * p.k;
+        const bool counts = lane < n && row < rows && (!p.lat.padded || p.lat.inside(row));
+        if (__any_sync(kAll, counts))
+            fetch_short(p.logits, row0, n, p.V, stage, bar, phase, polls, p.status);
+        const ShortRow<T> r(stage, p.V);
         float loss = 0.0f, c = 0.0f, inner = 0.0f, outside = -INFINITY, weight = 0.0f;
         float t_top = -INFINITY, top = -INFINITY;
         bool some = false;
-        if (lane < n && row < rows && (!p.lat.padded || p.lat.inside(row))) {
+        if (counts) {
             bool bad = false;
             float most = -INFINITY;
             r.each([&](int, T x) { most = max_nan(most, to_f32(x)); });

@@ -58,7 +58,7 @@ def rnnt_top_logits(logits: torch.Tensor, k: int, logit_lengths: torch.Tensor | 
     id; ``ids`` (..., k) int32 say which outputs they are; places left over hold
     -inf and -1.  ``rest`` (...) float32 is the log-sum-exp of the remaining logits /
     ``temperature``, -inf where there are none.  With padded logits the (B,) int32
-    lengths leave rows outside their sequence unread, and empty.  ``check``
+    lengths leave rows outside their sequence unused, and empty.  ``check``
     reads the device status word (one synchronisation) and raises on rows that hold
     NaN or +inf and on lengths outside the tensor; without it such a row is empty and such
     a length the nearer bound.  Not differentiable.

@@ -44,3 +44,29 @@ def test_top_of_rows_shorter_than_a_unit(V, dtype):
             for k in {1, V}:
                 for a, b in zip(rnnt_top_logits(x, k), rnnt_top_logits(x.clone(), k)):
                     assert torch.equal(a, b) or torch.allclose(a, b, rtol=4 * L.U32, atol=4 * L.U32)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("V", [7, 29, 64])
+def test_padded_short_rows_of_which_most_do_not_count(V, dtype):
+    """Whole batches of rows outside their sequence beside some inside: as from the compact layout."""
+    T, U, k = [2, 90, 0, 31], [3, 1, 3, 0], 4
+    owner, live = R.rows_of(T, U, True)
+    at = torch.as_tensor(live.nonzero()[0], device="cuda")
+    x = torch.full((len(owner), V), float("nan"), device="cuda", dtype=DT[dtype])
+    x[at] = torch.randn(len(at), V, device="cuda", generator=gen(V)).to(DT[dtype])
+    lead = (4, 90, 4)
+    few = x[at].clone().requires_grad_()
+    all_ = x.view(*lead, V).clone().requires_grad_()
+    top = rnnt_top_logits(few.detach(), k)
+    got = rnnt_top_logits(all_.detach(), k, i32(T), i32(U))
+    for a, b in zip(got, top):
+        assert torch.equal(a.view(len(owner), *b.shape[1:])[at], b)
+    dead = torch.as_tensor(~live, device="cuda")
+    assert (got[1].view(-1, k)[dead] == -1).all() and (got[2].view(-1)[dead] == -float("inf")).all()
+    one = rnnt_distill_loss(few, *top[:2], i32(T), i32(U), top[2], reduction="none")
+    two = rnnt_distill_loss(all_, *got[:2], i32(T), i32(U), got[2], reduction="none")
+    assert torch.equal(one, two)
+    g1, = torch.autograd.grad(one.sum(), few)
+    g2, = torch.autograd.grad(two.sum(), all_)
+    assert torch.equal(g2.view(len(owner), V)[at], g1) and (g2.view(len(owner), V)[dead] == 0).all()
