@@ -5,6 +5,7 @@ import torch
 
 import distill_ref as R
 import label_ref as L
+import test_gpu_distill as D
 from rnn_transducer_loss_gb300 import rnnt_distill_loss, rnnt_top_logits
 
 pytestmark = pytest.mark.gpu
@@ -56,17 +57,19 @@ def test_padded_short_rows_of_which_most_do_not_count(V, dtype):
     x = torch.full((len(owner), V), float("nan"), device="cuda", dtype=DT[dtype])
     x[at] = torch.randn(len(at), V, device="cuda", generator=gen(V)).to(DT[dtype])
     lead = (4, 90, 4)
-    few = x[at].clone().requires_grad_()
-    all_ = x.view(*lead, V).clone().requires_grad_()
-    top = rnnt_top_logits(few.detach(), k)
-    got = rnnt_top_logits(all_.detach(), k, i32(T), i32(U))
-    for a, b in zip(got, top):
-        assert torch.equal(a.view(len(owner), *b.shape[1:])[at], b)
-    dead = torch.as_tensor(~live, device="cuda")
-    assert (got[1].view(-1, k)[dead] == -1).all() and (got[2].view(-1)[dead] == -float("inf")).all()
-    one = rnnt_distill_loss(few, *top[:2], i32(T), i32(U), top[2], reduction="none")
-    two = rnnt_distill_loss(all_, *got[:2], i32(T), i32(U), got[2], reduction="none")
-    assert torch.equal(one, two)
-    g1, = torch.autograd.grad(one.sum(), few)
-    g2, = torch.autograd.grad(two.sum(), all_)
-    assert torch.equal(g2.view(len(owner), V)[at], g1) and (g2.view(len(owner), V)[dead] == 0).all()
+    x = x.view(*lead, V)
+    got = rnnt_top_logits(x, k, i32(T), i32(U))
+    D.check_top(torch.nan_to_num(x), k, 1.0, got, live)
+    # (the order in which a thread adds its row's terms turns with its place in the batch, so sums of
+    # the compact layout are held to the float64 form too, not to the padded one's bits)
+    rows = [t.reshape(len(owner), *t.shape[3:]) for t in got]
+    for padded in (True, False):
+        leaf = (x if padded else x.view(-1, V)[at]).clone().requires_grad_()
+        teacher = got if padded else [t[at].contiguous() for t in rows]
+        loss = rnnt_distill_loss(leaf, *teacher[:2], i32(T), i32(U), teacher[2], reduction="none")
+        grad, = torch.autograd.grad(loss.sum(), leaf)
+        o, l = (owner, live) if padded else (owner[live], live[live])
+        want = D.expected(torch.nan_to_num(leaf).detach().view(-1, V), *(t.reshape(len(o), -1) for t in teacher[:2]),
+                          teacher[2].reshape(-1), 1.0, o, l, 4, 1.0, "none")
+        D.check_distill(leaf, loss, grad, want, DT[dtype])
+        assert (grad.reshape(-1, V)[torch.as_tensor(~l, device="cuda")] == 0).all()
