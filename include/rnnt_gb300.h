@@ -511,8 +511,8 @@ rnnt_status_t rnnt_beam_reorder(const rnnt_state_t *states, int32_t n_states,
  *   values[r], ids[r]   the k largest logits above -inf in descending order, equal
  *                       ones by id; places left over get -inf and id -1.
  *   rest[r]             log sum exp(x_j / temperature) over the outputs without a
- *                       place; -inf where there is none.  A finite value below
-                       float32's range is its lowest.
+ *                       place; -inf where there is none.  A finite value outside
+ *                       float32's range is the nearer end of it.
  *
  *   logits         (rows, V) contiguous in dt.
  *   logit_lengths, target_lengths

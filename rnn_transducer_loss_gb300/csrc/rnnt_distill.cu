@@ -136,6 +136,11 @@ struct TopParams {
     int32_t* status;
 };
 
+// The logarithm of a rest whose largest is `first` and whose sum relative to it is `sum`; finite.
+__device__ __forceinline__ float rest_of(const TopParams& p, float sum, float first) {
+    return fminf(fmaxf(logf(sum) + first * p.inv_tau, -kMost), kMost);
+}
+
 constexpr int kLongThreads = 256;
 constexpr int kTopBuf = 1024;              // elements of a row that are ranked: 4 a thread
 
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(kLongThreads) k_top_long(const TopParams p) {
                     sum = block_sum<TH>(sum, space);
                     equal = block_sum<TH>(equal, space);
                     for (int i = 0; i < k; ++i) equal -= value_of(best[i]) == first ? 1.0f : 0.0f;
-                    rest = fmaxf(logf(sum + equal) + first * p.inv_tau, -kMost);
+                    rest = rest_of(p, sum + equal, first);
                 }
             }
         }
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(TH, 5) k_top(const TopParams p, const Ring rin
                         sum += terms_of(x.at(j), f, e);
                     }
                     sum = Gr::sum(sum, sh.space);
-                    rest = fmaxf(logf(sum) + first * p.inv_tau, -kMost);
+                    rest = rest_of(p, sum, first);
                 }
             }
         }
@@ -1140,7 +1145,7 @@ __global__ void __launch_bounds__(kShortThreads) k_top_short(const TopParams p, 
                     const Exponent f(best, p.scale, p.scale_low);
                     float sum = 0.0f;
                     r.each([&](int, T x) { sum += f(to_f32(x)); });
-                    rest = fmaxf(logf(sum) + best * p.inv_tau, -kMost);
+                    rest = rest_of(p, sum, best);
                 }
             }
         }

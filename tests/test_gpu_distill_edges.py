@@ -73,3 +73,18 @@ def test_padded_short_rows_of_which_most_do_not_count(V, dtype):
                           teacher[2].reshape(-1), 1.0, o, l, 4, 1.0, "none")
         D.check_distill(leaf, loss, grad, want, DT[dtype])
         assert (grad.reshape(-1, V)[torch.as_tensor(~l, device="cuda")] == 0).all()
+
+
+@pytest.mark.parametrize("V", [29, 200, 1024, 5000, 70000])
+def test_rest_outside_float32(V):
+    """A finite rest over a small temperature is the nearer end of float32's range, not infinite."""
+    most = torch.finfo(torch.float32).max
+    x = torch.randn(4, V, device="cuda", generator=gen(3))
+    x[0], x[1, :9], x[2] = 3e38, 1e38, -3e38
+    for dtype in (torch.float32, torch.bfloat16):
+        _, _, rest = rnnt_top_logits(x.to(dtype), 3, temperature=0.1)
+        assert rest[:3].tolist() == [most, most, -most] and abs(rest[3]) < 100
+        # and is a rest that the loss takes
+        loss = rnnt_distill_loss(x * 0, torch.zeros(4, 1, device="cuda"), i32(np.zeros((4, 1))), i32([4]), i32([0]),
+                                 rest, temperature=0.1)
+        assert torch.isfinite(loss)
