@@ -129,16 +129,18 @@ struct TopParams {
     Lattice lat;
     int32_t V, k;
     float scale, scale_low;                // log2 e / tau, in two parts
-    float inv_tau;
+    float inv_tau, inv_tau_low;            // 1 / tau, in two parts
     void* values;
     int32_t* ids;
     float* rest;
     int32_t* status;
 };
 
-// The logarithm of a rest whose largest is `first` and whose sum relative to it is `sum`; finite.
+// The logarithm of a rest whose largest is `first` and whose sum relative to it is `sum`; finite, and
+// rounded once: by a reciprocal rounded to one float32 all of a call's rests would be off the same way.
 __device__ __forceinline__ float rest_of(const TopParams& p, float sum, float first) {
-    return fminf(fmaxf(logf(sum) + first * p.inv_tau, -kMost), kMost);
+    const float low = __fmaf_rn(first, p.inv_tau_low, logf(sum));
+    return fminf(fmaxf(__fmaf_rn(first, p.inv_tau, low), -kMost), kMost);
 }
 
 constexpr int kLongThreads = 256;
@@ -1434,6 +1436,10 @@ bool lattice_ok(const Lattice& lat) {
 int64_t bytes_of(int64_t n, int64_t each, int size) {
     return n <= (INT64_MAX >> 8) / each / size ? n * each * size : -1;
 }
+void in_two_parts(double x, float& hi, float& lo) {
+    hi = (float)x;
+    lo = (float)(x - (double)hi);
+}
 bool temperature_ok(double tau) { return tau >= 1e-4 && tau <= 1e4; }
 dim3 row_grid(int64_t rows) { return dim3((unsigned)std::min<int64_t>(rows, kMostRows)); }
 
@@ -1610,7 +1616,7 @@ extern "C" rnnt_status_t rnnt_top_logits(const void* logits, rnnt_dtype_t dt, in
     p.V = V;
     p.k = k;
     parts_below(kLog2e / temperature, p.scale, p.scale_low);
-    p.inv_tau = (float)(1.0 / temperature);
+    in_two_parts(1.0 / temperature, p.inv_tau, p.inv_tau_low);
     p.values = values;
     p.ids = ids;
     p.rest = rest;

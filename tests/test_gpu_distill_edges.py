@@ -88,3 +88,18 @@ def test_rest_outside_float32(V):
         loss = rnnt_distill_loss(x * 0, torch.zeros(4, 1, device="cuda"), i32(np.zeros((4, 1))), i32([4]), i32([0]),
                                  rest, temperature=0.1)
         assert torch.isfinite(loss)
+
+
+@pytest.mark.parametrize("tau", [1.0, 1.5, 0.7, 3.0])
+@pytest.mark.parametrize("V", [29, 200, 1024, 5000, 70000])
+def test_rest_is_rounded_once(V, tau):
+    """Temperatures whose reciprocal is not a float32: the rest is off by half a step of its own and by what
+    the logarithm of a sum of ``V`` terms may be off (rows far from 0, where that is a tenth of a step)."""
+    x = torch.randn(300, V, device="cuda", generator=gen(V)) * 2 + torch.linspace(1e4, 2e4, 300, device="cuda")[:, None]
+    values, _, rest = rnnt_top_logits(x, 3, temperature=tau)
+    y = x.double() / tau
+    y.scatter_(1, torch.topk(x, 3, dim=1).indices, -float("inf"))
+    want = torch.logsumexp(y, 1).cpu().numpy()
+    far = np.log(V) + np.abs(want - y.max(1).values.cpu().numpy())
+    step = np.spacing(want.astype(np.float32)).astype(np.float64)
+    assert (np.abs(L.f64(rest) - want) <= step / 2 + R.SUM + R.EXPONENT * far + 4 * L.U32 * far).all()
