@@ -523,7 +523,7 @@ struct DistillParams {
     Lattice lat;
     int32_t V, k, teacher_dt;
     float scale, scale_low;                // log2 e / tau, in two parts
-    float inv_tau;
+    float inv_tau, inv_tau_low;            // 1 / tau, in two parts
     float grad_scale;                      // tau * weight, over the batch for the mean
     double loss_scale;                     // tau^2 * weight
     char* grad;                            // or NULL
@@ -544,6 +544,19 @@ __device__ __forceinline__ float teacher_logit(const DistillParams& p, int64_t a
     return to_f32(reinterpret_cast<const __nv_bfloat16*>(p.teacher)[at]);
 }
 
+// d / tau of a difference of logits.  By a reciprocal rounded to one float32 all rows would be off the
+// same way, by 3e-8 of their exponents.  A difference below float32's range counts as its lowest.
+__device__ __forceinline__ float over_tau(const DistillParams& p, float d) {
+    d = max_nan(d, -kMost);
+    return __fmaf_rn(d, p.inv_tau, d * p.inv_tau_low);
+}
+// rest - logit / tau; logit / tau outside float32's range is the nearer end of it (as in a rest).
+__device__ __forceinline__ float rest_above(const DistillParams& p, float rest, float logit) {
+    const float hi = logit * p.inv_tau;
+    if (fabsf(hi) >= kMost) return rest - copysignf(kMost, hi);
+    return (rest - hi) - __fmaf_rn(logit, p.inv_tau_low, __fmaf_rn(logit, p.inv_tau, -hi));
+}
+
 // Which of the warp's ids (of places 0 to 31, and 32 to 63) stand in a place before theirs: bits 0, 1.
 __device__ __noinline__ unsigned repeated(int id0, int id1) {
     const int lane = threadIdx.x & 31;
@@ -561,7 +574,7 @@ __device__ __noinline__ unsigned repeated(int id0, int id1) {
 template <int P>
 struct Teacher {
     int id[P];                             // -1: an empty place
-    float t[P];                            // logit / tau, -inf in an empty place
+    float t[P];                            // its logit, -inf in an empty place
     float rest;                            // -inf without one
 
     __device__ __forceinline__ void load(const DistillParams& a, int64_t row, int64_t place0) {
@@ -578,7 +591,7 @@ struct Teacher {
         }
         rest = a.rest ? a.rest[row] : -INFINITY;
     }
-    // Logits / tau; empties places without an output of the vocabulary; says what is not allowed.
+    // Empties places without an output of the vocabulary; says what is not allowed.
     __device__ __forceinline__ void check(const DistillParams& a) {
         bool bad = !(rest < INFINITY);
 #pragma unroll
@@ -588,9 +601,6 @@ struct Teacher {
                 id[q] = -1;
                 t[q] = -INFINITY;
             }
-            const float x = t[q];
-            t[q] *= a.inv_tau;
-            if (t[q] == -INFINITY && x != -INFINITY) t[q] = -kMost;
             bad |= !(t[q] < INFINITY);
         }
         if (bad) invalid(a.status);
@@ -615,15 +625,17 @@ struct Teacher {
     }
 };
 
-// A row's places, relative to the largest of their teacher's logits (`t_top`, with the rest) and of
-// their student's (`top`): w = exp(t - t_top), e = exp((x - top) / tau).  With W = the sum of
-// all w, S that of e, and the row's sum total = left * outer + S * inner relative to `base`,
+// A row's places, relative to the largest of their teacher's logits and of their student's (`t_top`,
+// `top`), the teacher's also to the rest where that is larger (`shift`, over tau):
+// w = exp((t - t_top) / tau - shift), e = exp((x - top) / tau).  With W = the sum of all w, S that of e,
+// and the row's sum total = left * outer + S * inner relative to `base`,
 //   sum of p log (p / q) over the places
-//     = [ sum w (t - t_top - (x - top) / tau) + (sum w) (log (total / W) - (top - base) / tau) ] / W,
+//     = [ sum w (log w - (x - top) / tau) + (sum w) (log (total / W) - (top - base) / tau) ] / W,
 // so that one exchange over the warp gives all sums.
 template <int P>
 struct Places {
-    float at[P], w[P], e[P], t_top, top, w_rest;
+    float at[P], w[P], e[P], top, w_rest;
+    float log_w_rest;                      // -inf without a rest
     float w_sum, w_log, sum;               // of this lane's, then of the warp's
 
     __device__ __forceinline__ void terms(const DistillParams& a, const Teacher<P>& te) {
@@ -633,22 +645,24 @@ struct Places {
             m = max_nan(m, te.t[q]);
             x = max_nan(x, at[q]);
         }
-        t_top = max_nan(warp_max_nan(m), te.rest);
+        const float t_top = warp_max_nan(m);
         top = warp_max_nan(x);
+        const float above = te.rest == -INFINITY || t_top == -INFINITY
+                                ? te.rest : rest_above(a, te.rest, t_top);
+        const float shift = t_top == -INFINITY ? above : fmaxf(above, 0.0f);
+        log_w_rest = above == -INFINITY ? above : above - shift;
         // few terms, of which the largest is exactly 1: by expf, which ex2.approx's corrected mean is
         // not good enough for
-        w_rest = te.rest == -INFINITY ? 0.0f : expf(te.rest - t_top);
+        w_rest = te.rest == -INFINITY ? 0.0f : expf(log_w_rest);
         w_sum = w_log = sum = 0.0f;
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            w[q] = te.t[q] == -INFINITY ? 0.0f : expf(te.t[q] - t_top);
-            e[q] = at[q] == -INFINITY ? 0.0f : expf((at[q] - top) * a.inv_tau);
+            const float log_w = over_tau(a, te.t[q] - t_top) - shift, log_e = over_tau(a, at[q] - top);
+            w[q] = te.t[q] == -INFINITY ? 0.0f : expf(log_w);
+            e[q] = at[q] == -INFINITY ? 0.0f : expf(log_e);
             w_sum += w[q];
             sum += e[q];
-            if (w[q] != 0.0f)
-                w_log += at[q] == -INFINITY
-                             ? INFINITY
-                             : w[q] * ((te.t[q] - t_top) - (at[q] - top) * a.inv_tau);
+            if (w[q] != 0.0f) w_log += at[q] == -INFINITY ? INFINITY : w[q] * (log_w - log_e);
         }
     }
     __device__ __forceinline__ void finish(float& left) {              // left: a fourth sum
@@ -664,8 +678,8 @@ struct Whole {
     __device__ __forceinline__ Whole(const DistillParams& a, float outside, float left, float top,
                                      float sum) {
         base = max_nan(outside, top);
-        outer = outside == -INFINITY ? 0.0f : expf((outside - base) * a.inv_tau);
-        inner = top == -INFINITY ? 0.0f : expf((top - base) * a.inv_tau);
+        outer = outside == -INFINITY ? 0.0f : expf(over_tau(a, outside - base));
+        inner = top == -INFINITY ? 0.0f : expf(over_tau(a, top - base));
         total = left * outer + sum * inner;
     }
     __device__ __forceinline__ bool good() const { return total > 0.0f && total < INFINITY; }
@@ -678,7 +692,7 @@ struct Whole {
     }
     // The row's divergence, of the warp's sums (the same in all lanes).
     template <int P>
-    __device__ __forceinline__ float loss(const DistillParams& a, const Places<P>& pl, float rest,
+    __device__ __forceinline__ float loss(const DistillParams& a, const Places<P>& pl,
                                           float outside, float left) const {
         // the two logarithms by two lanes
         const float all = pl.w_sum + pl.w_rest;            // divided by: reciprocals are off on average
@@ -686,9 +700,9 @@ struct Whole {
         const float ratio = __shfl_sync(kAll, mine, 0), log_left = __shfl_sync(kAll, mine, 1);
         float kl = pl.w_sum == 0.0f
                        ? 0.0f
-                       : pl.w_log + pl.w_sum * (ratio - (pl.top - base) * a.inv_tau);
+                       : pl.w_log + pl.w_sum * (ratio - over_tau(a, pl.top - base));
         if (pl.w_rest != 0.0f)
-            kl += pl.w_rest * ((rest - pl.t_top) - (outside - base) * a.inv_tau + ratio - log_left);
+            kl += pl.w_rest * (pl.log_w_rest - over_tau(a, outside - base) + ratio - log_left);
         return kl / all;
     }
     template <int P>
@@ -809,7 +823,7 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillPara
             pl.finish(left);
             const Whole w(p, outside, left, pl.top, pl.sum);
             if (!w.good()) invalid(p.status);              // NaN among them
-            const float kl = w.loss(p, pl, te.rest, outside, left);
+            const float kl = w.loss(p, pl, outside, left);
 #pragma unroll
             for (int q = 0; q < 2; ++q) te.t[q] = w.place(p, pl, q);
             if (lane == 0) {
@@ -1010,7 +1024,7 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
                 }
                 if (leads) {
                     if (!w.good()) invalid(p.status);      // NaN among them
-                    const float kl = w.loss(p, pl, te.rest, outside, left);
+                    const float kl = w.loss(p, pl, outside, left);
                     if (lane == 0) p.row_loss[row] = w.good() ? kl : NAN;
                 }
                 if (p.grad) {
@@ -1200,7 +1214,7 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
             fetch_short(p.logits, row0, n, p.V, stage, bar, phase, polls, p.status);
         const ShortRow<T> r(stage, p.V);
         float loss = 0.0f, c = 0.0f, inner = 0.0f, outside = -INFINITY, weight = 0.0f;
-        float t_top = -INFINITY, top = -INFINITY;
+        float t_top = -INFINITY, shift = 0.0f, top = -INFINITY;
         bool some = false;
         if (counts) {
             bool bad = false;
@@ -1216,9 +1230,7 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
                     if (r.bits(id) == kTaken && fine) {
                         bad = true;                        // an id again
                     } else {
-                        const float x = teacher_logit(p, first + q);
-                        float t = x * p.inv_tau;
-                        if (t == -INFINITY && x != -INFINITY) t = -kMost;
+                        const float t = teacher_logit(p, first + q);
                         bad |= !(t < INFINITY);
                         at = fine ? to_f32(r.s[id]) : -INFINITY;
                         r.bits(id) = kTaken;
@@ -1230,8 +1242,10 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
             }
             const float rest = p.rest ? p.rest[row] : -INFINITY;
             bad |= !(rest < INFINITY);
-            t_top = max_nan(t_top, rest);
-            some = t_top != -INFINITY;                     // NaN counts
+            some = t_top != -INFINITY || rest != -INFINITY;        // NaN counts
+            const float above = rest == -INFINITY || t_top == -INFINITY
+                                    ? rest : rest_above(p, rest, t_top);
+            shift = t_top == -INFINITY ? above : fmaxf(above, 0.0f);
             if (some) {
                 r.each([&](int i, T x) {
                     if (r.bits(i) != kTaken) outside = fmaxf(outside, to_f32(x));
@@ -1243,24 +1257,24 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
                 for (int q = 0; q < p.k; ++q) {
                     const float at = ats[q * 32 + lane];
                     if (at == INFINITY) continue;
-                    sum += at == -INFINITY ? 0.0f : expf((at - top) * p.inv_tau);
+                    const float log_e = over_tau(p, at - top);
+                    sum += at == -INFINITY ? 0.0f : expf(log_e);
                     const float x = teacher_logit(p, first + q);
                     if (x == -INFINITY) continue;
-                    const float t = fmaxf(x * p.inv_tau, -kMost) - t_top, w = x != x ? x : expf(t);
+                    const float log_w = over_tau(p, x - t_top) - shift, w = expf(log_w);
                     w_sum += w;
-                    if (w != 0.0f)
-                        w_log += at == -INFINITY ? INFINITY : w * (t - (at - top) * p.inv_tau);
+                    if (w != 0.0f) w_log += at == -INFINITY ? INFINITY : w * (log_w - log_e);
                 }
-                const float w_rest = rest == -INFINITY ? 0.0f : expf(rest - t_top);
+                const float log_w_rest = above - shift;
+                const float w_rest = rest == -INFINITY ? 0.0f : expf(log_w_rest);
                 const Whole w(p, outside, left, top, sum);
                 const bool good = fine && w.good();
                 bad |= !good;
                 const float all = w_sum + w_rest, ratio = logf(w.total / all);
                 float kl = w_sum == 0.0f ? 0.0f
-                                         : w_log + w_sum * (ratio - (top - w.base) * p.inv_tau);
+                                         : w_log + w_sum * (ratio - over_tau(p, top - w.base));
                 if (w_rest != 0.0f)
-                    kl += w_rest * ((rest - t_top) - (outside - w.base) * p.inv_tau + ratio -
-                                    logf(left));
+                    kl += w_rest * (log_w_rest - over_tau(p, outside - w.base) + ratio - logf(left));
                 loss = good ? kl / all : NAN;
                 c = good ? w.factor(p, left, w_rest / all) : NAN;
                 inner = good ? w.inner / w.total : NAN;
@@ -1282,9 +1296,9 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
                 const float at = ats[q * 32 + lane];
                 if (at == INFINITY) continue;
                 const float x = teacher_logit(p, first + q);
-                const float t = fmaxf(x * p.inv_tau, -kMost) - t_top;
-                const float prob = x == -INFINITY ? 0.0f : (x != x ? x : expf(t)) * weight;
-                const float e = at == -INFINITY ? 0.0f : expf((at - top) * p.inv_tau);
+                const float prob = x == -INFINITY
+                                       ? 0.0f : expf(over_tau(p, x - t_top) - shift) * weight;
+                const float e = at == -INFINITY ? 0.0f : expf(over_tau(p, at - top));
                 r.s[p.ids[first + q]] = from_f32<T>((e * inner - prob) * p.grad_scale);
             }
         } else if (lane < n) {
@@ -1705,7 +1719,7 @@ extern "C" rnnt_status_t rnnt_distill_loss(
     p.V = V;
     p.k = k;
     parts_below(kLog2e / temperature, p.scale, p.scale_low);
-    p.inv_tau = (float)(1.0 / temperature);
+    in_two_parts(1.0 / temperature, p.inv_tau, p.inv_tau_low);
     p.mean = reduction == RNNT_RED_MEAN;
     p.grad_scale = (float)(temperature * weight / (p.mean ? B : 1));
     p.loss_scale = temperature * temperature * weight;

@@ -103,3 +103,36 @@ def test_rest_is_rounded_once(V, tau):
     far = np.log(V) + np.abs(want - y.max(1).values.cpu().numpy())
     step = np.spacing(want.astype(np.float32)).astype(np.float64)
     assert (np.abs(L.f64(rest) - want) <= step / 2 + R.SUM + R.EXPONENT * far + 4 * L.U32 * far).all()
+
+
+@pytest.mark.parametrize("V,k", [(29, 8), (1024, 64)])
+def test_inexact_temperatures(V, k):
+    """A reciprocal of the temperature that is off shifts all rows' exponents the same way, which adds
+    up over rows: the sum of many is off by half a step of its own and at most as much again."""
+    N, tau = 40000, 1.5
+    x = torch.randn(N, V, device="cuda", generator=gen(V)) * 2
+    values, ids, rest = rnnt_top_logits(x + torch.randn(N, V, device="cuda", generator=gen(V + 1)), k, temperature=tau)
+    loss = rnnt_distill_loss(x, values, ids, i32([N]), i32([0]), rest, temperature=tau, reduction="sum")
+    want = 0.0
+    for at in torch.arange(N, device="cuda").split(10000):
+        log_q = torch.log_softmax(x[at].double() / tau, 1)
+        goal = torch.cat([values[at].double() / tau, rest[at, None].double()], 1)
+        mine = log_q.gather(1, ids[at].long())
+        left = torch.logsumexp(log_q.scatter(1, ids[at].long(), -float("inf")), 1, keepdim=True)
+        log_p = torch.log_softmax(goal, 1)
+        want += (log_p.exp() * (log_p - torch.cat([mine, left], 1))).sum().item() * tau * tau
+    assert abs(loss.item() - want) <= 2 * L.U32 * want
+
+
+@pytest.mark.parametrize("V", [29, 200, 1024, 5000, 70000])
+def test_far_teachers(V):
+    """Finite logits of a teacher, however large over the temperature: what counts is how far apart they are."""
+    x = torch.randn(3, V, device="cuda", generator=gen(4)).requires_grad_()
+    ids = i32([[3, 1, 5]] * 3)
+    far = torch.tensor([[3e38, 2.9e38, -3e38], [-3e38, -3.3e38, -float("inf")], [2e38, 2e38, 1e38]], device="cuda")
+    near = torch.tensor([[0.0, -1e4, -1e4], [0.0, -1e4, -float("inf")], [0.0, 0.0, -1e4]], device="cuda")
+    T, U = i32([1, 1, 1]), i32([0, 0, 0])
+    for rest in (None, torch.full((3,), -float("inf"), device="cuda")):
+        got, want = (rnnt_distill_loss(x, t, ids, T, U, rest, temperature=0.1, reduction="none") for t in (far, near))
+        assert torch.equal(got, want)
+        assert torch.equal(*(torch.autograd.grad(y.sum(), x)[0] for y in (got, want)))
