@@ -136,11 +136,20 @@ struct TopParams {
     int32_t* status;
 };
 
+// a + b + c for a c below a step of a + b, rounded once (Knuth's sum): added to a rounded a + b, a low
+// part of a product would be lost, in all rows the same way.
+__device__ __forceinline__ float sum_of(float a, float b, float c) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return __fadd_rn(s, __fadd_rn(__fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)), c));
+}
+
 // The logarithm of a rest whose largest is `first` and whose sum relative to it is `sum`; finite, and
 // rounded once: by a reciprocal rounded to one float32 all of a call's rests would be off the same way.
 __device__ __forceinline__ float rest_of(const TopParams& p, float sum, float first) {
-    const float low = __fmaf_rn(first, p.inv_tau_low, logf(sum));
-    return fminf(fmaxf(__fmaf_rn(first, p.inv_tau, low), -kMost), kMost);
+    const float hi = first * p.inv_tau;
+    if (!(fabsf(hi) < kMost)) return copysignf(kMost, hi);
+    const float low = __fmaf_rn(first, p.inv_tau_low, __fmaf_rn(first, p.inv_tau, -hi));
+    return fminf(fmaxf(sum_of(logf(sum), hi, low), -kMost), kMost);
 }
 
 constexpr int kLongThreads = 256;
@@ -523,9 +532,9 @@ struct DistillParams {
     Lattice lat;
     int32_t V, k, teacher_dt;
     float scale, scale_low;                // log2 e / tau, in two parts
-    float inv_tau, inv_tau_low;            // 1 / tau, in two parts
+    float tau, inv_tau, inv_tau_low;       // the reciprocal in two parts
     float grad_scale;                      // tau * weight, over the batch for the mean
-    double loss_scale;                     // tau^2 * weight
+    double loss_scale;                     // of a row's loss, which is tau times its divergence
     char* grad;                            // or NULL
     float* row_loss;                       // [rows], 0 where a row does not count
     double* part_loss;                     // [B][splits]
@@ -545,16 +554,37 @@ __device__ __forceinline__ float teacher_logit(const DistillParams& p, int64_t a
 }
 
 // d / tau of a difference of logits.  By a reciprocal rounded to one float32 all rows would be off the
-// same way, by 3e-8 of their exponents.  A difference below float32's range counts as its lowest.
+// same way, by 3e-8 of their exponents.  (Both parts are above 0, so that -inf stays it.)
 __device__ __forceinline__ float over_tau(const DistillParams& p, float d) {
-    d = max_nan(d, -kMost);
     return __fmaf_rn(d, p.inv_tau, d * p.inv_tau_low);
 }
 // rest - logit / tau; logit / tau outside float32's range is the nearer end of it (as in a rest).
 __device__ __forceinline__ float rest_above(const DistillParams& p, float rest, float logit) {
     const float hi = logit * p.inv_tau;
     if (fabsf(hi) >= kMost) return rest - copysignf(kMost, hi);
-    return (rest - hi) - __fmaf_rn(logit, p.inv_tau_low, __fmaf_rn(logit, p.inv_tau, -hi));
+    const float low = __fmaf_rn(logit, p.inv_tau_low, __fmaf_rn(logit, p.inv_tau, -hi));
+    return sum_of(rest, -hi, -low);
+}
+
+// tau times what a class adds to a row's divergence, for probabilities p of the teacher and q:
+// p (x + exp(-x) - 1) with x = log p - log q, which adds up to sum p x as p and q add up to 1 each.
+// Every class's part is positive, and an error of x counts p - q times only: the sum of p x would lose
+// a small divergence among its rounded logarithms, and keep what of their errors points one way.
+// d: x times tau, but for what is small beside 1e30, where x may leave float32; +inf where q is 0.
+struct Class {
+    float w, p, q, x, d;                   // w: p times W
+};
+__device__ __forceinline__ float divergence(const DistillParams& a, const Class& c) {
+    const float x = c.x;
+    float y = __fmaf_rn(x, 1.0f / 40320.0f, -1.0f / 5040.0f);          // the series, to 3e-8 of the value
+    y = __fmaf_rn(x, y, 1.0f / 720.0f);
+    y = __fmaf_rn(x, y, -1.0f / 120.0f);
+    y = __fmaf_rn(x, y, 1.0f / 24.0f);
+    y = __fmaf_rn(x, y, -1.0f / 6.0f);
+    y = __fmaf_rn(x, y, 0.5f);
+    y = a.tau * (fabsf(x) <= 0.5f ? c.p * (x * x * y) : __fmaf_rn(c.p, x - 1.0f, c.q));
+    if (c.d > 1e30f) y = c.d == INFINITY ? c.d : c.p * c.d;
+    return c.w == 0.0f ? a.tau * c.q : y;                  // (p may be rounded to 0 before w is)
 }
 
 // Which of the warp's ids (of places 0 to 31, and 32 to 63) stand in a place before theirs: bits 0, 1.
@@ -627,16 +657,15 @@ struct Teacher {
 
 // A row's places, relative to the largest of their teacher's logits and of their student's (`t_top`,
 // `top`), the teacher's also to the rest where that is larger (`shift`, over tau):
-// w = exp((t - t_top) / tau - shift), e = exp((x - top) / tau).  With W = the sum of all w, S that of e,
-// and the row's sum total = left * outer + S * inner relative to `base`,
-//   sum of p log (p / q) over the places
-//     = [ sum w (log w - (x - top) / tau) + (sum w) (log (total / W) - (top - base) / tau) ] / W,
-// so that one exchange over the warp gives all sums.
+// w = exp((t - t_top) / tau - shift), e = exp((x - top) / tau), gap = (t - t_top) - (x - top).  With W the
+// sum of all w and total the row's sum relative to `base`, a place has
+// p = w / W and log p - log q = (gap + base - top) / tau + log (total / W) - shift.
 template <int P>
 struct Places {
-    float at[P], w[P], e[P], top, w_rest;
+    float at[P], w[P], e[P], gap[P], top, w_rest, shift;
     float log_w_rest;                      // -inf without a rest
-    float w_sum, w_log, sum;               // of this lane's, then of the warp's
+    float w_sum, sum;                      // of this lane's, then of the warp's
+    float inv_all;                         // 1 / W
 
     __device__ __forceinline__ void terms(const DistillParams& a, const Teacher<P>& te) {
         float m = -INFINITY, x = -INFINITY;
@@ -649,67 +678,89 @@ struct Places {
         top = warp_max_nan(x);
         const float above = te.rest == -INFINITY || t_top == -INFINITY
                                 ? te.rest : rest_above(a, te.rest, t_top);
-        const float shift = t_top == -INFINITY ? above : fmaxf(above, 0.0f);
+        shift = t_top == -INFINITY ? above : fmaxf(above, 0.0f);
         log_w_rest = above == -INFINITY ? above : above - shift;
         // few terms, of which the largest is exactly 1: by expf, which ex2.approx's corrected mean is
         // not good enough for
         w_rest = te.rest == -INFINITY ? 0.0f : expf(log_w_rest);
-        w_sum = w_log = sum = 0.0f;
+        w_sum = sum = 0.0f;
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            const float log_w = over_tau(a, te.t[q] - t_top) - shift, log_e = over_tau(a, at[q] - top);
-            w[q] = te.t[q] == -INFINITY ? 0.0f : expf(log_w);
-            e[q] = at[q] == -INFINITY ? 0.0f : expf(log_e);
+            const float t = te.t[q] - t_top, x = at[q] - top;
+            w[q] = te.t[q] == -INFINITY ? 0.0f : expf(over_tau(a, t) - shift);
+            e[q] = at[q] == -INFINITY ? 0.0f : expf(over_tau(a, x));
+            gap[q] = at[q] == -INFINITY ? INFINITY : fminf(t - x, kMost);
             w_sum += w[q];
             sum += e[q];
-            if (w[q] != 0.0f) w_log += at[q] == -INFINITY ? INFINITY : w[q] * (log_w - log_e);
         }
     }
-    __device__ __forceinline__ void finish(float& left) {              // left: a fourth sum
-        const float4 s = warp_sum4(w_sum, w_log, sum, left);
-        w_sum = s.x, w_log = s.y, sum = s.z, left = s.w;
+    __device__ __forceinline__ void finish(float& left) {              // left: a third sum
+        const float4 s = warp_sum4(w_sum, sum, left, 0.0f);
+        w_sum = s.x, sum = s.y, left = s.z;
+        inv_all = rounded_reciprocal(w_sum + w_rest);
     }
 };
 
 // The sum of a row whose outputs without a place have their largest at `outside` and a sum `left`
 // relative to it, and whose places have `top` and `sum`.
 struct Whole {
-    float base, outer, inner, total;       // 2^((outside - base) c), 2^((top - base) c)
+    float base, outer, inner;              // exp((outside - base) / tau), exp((top - base) / tau)
+    float total, inv_total;
     __device__ __forceinline__ Whole(const DistillParams& a, float outside, float left, float top,
                                      float sum) {
         base = max_nan(outside, top);
         outer = outside == -INFINITY ? 0.0f : expf(over_tau(a, outside - base));
         inner = top == -INFINITY ? 0.0f : expf(over_tau(a, top - base));
         total = left * outer + sum * inner;
+        inv_total = rounded_reciprocal(total);
     }
     __device__ __forceinline__ bool good() const { return total > 0.0f && total < INFINITY; }
     // of the terms relative to `outside`
     __device__ __forceinline__ float factor(const DistillParams& a, float left,
                                             float p_rest) const {
-        float c = outer * reciprocal(total);
+        float c = outer * inv_total;
         if (a.rest && left > 0.0f) c -= p_rest * reciprocal(left);
         return c * a.grad_scale;
     }
-    // The row's divergence, of the warp's sums (the same in all lanes).
+    // Classes of the divergence: a place's, and that of all outputs without one.  log_ratio: of total / W.
+    __device__ __forceinline__ Class class_of_place(const DistillParams& a, float w, float e, float gap,
+                                                    float top, float shift, float log_ratio,
+                                                    float inv_all) const {
+        const float d = gap == INFINITY ? gap : fminf(gap + (base - top), kMost);
+        // (a sum with the low part first would round it away, in all rows the same way)
+        return {w, w * inv_all, e * (inner * inv_total), over_tau(a, d) + (log_ratio - shift), d};
+    }
+    __device__ __forceinline__ Class class_of_rest(const DistillParams& a, float w, float log_w,
+                                                   float outside, float left, float log_ratio,
+                                                   float log_left, float inv_all) const {
+        return {w, w * inv_all, left * outer * inv_total,
+                log_w - over_tau(a, outside - base) + (log_ratio - log_left),
+                left > 0.0f ? fminf(base - outside, kMost) : INFINITY};
+    }
+    // tau times the row's divergence, of the warp's sums (the same in all lanes).
     template <int P>
-    __device__ __forceinline__ float loss(const DistillParams& a, const Places<P>& pl,
-                                          float outside, float left) const {
-        // the two logarithms by two lanes
-        const float all = pl.w_sum + pl.w_rest;            // divided by: reciprocals are off on average
-        const float mine = logf((threadIdx.x & 1) ? left : total / all);
+    __device__ __forceinline__ float loss(const DistillParams& a, const Places<P>& pl, float outside,
+                                          float left) const {
+        const int lane = threadIdx.x & 31;
+        const float mine = logf((lane & 1) ? left : total * pl.inv_all);   // the two logarithms by two lanes
         const float ratio = __shfl_sync(kAll, mine, 0), log_left = __shfl_sync(kAll, mine, 1);
-        float kl = pl.w_sum == 0.0f
-                       ? 0.0f
-                       : pl.w_log + pl.w_sum * (ratio - over_tau(a, pl.top - base));
-        if (pl.w_rest != 0.0f)
-            kl += pl.w_rest * (pl.log_w_rest - over_tau(a, outside - base) + ratio - log_left);
-        return kl / all;
+        const Class rest = class_of_rest(a, pl.w_rest, pl.log_w_rest, outside, left, ratio, log_left,
+                                         pl.inv_all);
+        const bool spare = a.k < 32 * P;                   // a lane without a place takes the rest
+        float sum = spare || lane ? 0.0f : divergence(a, rest);
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            Class c = class_of_place(a, pl.w[q], pl.e[q], pl.gap[q], pl.top, pl.shift, ratio,
+                                     pl.inv_all);
+            if (lane + 32 * q == a.k) c = rest;
+            sum += divergence(a, c);
+        }
+        return warp_sum(sum);
     }
     template <int P>
     __device__ __forceinline__ float place(const DistillParams& a, const Places<P>& pl,
                                            int q) const {
-        return (pl.e[q] * (inner * reciprocal(total)) -
-                pl.w[q] * reciprocal(pl.w_sum + pl.w_rest)) * a.grad_scale;
+        return (pl.e[q] * (inner * inv_total) - pl.w[q] * pl.inv_all) * a.grad_scale;
     }
 };
 
@@ -829,7 +880,7 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillPara
             if (lane == 0) {
                 p.row_loss[row] = w.good() ? kl : NAN;
                 s_base = outside == -INFINITY ? 0.0f : outside;
-                s_coef = w.good() ? w.factor(p, left, pl.w_rest / (pl.w_sum + pl.w_rest)) : NAN;
+                s_coef = w.good() ? w.factor(p, left, pl.w_rest * pl.inv_all) : NAN;
             }
         }
         __syncthreads();
@@ -860,12 +911,50 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillPara
     }
 }
 
+// What a block's last warp needs of a row's places for its loss.
+struct Kept {
+    float w[RNNT_MAX_TOP], e[RNNT_MAX_TOP], gap[RNNT_MAX_TOP];
+    float inv_all, w_rest, shift, log_w_rest, outside, left;
+    template <int P>
+    __device__ __forceinline__ void put(const Places<P>& pl) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            w[lane + 32 * q] = pl.w[q];
+            e[lane + 32 * q] = pl.e[q];
+            gap[lane + 32 * q] = pl.gap[q];
+        }
+        if (lane == 0) {
+            inv_all = pl.inv_all;
+            w_rest = pl.w_rest;
+            shift = pl.shift;
+            log_w_rest = pl.log_w_rest;
+        }
+    }
+    template <int P>
+    __device__ __forceinline__ void get(Places<P>& pl) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            pl.w[q] = w[lane + 32 * q];
+            pl.e[q] = e[lane + 32 * q];
+            pl.gap[q] = gap[lane + 32 * q];
+        }
+        pl.inv_all = inv_all;
+        pl.w_rest = w_rest;
+        pl.shift = shift;
+        pl.log_w_rest = log_w_rest;
+    }
+};
+struct None {};
+
 template <int G>
 struct DistillScratch {
     uint64_t bar[kMostStages];
     typename Group<G>::Space space;
     float top, sum, p_rest;                // of the places, for a block
     int some;
+    std::conditional_t<(G > 32), Kept, None> kept;
 };
 
 // Rows through a ring of shared memory, a group of threads each, one read and one write.  The places'
@@ -921,6 +1010,7 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
     if (leads && live[0]) ahead.load(p, first_row, place0);
     for (int64_t row = first_row; row < p.lat.rows; row += groups) {
         const bool counts = live[0];
+        bool weighed = false;
         te = ahead;
         place0 += place_step;
         if (leads && live[1]) ahead.load(p, row + groups, place0);     // one row ahead
@@ -976,10 +1066,11 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
                     if constexpr (G > 32) {
                         float none = 0.0f;
                         pl.finish(none);
+                        sh.kept.put(pl);
                         if (lane == 0) {
                             sh.top = pl.top;
                             sh.sum = pl.sum;
-                            sh.p_rest = pl.w_rest * reciprocal(pl.w_sum + pl.w_rest);
+                            sh.p_rest = pl.w_rest * pl.inv_all;
                         }
                     }
                 }
@@ -1002,7 +1093,7 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
                 if (p.grad) {
                     const float c = w.good() ? w.factor(p, left,
                                                        G > 32 ? sh.p_rest
-                                                              : pl.w_rest * reciprocal(pl.w_sum + pl.w_rest)) : NAN;
+                                                              : pl.w_rest * pl.inv_all) : NAN;
                     const float2 c2 = make_float2(c, c);
                     const auto put = [&](int j, float2 (&y)[E / 2]) {
                         Pack<T, 16> v;
@@ -1022,10 +1113,16 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
                         }
                     }
                 }
-                if (leads) {
-                    if (!w.good()) invalid(p.status);      // NaN among them
+                if (leads && !w.good()) invalid(p.status); // NaN among them
+                if constexpr (G == 32) {
                     const float kl = w.loss(p, pl, outside, left);
                     if (lane == 0) p.row_loss[row] = w.good() ? kl : NAN;
+                } else {
+                    weighed = true;
+                    if (me == 0) {
+                        sh.kept.outside = outside;
+                        sh.kept.left = left;
+                    }
                 }
                 if (p.grad) {
                     Gr::sync();                            // behind the rest's stores
@@ -1044,6 +1141,18 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
         if (me == 0 && live[ring.stages]) {
             fence_proxy_async();
             staged(row + ring.stages * groups, st).fetch(&sh.bar[st]);
+        }
+        if constexpr (G > 32) {
+            // the loss by the last warp, while the first one looks at the next row's teacher (whose
+            // places take the place of these behind a barrier)
+            if (weighed && threadIdx.x >= TH - 32) {
+                sh.kept.get(pl);
+                pl.top = sh.top;
+                const float outside = sh.kept.outside, left = sh.kept.left;
+                const Whole w(p, outside, left, pl.top, sh.sum);
+                const float kl = w.loss(p, pl, outside, left);
+                if (lane == 0) p.row_loss[row] = w.good() ? kl : NAN;
+            }
         }
         live.advance(p.lat, row + groups, groups, rows);
         st = st + 1 == ring.stages ? 0 : st + 1;
@@ -1213,8 +1322,7 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
         if (__any_sync(kAll, counts))
             fetch_short(p.logits, row0, n, p.V, stage, bar, phase, polls, p.status);
         const ShortRow<T> r(stage, p.V);
-        float loss = 0.0f, c = 0.0f, inner = 0.0f, outside = -INFINITY, weight = 0.0f;
-        float t_top = -INFINITY, shift = 0.0f, top = -INFINITY;
+        float loss = 0.0f, outside = -INFINITY, t_top = -INFINITY, top = -INFINITY;
         bool some = false;
         if (counts) {
             bool bad = false;
@@ -1245,7 +1353,7 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
             some = t_top != -INFINITY || rest != -INFINITY;        // NaN counts
             const float above = rest == -INFINITY || t_top == -INFINITY
                                     ? rest : rest_above(p, rest, t_top);
-            shift = t_top == -INFINITY ? above : fmaxf(above, 0.0f);
+            const float shift = t_top == -INFINITY ? above : fmaxf(above, 0.0f);
             if (some) {
                 r.each([&](int i, T x) {
                     if (r.bits(i) != kTaken) outside = fmaxf(outside, to_f32(x));
@@ -1253,32 +1361,48 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
                 const Exponent f(outside == -INFINITY ? 0.0f : outside, p.scale, p.scale_low);
                 float left = 0.0f;
                 r.each([&](int i, T x) { left += r.bits(i) != kTaken ? f(to_f32(x)) : 0.0f; });
-                float sum = 0.0f, w_sum = 0.0f, w_log = 0.0f;
+                const auto weight = [&](int q) {           // of a place
+                    const float x = teacher_logit(p, first + q);
+                    return x == -INFINITY ? 0.0f : expf(over_tau(p, x - t_top) - shift);
+                };
+                const auto term = [&](float at) {
+                    return at == -INFINITY ? 0.0f : expf(over_tau(p, at - top));
+                };
+                float sum = 0.0f, w_sum = 0.0f;
                 for (int q = 0; q < p.k; ++q) {
                     const float at = ats[q * 32 + lane];
                     if (at == INFINITY) continue;
-                    const float log_e = over_tau(p, at - top);
-                    sum += at == -INFINITY ? 0.0f : expf(log_e);
-                    const float x = teacher_logit(p, first + q);
-                    if (x == -INFINITY) continue;
-                    const float log_w = over_tau(p, x - t_top) - shift, w = expf(log_w);
-                    w_sum += w;
-                    if (w != 0.0f) w_log += at == -INFINITY ? INFINITY : w * (log_w - log_e);
+                    sum += term(at);
+                    w_sum += weight(q);
                 }
                 const float log_w_rest = above - shift;
                 const float w_rest = rest == -INFINITY ? 0.0f : expf(log_w_rest);
                 const Whole w(p, outside, left, top, sum);
                 const bool good = fine && w.good();
                 bad |= !good;
-                const float all = w_sum + w_rest, ratio = logf(w.total / all);
-                float kl = w_sum == 0.0f ? 0.0f
-                                         : w_log + w_sum * (ratio - over_tau(p, top - w.base));
-                if (w_rest != 0.0f)
-                    kl += w_rest * (log_w_rest - over_tau(p, outside - w.base) + ratio - logf(left));
-                loss = good ? kl / all : NAN;
-                c = good ? w.factor(p, left, w_rest / all) : NAN;
-                inner = good ? w.inner / w.total : NAN;
-                weight = 1.0f / all;
+                const float all = w_sum + w_rest, inv_all = rounded_reciprocal(all);
+                const float ratio = logf(w.total * inv_all);
+                loss = divergence(p, w.class_of_rest(p, w_rest, log_w_rest, outside, left, ratio, logf(left),
+                                                     inv_all));
+                if (p.grad) {
+                    const float c = good ? w.factor(p, left, w_rest * inv_all) : NAN;
+                    r.each([&](int i, T x) {
+                        if (r.bits(i) != kTaken || c != c) r.s[i] = from_f32<T>(f(to_f32(x)) * c);
+                    });
+                }
+                for (int q = 0; q < p.k; ++q) {
+                    const float at = ats[q * 32 + lane];
+                    if (at == INFINITY) continue;
+                    const float e = term(at), wq = weight(q);
+                    const float gap = at == -INFINITY
+                                          ? INFINITY
+                                          : fminf((teacher_logit(p, first + q) - t_top) - (at - top), kMost);
+                    loss += divergence(p, w.class_of_place(p, wq, e, gap, top, shift, ratio, inv_all));
+                    if (p.grad)
+                        r.s[p.ids[first + q]] = from_f32<T>(
+                            good ? (e * (w.inner * w.inv_total) - wq * inv_all) * p.grad_scale : NAN);
+                }
+                if (!good) loss = NAN;
             }
             if (bad) invalid(p.status);
         }
@@ -1287,23 +1411,8 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
             __syncwarp();
             continue;
         }
-        if (lane < n && some) {
-            const Exponent f(outside == -INFINITY ? 0.0f : outside, p.scale, p.scale_low);
-            r.each([&](int i, T x) {
-                if (r.bits(i) != kTaken || c != c) r.s[i] = from_f32<T>(f(to_f32(x)) * c);
-            });
-            for (int q = 0; q < p.k; ++q) {
-                const float at = ats[q * 32 + lane];
-                if (at == INFINITY) continue;
-                const float x = teacher_logit(p, first + q);
-                const float prob = x == -INFINITY
-                                       ? 0.0f : expf(over_tau(p, x - t_top) - shift) * weight;
-                const float e = at == -INFINITY ? 0.0f : expf(over_tau(p, at - top));
-                r.s[p.ids[first + q]] = from_f32<T>((e * inner - prob) * p.grad_scale);
-            }
-        } else if (lane < n) {
+        if (lane < n && !some)
             for (int i = 0; i < p.V; ++i) r.s[i] = from_f32<T>(0.0f);
-        }
         fence_proxy_async();
         __syncwarp();
         T* const y = reinterpret_cast<T*>(p.grad) + row0 * p.V;
@@ -1449,10 +1558,6 @@ bool lattice_ok(const Lattice& lat) {
 // Bytes of `n` rows of `each` elements of `size`, or -1 beyond what an address holds.
 int64_t bytes_of(int64_t n, int64_t each, int size) {
     return n <= (INT64_MAX >> 8) / each / size ? n * each * size : -1;
-}
-void in_two_parts(double x, float& hi, float& lo) {
-    hi = (float)x;
-    lo = (float)(x - (double)hi);
 }
 bool temperature_ok(double tau) { return tau >= 1e-4 && tau <= 1e4; }
 dim3 row_grid(int64_t rows) { return dim3((unsigned)std::min<int64_t>(rows, kMostRows)); }
@@ -1630,7 +1735,7 @@ extern "C" rnnt_status_t rnnt_top_logits(const void* logits, rnnt_dtype_t dt, in
     p.V = V;
     p.k = k;
     parts_below(kLog2e / temperature, p.scale, p.scale_low);
-    in_two_parts(1.0 / temperature, p.inv_tau, p.inv_tau_low);
+    parts_below(1.0 / temperature, p.inv_tau, p.inv_tau_low);
     p.values = values;
     p.ids = ids;
     p.rest = rest;
@@ -1719,10 +1824,11 @@ extern "C" rnnt_status_t rnnt_distill_loss(
     p.V = V;
     p.k = k;
     parts_below(kLog2e / temperature, p.scale, p.scale_low);
-    in_two_parts(1.0 / temperature, p.inv_tau, p.inv_tau_low);
+    parts_below(1.0 / temperature, p.inv_tau, p.inv_tau_low);
     p.mean = reduction == RNNT_RED_MEAN;
     p.grad_scale = (float)(temperature * weight / (p.mean ? B : 1));
-    p.loss_scale = temperature * temperature * weight;
+    p.tau = (float)temperature;
+    p.loss_scale = temperature * temperature * weight / p.tau;
     p.grad = static_cast<char*>(grad);
     p.row_loss = reinterpret_cast<float*>(ws + L.row_loss);
     p.part_loss = reinterpret_cast<double*>(ws + L.part_loss);

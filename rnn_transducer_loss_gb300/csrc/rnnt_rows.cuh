@@ -69,6 +69,10 @@ __device__ __forceinline__ float reciprocal(float x) {          // to one step
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float rounded_reciprocal(float x) {  // of x >= 1: a Newton step more
+    const float r = reciprocal(x);
+    return __fmaf_rn(r, __fmaf_rn(-x, r, 1.0f), r);
+}
 __device__ __forceinline__ float warp_max_nan(float x) {
     float y;
     asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));

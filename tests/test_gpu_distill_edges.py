@@ -105,7 +105,7 @@ def test_rest_is_rounded_once(V, tau):
     assert (np.abs(L.f64(rest) - want) <= step / 2 + R.SUM + R.EXPONENT * far + 4 * L.U32 * far).all()
 
 
-@pytest.mark.parametrize("V,k", [(29, 8), (1024, 64)])
+@pytest.mark.parametrize("V,k", [(29, 8), (1024, 64), (5000, 32)])
 def test_inexact_temperatures(V, k):
     """A reciprocal of the temperature that is off shifts all rows' exponents the same way, which adds
     up over rows: the sum of many is off by half a step of its own and at most as much again."""
@@ -136,3 +136,51 @@ def test_far_teachers(V):
         got, want = (rnnt_distill_loss(x, t, ids, T, U, rest, temperature=0.1, reduction="none") for t in (far, near))
         assert torch.equal(got, want)
         assert torch.equal(*(torch.autograd.grad(y.sum(), x)[0] for y in (got, want)))
+
+
+@pytest.mark.parametrize("V,k,tau", [(29, 8, 4.0), (1024, 8, 2.0), (1024, 8, 8.0), (5000, 32, 3.0), (60000, 64, 3.0)])
+def test_small_divergences(V, k, tau):
+    """Teachers next to their students, where the divergence is small beside the logarithms it is made of.
+    Off by: half a step of the sum; two roundings of each row's parts; and 3e-8 of the rest's logarithm,
+    which is what ex2's mean error may leave of it and which counts |p_r - q_r| times a row."""
+    N = 2000 if V > 10000 else 20000
+    x = torch.randn(N, V, device="cuda", generator=gen(V)) * 2
+    values, ids, rest = rnnt_top_logits(x + torch.randn(N, V, device="cuda", generator=gen(V + 1)), k, temperature=tau)
+    loss = rnnt_distill_loss(x, values, ids, i32([N]), i32([0]), rest, temperature=tau, reduction="sum")
+    want = apart = 0.0
+    for at in torch.arange(N, device="cuda").split(1000):
+        log_q = torch.log_softmax(x[at].double() / tau, 1)
+        goal = torch.cat([values[at].double() / tau, rest[at, None].double()], 1)
+        mine = log_q.gather(1, ids[at].long())
+        left = torch.logsumexp(log_q.scatter(1, ids[at].long(), -float("inf")), 1, keepdim=True)
+        log_p = torch.log_softmax(goal, 1)
+        want += (log_p.exp() * (log_p - torch.cat([mine, left], 1))).sum().item()
+        apart += (log_p[:, -1].exp() - left[:, 0].exp()).abs().sum().item()
+    assert abs(loss.item() / tau ** 2 - want) <= 3 * L.U32 * want + 3e-8 * apart
+
+
+@pytest.mark.parametrize("V", [29, 200, 1024, 5000, 70000])
+def test_lowest_logits_of_a_student(V):
+    """A teacher's output that the student rules out by the type's lowest value, over a temperature below 1:
+    a large divergence that float32 holds, and a finite gradient."""
+    tau, least = 0.7, torch.finfo(torch.float32).min
+    x = torch.randn(2, V, device="cuda", generator=gen(V))
+    values, ids = torch.tensor([[1.0, 0.5]] * 2, device="cuda"), i32([[2, 4]] * 2)
+    x[:, 4] = least
+    x.requires_grad_()
+    for rest in (None, torch.zeros(2, device="cuda")):
+        loss = rnnt_distill_loss(x, values, ids, i32([1, 1]), i32([0, 0]), rest, temperature=tau, weight=0.25,
+                                 reduction="none")
+        goal = np.array([1.0 / tau, 0.5 / tau] + ([0.0] if rest is not None else []))
+        p = np.exp(goal - np.log(np.exp(goal).sum()))
+        want = 0.25 * tau * p[1] * -least
+        assert (np.abs(L.f64(loss) - want) <= 8 * L.U32 * want).all()
+        grad, = torch.autograd.grad(loss.sum(), x)
+        assert torch.isfinite(grad).all() and (grad[:, 4] < 0).all()
+    # the outputs without a place ruled out, which the teacher's rest has
+    y = torch.full((1, V), least, device="cuda")
+    y[0, 2], y[0, 4] = 0.0, 1.0
+    loss = rnnt_distill_loss(y, values[:1], ids[:1], i32([1]), i32([0]), torch.zeros(1, device="cuda"),
+                             temperature=tau, weight=0.25)
+    want = 0.25 * tau * p[2] * -least
+    assert abs(loss.item() - want) <= 8 * L.U32 * want
