@@ -278,10 +278,10 @@ inline void parts_below(double c, float& hi, float& lo) {
     if ((double)hi >= c) hi = std::nextafter(hi, 0.0f);
     lo = (float)(c - (double)hi);
 }
-// ex2.approx comes out low on average: by 2e-8 for exponents above -1, by 5e-8 below (measured over 2^20
-// of them an order).  kLow, in the exponent, makes up for 3e-8, which leaves logarithms of sums off
-// by 1e-8 on average, for rows of normal logits at temperatures of 1 to 4.
-constexpr float kLow = 4.4e-8f;
+// ex2.approx comes out low on average: over all float32 of a binary order by 2.2e-8 for exponents above
+// -1 and by 4.9e-8 to 5.2e-8 in every order below.  kLow, in the exponent, makes up for 2.2e-8: logarithms
+// of sums are then off by -2e-8 (exponents below -1) to 3e-8 (all above -1) on average, logf included.
+constexpr float kLow = 3.2e-8f;
 struct Exponent {
     float2 ref, hi, lo;                    // -ref, c
     __device__ __forceinline__ Exponent(float at, float h, float l)

@@ -184,3 +184,18 @@ def test_lowest_logits_of_a_student(V):
                              temperature=tau, weight=0.25)
     want = 0.25 * tau * p[2] * -least
     assert abs(loss.item() - want) <= 8 * L.U32 * want
+
+
+@pytest.mark.parametrize("V", [29, 512, 5000])
+def test_mean_of_rests(V):
+    """Logarithms of sums over many rows, flat ones and peaked ones: what of their errors points one way is
+    below half a step of float32 at 1.  (Sums of about 1, so that the results' own rounding is not seen.)"""
+    u = torch.rand(6000, V, device="cuda", generator=gen(V), dtype=torch.float64)
+    z = torch.randn(6000, V, device="cuda", generator=gen(V), dtype=torch.float64)
+    for x in (-0.69 * u, -0.7 - 6 * u, u.clamp_min(1e-9).log(), 2 * z):
+        x[:, :2] = x.amax(1, keepdim=True)
+        x = (x - torch.logsumexp(x, 1, keepdim=True)).float()
+        rest = rnnt_top_logits(x, 1)[2].double()
+        y = x.double().scatter(1, x.argmax(1, keepdim=True), -float("inf"))
+        err = rest - torch.logsumexp(y, 1)
+        assert err.mean().abs() <= L.U32 + 5 * err.std() / 6000 ** 0.5
