@@ -53,3 +53,27 @@ def finish(where, status, wanted):
         raise ValueError(f"{where}: {N.status_string(code)} (wanted: {wanted})")
     if code != N.RNNT_OK:
         raise N.RNNTError(code, where)
+
+
+class _NoGradient(torch.autograd.Function):
+    """Outputs of an operator without derivatives, so that a backward pass through them raises (and a
+    tangent of the inputs does at once) instead of being dropped."""
+
+    @staticmethod
+    def forward(ctx, where, inputs, *outputs):
+        ctx.where = where
+        ctx.mark_non_differentiable(*(t for t in outputs if not t.is_floating_point()))
+        return outputs
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.where} is not differentiable: detach its inputs, or call it under "
+                           "torch.no_grad()")
+
+
+def without_gradient(where, inputs, outputs):
+    """The outputs, of which autograd knows that they depend on `inputs` where it has to."""
+    for t in inputs:
+        if differentiated(t):
+            outputs = _NoGradient.apply(where, t, *outputs)
+    return outputs

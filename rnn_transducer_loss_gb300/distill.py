@@ -12,7 +12,7 @@ import torch
 
 from . import _native as N
 from ._host import DTYPES as _DT
-from ._host import call, differentiated, finish, int32, status_word
+from ._host import call, differentiated, finish, int32, status_word, without_gradient
 
 _F32, _I32 = torch.float32, torch.int32
 
@@ -61,8 +61,14 @@ def rnnt_top_logits(logits: torch.Tensor, k: int, logit_lengths: torch.Tensor | 
     lengths leave rows outside their sequence unused, and empty.  ``check``
     reads the device status word (one synchronisation) and raises on rows that hold
     NaN or +inf and on lengths outside the tensor; without it such a row is empty and such
-    a length the nearer bound.  Not differentiable.
+    a length the nearer bound.  Not differentiable: a backward pass through the results raises, and
+    so does a forward-mode derivative.
     """
+    return without_gradient("rnnt_top_logits", (logits,),
+                            _top_logits(logits, k, logit_lengths, target_lengths, temperature, check))
+
+
+def _top_logits(logits, k, logit_lengths, target_lengths, temperature, check):
     dt = _logits("logits", logits)
     device, V = logits.device, logits.shape[-1]
     k = int(k)

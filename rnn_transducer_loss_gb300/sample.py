@@ -6,7 +6,7 @@ import torch
 
 from . import _native as N
 from ._host import DTYPES as _DT
-from ._host import call, finish, status_word
+from ._host import call, finish, status_word, without_gradient
 
 _F32, _I32 = torch.float32, torch.int32
 
@@ -33,8 +33,15 @@ def rnnt_sample(logits: torch.Tensor, scores: torch.Tensor, random: torch.Tensor
     score -inf and token -1.  ``check`` reads the device status word (one
     synchronisation) and raises on scores or logits that are NaN or +inf and on random
     numbers outside [0, 1); without it such a hypothesis gets score -inf and token -1.
-    Not differentiable.
+    Not differentiable: a backward pass through the scores raises, and so does a forward-mode
+    derivative.
     """
+    return without_gradient("rnnt_sample", (logits, scores),
+                            _sample(logits, scores, random, temperature, top_k, top_p, min_p, finished,
+                                    fused_log_softmax, check))
+
+
+def _sample(logits, scores, random, temperature, top_k, top_p, min_p, finished, fused_log_softmax, check):
     dt = _DT.get(logits.dtype)
     device = logits.device
     if device.type != "cuda":
