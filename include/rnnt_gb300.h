@@ -589,7 +589,8 @@ rnnt_status_t rnnt_distill_loss(const void *logits, rnnt_dtype_t dt, int64_t row
 /*
  * rnnt_distill_grad_scale -- multiplies a gradient of rnnt_distill_loss in place by upstream
  * factors: factors[0], or with per_sample != 0 factors[b] for sample b's rows.  A
- * factor of 1 leaves its rows as they are.
+ * factor of 1 leaves its rows as they are.  The gradient has been rounded to its type
+ * before: a factor that is known ahead (a gradient scaler's) belongs into the weight.
  *
  *   rows_each      rows of a sample of the padded layout, max_T * (max_U + 1); 0 for the
  *                  compact one.

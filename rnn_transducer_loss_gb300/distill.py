@@ -220,9 +220,14 @@ def rnnt_distill_loss(logits: torch.Tensor, teacher_logits: torch.Tensor,
     both.  A row whose teacher holds nothing adds nothing.  Returns float32
     per-sample sums (reduction="none") or their float32 sum or mean.
 
-    The gradient is computed with the loss; backward multiplies it in place by the
-    upstream gradient (nothing to do where that is 1: give the term's ``weight`` here), so
-    it runs once per call.  ``check`` reads the device status word (one
+    The gradient is computed with the loss, in the type of ``logits``; backward multiplies
+    it in place by the upstream gradient (nothing to do where that is 1: give the term's
+    ``weight`` here), so it runs once per call.  A float16 gradient has then been rounded
+    before a gradient scaler's factor: what the scaler is there to save may be 0 already, and
+    the second pass reads and writes the whole gradient.  With a scaler, its scale belongs
+    into the weight and the term behind the scaler:
+    ``scaler.scale(loss) + rnnt_distill_loss(..., weight=w * scaler.get_scale())``.
+    ``check`` reads the device status word (one
     synchronisation) and raises on lengths that do not fit, ids at or above V or twice in a
     row, and NaN or +inf; without it such an id's place counts as empty.  A step is captured
     into a CUDA graph with ``check=False`` and with no eager graph of the same leaf alive.

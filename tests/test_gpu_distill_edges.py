@@ -199,3 +199,24 @@ def test_mean_of_rests(V):
         y = x.double().scatter(1, x.argmax(1, keepdim=True), -float("inf"))
         err = rest - torch.logsumexp(y, 1)
         assert err.mean().abs() <= L.U32 + 5 * err.std() / 6000 ** 0.5
+
+
+@pytest.mark.parametrize("V", [29, 1024, 5000])
+def test_gradient_scaler(V):
+    """float16 gradients that are too small for the type survive with the scaler's scale in the weight: off
+    by half a step of the scaled values, where scaling behind the call finds zeros."""
+    N, scale, weight = 500, 65536.0, 1e-7
+    owner, live = np.zeros(N, dtype=np.int64), np.ones(N, dtype=bool)
+    x = (torch.randn(N, V, device="cuda", generator=gen(V)) * 2).half()
+    values, ids, rest = D.make_teacher(x, 8, 2.0, "plain", 5)
+    scaler = torch.amp.GradScaler("cuda", init_scale=scale)
+    leaf = x.clone().requires_grad_()
+    main = torch.zeros(3, device="cuda", requires_grad=True).sum()
+    T, U = i32([N]), i32([0])
+    loss = scaler.scale(main) + rnnt_distill_loss(leaf, values, ids, T, U, rest, 2.0, weight * scaler.get_scale())
+    loss.backward()
+    want = D.expected(x, values, ids, rest, 2.0, owner, live, 1, weight * scale, "mean")
+    D.check_distill(leaf, loss, leaf.grad, want, torch.float16)
+    late = x.clone().requires_grad_()
+    (rnnt_distill_loss(late, values, ids, T, U, rest, 2.0, weight) * scale).backward()
+    assert ((late.grad == 0) & (leaf.grad != 0)).any() and (leaf.grad[late.grad != 0] != 0).all()
