@@ -320,9 +320,11 @@ struct TopScratch {
     int count;
 };
 
-// The c-th largest of the warp's values.
+// The c-th largest of the warp's values: one by one, or sorted, which costs the same for c = 7 or so
+// (100000 rows of 1024 float16: c = 5 84 us and 86, c = 9 93 and 90, c = 12 100 and 93, c = 21 133
+// and 116).
 __device__ __forceinline__ float warp_cth(float x, int c) {
-    if (c > 12) return __shfl_sync(kAll, warp_sorted(x), c - 1);
+    if (c > 7) return __shfl_sync(kAll, warp_sorted(x), c - 1);
     for (int n = 0;;) {
         const float m = warp_max(x);
         n += __popc(__ballot_sync(kAll, x == m));
@@ -1169,7 +1171,7 @@ struct ShortBatch {
     int32_t stage_bytes, warp_bytes;       // of a warp: the rows; with what is behind them
 };
 constexpr int kShortThreads = 128;
-constexpr int kShortRow = 512;             // bytes of a row, at most
+constexpr int kShortRow = 512;             // bytes of a row, at most: 16 KB a warp
 
 // A thread's row in shared memory.  Its elements are gone through from `start` on, which turns with
 // the thread so that a warp's accesses lie in different banks where V is even.
@@ -1744,7 +1746,12 @@ extern "C" rnnt_status_t rnnt_top_logits(const void* logits, rnnt_dtype_t dt, in
     if (!distill_prepared() || !clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
     with_type(dt, [&](auto t) {
         using T = decltype(t);
-        // the best are taken one by one, in k + 1 looks at the row
+        // the best are taken one by one, in k + 1 looks at the row.  172000 rows by a thread and by a warp
+        // each, us: float32 V = 29, k = 8 20 and 174; 64, 4 100 and 107; 64, 8 158 and 127; 96, 16 298 and 163;
+        // 128, 1 73 and 95; 128, 16 (a warp's from here on) 417 and 155; float16 48, 16 132 and 220; 80, 16
+        // 179 and 312; 96, 4 97 and 115; 128, 8 269 and 132; 256, 8 (a warp's) 341 and 125.  A warp is slow
+        // where a row has fewer vectors than k + 1, a thread where V is a power of 2; over 60 pairs of
+        // V and k up to the border the rule's choice took 8 % more than the better one.
         if (short_rows(logits, V, es) && (k + 1) * V <= 2048) {
             const ShortBatch sb = short_batch(V, es, (size_t)256 * k);
             const size_t shared = (size_t)sb.warp_bytes * (kShortThreads / 32);
@@ -1842,7 +1849,12 @@ extern "C" rnnt_status_t rnnt_distill_loss(
     if (!distill_prepared() || !clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
     with_type(dt, [&](auto t) {
         using T = decltype(t);
-        if (short_rows(logits, V, es)) {
+        // A thread looks at its row four times and at every place three times; a warp takes about as long
+        // for any row up to 512 bytes.  172000 rows with their gradient, a thread and a warp each, us: float32
+        // V = 29, k = 8 42 and 142; 33, 16 90 and 142; 33, 32 244 and 142; 64, 8 105 and 122; 80, 16 146
+        // and 123; 96, 8 127 and 123; 96, 16 145 and 123; 128, 4 120 and 122; 64, 64 405 and 143; float16 96,
+        // 8 105 and 130; 128, 4 150 and 130.
+        if (short_rows(logits, V, es) && V + 4 * k <= 144) {
             const ShortBatch sb = short_batch(V, es, (size_t)128 * k);
             const size_t shared = (size_t)sb.warp_bytes * (kShortThreads / 32);
             k_distill_short<T>

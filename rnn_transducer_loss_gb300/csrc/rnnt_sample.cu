@@ -909,6 +909,11 @@ template <typename T>
 void launch_sample(const SampleParams& p, cudaStream_t st) {
     const unsigned rows = (unsigned)(p.B * p.K);
     const size_t bytes = ((size_t)p.V * sizeof(T) + 30) / 16 * 16;         // at any alignment
+    // Fewer threads have shorter chains of barriers, more read a row sooner.  float16, us of unfiltered draws /
+    // top_k 40 / top_p 0.9, of 4 and of 1024 rows, by 128, 256 and 512 threads:
+    //   4000 bytes   7/10/15 and 16/19/27   7/10/14 and 17/27/35   8/12/14 and 32/47/61
+    //   8000         8/13/19 and 21/23/42   7/12/16 and 23/31/49   8/13/15 and 33/55/73
+    //  32000         12/18/47 and 48/45/146  10/16/54 and 45/43/131  10/16/25 and 53/69/138
     if (bytes <= 4 << 10) k_sample<T, 128, true><<<rows, 128, bytes, st>>>(p);
     else if (bytes <= 32 << 10) k_sample<T, 256, true><<<rows, 256, bytes, st>>>(p);
     else if (bytes <= kHere) k_sample<T, 512, true><<<rows, 512, bytes, st>>>(p);

@@ -220,3 +220,30 @@ def test_gradient_scaler(V):
     late = x.clone().requires_grad_()
     (rnnt_distill_loss(late, values, ids, T, U, rest, 2.0, weight) * scale).backward()
     assert ((late.grad == 0) & (leaf.grad != 0)).any() and (leaf.grad[late.grad != 0] != 0).all()
+
+
+@pytest.mark.parametrize("padded", [False, True], ids=["compact", "padded"])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("V", [1, 2, 3, 5, 7, 17, 40, 64, 100, 128])
+def test_short_rows_with_many_places(V, dtype, padded):
+    """Few outputs and up to 64 places, empty ones among them: rows that share 16-byte units."""
+    T, U, tau = [9, 0, 14], [2, 1, 0], 2.0
+    owner, live = R.rows_of(T, U, padded)
+    for k in (20, 33, 64):
+        x = (torch.randn(len(owner), V, device="cuda", generator=gen(k)) * 2).to(DT[dtype])
+        values = torch.randn(len(owner), k, device="cuda", generator=gen(k + 1))
+        order = torch.rand(len(owner), max(V, k), device="cuda", generator=gen(k + 2)).argsort(1).int()[:, :k]
+        ids = torch.where(order < V, order, -1).contiguous()
+        rest = torch.randn(len(owner), device="cuda", generator=gen(k + 3))
+        if V <= k:
+            rest = rest * 0 - float("inf")              # no output is without a place
+        want = D.expected(x, values, ids, rest, tau, owner, live, 3, 1.0, "sum")
+        lead = (3, max(T), max(U) + 1) if padded else (len(owner),)
+        if padded:
+            x[torch.as_tensor(~live, device="cuda")] = float("nan")
+        leaf = x.view(*lead, V).clone().requires_grad_()
+        loss = rnnt_distill_loss(leaf, values.view(*lead, k), ids.view(*lead, k), i32(T), i32(U), rest.view(lead),
+                                 temperature=tau, reduction="sum")
+        grad, = torch.autograd.grad(loss, leaf)
+        D.check_distill(leaf, loss, grad, want, DT[dtype])
+        assert (grad.reshape(-1, V)[torch.as_tensor(~live, device="cuda")] == 0).all()
