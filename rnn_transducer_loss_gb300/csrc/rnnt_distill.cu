@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(TH, 5) k_top(const TopParams p, const Ring rin
                         sum += terms_of(x.at(j), f, e);
                     }
                     sum = Gr::sum(sum, sh.space);
-                    rest = rest_of(p, sum, first);
+                    if (G == 32 || me < 32) rest = rest_of(p, sum, first);         // thread 0 stores it
                 }
             }
         }
