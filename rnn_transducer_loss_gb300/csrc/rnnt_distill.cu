@@ -711,8 +711,10 @@ struct Whole {
     __device__ __forceinline__ Whole(const DistillParams& a, float outside, float left, float top,
                                      float sum) {
         base = max_nan(outside, top);
-        outer = outside == -INFINITY ? 0.0f : expf(over_tau(a, outside - base));
-        inner = top == -INFINITY ? 0.0f : expf(over_tau(a, top - base));
+        const bool out = outside >= top;                   // one of the two is 1
+        const float other = expf(over_tau(a, (out ? top : outside) - base));
+        outer = out ? 1.0f : other;
+        inner = out ? other : 1.0f;
         total = left * outer + sum * inner;
         inv_total = rounded_reciprocal(total);
     }
