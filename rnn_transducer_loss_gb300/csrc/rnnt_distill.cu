@@ -573,20 +573,17 @@ __device__ __forceinline__ float rest_above(const DistillParams& p, float rest, 
 // Every class's part is positive, and an error of x counts p - q times only: the sum of p x would lose
 // a small divergence among its rounded logarithms, and keep what of their errors points one way.
 // d: x times tau, but for what is small beside 1e30, where x may leave float32; +inf where q is 0.
-struct Class {
-    float w, p, q, x, d;                   // w: p times W
-};
-__device__ __forceinline__ float divergence(const DistillParams& a, const Class& c) {
-    const float x = c.x;
+__device__ __forceinline__ float divergence(const DistillParams& a, float w, float p, float q, float x,
+                                            float d) {
     float y = __fmaf_rn(x, 1.0f / 40320.0f, -1.0f / 5040.0f);          // the series, to 3e-8 of the value
     y = __fmaf_rn(x, y, 1.0f / 720.0f);
     y = __fmaf_rn(x, y, -1.0f / 120.0f);
     y = __fmaf_rn(x, y, 1.0f / 24.0f);
     y = __fmaf_rn(x, y, -1.0f / 6.0f);
     y = __fmaf_rn(x, y, 0.5f);
-    y = a.tau * (fabsf(x) <= 0.5f ? c.p * (x * x * y) : __fmaf_rn(c.p, x - 1.0f, c.q));
-    if (c.d > 1e30f) y = c.d == INFINITY ? c.d : c.p * c.d;
-    return c.w == 0.0f ? a.tau * c.q : y;                  // (p may be rounded to 0 before w is)
+    y = a.tau * (fabsf(x) <= 0.5f ? p * (x * x * y) : __fmaf_rn(p, x - 1.0f, q));
+    if (d > 1e30f) y = d == INFINITY ? d : p * d;
+    return w == 0.0f ? a.tau * q : y;                      // (p may be rounded to 0 before w is)
 }
 
 // Which of the warp's ids (of places 0 to 31, and 32 to 63) stand in a place before theirs: bits 0, 1.
@@ -691,7 +688,7 @@ struct Places {
             const float t = te.t[q] - t_top, x = at[q] - top;
             w[q] = te.t[q] == -INFINITY ? 0.0f : expf(over_tau(a, t) - shift);
             e[q] = at[q] == -INFINITY ? 0.0f : expf(over_tau(a, x));
-            gap[q] = at[q] == -INFINITY ? INFINITY : fminf(t - x, kMost);
+            gap[q] = at[q] == -INFINITY ? INFINITY : t - x;
             w_sum += w[q];
             sum += e[q];
         }
@@ -726,20 +723,24 @@ struct Whole {
         if (a.rest && left > 0.0f) c -= p_rest * reciprocal(left);
         return c * a.grad_scale;
     }
-    // Classes of the divergence: a place's, and that of all outputs without one.  log_ratio: of total / W.
-    __device__ __forceinline__ Class class_of_place(const DistillParams& a, float w, float e, float gap,
-                                                    float top, float shift, float log_ratio,
-                                                    float inv_all) const {
-        const float d = gap == INFINITY ? gap : fminf(gap + (base - top), kMost);
-        // (a sum with the low part first would round it away, in all rows the same way)
-        return {w, w * inv_all, e * (inner * inv_total), over_tau(a, d) + (log_ratio - shift), d};
+    // Classes of the divergence: a place's, and that of all outputs without one.  With the sums' logarithms
+    // log_ratio (of total / W) and log_left a class has w, e, q = e * unit and
+    // log p - log q = d / tau + offset.
+    struct Part {
+        float w, e, unit, d, offset;
+    };
+    __device__ __forceinline__ Part part_of_place(float w, float e, float gap, float top, float shift,
+                                                  float log_ratio) const {
+        return {w, e, inner * inv_total, gap + (base - top), log_ratio - shift};
     }
-    __device__ __forceinline__ Class class_of_rest(const DistillParams& a, float w, float log_w,
-                                                   float outside, float left, float log_ratio,
-                                                   float log_left, float inv_all) const {
-        return {w, w * inv_all, left * outer * inv_total,
-                log_w - over_tau(a, outside - base) + (log_ratio - log_left),
-                left > 0.0f ? fminf(base - outside, kMost) : INFINITY};
+    __device__ __forceinline__ Part part_of_rest(float w, float log_w, float outside, float left,
+                                                 float log_ratio, float log_left) const {
+        return {w, left, outer * inv_total, left > 0.0f ? base - outside : INFINITY,
+                log_w + (log_ratio - log_left)};
+    }
+    __device__ __forceinline__ float divergence_of(const DistillParams& a, const Part& c,
+                                                   float inv_all) const {
+        return divergence(a, c.w, c.w * inv_all, c.e * c.unit, over_tau(a, c.d) + c.offset, c.d);
     }
     // tau times the row's divergence, of the warp's sums (the same in all lanes).
     template <int P>
@@ -748,16 +749,15 @@ struct Whole {
         const int lane = threadIdx.x & 31;
         const float mine = logf((lane & 1) ? left : total * pl.inv_all);   // the two logarithms by two lanes
         const float ratio = __shfl_sync(kAll, mine, 0), log_left = __shfl_sync(kAll, mine, 1);
-        const Class rest = class_of_rest(a, pl.w_rest, pl.log_w_rest, outside, left, ratio, log_left,
-                                         pl.inv_all);
+        const Part rest = part_of_rest(pl.w_rest, pl.log_w_rest, outside, left, ratio, log_left);
         const bool spare = a.k < 32 * P;                   // a lane without a place takes the rest
-        float sum = spare || lane ? 0.0f : divergence(a, rest);
+        float sum = 0.0f;
+        if (!spare && lane == 0) sum = divergence_of(a, rest, pl.inv_all);
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            Class c = class_of_place(a, pl.w[q], pl.e[q], pl.gap[q], pl.top, pl.shift, ratio,
-                                     pl.inv_all);
+            Part c = part_of_place(pl.w[q], pl.e[q], pl.gap[q], pl.top, pl.shift, ratio);
             if (lane + 32 * q == a.k) c = rest;
-            sum += divergence(a, c);
+            sum += divergence_of(a, c, pl.inv_all);
         }
         return warp_sum(sum);
     }
@@ -1386,8 +1386,8 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
                 bad |= !good;
                 const float all = w_sum + w_rest, inv_all = rounded_reciprocal(all);
                 const float ratio = logf(w.total * inv_all);
-                loss = divergence(p, w.class_of_rest(p, w_rest, log_w_rest, outside, left, ratio, logf(left),
-                                                     inv_all));
+                loss = w.divergence_of(
+                    p, w.part_of_rest(w_rest, log_w_rest, outside, left, ratio, logf(left)), inv_all);
                 if (p.grad) {
                     const float c = good ? w.factor(p, left, w_rest * inv_all) : NAN;
                     r.each([&](int i, T x) {
@@ -1400,8 +1400,8 @@ __global__ void __launch_bounds__(kShortThreads) k_distill_short(const DistillPa
                     const float e = term(at), wq = weight(q);
                     const float gap = at == -INFINITY
                                           ? INFINITY
-                                          : fminf((teacher_logit(p, first + q) - t_top) - (at - top), kMost);
-                    loss += divergence(p, w.class_of_place(p, wq, e, gap, top, shift, ratio, inv_all));
+                                          : (teacher_logit(p, first + q) - t_top) - (at - top);
+                    loss += w.divergence_of(p, w.part_of_place(wq, e, gap, top, shift, ratio), inv_all);
                     if (p.grad)
                         r.s[p.ids[first + q]] = from_f32<T>(
                             good ? (e * (w.inner * w.inv_total) - wq * inv_all) * p.grad_scale : NAN);
