@@ -1851,12 +1851,17 @@ extern "C" rnnt_status_t rnnt_distill_loss(
     if (!distill_prepared() || !clear_status(status_dev, st)) return RNNT_LAUNCH_FAILED;
     with_type(dt, [&](auto t) {
         using T = decltype(t);
-        // A thread looks at its row four times and at every place three times; a warp takes about as long
-        // for any row up to 512 bytes.  172000 rows with their gradient, a thread and a warp each, us: float32
-        // V = 29, k = 8 42 and 142; 33, 16 90 and 142; 33, 32 244 and 142; 64, 8 105 and 122; 80, 16 146
-        // and 123; 96, 8 127 and 123; 96, 16 145 and 123; 128, 4 120 and 122; 64, 64 405 and 143; float16 96,
-        // 8 105 and 130; 128, 4 150 and 130.
-        if (short_rows(logits, V, es) && V + 4 * k <= 144) {
+        // A thread's time goes with its looks at the row and at the places, a warp's is nearly the same for any
+        // row up to 512 bytes, longer where rows are not whole units; V of a power of 2 costs a thread bank
+        // conflicts.  172000 rows, by a thread and by a warp each, us.  Loss alone: float32 V = 29, k = 4 27
+        // and 122; 64, 16 105 and 106; 128, 16 129 and 107; 33, 32 200 and 125; float16 128, 4 93 and 114;
+        // 205, 16 92 and 132; 256, 16 152 and 117; 184, 32 167 and 119.  With the gradient: float32 29, 8 42
+        // and 137; 96, 4 115 and 118; 64, 16 138 and 117; 33, 32 242 and 140; float16 160, 4 113 and 130;
+        // 192, 1 178 and 130; 205, 16 147 and 156; 251, 4 130 and 202; 256, 64 688 and 165.  Over 210 such
+        // pairs the choice took 1.6 % (loss alone) and 3 % more than the better one.  It is the same with and
+        // without a gradient, and so are the loss's bits.
+        const int most = (size_t)V * es % 16 ? 384 : 248;
+        if (short_rows(logits, V, es) && V + 8 * k <= most) {
             const ShortBatch sb = short_batch(V, es, (size_t)128 * k);
             const size_t shared = (size_t)sb.warp_bytes * (kShortThreads / 32);
             k_distill_short<T>
