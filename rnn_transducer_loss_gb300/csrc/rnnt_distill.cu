@@ -339,9 +339,9 @@ __device__ __forceinline__ float warp_cth(float x, int c) {
 // ranked by counting.  They are then taken out of the row, which leaves the rest: its largest
 // element (the k + 1-st best, if it reached the bound) and the sum relative to it.
 //
-// Issue slots bound it: 480000 rows of 1024 float16 with k = 8 take 420 us (2.4 TB/s; 840 warp
-// instructions a row, of which 200 touch elements, in 77 % of the slots), 226000 of 5000 float32 with
-// k = 32 1797 us (2.9 TB/s).  Rows of up to 4 KB by warps, longer ones by blocks: a warp has
+// Issue slots bound it: 480000 rows of 1024 float16 with k = 8 take 414 us (2.4 TB/s; 834 warp
+// instructions a row, of which 200 touch elements, in 76 % of the slots), 226000 of 5000 float32 with
+// k = 32 1766 us (3.0 TB/s).  Rows of up to 4 KB by warps, longer ones by blocks: a warp has
 // no barriers, but its ring of longer rows would leave an SM with few warps.
 template <typename T, int TH, int G, bool WHOLE>
 __global__ void __launch_bounds__(TH, 5) k_top(const TopParams p, const Ring ring) {
@@ -965,12 +965,12 @@ struct DistillScratch {
 // logits are picked out of the staged row and -inf is left in their stead, so that what the threads
 // then read is the rest alone; its terms stay in registers from their sum to the gradient (NV vectors
 // a thread; NV = 0: rows too long for that are read from the stage again).  A group's first warp
-// looks after the teacher.
+// looks after the teacher, a block's last one after the loss, while the first is at the next row.
 //
-// Long rows are bound by memory: 226000 of 5000 float32 with 32 places take 1.65 ms (6.3 TB/s, 0.93
-// of the copy's); rows of 1024 by issue slots: 480000 of float16 with 8 places 450 us (4.4 TB/s; 720
-// warp instructions a row, 220 of them on elements).  3 blocks an SM of 80 registers against 2 of 87:
-// 487 and 579 us.  Two stages a warp: more would cost blocks.
+// Long rows are bound by memory: 226000 of 5000 float32 with 32 places take 1.66 ms (6.3 TB/s, 0.93
+// of the copy's); rows of 1024 by issue slots: 480000 of float16 with 8 places 480 us (4.1 TB/s; 858
+// warp instructions a row, 220 of them on elements, in 68 % of the slots).  3 blocks an SM of 80 registers
+// against 2 of 87, at an earlier step: 487 and 579 us.  Two stages a warp: more would cost blocks.
 template <typename T, int TH, int G, int NV, int P, bool WHOLE>
 __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 || NV == 1 ? 4 : 3)
     k_distill(const DistillParams p, const Ring ring) {
@@ -1166,9 +1166,8 @@ __global__ void __launch_bounds__(TH, NV == 8 && sizeof(T) == 2 ? 2 : NV == 0 ||
 // ------------------------------------------------------------------ short rows
 // A warp takes 32 consecutive rows, which are one aligned piece of memory whatever V is, through its
 // part of shared memory (unless none of them counts), and a thread each of them: no reductions, no idle
-// lanes.  172000 rows of
-// 29 float32 with 8 places take 24 us with the gradient (a warp a row: 150); 1.7 TB/s, bound by
-// latency: a thread's looks at its row follow one another.
+// lanes.  172000 rows of 29 float32 with 8 places take 27 us with the gradient (a warp a row: 130); 1.9
+// TB/s, bound by latency: a thread's looks at its row follow one another.
 struct ShortBatch {
     int32_t stage_bytes, warp_bytes;       // of a warp: the rows; with what is behind them
 };

@@ -19,7 +19,7 @@ using namespace rnnt_rows;
 namespace {
 
 // ------------------------------------------------------------ pairs of floats
-// Their exact sum is the value: about 47 bits on float32 units, of which there are 64 times as many
+// (Knuth's sum of two, Dekker's where one is the larger.)  Their exact sum is the value: about 47 bits on float32 units, of which there are 64 times as many
 // as of float64 ones.  The compiler neither reorders nor contracts what is spelt with intrinsics.
 struct Pair { float h, l; };
 __device__ __forceinline__ Pair two_sum(float a, float b) {
@@ -212,9 +212,10 @@ struct Floor {
 
 // A draw by a block of TH threads; the row lies in shared memory (HERE) or is read from the cache.
 // Blocks of 128, 256 and 512 threads for rows of up to 4 KB, 32 KB and beyond.  Latency bounds short
-// rows (4 of 1024 float16 with top_k 40: 8.9 us, one chain of barriers); issue slots and barriers long
-// ones, of which two fit an SM: 1024 rows of 50000 bfloat16 take 100 us unfiltered, 145 with
-// top_p 0.9 and min_p 0.002, 66 where few elements are kept.
+// rows (4 of 1024 float16 with top_k 40: 9 us, one chain of barriers); issue slots and barriers long
+// ones, of which two fit an SM: 1024 rows of 50000 bfloat16 take 110 us unfiltered, 147 with
+// top_p 0.9 and min_p 0.002, 66 where few elements are kept.  What is seldom run is not inlined and gets a
+// copy of this object: 200 to 290 bytes of a thread's stack, in the L1, beside 64 to 80 registers.
 template <typename T, int TH, bool HERE>
 struct Draw {
     static constexpr int E = 16 / (int)sizeof(T), WARPS = TH / 32;
