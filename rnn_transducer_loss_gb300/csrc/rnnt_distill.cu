@@ -140,6 +140,7 @@ struct TopParams {
 // part of a product would be lost, in all rows the same way.
 __device__ __forceinline__ float sum_of(float a, float b, float c) {
     const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    if (!(fabsf(s) < INFINITY)) return s;
     return __fadd_rn(s, __fadd_rn(__fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)), c));
 }
 
@@ -560,12 +561,13 @@ __device__ __forceinline__ float teacher_logit(const DistillParams& p, int64_t a
 __device__ __forceinline__ float over_tau(const DistillParams& p, float d) {
     return __fmaf_rn(d, p.inv_tau, d * p.inv_tau_low);
 }
-// rest - logit / tau; logit / tau outside float32's range is the nearer end of it (as in a rest).
+// rest - logit / tau; logit / tau outside float32's range is the nearer end of it (as in a rest), and so is
+// a difference above it.
 __device__ __forceinline__ float rest_above(const DistillParams& p, float rest, float logit) {
-    const float hi = logit * p.inv_tau;
-    if (fabsf(hi) >= kMost) return rest - copysignf(kMost, hi);
+    const float hi = logit * p.inv_tau, far = rest - copysignf(kMost, hi);
     const float low = __fmaf_rn(logit, p.inv_tau_low, __fmaf_rn(logit, p.inv_tau, -hi));
-    return sum_of(rest, -hi, -low);
+    const float d = fabsf(hi) >= kMost ? far : sum_of(rest, -hi, -low);
+    return rest < INFINITY ? fminf(d, kMost) : rest;
 }
 
 // tau times what a class adds to a row's divergence, for probabilities p of the teacher and q:

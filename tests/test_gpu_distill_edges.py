@@ -247,3 +247,19 @@ def test_short_rows_with_many_places(V, dtype, padded):
         grad, = torch.autograd.grad(loss, leaf)
         D.check_distill(leaf, loss, grad, want, DT[dtype])
         assert (grad.reshape(-1, V)[torch.as_tensor(~live, device="cuda")] == 0).all()
+
+
+@pytest.mark.parametrize("V", [29, 200, 1024, 5000, 70000])
+def test_rests_far_from_the_places(V):
+    """A rest and places at opposite ends of float32: one has all the weight, and the loss is that of it alone."""
+    x = torch.randn(4, V, device="cuda", generator=gen(6)).requires_grad_()
+    ids, T, U = i32([[3, 1]] * 4), i32([1] * 4), i32([0] * 4)
+    values = torch.tensor([[3e38, 3e38], [-3e38, -3e38], [3e38, -3e38], [-3e38, -float("inf")]], device="cuda")
+    rest = torch.tensor([-3e38, 3e38, -3.4e38, 3.4e38], device="cuda")
+    places = torch.tensor([[0.0, 0.0], [-float("inf")] * 2, [0.0, -float("inf")], [-float("inf")] * 2], device="cuda")
+    rests = torch.tensor([-float("inf"), 0.0, -float("inf"), 0.0], device="cuda")
+    for tau in (1.0, 0.1, 7.0):
+        got, want = (rnnt_distill_loss(x, v, ids, T, U, r, temperature=tau, reduction="none")
+                     for v, r in ((values, rest), (places, rests)))
+        assert torch.isfinite(got).all() and torch.equal(got, want)
+        assert torch.equal(*(torch.autograd.grad(y.sum(), x)[0] for y in (got, want)))
