@@ -19,8 +19,9 @@ using namespace rnnt_rows;
 namespace {
 
 // ------------------------------------------------------------ pairs of floats
-// (Knuth's sum of two, Dekker's where one is the larger.)  Their exact sum is the value: about 47 bits on float32 units, of which there are 64 times as many
-// as of float64 ones.  The compiler neither reorders nor contracts what is spelt with intrinsics.
+// Knuth's sum of two, Dekker's where one is the larger.  Their exact sum is the value: about 47 bits on
+// float32 units, of which there are 64 times as many as of float64 ones.  The compiler neither reorders nor
+// contracts what is spelt with intrinsics.
 struct Pair { float h, l; };
 __device__ __forceinline__ Pair two_sum(float a, float b) {
     const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
