@@ -263,3 +263,32 @@ def test_rests_far_from_the_places(V):
                      for v, r in ((values, rest), (places, rests)))
         assert torch.isfinite(got).all() and torch.equal(got, want)
         assert torch.equal(*(torch.autograd.grad(y.sum(), x)[0] for y in (got, want)))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_largest_vocabulary(dtype):
+    V, k = 1 << 20, 64
+    x = torch.randn(3, V, device="cuda", generator=gen(9)).to(DT[dtype])
+    top = rnnt_top_logits(x, k, temperature=2.0)
+    order = torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(top[1], order.int()) and torch.equal(top[0], x.gather(1, order))
+    y = x.double() / 2.0
+    want = torch.logsumexp(y.scatter(1, order, -float("inf")), 1)
+    assert (top[2].double() - want).abs().max() <= R.SUM * 20          # 1024 terms a thread instead of 256
+    student = (x.float() + torch.randn(3, V, device="cuda", generator=gen(10))).to(DT[dtype]).requires_grad_()
+    loss = rnnt_distill_loss(student, *top[:2], i32([2, 1]), i32([0, 0]), top[2], temperature=2.0, reduction="none")
+    grad, = torch.autograd.grad(loss.sum(), student)
+    log_q = torch.log_softmax(student.detach().double() / 2.0, 1)
+    log_p = torch.log_softmax(torch.cat([top[0].double() / 2.0, top[2].double()[:, None]], 1), 1)
+    left = torch.logsumexp(log_q.scatter(1, order, -float("inf")), 1, keepdim=True)
+    rows = 4.0 * (log_p.exp() * (log_p - torch.cat([log_q.gather(1, order), left], 1))).sum(1)
+    rows = torch.stack([rows[0] + rows[1], rows[2]])
+    # the rest's sum may be off by SUM * 20 of itself, which counts |p_r - q_r| times
+    apart = 4.0 * (log_p[:, -1].exp() - left[:, 0].exp()).abs().sum()
+    assert ((loss.double() - rows).abs() <= R.SUM * 20 * apart + 1e-6 * rows).all()
+    q = log_q.exp()
+    g = 2.0 * (q - q * (log_p[:, -1:] - left).exp()).scatter(1, order, 0.0)
+    g = g.scatter(1, order, 2.0 * (q.gather(1, order) - log_p[:, :k].exp()))
+    part = 2.0 * (q + q * (log_p[:, -1:] - left).exp()).scatter(1, order, 1.0)
+    limit = part * R.SUM * 20 + g.abs() * L.half_step(DT[dtype]) * 1.001 + L.smallest(DT[dtype])
+    assert ((grad.double() - g).abs() <= limit).all()

@@ -85,3 +85,17 @@ def test_top_p_beside_running_sums(values, V):
     for at in np.random.default_rng(V).integers(0, V - 1, size=4):
         for off in (-2e-8, -3e-9, 3e-9, 2e-8):
             check(x, [MOST, 0.5], top_p=sums[at] / sums[-1] + off)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_largest_vocabulary(dtype):
+    V = 1 << 20
+    x = torch.randn(V, generator=torch.Generator().manual_seed(3)) * 2
+    x = x.to(dtype)
+    for kw in (dict(), dict(top_p=0.9), dict(tau=0.5, top_p=0.99)):
+        check(x, [0.0, 0.3, 0.77, MOST], **kw)
+    check(few_values(V, VALUES[1], dtype), [0.0, 0.3, 0.77, MOST], top_p=0.9)
+    # and between two 16-byte units
+    u = torch.tensor([[0.4]], device="cuda")
+    a, b = (rnnt_sample(t[None, None], u * 0, u, top_p=0.8)[1] for t in (x.cuda(), torch.cat([x[:1], x]).cuda()[1:]))
+    assert torch.equal(a, b)
